@@ -1,0 +1,744 @@
+// Decoding over a paged key/value cache, and writing tokens into its pages.
+//
+// Decode: one new query token per sequence, so each K and V row is used by
+// the H / h_kv query heads of its group and then never again: 4 d bytes a
+// token and K/V head against 4 d G flops, far below the tensor core's
+// balance.  The bound is HBM, and the kernel is built to keep loads in
+// flight: cp.async into per-warp rings in shared memory, no barrier between
+// the warps while they stream.  The products run on mma.sync m16n8k16 with
+// the group's heads as the 16 rows of a tile (a tcgen05 tile would be 128
+// rows, of which a group fills 1 to 16, and its tensor-memory round trip
+// costs more than the products).
+//
+//   s_j = scale q.k_j,  m = max s_j,  l = sum exp(s_j - m),
+//   O = sum exp(s_j - m) v_j / l,  LSE = m + ln l
+// over the visible keys, in one pass with the running m and l (fp32); P is
+// rounded to bf16 for the P V product (half a step, 2^-9 of a weight), l adds
+// the unrounded values, O stays in fp32 registers.
+//
+// Work split.  A tile is 64 token positions of one (sequence, K/V head, 16
+// query heads).  Every CTA computes the same prefix sums over kv_len and takes
+// tiles [c T / G, (c + 1) T / G) of the T there are: equal shares whatever
+// the lengths, a pure function of kv_len.  A share may end inside a (sequence,
+// head): such a part leaves its normalised O and LSE (base 2) in the
+// workspace, at most two parts a CTA, and a second kernel joins them,
+//   LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i,
+// in the order of the CTAs.  Loads run ahead across the boundary between two
+// heads or sequences.
+#include <climits>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/fa.h"
+#include "fa_internal.h"
+#include "fa_paged.cuh"
+#include "fa_window.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace ptx;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kWarpTokens = 16;                   // tokens of a warp's stage (the K of P V)
+constexpr int kTileTokens = kWarps * kWarpTokens;
+constexpr int kRows = 16;                         // query heads of a tile (M of the mma)
+
+struct DecodeParams {
+  PagePool pool;
+  const __nv_bfloat16* q;       // [B, H, d]
+  __nv_bfloat16* o;             // [B, H, d]
+  float* lse;                   // [B, H]
+  const int* table;             // [B, max_pages]
+  const int* kv_len;            // [B]
+  int max_pages, max_len;       // max_len = max_pages * page_size
+  int B, H, group, row_tiles;   // group = H / h_kv, row_tiles = ceil(group / 16)
+  int wl, sinks;
+  float scale_log2;
+  int parts;                    // CTAs of the split kernel
+  float* o_part;                // [2 parts, 16, d]
+  float* lse_part;              // [2 parts, 16]
+};
+
+// The visible tiles of a sequence: `first` tiles from position 0 (the sinks),
+// then the tiles from `shift` further on (the window) to the end.
+struct Span {
+  int len, lo;                  // visible: pos < len and (pos >= lo or pos < sinks)
+  int first, shift, tiles;
+};
+
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
+  Span s;
+  int len = __ldg(p.kv_len + b);
+  len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
+  s.len = len;
+  s.lo = len - 1 - p.wl > 0 ? len - 1 - p.wl : 0;
+  const int send = p.sinks < s.lo ? p.sinks : s.lo;
+  const int w0 = s.lo / kTileTokens;
+  const int ns = (send + kTileTokens - 1) / kTileTokens;
+  s.first = ns < w0 ? ns : w0;
+  s.shift = w0 - s.first;
+  s.tiles = len > 0 ? s.first + (len + kTileTokens - 1) / kTileTokens - w0 : 0;
+  return s;
+}
+
+// A place in the order of tiles: sequence, then (K/V head, row tile), then
+// tile.
+struct Cursor {
+  int b, hr, tile;
+  Span s;
+};
+
+__device__ __forceinline__ void cursor_at(const DecodeParams& p, int b, int rem, Cursor& c) {
+  c.b = b;
+  c.s = span_of(p, b);
+  c.hr = rem / c.s.tiles;
+  c.tile = rem - c.hr * c.s.tiles;
+}
+
+// The next tile; the caller knows that there is one.
+__device__ __forceinline__ void cursor_next(const DecodeParams& p, Cursor& c) {
+  if (++c.tile < c.s.tiles) return;
+  c.tile = 0;
+  if (++c.hr < p.pool.h_kv * p.row_tiles) return;
+  c.hr = 0;
+  do {
+    ++c.b;
+    c.s = span_of(p, c.b);
+  } while (c.s.tiles == 0 && c.b + 1 < p.B);
+}
+
+// Sum over the block of v (and the sum before this thread), through `warp_sum`.
+template <int THREADS>
+__device__ __forceinline__ int block_scan(int v, int* warp_sum, int& before) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int total = 0, pre = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) pre += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before = pre + x - v;
+  return total;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct DecodeCfg {
+  static constexpr int ROW = 2 * D;                        // bytes of a token's K or V row
+  static constexpr int HALF = kWarpTokens * ROW;           // K (or V) of a stage
+  static constexpr int STAGE = 2 * HALF;
+  // 96 KB of loads in flight a CTA and two CTAs an SM (d = 256: 192 KB, one)
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int CTAS = D == 256 ? 1 : 2;
+  static constexpr bool QREG = D <= 128;                   // Q fragments in registers
+  static constexpr int RED = 40;                           // floats of a reduction row (32 + pad)
+};
+
+template <int D>
+struct DecodeSmem {
+  using C = DecodeCfg<D>;
+  alignas(128) uint8_t ring[kWarps][C::STAGES][C::STAGE];
+  alignas(128) uint8_t q[kRows * C::ROW];
+  float red[kWarps][kRows][C::RED];
+  float ml[kWarps][kRows][2];
+  uint32_t vis[kWarps][C::STAGES];
+  int warp_sum[kWarps];
+  int start_b, start_rem;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
+    paged_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using C = DecodeCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  DecodeSmem<D>& sm = *reinterpret_cast<DecodeSmem<D>*>(smem_raw);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int heads = p.pool.h_kv * p.row_tiles;
+  launch_dependents();
+
+  // ---- this CTA's share of the tiles
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+  int mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += span_of(p, b).tiles;
+  int before;
+  const int total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
+  const int parts = min(p.parts, total);
+  const int cta = blockIdx.x;
+  if (cta >= parts) return;
+  const int ta = static_cast<int>(static_cast<long long>(cta) * total / parts);
+  const int tb = static_cast<int>(static_cast<long long>(cta + 1) * total / parts);
+  if (ta >= before * heads && ta < (before + mine) * heads) {
+    int b = b_lo, base = before * heads;
+    for (;; ++b) {
+      const int n = span_of(p, b).tiles * heads;
+      if (ta < base + n) break;
+      base += n;
+    }
+    sm.start_b = b;
+    sm.start_rem = ta - base;
+  }
+  __syncthreads();
+  const int count = tb - ta;
+
+  // ---- the loading side: one tile ahead, the page of this lane's token
+  Cursor next;
+  cursor_at(p, sm.start_b, sm.start_rem, next);
+  const int tok = lane & 15;
+  int page = -1;                 // page number of the prefetched token
+  long long part_off = 0;        // its slot's and head's offset
+  auto look_up = [&]() {
+    const int t = next.tile < next.s.first ? next.tile : next.tile + next.s.shift;
+    const int pos = t * kTileTokens + warp * kWarpTokens + tok;
+    page = -1;
+    if (pos < next.s.len && (pos >= next.s.lo || pos < p.sinks)) {
+      const int j = static_cast<int>(static_cast<unsigned>(pos) /
+                                     static_cast<unsigned>(p.pool.page_size));
+      page = __ldg(p.table + static_cast<size_t>(next.b) * p.max_pages + j);
+      part_off = static_cast<long long>(pos - j * p.pool.page_size) * p.pool.token_stride +
+                 static_cast<long long>(next.hr / p.row_tiles) * p.pool.head_stride;
+    }
+  };
+  const uint32_t ring = smem_u32(sm.ring[warp][0]);
+  int looked = 0, issued = 0;
+  look_up();
+  looked = 1;
+  // issues the prefetched tile's loads into its stage and prefetches the next
+  auto issue = [&]() {
+    if (issued < count) {
+      const int slot = issued % C::STAGES;
+      const bool ok = page >= 0 && page < p.pool.num_pages;
+      const long long off = ok ? page * p.pool.page_stride + part_off : 0;
+      const uint32_t vis = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      if (lane == 0) sm.vis[warp][slot] = vis;
+      if (looked < count) {
+        cursor_next(p, next);
+        look_up();
+        ++looked;
+      }
+      if (vis) {
+        constexpr int CH = C::ROW / 16;             // 16-byte chunks of a row
+        constexpr int RPI = 32 / CH;                // rows of one warp instruction
+        const uint32_t dst = ring + slot * C::STAGE;
+#pragma unroll
+        for (int r = 0; r < kWarpTokens / RPI; ++r) {
+          const int row = r * RPI + (RPI > 1 ? lane / CH : 0);
+          const int ch = lane % CH;
+          const long long ro = __shfl_sync(0xffffffffu, off, row);
+          const int bytes = (vis >> row) & 1u ? 16 : 0;    // 0: the row is filled with zeros
+          const uint32_t d = dst + row * C::ROW + ((ch ^ (row & 7)) << 4);
+          cp_async16(d, p.pool.k + ro + ch * 8, bytes);
+          cp_async16(d + C::HALF, p.pool.v + ro + ch * 8, bytes);
+        }
+      }
+      ++issued;
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::STAGES - 1; ++i) issue();
+
+  // ---- the computing side
+  Cursor cur;
+  cursor_at(p, sm.start_b, sm.start_rem, cur);
+  int seg0 = ta - cur.tile;      // first tile of the current (sequence, head, row tile)
+  const int g = lane / 4, t4 = lane % 4;
+  float acc[D / 8][4];
+  float m[2], l[2];
+  uint32_t qf[C::QREG ? D / 16 : 1][4];
+  const uint32_t qs = smem_u32(sm.q);
+  auto q_addr = [&](int ks) {
+    const int row = lane & 15;
+    return qs + row * C::ROW + (((2 * ks + lane / 16) ^ (row & 7)) << 4);
+  };
+  bool fresh = true;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const int kvh = cur.hr / p.row_tiles, rt = cur.hr - kvh * p.row_tiles;
+    const int rows = min(kRows, p.group - rt * kRows);
+    const size_t row0 = static_cast<size_t>(cur.b) * p.H + kvh * p.group + rt * kRows;
+    if (fresh) {
+      fresh = false;
+      // Q of the group into shared memory (rows past it zero), then registers
+      for (int e = threadIdx.x; e < kRows * (C::ROW / 16); e += kThreads) {
+        const int row = e / (C::ROW / 16), ch = e % (C::ROW / 16);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + row) * D) + ch);
+        *reinterpret_cast<uint4*>(sm.q + row * C::ROW + ((ch ^ (row & 7)) << 4)) = x;
+      }
+      __syncthreads();
+      if constexpr (C::QREG) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) ldsm_x4(qf[ks], q_addr(ks));
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+    }
+    cp_async_wait<C::STAGES - 2>();
+    __syncwarp();
+    const int slot = i % C::STAGES;
+    const uint32_t vis = sm.vis[warp][slot];
+    issue();                     // into the stage that the previous tile left
+    if (vis) {
+      const uint32_t kb = ring + slot * C::STAGE;
+      float s[2][2][4];          // [even and odd k steps][n tile]
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[a][n][e] = 0.f;
+      {
+        const int row = (lane / 16) * 8 + (lane & 7);
+        const uint32_t ka = kb + row * C::ROW;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t bf[4];
+          ldsm_x4(bf, ka + (((2 * ks + ((lane / 8) & 1)) ^ (row & 7)) << 4));
+          if constexpr (C::QREG) {
+            mma16816(s[ks & 1][0], qf[ks], bf[0], bf[1]);
+            mma16816(s[ks & 1][1], qf[ks], bf[2], bf[3]);
+          } else {
+            uint32_t af[4];
+            ldsm_x4(af, q_addr(ks));
+            mma16816(s[ks & 1][0], af, bf[0], bf[1]);
+            mma16816(s[ks & 1][1], af, bf[2], bf[3]);
+          }
+        }
+      }
+      // rows g (elements 0, 1) and g + 8 (2, 3); columns 8 n + 2 t4 + {0, 1}
+      float x[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool on = (vis >> (8 * n + 2 * t4 + (e & 1))) & 1u;
+          x[n][e] = on ? (s[0][n][e] + s[1][n][e]) * p.scale_log2 : -INFINITY;
+        }
+      float base[2];
+      bool moved = false;
+      float alpha[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], mx);
+        alpha[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
+        moved = moved || mn > m[r];
+        m[r] = mn;
+        base[r] = mn == -INFINITY ? 0.f : mn;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        l[0] *= alpha[0];
+        l[1] *= alpha[1];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          acc[n][0] *= alpha[0];
+          acc[n][1] *= alpha[0];
+          acc[n][2] *= alpha[1];
+          acc[n][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[n][e] = ex2_approx(x[n][e] - base[e / 2]);
+          l[e / 2] += x[n][e];
+        }
+      uint32_t pf[4] = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
+                        pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
+      {
+        const int row = ((lane / 8) & 1) * 8 + (lane & 7);
+        const uint32_t va = kb + C::HALF + row * C::ROW;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t bf[4];
+          ldsm_x4_t(bf, va + (((2 * j + lane / 16) ^ (row & 7)) << 4));
+          mma16816(acc[2 * j], pf, bf[0], bf[1]);
+          mma16816(acc[2 * j + 1], pf, bf[2], bf[3]);
+        }
+      }
+    }
+    __syncwarp();                // every lane has read the stage
+    const bool ends = cur.tile + 1 == cur.s.tiles;
+    if (!ends && i + 1 < count) {
+      ++cur.tile;
+      continue;
+    }
+    // ---- the end of a (sequence, head) or of the share: merge the warps
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t4 == 0) {
+        sm.ml[warp][g + 8 * r][0] = m[r];
+        sm.ml[warp][g + 8 * r][1] = l[r];
+      }
+    }
+    const bool whole = seg0 >= ta && ends;
+    const int part = 2 * cta + (seg0 > ta ? 1 : 0);
+    const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
+    float w[kWarps], lse2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        *reinterpret_cast<float2*>(&sm.red[warp][g][8 * n + 2 * t4]) =
+            make_float2(acc[4 * c + n][0], acc[4 * c + n][1]);
+        *reinterpret_cast<float2*>(&sm.red[warp][g + 8][8 * n + 2 * t4]) =
+            make_float2(acc[4 * c + n][2], acc[4 * c + n][3]);
+      }
+      __syncthreads();
+      if (row < rows) {
+        if (c == 0) {
+          float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm.ml[k][row][0]);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float mk = sm.ml[k][row][0];
+            w[k] = mk == -INFINITY ? 0.f : ex2_approx(mk - mx);
+            sum += w[k] * sm.ml[k][row][1];
+          }
+          // a NaN sum (a NaN score) stays one
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) w[k] *= inv;
+          lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(&sm.red[k][row][col]);
+          x.x = fmaf(w[k], y.x, x.x);
+          x.y = fmaf(w[k], y.y, x.y);
+          x.z = fmaf(w[k], y.z, x.z);
+          x.w = fmaf(w[k], y.w, x.w);
+        }
+        if (whole) {
+          *reinterpret_cast<uint2*>(p.o + (row0 + row) * D + 32 * c + col) =
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+        } else {
+          *reinterpret_cast<float4*>(p.o_part + (static_cast<size_t>(part) * kRows + row) * D +
+                                     32 * c + col) = x;
+        }
+      }
+      __syncthreads();
+    }
+    if (row < rows && col == 0) {
+      if (whole)
+        p.lse[row0 + row] = lse2 * 0.69314718055994531f;
+      else
+        p.lse_part[part * kRows + row] = lse2;
+    }
+    if (i + 1 < count) {
+      seg0 = ta + i + 1;
+      cursor_next(p, cur);
+      fresh = true;
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the parts of every (sequence, head, row tile) that the split kernel
+// left in more than one, and writes O = 0, LSE = -inf for sequences without
+// tiles.  Launched as a dependent of the split kernel: the prefix sums, which
+// read kv_len alone, overlap it.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ int warp_sum[8];
+  __shared__ int upto;
+  __shared__ float w_sum[8];
+  __shared__ float w_acc[8][D];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int heads = p.pool.h_kv * p.row_tiles;
+  const int b = blockIdx.x / heads, hr = blockIdx.x % heads;
+  const int per = (p.B + 255) / 256;
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+  int mine = 0, at = 0;
+  for (int x = b_lo; x < b_hi; ++x) {
+    if (x == b) at = mine;
+    mine += span_of(p, x).tiles;
+  }
+  int before;
+  const int total = block_scan<256>(mine, warp_sum, before) * heads;
+  if (b >= b_lo && b < b_hi) upto = before + at;
+  __syncthreads();
+  const int tiles = span_of(p, b).tiles;
+  const int kvh = hr / p.row_tiles, rt = hr - kvh * p.row_tiles;
+  const int rows = min(kRows, p.group - rt * kRows);
+  const size_t row0 = static_cast<size_t>(b) * p.H + kvh * p.group + rt * kRows;
+  int c0 = 0, n = 0;
+  bool second = false;           // part 0 is its CTA's second
+  if (tiles > 0) {
+    const long long parts = min(p.parts, total);
+    const long long t0 = static_cast<long long>(upto) * heads + static_cast<long long>(hr) * tiles;
+    c0 = static_cast<int>(((t0 + 1) * parts - 1) / total);
+    n = static_cast<int>(((t0 + tiles) * parts - 1) / total) - c0 + 1;
+    second = c0 * static_cast<long long>(total) / parts != t0;
+  }
+  // every CTA waits, also one with nothing to join: work behind this grid in
+  // the stream then finds the split kernel complete
+  grid_dependency_wait();
+  if (n == 1) return;            // whole in one CTA
+  // a warp takes a row, or with fewer than eight rows every k-th part of one
+  const int k = rows >= 8 ? 1 : (rows >= 3 ? 2 : (rows == 2 ? 4 : 8));
+  constexpr int PER = D / 32;
+  for (int r0 = 0; r0 < rows; r0 += 8 / k) {
+    const int row = r0 + warp / k, sub = warp % k;
+    float mx = -INFINITY, sum = 0.f, acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    if (row < rows) {
+      auto slot = [&](int i) {
+        return static_cast<size_t>(2 * (c0 + i) + (i == 0 && second ? 1 : 0)) * kRows + row;
+      };
+      for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.lse_part[slot(i)]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+      for (int i = sub; i < n; i += k) {
+        const size_t s = slot(i);
+        const float w = ex2_approx(p.lse_part[s] - base);
+        sum += w;
+        const float* src = p.o_part + s * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+      }
+    }
+    if (k > 1) {
+      w_sum[warp] = sum;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) w_acc[warp][lane * PER + e] = acc[e];
+      __syncthreads();
+      if (sub == 0) {
+        for (int o = 1; o < k; ++o) {
+          sum += w_sum[warp + o];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[e] += w_acc[warp + o][lane * PER + e];
+        }
+      }
+      __syncthreads();
+    }
+    if (sub == 0 && row < rows) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + lane * PER);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0)
+        p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
+  constexpr int smem = sizeof(DecodeSmem<D>);
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<D><<<p.parts, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.pool.h_kv * p.row_tiles);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+}
+
+// CTAs of the split kernel: as many as are resident at once.
+int decode_parts(int d, int num_sms) { return num_sms * (d == 256 ? 1 : 2); }
+
+size_t part_floats(int d, int num_sms) {
+  return static_cast<size_t>(2) * decode_parts(d, num_sms) * kRows;
+}
+
+// New tokens into pages: a thread copies 16 bytes of K and of V.  Bound by
+// the copied bytes; every row is contiguous on both sides.
+template <int D>
+__global__ void __launch_bounds__(256)
+    paged_append_kernel(const __grid_constant__ PagePool pool, const uint4* __restrict__ k_new,
+                        const uint4* __restrict__ v_new, const int* __restrict__ table,
+                        int max_pages, const int* __restrict__ start,
+                        const int* __restrict__ kv_len, int Nq, int bh_count) {
+  constexpr int CH = D / 8;
+  const unsigned e = blockIdx.x * 256u + threadIdx.x;   // the launch keeps Nq * CH below 2^31
+  const int t = static_cast<int>(e / CH), ch = static_cast<int>(e % CH);
+  if (t >= Nq) return;
+  for (int bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
+    const int b = bh / pool.h_kv, h = bh - b * pool.h_kv;
+    const long long at = static_cast<long long>(__ldg(start + b)) + t;
+    if (at < 0 || at >= __ldg(kv_len + b)) continue;
+    const int pos = static_cast<int>(at);
+    const int j = pos / pool.page_size;
+    if (j >= max_pages) continue;
+    const int page = __ldg(table + static_cast<size_t>(b) * max_pages + j);
+    if (page < 0 || page >= pool.num_pages) continue;
+    const long long dst = page * pool.page_stride + h * pool.head_stride +
+                          (pos - j * pool.page_size) * pool.token_stride + ch * 8;
+    const size_t src = (static_cast<size_t>(bh) * Nq + t) * CH + ch;
+    const uint4 a = __ldg(k_new + src), c = __ldg(v_new + src);
+    *reinterpret_cast<uint4*>(pool.k + dst) = a;
+    *reinterpret_cast<uint4*>(pool.v + dst) = c;
+  }
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d) {
+  if (H < 1 || h_kv < 1 || H % h_kv || (d != 64 && d != 128 && d != 256)) return 0;
+  int sms = 0;
+  if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
+  const size_t rows = fa::part_floats(d, sms);
+  return rows * d * sizeof(float) + (rows * sizeof(float) + 255) / 256 * 256;
+}
+
+fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer,
+                            const int* block_table, int max_pages, const int* kv_len, void* o,
+                            float* lse, int B, int H, float scale, int window_left, int sinks,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !o || !lse || !kv_len || !workspace || layer < 0) return FA_ERR_INVALID_ARG;
+  if (!fa::aligned_to(q, 16) || !fa::aligned_to(o, 16) || !fa::aligned_to(lse, 4) ||
+      !fa::aligned_to(kv_len, 4) || !fa::aligned_to(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  fa::DecodeParams p;
+  const fa_status_t ps = fa::resolve_pool(cache, layer, &p.pool);
+  if (ps != FA_OK) return ps;
+  if (!fa::table_ok(block_table, max_pages, p.pool.page_size)) return FA_ERR_INVALID_ARG;
+  if (B < 1 || H < 1 || H % p.pool.h_kv || window_left < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f && scale <= 3.402823466e38f)) return FA_ERR_INVALID_ARG;
+  p.group = H / p.pool.h_kv;
+  p.row_tiles = (p.group + fa::kRows - 1) / fa::kRows;
+  p.max_len = max_pages * p.pool.page_size;
+  const long long heads = static_cast<long long>(p.pool.h_kv) * p.row_tiles;
+  const long long tiles = (p.max_len + fa::kTileTokens - 1) / fa::kTileTokens;
+  if (static_cast<long long>(B) * H >= INT_MAX || B * heads >= INT_MAX / tiles)
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_decode_paged_workspace_bytes(H, p.pool.h_kv, p.pool.d))
+    return FA_ERR_INVALID_ARG;
+  int sms = 0;
+  const fa_status_t ds = fa::device_facts(&sms, nullptr);
+  if (ds != FA_OK) return ds;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.table = block_table;
+  p.kv_len = kv_len;
+  p.max_pages = max_pages;
+  p.B = B;
+  p.H = H;
+  p.wl = window_left < 0 || window_left > fa::kUnbounded ? fa::kUnbounded : window_left;
+  p.sinks = sinks;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.parts = fa::decode_parts(p.pool.d, sms);
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = p.o_part + fa::part_floats(p.pool.d, sms) * p.pool.d;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (p.pool.d) {
+    case 64: e = fa::launch_decode_t<64>(p, s); break;
+    case 128: e = fa::launch_decode_t<128>(p, s); break;
+    default: e = fa::launch_decode_t<256>(p, s); break;
+  }
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged_kv_t* cache,
+                            int layer, const int* block_table, int max_pages, const int* start,
+                            const int* kv_len, int B, int Nq, void* stream) {
+  if (!k_new || !v_new || !start || !kv_len || layer < 0) return FA_ERR_INVALID_ARG;
+  if (!fa::aligned_to(k_new, 16) || !fa::aligned_to(v_new, 16) || !fa::aligned_to(start, 4) ||
+      !fa::aligned_to(kv_len, 4))
+    return FA_ERR_INVALID_ARG;
+  fa::PagePool pool;
+  const fa_status_t ps = fa::resolve_pool(cache, layer, &pool);
+  if (ps != FA_OK) return ps;
+  if (!fa::table_ok(block_table, max_pages, pool.page_size)) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Nq < 1 || Nq >= fa::kMaxPositions) return FA_ERR_INVALID_ARG;
+  const long long bh = static_cast<long long>(B) * pool.h_kv;
+  const long long vec = static_cast<long long>(Nq) * (pool.d / 8);
+  if (vec >= INT_MAX - 256 || bh >= INT_MAX) return FA_ERR_INVALID_ARG;
+  const fa_status_t ds = fa::device_facts(nullptr, nullptr);
+  if (ds != FA_OK) return ds;
+  const uint4* kn = static_cast<const uint4*>(k_new);
+  const uint4* vn = static_cast<const uint4*>(v_new);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int rows = static_cast<int>(bh);
+  const dim3 grid(static_cast<unsigned>((vec + 255) / 256), rows < 65535 ? rows : 65535);
+  switch (pool.d) {
+    case 64:
+      fa::paged_append_kernel<64><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages, start,
+                                                       kv_len, Nq, rows);
+      break;
+    case 128:
+      fa::paged_append_kernel<128><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages,
+                                                        start, kv_len, Nq, rows);
+      break;
+    default:
+      fa::paged_append_kernel<256><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages,
+                                                        start, kv_len, Nq, rows);
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,53 @@
+// What the paged-cache kernels share: the pool's layout as the kernels see it
+// and the host checks of the public structure.
+#pragma once
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// One layer of the pool, or (layers > 1) all of them.
+struct PagePool {
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  long long layer_stride, page_stride, head_stride, token_stride;   // elements
+  int layers, num_pages, page_size, h_kv, d;
+};
+
+constexpr long long kMaxPositions = 1ll << 30;   // max_pages * page_size stays below
+
+inline bool aligned_to(const void* p, unsigned n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// The structure's own rules (see fa.h); *out is layer `layer`, or the whole
+// pool when layer < 0.
+inline fa_status_t resolve_pool(const fa_paged_kv_t* c, int layer, PagePool* out) {
+  if (!c || !c->k || !c->v || !aligned_to(c->k, 16) || !aligned_to(c->v, 16))
+    return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED;
+  if (c->num_layers < 1 || c->num_pages < 1 || c->page_size < 1 || c->h_kv < 1 ||
+      c->page_size >= kMaxPositions || layer >= c->num_layers ||
+      static_cast<long long>(c->num_layers) * c->h_kv > 0x7fffffffll)
+    return FA_ERR_INVALID_ARG;
+  const long long st[4] = {c->layer_stride, c->page_stride, c->head_stride, c->token_stride};
+  for (long long s : st)
+    if (s < 0 || (s & 7)) return FA_ERR_INVALID_ARG;
+  const long long off = layer > 0 ? layer * c->layer_stride : 0;
+  *out = PagePool{static_cast<__nv_bfloat16*>(c->k) + off, static_cast<__nv_bfloat16*>(c->v) + off,
+                  c->layer_stride, c->page_stride, c->head_stride, c->token_stride,
+                  layer < 0 ? c->num_layers : 1, c->num_pages, c->page_size, c->h_kv, c->d};
+  return FA_OK;
+}
+
+// A block table over the pool: its width and address.
+inline bool table_ok(const int* table, int max_pages, int page_size) {
+  return table && aligned_to(table, 4) && max_pages >= 1 &&
+         static_cast<long long>(max_pages) * page_size < kMaxPositions;
+}
+
+}  // namespace fa

@@ -32,6 +32,16 @@ class FaVariant(ctypes.Structure):
                 ("block_mask_host", ctypes.c_void_p)]
 
 
+class FaPagedKV(ctypes.Structure):
+    """fa_paged_kv_t: the K and V pools, their strides in elements, and their
+    sizes (see include/fa.h; paged.PagedKV fills one from two tensors)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("num_layers", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
 class BlockMask:
     """A block mask on the device together with its host copy.  Any function
     taking block_mask= accepts one in place of the CUDA tensor; the library
@@ -93,6 +103,23 @@ def load():
         lib.fa_fp8_quantize.restype = i
         lib.fa_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, varp, vp]
         lib.fa_fwd_fp8.restype = i
+        pool = ctypes.POINTER(FaPagedKV)
+        lib.fa_decode_paged_workspace_bytes.argtypes = [i, i, i]
+        lib.fa_decode_paged_workspace_bytes.restype = sz
+        lib.fa_decode_paged.argtypes = [vp, pool, i, vp, i, vp, vp, vp, i, i, f, i, i, vp, sz, vp]
+        lib.fa_decode_paged.restype = i
+        lib.fa_paged_append.argtypes = [vp, vp, pool, i, vp, i, vp, vp, i, i, vp]
+        lib.fa_paged_append.restype = i
+        lib.fa_pages_workspace_bytes.argtypes = [i, i]
+        lib.fa_pages_workspace_bytes.restype = sz
+        lib.fa_pages_reserve.argtypes = [vp, i, i, vp, vp, vp, i, i, vp, vp, vp, vp, sz, vp]
+        lib.fa_pages_reserve.restype = i
+        lib.fa_pages_fork.argtypes = [pool, vp, i, vp, vp, i, vp, i, vp, vp, vp, vp, vp, sz, vp]
+        lib.fa_pages_fork.restype = i
+        lib.fa_pages_trim.argtypes = [vp, i, i, vp, vp, i, i, i, i, vp, vp, vp]
+        lib.fa_pages_trim.restype = i
+        lib.fa_pages_compact.argtypes = [pool, vp, i, vp, i, vp, vp, vp, vp, sz, vp]
+        lib.fa_pages_compact.restype = i
         lib.fa_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
         lib.fa_selftest_wait_timeout.restype = i
         lib.fa_check.argtypes = [vp]
@@ -108,6 +135,9 @@ def load():
 EXPORTS = ("fa_fwd", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_prep", "fa_bwd_dkdv",
            "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_v", "fa_bwd_v", "fa_bwd_dkdv_v",
            "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode",
+           "fa_decode_paged_workspace_bytes", "fa_decode_paged", "fa_paged_append",
+           "fa_pages_workspace_bytes", "fa_pages_reserve", "fa_pages_fork", "fa_pages_trim",
+           "fa_pages_compact",
            "fa_fp8_quantize", "fa_fwd_fp8", "fa_selftest_wait_timeout", "fa_check",
            "fa_status_string", "fa_version")
 

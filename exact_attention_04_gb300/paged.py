@@ -1,0 +1,243 @@
+"""A key/value cache in pages: decoding over it, writing into it, and keeping it.
+
+``PagedKV`` wraps the K and V pools; the functions here take it with a block
+table, the rows' lengths and the pages' reference counts (int32 CUDA tensors)
+and call the C ABI (include/fa.h states each call's rules).  Nothing
+synchronises or copies to the host.  Outputs are allocated with torch on the
+stream that the call runs on; all tensors live on the current CUDA device.
+
+A serving loop::
+
+    cache = PagedKV(k_pool, v_pool)            # [layers, pages, h_kv, page_size, d]
+    table, kv_len, ref = cache.empty(rows=64, max_pages=512)
+    new_len, ref, info = reserve(cache, table, kv_len, ref, n_new)
+    for layer in range(cache.num_layers):
+        append(k_new, v_new, cache, layer, table, kv_len, new_len)
+        o, lse = decode(q, cache, layer, table, new_len, window=(4095, 0), sinks=4)
+    kv_len = new_len
+    table, ref = trim(cache, table, kv_len, ref, 4095, 4)
+    table, kv_len, ref, info = fork(cache, table, kv_len, ref, parent)
+"""
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from . import fa
+
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The context that outputs are allocated in, and the raw stream."""
+    if stream is None:
+        return _NO_STREAM, torch.cuda.current_stream().cuda_stream
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+class PagedKV:
+    """The K and V pools: two bf16 CUDA tensors [layers, pages, h_kv,
+    page_size, d] (or [pages, h_kv, page_size, d], one layer) of the same shape
+    and strides, d contiguous and the other strides multiples of 8 (a
+    transposed view of [layers, pages, page_size, h_kv, d] serves as well).
+    Holds the tensors and the structure that the library reads."""
+
+    def __init__(self, k, v):
+        if k.dim() == 4:
+            k, v = k[None], v[None]
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != torch.bfloat16 \
+                or v.dtype != torch.bfloat16 or not k.is_cuda or k.device != v.device:
+            raise ValueError("k, v: expected bf16 CUDA tensors [layers, pages, h_kv, page_size, "
+                             "d] of one shape")
+        strides = [s if n > 1 else 0 for n, s in zip(k.shape, k.stride())]
+        if strides != [s if n > 1 else 0 for n, s in zip(v.shape, v.stride())]:
+            raise ValueError("k, v: the strides differ")
+        if k.numel() == 0:
+            raise ValueError("k, v: empty pools")
+        if strides[4] != 1 or any(s % 8 or (s == 0 and n > 1)
+                                  for n, s in zip(k.shape[:4], strides)):
+            raise ValueError("k, v: d must be contiguous and the other strides multiples of 8")
+        if k.data_ptr() % 16 or v.data_ptr() % 16:
+            raise ValueError("k, v: expected 16-byte aligned pools")
+        self.k, self.v = k, v
+        self.num_layers, self.num_pages, self.h_kv, self.page_size, self.d = k.shape
+        self.device = k.device
+        self.index = k.get_device()
+        self.struct = fa.FaPagedKV(k.data_ptr(), v.data_ptr(), *strides[:4], self.num_layers,
+                                   self.num_pages, self.page_size, self.h_kv, self.d)
+        self.ref = ctypes.byref(self.struct)
+        self.scale = 1.0 / math.sqrt(self.d)
+
+    def empty(self, rows, max_pages):
+        """(table, kv_len, ref) of a cache without tokens."""
+        ints = dict(dtype=torch.int32, device=self.device)
+        return (torch.full((rows, max_pages), -1, **ints), torch.zeros(rows, **ints),
+                torch.zeros(self.num_pages, **ints))
+
+
+def _ints(name, t, shape, index):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() \
+            or t.get_device() != index:
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor {list(shape)} on the "
+                         "cache's device")
+    return t.data_ptr()
+
+
+def _table(cache, table):
+    if table.dim() != 2:
+        raise ValueError("table: expected int32 [rows, max_pages]")
+    if cache.index != torch.cuda.current_device():
+        raise ValueError("the cache is not on the current CUDA device")
+    return _ints("table", table, table.shape, cache.index), table.shape[0], table.shape[1]
+
+
+def _check(status, where):
+    if status:
+        raise fa.FAError(status, where)
+
+
+def _bytes(ws, need):
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous CUDA tensor")
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} bytes are needed")
+    return ws.data_ptr()
+
+
+def workspace(cache, rows=1):
+    """A workspace for reserve, fork and compact of up to `rows` rows."""
+    n = fa.load().fa_pages_workspace_bytes(cache.num_pages, rows)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def decode_workspace(cache, H):
+    """A workspace for decode with H query heads."""
+    n = fa.load().fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=None, stream=None):
+    """(O, LSE): attention of each row's newest token (position kv_len - 1)
+    over its pages; q [B, H, 1, d], O like q, LSE fp32 [B, H, 1].  window:
+    (left, right), of which only left matters here, or None; sinks: first
+    tokens that stay visible.  ws: decode_workspace(), else allocated."""
+    tp, rows, max_pages = _table(cache, table)
+    if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.shape[0] != rows or q.shape[2] != 1 \
+            or q.shape[3] != cache.d or not q.is_contiguous() or q.get_device() != cache.index:
+        raise ValueError("q: expected a contiguous bf16 CUDA tensor [rows, H, 1, d]")
+    lp = _ints("kv_len", kv_len, (rows,), cache.index)
+    H = q.shape[1]
+    lib = fa.load()
+    need = lib.fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
+    ctx, raw = _on(stream)
+    with ctx:
+        o = torch.empty_like(q)
+        lse = torch.empty((rows, H, 1), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib.fa_decode_paged(q.data_ptr(), cache.ref, layer, tp, max_pages, lp, o.data_ptr(),
+                               lse.data_ptr(), rows, H, cache.scale if scale is None else scale,
+                               -1 if window is None else int(window[0]), sinks, _bytes(ws, need),
+                               need, raw), "fa_decode_paged")
+    return o, lse
+
+
+def append(k_new, v_new, cache, layer, table, start, kv_len, stream=None):
+    """Writes k_new, v_new [rows, h_kv, n, d]: token t of a row to position
+    start + t where that is below kv_len."""
+    tp, rows, max_pages = _table(cache, table)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.shape != k_new.shape \
+                or t.shape[0] != rows or t.shape[1] != cache.h_kv or t.shape[3] != cache.d \
+                or not t.is_contiguous() or t.get_device() != cache.index:
+            raise ValueError(f"{name}: expected a contiguous bf16 CUDA tensor [rows, h_kv, n, d]")
+    _check(fa.load().fa_paged_append(k_new.data_ptr(), v_new.data_ptr(), cache.ref, layer, tp,
+                                     max_pages, _ints("start", start, (rows,), cache.index),
+                                     _ints("kv_len", kv_len, (rows,), cache.index), rows,
+                                     k_new.shape[2], _on(stream)[1]), "fa_paged_append")
+
+
+def reserve(cache, table, kv_len, ref, n_new, ws=None, stream=None):
+    """(kv_len, ref, info) after every row has got the pages for n_new more
+    tokens; the table is updated in place.  info = [free pages left, pages that
+    were missing]."""
+    tp, rows, max_pages = _table(cache, table)
+    lib = fa.load()
+    need = lib.fa_pages_workspace_bytes(cache.num_pages, rows)
+    ctx, raw = _on(stream)
+    with ctx:
+        len_out, ref_out = torch.empty_like(kv_len), torch.empty_like(ref)
+        info = torch.empty(2, dtype=torch.int32, device=ref.device)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
+    _check(lib.fa_pages_reserve(tp, max_pages, cache.page_size,
+                                _ints("kv_len", kv_len, (rows,), cache.index),
+                                _ints("n_new", n_new, (rows,), cache.index),
+                                _ints("ref", ref, (cache.num_pages,), cache.index),
+                                cache.num_pages, rows, len_out.data_ptr(), ref_out.data_ptr(),
+                                info.data_ptr(), _bytes(ws, need), need, raw), "fa_pages_reserve")
+    return len_out, ref_out, info
+
+
+def fork(cache, table, kv_len, ref, parent, ws=None, stream=None):
+    """(table, kv_len, ref, info) of the cache whose row r continues row
+    parent[r] (-1: an empty row): beams are reordered, rows forked, and rows
+    that nobody continues freed.  Partly filled pages that several rows
+    continue are copied.  info as of reserve."""
+    tp, rows, max_pages = _table(cache, table)
+    if parent.dim() != 1 or parent.numel() < 1:
+        raise ValueError("parent: expected int32 [new rows]")
+    new_rows = parent.numel()
+    lib = fa.load()
+    need = lib.fa_pages_workspace_bytes(cache.num_pages, max(rows, new_rows))
+    ctx, raw = _on(stream)
+    with ctx:
+        ints = dict(dtype=torch.int32, device=ref.device)
+        table_out = torch.empty((new_rows, max_pages), **ints)
+        len_out, ref_out = torch.empty(new_rows, **ints), torch.empty_like(ref)
+        info = torch.empty(2, **ints)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
+    _check(lib.fa_pages_fork(cache.ref, tp, max_pages,
+                             _ints("kv_len", kv_len, (rows,), cache.index),
+                             _ints("ref", ref, (cache.num_pages,), cache.index), rows,
+                             _ints("parent", parent, (new_rows,), cache.index), new_rows,
+                             table_out.data_ptr(), len_out.data_ptr(), ref_out.data_ptr(),
+                             info.data_ptr(), _bytes(ws, need), need, raw), "fa_pages_fork")
+    return table_out, len_out, ref_out, info
+
+
+def trim(cache, table, kv_len, ref, window_left, sinks=0, stream=None):
+    """(table, ref) without the pages that no later token sees under a window
+    of window_left and `sinks` first tokens."""
+    tp, rows, max_pages = _table(cache, table)
+    ctx, raw = _on(stream)
+    with ctx:
+        table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
+    _check(fa.load().fa_pages_trim(tp, max_pages, cache.page_size,
+                                   _ints("kv_len", kv_len, (rows,), cache.index),
+                                   _ints("ref", ref, (cache.num_pages,), cache.index),
+                                   cache.num_pages, rows, window_left, sinks,
+                                   table_out.data_ptr(), ref_out.data_ptr(), raw),
+           "fa_pages_trim")
+    return table_out, ref_out
+
+
+def compact(cache, table, ref, ws=None, stream=None):
+    """(table, ref, info) after the pages in use have moved to the front of the
+    pool.  info = [pages in use, pages moved]."""
+    tp, rows, max_pages = _table(cache, table)
+    lib = fa.load()
+    need = lib.fa_pages_workspace_bytes(cache.num_pages, rows)
+    ctx, raw = _on(stream)
+    with ctx:
+        table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
+        info = torch.empty(2, dtype=torch.int32, device=ref.device)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
+    _check(lib.fa_pages_compact(cache.ref, tp, max_pages,
+                                _ints("ref", ref, (cache.num_pages,), cache.index), rows,
+                                table_out.data_ptr(), ref_out.data_ptr(), info.data_ptr(),
+                                _bytes(ws, need), need, raw), "fa_pages_compact")
+    return table_out, ref_out, info

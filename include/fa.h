@@ -227,6 +227,152 @@ fa_status_t fa_decode(const void* q, const void* k, const void* v, void* o, floa
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A key/value cache in pages.
+ *
+ * The pool holds num_layers x num_pages pages of page_size tokens, each token
+ * a row of d values for every one of h_kv K/V heads, once for K and once for V
+ * (bf16).  The element (layer, page, head, slot, c) of K is
+ *   k[layer layer_stride + page page_stride + head head_stride +
+ *     slot token_stride + c]
+ * and V has the same layout; the strides count elements and are multiples of
+ * 8 (0 is allowed for an axis of one), so [pages, h_kv, page_size, d],
+ * [pages, page_size, h_kv, d] and views of a larger pool all serve.  Offsets
+ * are 64-bit: a pool may be larger than 2^31 elements.  k and v are 16-byte
+ * aligned; d is 64, 128 or 256; page_size >= 1; num_pages < 2^31.
+ *
+ * A row of the block table (int32 [rows, max_pages], row-major) lists a
+ * sequence's pages: token position x sits in slot x % page_size of page
+ * table[row][x / page_size].  An entry outside [0, num_pages) (by convention
+ * -1) is no page: its tokens are never read or written.  max_pages *
+ * page_size must be below 2^30.  A contiguous cache [B, h_kv, N, d] is the
+ * pool with num_pages = B, page_size = N and the table [[0], [1], ...].
+ *
+ * Integer metadata (table, kv_len, reference counts, free pages) lives in
+ * device memory and every call here only enqueues work, so that serving
+ * steps can be captured into a graph.  No result depends on the order in
+ * which threads run.
+ */
+typedef struct fa_paged_kv {
+  void* k;
+  void* v;
+  long long layer_stride;
+  long long page_stride;
+  long long head_stride;
+  long long token_stride;
+  int num_layers;
+  int num_pages;
+  int page_size;
+  int h_kv;
+  int d;
+} fa_paged_kv_t;
+
+/*
+ * Attention of one new token per sequence over a paged cache, split over the
+ * cache's length and joined.  q and o: bf16 [B, H, d] ([B, H, 1, d] is the
+ * same memory); lse: fp32 [B, H].  Query head h reads K/V head h / (H / h_kv)
+ * (any group size).  kv_len: int32[B], the tokens of each row including the
+ * new one, clamped to [0, max_pages * page_size]; the new token's position is
+ * kv_len - 1.  It sees key j < kv_len whose page exists and, unless
+ * window_left is -1, only j >= kv_len - 1 - window_left or j < sinks (a
+ * sliding window with the first `sinks` tokens kept).  A row that sees no key
+ * gets O = 0, LSE = -inf.  Slots that are not seen may hold anything, NaN
+ * included.  The work is divided among the SMs by the device from kv_len, in
+ * equal shares whatever the lengths; the result repeats bit for bit.
+ *
+ * workspace: fa_decode_paged_workspace_bytes(H, h_kv, d) bytes (0 for
+ * invalid sizes), 256-byte aligned, its contents irrelevant on entry; calls
+ * that may overlap on the GPU need one each.
+ */
+size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d);
+fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer,
+                            const int* block_table, int max_pages, const int* kv_len, void* o,
+                            float* lse, int B, int H, float scale, int window_left, int sinks,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Writes new tokens into the pages of one layer: k_new, v_new are bf16
+ * [B, h_kv, Nq, d], and token t of row b goes to position start[b] + t if
+ * that is at least 0 and below kv_len[b] (both int32[B]; kv_len as
+ * fa_pages_reserve returned it).  Other tokens, and tokens whose page does
+ * not exist, are not written.
+ */
+fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged_kv_t* cache,
+                            int layer, const int* block_table, int max_pages, const int* start,
+                            const int* kv_len, int B, int Nq, void* stream);
+
+/*
+ * Pages of a cache: reserving, forking, freeing, compacting.
+ *
+ * ref: int32[num_pages], for each page the number of table entries that hold
+ * it (the caller may add references of its own); a page with ref = 0 is free.
+ * Of a row only the first ceil(kv_len / page_size) entries count, kv_len
+ * clamped to [0, max_pages * page_size]; an entry outside [0, num_pages) is no
+ * page.  Fresh pages are always the free pages of lowest number, handed out
+ * in the order of rows (within a row, of positions).  info: int32[2], written
+ * by the call.  workspace: fa_pages_workspace_bytes(num_pages, rows) bytes
+ * (rows: the larger of a call's row counts; 0 for invalid sizes), 256-byte
+ * aligned, its contents irrelevant on entry; calls that may overlap on the
+ * GPU need one each.
+ */
+size_t fa_pages_workspace_bytes(int num_pages, int rows);
+
+/*
+ * Gives row r the pages that it needs to grow by n_new[r] tokens (negative
+ * counts as 0; the new length is clamped to max_pages * page_size): entries
+ * from ceil(kv_len / page_size) up to ceil(new length / page_size) of
+ * block_table are overwritten with fresh pages.  kv_len_out: the new lengths.
+ * When the free pages run out, the remaining entries become -1 and the row's
+ * new length ends with its last page.  kv_len_out and ref_out may be kv_len
+ * and ref.  info = {free pages left, pages that were missing}.
+ */
+fa_status_t fa_pages_reserve(int* block_table, int max_pages, int page_size, const int* kv_len,
+                             const int* n_new, const int* ref, int num_pages, int rows,
+                             int* kv_len_out, int* ref_out, int* info, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Row r of the new table continues row parent[r] of the old one (a parent
+ * outside [0, rows) leaves an empty row), so one call reorders beams, forks
+ * rows and frees those that nobody continues.  Full pages are shared.  A
+ * partly filled last page stays with the first row that continues its parent;
+ * every further one gets a fresh page with a copy of the filled slots, K and
+ * V, all layers (slots behind them are left as they were).  Fresh pages are
+ * taken after the old rows' references are gone.  When they run out, the
+ * entry becomes -1 and the row's length ends with its last full page.  Entries
+ * past a row's pages become -1.  table_out [new_rows, max_pages], kv_len_out
+ * [new_rows] and ref_out are buffers of their own.  info = {free pages left,
+ * pages that were missing}.  fa_pages_workspace_bytes takes max(rows,
+ * new_rows).
+ */
+fa_status_t fa_pages_fork(const fa_paged_kv_t* cache, const int* block_table, int max_pages,
+                          const int* kv_len, const int* ref, int rows, const int* parent,
+                          int new_rows, int* table_out, int* kv_len_out, int* ref_out, int* info,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Frees the pages that no later token will see under a window of window_left
+ * (>= 0) and `sinks` first tokens, once the attention of the token at kv_len
+ * - 1 has run: the pages whose tokens all lie at sinks or later and before
+ * kv_len - window_left.  Their entries become -1 and lose their reference.
+ * table_out and ref_out may be block_table and ref.
+ */
+fa_status_t fa_pages_trim(const int* block_table, int max_pages, int page_size,
+                          const int* kv_len, const int* ref, int num_pages, int rows,
+                          int window_left, int sinks, int* table_out, int* ref_out,
+                          void* stream);
+
+/*
+ * Moves the pages in use (ref > 0) to the front of the pool: with n of them,
+ * the k-th page in use at n or later moves into the k-th free page before n,
+ * K and V, all layers.  Tables and references follow (of all `rows` rows,
+ * whole rows; entries outside [0, num_pages) become -1).  table_out and
+ * ref_out may be block_table and ref.  info = {n, pages moved}.
+ */
+fa_status_t fa_pages_compact(const fa_paged_kv_t* cache, const int* block_table, int max_pages,
+                             const int* ref, int rows, int* table_out, int* ref_out, int* info,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * FP8 (E4M3) forward ("4. FlashAttention 深度剖析" 4.5.4: E4M3 operands for
  * the forward, a scale per block applied at load, FP32 accumulation).
  *
