@@ -189,6 +189,43 @@ fa_status_t resolve_variant(const fa_variant_t* var, int H, int causal, Variant*
   return FA_OK;
 }
 
+// A window side past every position is unbounded (so that i +- it stays an
+// int in the kernels).
+void bound_window(Variant* v) {
+  v->wl = std::min(v->wl, fa::kUnbounded);
+  v->wr = std::min(v->wr, fa::kUnbounded);
+}
+
+// How the backward cuts the queries that see a key block only through its
+// sinks (those past the window of the block's last key).  In blocks of 128
+// rows, `far` are left past the first block's window; a chunk is at least as
+// long as a window item (so that items stay alike) and 8 blocks, and there are
+// at most 32 chunks over all sink blocks.  No such block: the window items of
+// the sink blocks run to the last query.
+struct SinkPlan {
+  int nsb, nfar, far_rows;
+};
+
+SinkPlan plan_sinks(int N, int wl, int sinks) {
+  SinkPlan s{0, 0, 0};
+  if (sinks < 1) return s;
+  s.nsb = static_cast<int>((std::min(sinks, N) + 127ll) / 128);
+  const long long T = (N + 127ll) / 128;
+  const long long far = T - (128ll + wl + 127) / 128;
+  if (far < 1) return s;
+  const long long most = std::max(1, 32 / s.nsb);
+  const long long len = std::max({(wl + 127ll) / 128 + 2, 8ll, (far + most - 1) / most});
+  s.nfar = static_cast<int>((far + len - 1) / len);
+  s.far_rows = static_cast<int>(std::min(len, T) * 128);
+  return s;
+}
+
+size_t sink_part_bytes(const SinkPlan& s, long long heads, int d) {
+  if (s.nfar == 0) return 0;
+  return round_up256(static_cast<size_t>(heads) * s.nsb * (s.nfar + 1) * 2 * 128 * d *
+                     sizeof(float));
+}
+
 }  // namespace
 
 namespace fa {
@@ -376,7 +413,7 @@ void plan_mask_tail(const uint8_t* bm_host, int BH, int T, int nsplit, int G, bo
 
 extern "C" {
 
-int fa_version(void) { return 1 * 10000 + 2 * 100 + 0; }
+int fa_version(void) { return 1 * 10000 + 3 * 100 + 0; }
 
 const char* fa_status_string(fa_status_t s) {
   switch (s) {
@@ -395,9 +432,14 @@ fa_status_t fa_fwd(const void* q, const void* k, const void* v, void* o, float* 
   return fa_fwd_v(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, nullptr, stream);
 }
 
-fa_status_t fa_fwd_v(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+}  // extern "C"
+
+namespace {
+
+// fa_fwd_v, and fa_fwd_sinks (sinks >= 0; -1: fa_fwd_v).
+fa_status_t fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                      int H, int N, int d, float scale, int causal, const int* kv_len,
-                     const fa_variant_t* variant, void* stream) {
+                     const fa_variant_t* variant, int sinks, void* stream) {
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
@@ -408,6 +450,10 @@ fa_status_t fa_fwd_v(const void* q, const void* k, const void* v, void* o, float
   Variant var;
   const fa_status_t vs = resolve_variant(variant, H, causal, &var);
   if (vs != FA_OK) return vs;
+  if (sinks >= 0) {
+    if (var.bm) return FA_ERR_UNSUPPORTED;
+    bound_window(&var);
+  }
   DeviceInfo* di = device_info(nullptr);
   if (!di || di->err != cudaSuccess) return FA_ERR_CUDA;
   if (!di->supported) return FA_ERR_UNSUPPORTED;
@@ -434,9 +480,28 @@ fa_status_t fa_fwd_v(const void* q, const void* k, const void* v, void* o, float
   p.cost_sorted = (var.bm && !var.bmh && !p.causal && p.bm_t <= fa::kFwdOrderMaxT) ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.status = di->status;
-  if (fa::launch_fwd(p, d, di->num_sms, di->max_smem, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return FA_OK;
+  p.sinks = sinks;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = sinks >= 0 ? fa::launch_fwd_sinks(p, d, di->num_sms, di->max_smem, s)
+                                   : fa::launch_fwd(p, d, di->num_sms, di->max_smem, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_fwd_v(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                     int H, int N, int d, float scale, int causal, const int* kv_len,
+                     const fa_variant_t* variant, void* stream) {
+  return fwd_impl(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant, -1, stream);
+}
+
+fa_status_t fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                         int H, int N, int d, float scale, int causal, const int* kv_len,
+                         const fa_variant_t* variant, int sinks, void* stream) {
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
+  return fwd_impl(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant, sinks, stream);
 }
 
 // Workspace layout: D [B*H, Npad] fp32, L2 [B*H, Npad] fp32, dQ_acc of
@@ -556,7 +621,8 @@ fa_status_t bwd_prep_impl(const fa::BwdParams& p, int d, void* stream) {
 }
 
 fa_status_t bwd_main_impl(fa::BwdParams& p, const DeviceInfo* di, const void* q, const void* k,
-                          const void* v, const void* dO, int d, void* stream) {
+                          const void* v, const void* dO, int d, void* stream,
+                          bool sinks = false) {
   const int BH = p.B * p.H;
   // d = 64: 128-query steps with dQ in query rows (fa_bwd_d64.cu); d = 128,
   // 256: 64-query steps with dQ^T in head-dimension rows (fa_bwd_dt.cu).
@@ -571,8 +637,9 @@ fa_status_t bwd_main_impl(fa::BwdParams& p, const DeviceInfo* di, const void* q,
   p.v = v;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.cost_order && fa::launch_bwd_order(p, s) != cudaSuccess) return FA_ERR_CUDA;
-  const cudaError_t e = dt ? fa::launch_bwd_main_dt(p, d, di->num_sms, di->max_smem, s)
-                           : fa::launch_bwd_main_d64(p, di->num_sms, di->max_smem, s);
+  cudaError_t e = dt ? fa::launch_bwd_main_dt(p, d, di->num_sms, di->max_smem, s, sinks)
+                     : fa::launch_bwd_main_d64(p, di->num_sms, di->max_smem, s, sinks);
+  if (e == cudaSuccess && sinks && p.nfar > 0) e = fa::launch_bwd_sinks_join(p, d, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -670,6 +737,56 @@ fa_status_t fa_bwd_v(const void* q, const void* k, const void* v, const void* o,
   p.dv = dv;
   fa_status_t r = bwd_prep_impl(p, d, stream);
   if (r == FA_OK) r = bwd_main_impl(p, di, q, k, v, dO, d, stream);
+  if (r == FA_OK) r = bwd_post_impl(p, d, stream);
+  return r;
+}
+
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int h_kv, int N, int d, int window_left,
+                                    int sinks) {
+  const size_t base = fa_bwd_workspace_bytes(B, H, N, d);
+  if (base == 0 || h_kv < 1 || h_kv > H || H % h_kv || window_left < -1 || sinks < 0) return 0;
+  const int wl = window_left < 0 ? fa::kUnbounded : std::min(window_left, fa::kUnbounded);
+  return base + sink_part_bytes(plan_sinks(N, wl, sinks), static_cast<long long>(B) * h_kv, d);
+}
+
+fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                         const void* dO, const float* lse, void* dq, void* dk, void* dv, int B,
+                         int H, int N, int d, float scale, int causal, const int* kv_len,
+                         const fa_variant_t* variant, int sinks, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv || sinks < 0)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dv))
+    return FA_ERR_INVALID_ARG;
+  if (variant && variant->block_mask) return FA_ERR_UNSUPPORTED;
+  // (0 for sizes that bwd_setup refuses)
+  if (workspace_bytes < fa_bwd_sinks_workspace_bytes(B, H, variant ? variant->h_kv : H, N, d,
+                                                     variant ? variant->window_left : -1, sinks))
+    return FA_ERR_INVALID_ARG;
+  fa::BwdParams p;
+  DeviceInfo* di = nullptr;
+  const fa_status_t st = bwd_setup(&p, &di, B, H, N, d, scale, causal, kv_len, variant, workspace,
+                                   workspace_bytes);
+  if (st != FA_OK) return st;
+  p.wl = std::min(p.wl, fa::kUnbounded);
+  p.wr = std::min(p.wr, fa::kUnbounded);
+  const SinkPlan plan = plan_sinks(N, p.wl, sinks);
+  p.sinks = sinks;
+  p.nsb = plan.nsb;
+  p.nfar = plan.nfar;
+  p.far_rows = plan.far_rows;
+  p.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         fa_bwd_workspace_bytes(B, H, N, d));
+  p.o = o;
+  p.dO = dO;
+  p.lse = lse;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  fa_status_t r = bwd_prep_impl(p, d, stream);
+  if (r == FA_OK) r = bwd_main_impl(p, di, q, k, v, dO, d, stream, true);
   if (r == FA_OK) r = bwd_post_impl(p, d, stream);
   return r;
 }

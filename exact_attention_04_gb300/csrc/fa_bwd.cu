@@ -129,6 +129,36 @@ __global__ void __launch_bounds__(256) bwd_post_t_kernel(const __grid_constant__
   }
 }
 
+// dV and dK of the key blocks that hold sinks: the sum of their items' fp32
+// rows, the window's first, then the far chunks in order; 8 elements a thread.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sinks_join_kernel(const __grid_constant__ BwdParams p,
+                                                             long long total) {
+  const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= total) return;
+  constexpr int D8 = D / 8;
+  const int c = static_cast<int>(t % D8) * 8;
+  const int r = static_cast<int>(t / D8 % 128);
+  const long long item = t / (D8 * 128);              // (K/V head, block, dV or dK)
+  const int which = static_cast<int>(item % 2);
+  const long long kn = item / 2;
+  const int n = static_cast<int>(kn % p.nsb);
+  const long long kvbh = kn / p.nsb;
+  const int key = n * 128 + r;
+  if (key >= p.N) return;
+  const float* src = p.sink_part + ((kn * (p.nfar + 1)) * 2 + which) * 128 * D + r * D + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  for (int s = 0; s <= p.nfar; ++s, src += 2 * 128 * D) {
+    const float4 x = reinterpret_cast<const float4*>(src)[0];
+    const float4 y = reinterpret_cast<const float4*>(src)[1];
+    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+  }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + (kvbh * p.N + key) * D + c;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
+                                              pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
+
 template <int D>
 cudaError_t launch_prep(const BwdParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.B) * p.H * p.Npad;
@@ -179,6 +209,18 @@ cudaError_t launch_bwd_order(const BwdParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const int threads = (p.bm_t + 31) / 32 * 32;
   bwd_order_kernel<<<1, threads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_sinks_join(const BwdParams& p, int d, cudaStream_t stream) {
+  const long long total = static_cast<long long>(p.B) * p.H_kv * p.nsb * 2 * 128 * (d / 8);
+  const unsigned grid = static_cast<unsigned>((total + 255) / 256);
+  switch (d) {
+    case 64: bwd_sinks_join_kernel<64><<<grid, 256, 0, stream>>>(p, total); break;
+    case 128: bwd_sinks_join_kernel<128><<<grid, 256, 0, stream>>>(p, total); break;
+    case 256: bwd_sinks_join_kernel<256><<<grid, 256, 0, stream>>>(p, total); break;
+    default: return cudaErrorInvalidValue;
+  }
   return cudaGetLastError();
 }
 

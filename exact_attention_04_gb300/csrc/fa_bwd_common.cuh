@@ -74,10 +74,11 @@ struct DtSched {
   int T, P, per_bh, units, causal, nsplit;   // units: the round-robin units
   int BH;
   const uint32_t* order;                     // the cost-sorted order, or nullptr
+  // extra: items past a head's key blocks (the far chunks of its sinks)
   __device__ DtSched(int BH_, int N, int causal_, int nsplit_, int tail_heads,
-                     const uint32_t* order_)
+                     const uint32_t* order_, int extra = 0)
       : causal(causal_), nsplit(nsplit_), BH(BH_), order(order_) {
-    T = (N + BK - 1) / BK;
+    T = (N + BK - 1) / BK + extra;
     P = (T + 1) / 2;
     per_bh = causal ? P : T;
     units = (BH - tail_heads) * per_bh * nsplit;
@@ -139,17 +140,66 @@ __device__ __forceinline__ int dt_len(const BwdParams& p, int kvbh) {
   return len;
 }
 
-// Query-step range [i0, i1) (blocks of 64) that key block n is visible to
-// (kv_len, causal and window); empty when no query sees any of its keys.
-__device__ __forceinline__ void dt_range(const BwdParams& p, int n, int len, int& i0, int& i1) {
+// The key block and the step range of item n of a head, in steps of STEP
+// rows.  With sinks, item n may be a far chunk of one of the first nsb blocks
+// (n past the head's blocks); n becomes its block, and slot the place of its
+// dV, dK in sink_part (-1: written to dV, dK as for any block).  The window
+// item of such a block ends where the first chunk starts: at the first step
+// whose queries are all past the window of its last key.
+template <int MK, int STEP>
+__device__ __forceinline__ void item_range(const BwdParams& p, int& n, int len, int& i0, int& i1,
+                                           int& slot) {
+  slot = -1;
+  if constexpr (MK == kMaskSinks) {
+    const int T = (p.N + BK - 1) / BK;
+    int c = -1;
+    if (n >= T) {
+      c = (n - T) % p.nfar;
+      n = (n - T) / p.nfar;
+    }
+    if (n < p.nsb) {
+      const int steps = (p.N + STEP - 1) / STEP;
+      int far0 = steps;
+      if (p.nfar > 0) {
+        slot = c + 1;
+        far0 = min(steps, (n * BK + BK + p.wl + STEP - 1) / STEP);
+      }
+      if (c < 0) {
+        i0 = max(0, n * BK - p.wr) / STEP;
+        i1 = far0;
+      } else {
+        const int cs = p.far_rows / STEP;
+        i0 = min(steps, far0 + c * cs);
+        i1 = c == p.nfar - 1 ? steps : min(steps, far0 + (c + 1) * cs);
+      }
+      if (n * BK >= len || i0 >= i1) i0 = i1 = 0;
+      return;
+    }
+  }
   int q_lo, q_hi;
   visible_queries(n * BK, BK, len, p.N, p.wl, p.wr, q_lo, q_hi);
   if (q_hi <= q_lo) {
     i0 = i1 = 0;
     return;
   }
-  i0 = q_lo / BQ;
-  i1 = (q_hi + BQ - 1) / BQ;
+  i0 = q_lo / STEP;
+  i1 = (q_hi + STEP - 1) / STEP;
+}
+
+// The dV (0) or dK (1) rows of an item of a sink block: [128, d] floats.
+__device__ __forceinline__ float* sink_rows(const BwdParams& p, int kvbh, int n, int slot, int d,
+                                            int which) {
+  return p.sink_part +
+         (((static_cast<size_t>(kvbh) * p.nsb + n) * (p.nfar + 1) + slot) * 2 + which) * BK * d;
+}
+
+// Rows [left, 128) of a tile of `chunks` 128-byte column chunks become
+// zero, by a whole warp: keys past the sequence may hold anything, and their
+// zero weights times NaN would be NaN.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int chunks, int left, int lane) {
+  for (int c = 0; c < chunks; ++c)
+    for (int e = left * 8 + lane; e < BK * 8; e += 32)
+      *reinterpret_cast<uint4*>(tile + c * KCH + e * 16) = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace

@@ -90,38 +90,29 @@ __device__ __forceinline__ constexpr uint32_t scol(int kk) {
   return static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8);
 }
 
-// Query-block range [i0, i1) (blocks of 128) that key block n is visible to.
-__device__ __forceinline__ void s_range(const BwdParams& p, int n, int len, int& i0, int& i1) {
-  int q_lo, q_hi;
-  visible_queries(n * BK, BK, len, p.N, p.wl, p.wr, q_lo, q_hi);
-  if (q_hi <= q_lo) {
-    i0 = i1 = 0;
-    return;
-  }
-  i0 = q_lo / SQ;
-  i1 = (q_hi + SQ - 1) / SQ;
-}
-
 // The steps of the item: (query head, query block) pairs, or none.
 struct SItem {
   int i0, i1, nsteps;
+  int slot;                             // as item_range's
   StepMask sk;
 };
 
-template <bool BS>
-__device__ __forceinline__ SItem s_item(const BwdParams& p, int kvbh, int n, int G) {
+// n becomes the item's key block (item_range).
+template <int MK>
+__device__ __forceinline__ SItem s_item(const BwdParams& p, int kvbh, int& n, int G) {
   SItem w;
-  s_range(p, n, dt_len(p, kvbh), w.i0, w.i1);
-  w.sk = StepMask{BS ? p.block_mask + n : nullptr, p.bm_t, 1};
+  item_range<MK, SQ>(p, n, dt_len(p, kvbh), w.i0, w.i1, w.slot);
+  w.sk = StepMask{MK == kMaskBlocks ? p.block_mask + n : nullptr, p.bm_t, 1};
   const int nst = count_steps(w.sk, w.i0, w.i1);
   if (nst == 0) w.i1 = w.i0;
   w.nsteps = nst * G;
   return w;
 }
 
-template <bool BS>
+template <int MK>
 __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_constant__ BwdParams p,
                                                                const __grid_constant__ TailTable tail) {
+  constexpr bool SK = MK == kMaskSinks;
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
@@ -169,7 +160,9 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  const DtSched sched(p.B * p.H_kv, p.N, p.causal, 1, tail.heads, BS ? p.cost_order : nullptr);
+  const DtSched sched(p.B * p.H_kv, p.N, p.causal, 1, tail.heads,
+                      MK == kMaskBlocks ? p.cost_order : nullptr,
+                      SK ? p.nsb * p.nfar : 0);
   const int G = p.H / p.H_kv;                     // query heads per K/V head
 
   // Registers: the launch gives every thread 96.  The first warpgroup
@@ -196,7 +189,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         bool ok = true;
         DtIter it{static_cast<int>(blockIdx.x), 0, 0};
         for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-          const SItem wi = s_item<BS>(p, kvbh, n, G);
+          const SItem wi = s_item<MK>(p, kvbh, n, G);
           if (wi.nsteps == 0) continue;
           if (!dlane) {
             if (!mbar_wait(&sm.kv_empty, (w_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
@@ -249,12 +242,21 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       bool ok = true;
       DtIter it{static_cast<int>(blockIdx.x), 0, 0};
       for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        const SItem wi = s_item<BS>(p, kvbh, n, G);
+        const SItem wi = s_item<MK>(p, kvbh, n, G);
         if (wi.nsteps == 0) continue;
         if (!mbar_wait_warp(&sm.kv_full, w_it & 1, abort, kWaitTimeoutNs)) {
           issuer_fail(p.status, abort, lane, kSiteMmaKV);
           ok = false;
           break;
+        }
+        if constexpr (SK) {
+          const int left = dt_len(p, kvbh) - n * BK;
+          if (left < BK) {
+            zero_rows(sm.k, 1, left, lane);
+            zero_rows(sm.v, 1, left, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
         }
         for (int s = 0; s < wi.nsteps; ++s, ++g) {
           const int st = g & 1;
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       };
       DtIter it{static_cast<int>(blockIdx.x), 0, 0};
       for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        const SItem wi = s_item<BS>(p, kvbh, n, G);
+        const SItem wi = s_item<MK>(p, kvbh, n, G);
         if (wi.nsteps == 0) continue;
         for (int s = 0; s < wi.nsteps; ++s, ++g) {
           const int st = g & 1;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         bool ok = true;
         DtIter it{static_cast<int>(blockIdx.x), 0, 0};
         for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-          const SItem wi = s_item<BS>(p, kvbh, n, G);
+          const SItem wi = s_item<MK>(p, kvbh, n, G);
           StepWalk wk(wi.i0, wi.i1, q_head_of(kvbh, 0, p.H, p.H_kv), wi.sk);
           for (int s = 0; s < wi.nsteps; ++s, ++g, wk.next()) {
             const int b = g & 1;
@@ -472,12 +474,20 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
     DtIter it{static_cast<int>(blockIdx.x), 0, 0};
     for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
       const int len = dt_len(p, kvbh);
-      const SItem wi = s_item<BS>(p, kvbh, n, G);
+      const SItem wi = s_item<MK>(p, kvbh, n, G);
       const int key = n * BK + r;
       const size_t out_off = (static_cast<size_t>(kvbh) * p.N + key) * SD + 16 * j4;
       if (wi.nsteps == 0) {
         // key block seen by no query: zero gradients
-        if (key < p.N) {
+        if (SK && wi.slot >= 0) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float4* a = reinterpret_cast<float4*>(sink_rows(p, kvbh, n, wi.slot, SD, w) + r * SD +
+                                                  16 * j4);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        } else if (key < p.N) {
           uint4* a = reinterpret_cast<uint4*>(dk_out + out_off);
           uint4* bq = reinterpret_cast<uint4*>(dv_out + out_off);
 #pragma unroll
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         // visible columns c (query q = q0 + 32*j4 + c) of this key row:
         // [c_lo, c_hi]; none when the key is past len
         const int c_lo = key - p.wr - q0 - 32 * j4;
-        const int c_hi = (key < len) ? key + p.wl - q0 - 32 * j4 : -1;
+        const int c_hi = (key < len) ? (SK && key < p.sinks ? 31 : key + p.wl - q0 - 32 * j4) : -1;
         const uint32_t t_s = t_lane + TM_S + 32 * j4;
         float pr[32];
         {
@@ -620,7 +630,18 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_free);
-        if (key < p.N) {
+        if (SK && wi.slot >= 0) {
+          const int at = r * SD + 16 * j4;
+          float* dvp = sink_rows(p, kvbh, n, wi.slot, SD, 0) + at;
+          float* dkp = sink_rows(p, kvbh, n, wi.slot, SD, 1) + at;
+#pragma unroll
+          for (int t = 0; t < 16; ++t) bb[t] = __float_as_uint(__uint_as_float(bb[t]) * p.scale);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            st_global_v8(dvp + 8 * t, a + 8 * t);
+            st_global_v8(dkp + 8 * t, bb + 8 * t);
+          }
+        } else if (key < p.N) {
           uint32_t pv[8], pkk[8];
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
@@ -656,19 +677,19 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
   }
 }
 
-template <bool BS>
+template <int MK>
 cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
   const size_t smem = smem_request(sizeof(SSmem), max_smem);
-  cudaError_t e = cudaFuncSetAttribute(bwd_d64_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(bwd_d64_kernel<MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int T = (p.N + BK - 1) / BK;
+  const int T = (p.N + BK - 1) / BK + (MK == kMaskSinks ? p.nsb * p.nfar : 0);
   const int BH = p.B * p.H_kv;
   const long long per_bh = p.causal ? (T + 1) / 2 : T;
   long long units = static_cast<long long>(BH) * per_bh;
   TailTable tail;
   tail.heads = 0;
-  if (p.causal || (BS && p.block_mask_host && T == p.bm_t)) {
+  if (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t)) {
     // single key blocks in the tail: up to one CTA per block; the tail's
     // K/V heads share their group's Q and dO through L2
     const long long blocks = static_cast<long long>(BH) * T;
@@ -682,16 +703,17 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  bwd_d64_kernel<BS><<<grid, kSThreads, smem, stream>>>(p, tail);
+  bwd_d64_kernel<MK><<<grid, kSThreads, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_main_d64(const BwdParams& p, int num_sms, int max_smem,
-                                cudaStream_t stream) {
-  return p.block_mask ? launch<true>(p, num_sms, max_smem, stream)
-                      : launch<false>(p, num_sms, max_smem, stream);
+                                cudaStream_t stream, bool sinks) {
+  return sinks          ? launch<kMaskSinks>(p, num_sms, max_smem, stream)
+         : p.block_mask ? launch<kMaskBlocks>(p, num_sms, max_smem, stream)
+                        : launch<kMaskNone>(p, num_sms, max_smem, stream);
 }
 
 }  // namespace fa

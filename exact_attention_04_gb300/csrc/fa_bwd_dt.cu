@@ -121,12 +121,14 @@ struct DtSmem {
 static_assert(sizeof(DtSmem<128>) <= 232448 && sizeof(DtSmem<256>) <= 232448,
               "shared-memory layout exceeds the per-block limit");
 
-// BS: the launch carries a block mask (its own instantiation, so that the
-// kernel without one keeps the plain step walk).
-template <int D, bool BS>
+// MK: the launch carries a block mask or sinks (instantiations of their own,
+// so that the kernel without them keeps the plain step walk).
+template <int D, int MK>
 __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_constant__ BwdParams p,
                                                                  const __grid_constant__ TailTable tail) {
   using C = DtCfg<D>;
+  constexpr bool BS = MK == kMaskBlocks;
+  constexpr bool SK = MK == kMaskSinks;
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   const DtSched sched(p.B * p.H_kv, p.N, p.causal, C::NSPLIT, tail.heads,
-                      BS ? p.cost_order : nullptr);
+                      BS ? p.cost_order : nullptr, SK ? p.nsb * p.nfar : 0);
   const int G = p.H / p.H_kv;                     // query heads per K/V head
 
   if (warp == 0) {
@@ -199,8 +201,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       DtIter it{static_cast<int>(blockIdx.x), 0, 0};
       for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
         {
-          int i0, i1;
-          dt_range(p, n, dt_len(p, kvbh), i0, i1);
+          int i0, i1, slot;
+          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
           const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
           const int nst = count_steps(sk, i0, i1);
           if (nst == 0) i1 = i0;
@@ -287,8 +289,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       DtIter it{static_cast<int>(blockIdx.x), 0, 0};
       for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
         {
-          int i0, i1;
-          dt_range(p, n, dt_len(p, kvbh), i0, i1);
+          int i0, i1, slot;
+          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
           const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
           const int nst = count_steps(sk, i0, i1);
           if (nst == 0) i1 = i0;
@@ -298,6 +300,15 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
             issuer_fail(p.status, abort, lane, kSiteMmaKV);
             ok = false;
             break;
+          }
+          if constexpr (SK) {
+            const int left = dt_len(p, kvbh) - n * BK;
+            if (left < BK) {
+              zero_rows(sm.k, C::NCH, left, lane);
+              if constexpr (!C::V_TMEM) zero_rows(sm.v, C::NCH, left, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
           // S^T(gg) = K Q^T into S buffer gg%NSB once dV(gg-NSB) has read
           // P^T(gg-NSB) out of it
@@ -393,8 +404,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
         // K[:, h] as the MN-major A operand of dQ^T: 64-column chunks 2h, 2h+1
         const uint64_t dKmn = sdesc_sw128(smem_u32(sm.k) + 2 * h * KCH, KCH, 1024);
         {
-          int i0, i1;
-          dt_range(p, n, dt_len(p, kvbh), i0, i1);
+          int i0, i1, slot;
+          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
           const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
           const int nst = count_steps(sk, i0, i1);
           if (nst == 0) i1 = i0;
@@ -484,14 +495,25 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
     for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
       {
         const int len = dt_len(p, kvbh);
-        int i0, i1;
-        dt_range(p, n, len, i0, i1);
+        int i0, i1, slot;
+        item_range<MK, BQ>(p, n, len, i0, i1, slot);
         const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
         const int nst = count_steps(sk, i0, i1);
         if (nst == 0) i1 = i0;
         const int key = n * BK + r;
         const size_t out_off = (static_cast<size_t>(kvbh) * p.N + key) * D + h * DH + 64 * hh;
         if (i0 >= i1) {
+          if (SK && slot >= 0) {
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              float4* a = reinterpret_cast<float4*>(sink_rows(p, kvbh, n, slot, D, w) + r * D +
+                                                    h * DH + 64 * hh);
+#pragma unroll
+              for (int t = 0; t < 16; ++t) a[t] = z;
+            }
+            continue;
+          }
           // key block entirely past the sequence: zero gradients
           if (key < p.N) {
             uint4* a = reinterpret_cast<uint4*>(dk_out + out_off);
@@ -522,7 +544,7 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
             uint32_t vr[32];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-              const uint4 x = key < p.N ? __ldg(vrow + 8 * c + t) : make_uint4(0, 0, 0, 0);
+              const uint4 x = key < (SK ? len : p.N) ? __ldg(vrow + 8 * c + t) : make_uint4(0, 0, 0, 0);
               vr[4 * t] = x.x;
               vr[4 * t + 1] = x.y;
               vr[4 * t + 2] = x.z;
@@ -556,7 +578,7 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
           // [c_lo, c_hi], the queries whose window [q - wl, q + wr] holds the
           // key; none when the key is past len
           const int c_lo = key - p.wr - q0 - 32 * hh;
-          const int c_hi = (key < len) ? key + p.wl - q0 - 32 * hh : -1;
+          const int c_hi = (key < len) ? (SK && key < p.sinks ? 31 : key + p.wl - q0 - 32 * hh) : -1;
           float pr[32];
           const uint64_t c2x2 = f2_make(c2, c2);
           {
@@ -663,7 +685,18 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
           tmem_wait_ld();
           reg_fence<32>(a);
           reg_fence<32>(bb);
-          if (key < p.N) {
+          if (SK && slot >= 0) {
+            const size_t at = static_cast<size_t>(r) * D + h * DH + 64 * hh + 32 * c4;
+            float* dvp = sink_rows(p, kvbh, n, slot, D, 0) + at;
+            float* dkp = sink_rows(p, kvbh, n, slot, D, 1) + at;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) bb[t] = __float_as_uint(__uint_as_float(bb[t]) * p.scale);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              st_global_v8(dvp + 8 * t, a + 8 * t);
+              st_global_v8(dkp + 8 * t, bb + 8 * t);
+            }
+          } else if (key < p.N) {
             uint32_t pv[16], pkk[16];
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
@@ -707,8 +740,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
     DtIter it{static_cast<int>(blockIdx.x), 0, 0};
     for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
       {
-        int i0, i1;
-        dt_range(p, n, dt_len(p, kvbh), i0, i1);
+        int i0, i1, slot;
+        item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
         const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
         const int nst = count_steps(sk, i0, i1);
         if (nst == 0) i1 = i0;
@@ -801,8 +834,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       bool ok = true;
       DtIter it{static_cast<int>(blockIdx.x), 0, 0};
       for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        int i0, i1;
-        dt_range(p, n, dt_len(p, kvbh), i0, i1);
+        int i0, i1, slot;
+        item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
         const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
         const int nst = count_steps(sk, i0, i1);
         if (nst == 0) i1 = i0;
@@ -837,20 +870,20 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
   }
 }
 
-template <int D, bool BS>
+template <int D, int MK>
 cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
   const size_t smem = smem_request(sizeof(DtSmem<D>), max_smem);
-  cudaError_t e = cudaFuncSetAttribute(bwd_dt_kernel<D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(bwd_dt_kernel<D, MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int T = (p.N + BK - 1) / BK;
+  const int T = (p.N + BK - 1) / BK + (MK == kMaskSinks ? p.nsb * p.nfar : 0);
   const int BH = p.B * p.H_kv;
   constexpr int NS = DtCfg<D>::NSPLIT;
   const long long per_bh = p.causal ? (T + 1) / 2 : T;
   long long units = static_cast<long long>(BH) * per_bh * NS;
   TailTable tail;
   tail.heads = 0;
-  if (p.causal || (BS && p.block_mask_host && T == p.bm_t)) {
+  if (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t)) {
     // single key blocks in the tail: up to one CTA per block
     const long long blocks = static_cast<long long>(BH) * T * NS;
     const int g = static_cast<int>(blocks < num_sms ? blocks : num_sms);
@@ -864,21 +897,23 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  bwd_dt_kernel<D, BS><<<grid, DtCfg<D>::THREADS, smem, stream>>>(p, tail);
+  bwd_dt_kernel<D, MK><<<grid, DtCfg<D>::THREADS, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_main_dt(const BwdParams& p, int d, int num_sms, int max_smem,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, bool sinks) {
   switch (d) {
     case 128:
-      return p.block_mask ? launch<128, true>(p, num_sms, max_smem, stream)
-                          : launch<128, false>(p, num_sms, max_smem, stream);
+      return sinks          ? launch<128, kMaskSinks>(p, num_sms, max_smem, stream)
+             : p.block_mask ? launch<128, kMaskBlocks>(p, num_sms, max_smem, stream)
+                            : launch<128, kMaskNone>(p, num_sms, max_smem, stream);
     case 256:
-      return p.block_mask ? launch<256, true>(p, num_sms, max_smem, stream)
-                          : launch<256, false>(p, num_sms, max_smem, stream);
+      return sinks          ? launch<256, kMaskSinks>(p, num_sms, max_smem, stream)
+             : p.block_mask ? launch<256, kMaskBlocks>(p, num_sms, max_smem, stream)
+                            : launch<256, kMaskNone>(p, num_sms, max_smem, stream);
     default: return cudaErrorNotSupported;
   }
 }

@@ -258,15 +258,16 @@ struct Tile {
   int qlo, qhi;        // query positions of the tile's first and last row
   int jlo, nkv;        // key blocks [jlo, jend), nkv of them not masked out
   int jend;
+  int ns;              // sinks: the first ns blocks of the walk are blocks 0 .. ns - 1
   const uint8_t* bmrow;  // block-mask row of the tile's query block, or nullptr
   long long out0;      // output row of tile row 0
   int rows;            // rows of the tile that are real queries
   int qs;              // index of the tile's Q scale (FP8)
 };
 
-// BS: the launch carries a block mask (a separate instantiation, so that the
-// kernels without one keep the plain block walk).
-template <bool DEC, bool BS = false>
+// MK: the launch carries a block mask, or sinks (separate instantiations, so
+// that the kernels without them keep the plain block walk).
+template <bool DEC, int MK = kMaskNone>
 __device__ __forceinline__ void make_tile(const FwdParams& p, int u, int bh, int m, Tile& t,
                                           const int* kvl) {
   if constexpr (!DEC) {
@@ -279,7 +280,14 @@ __device__ __forceinline__ void make_tile(const FwdParams& p, int u, int bh, int
     t.nkv = tile_blocks(p, m, t.len, t.jlo);
     t.jend = t.jlo + t.nkv;
     t.bmrow = nullptr;
-    if constexpr (BS) {
+    if constexpr (MK == kMaskSinks) {
+      // blocks of sinks left of the window's first block (with no window
+      // block, the tile lies past the sequence and sees the sinks alone)
+      const int ns = ((p.sinks < t.len ? p.sinks : t.len) + BN - 1) / BN;
+      t.ns = t.nkv > 0 && ns > t.jlo ? t.jlo : ns;
+      t.nkv += t.ns;
+    }
+    if constexpr (MK == kMaskBlocks) {
       t.bmrow = p.block_mask + static_cast<size_t>(m) * p.bm_t;
       int n = 0;
       for (int jb = t.jlo; jb < t.jend; ++jb) n += __ldg(t.bmrow + jb) != 0;
@@ -315,11 +323,20 @@ __device__ __forceinline__ void make_tile(const FwdParams& p, int u, int bh, int
 // The first key block at or after jb that the tile computes: every block of
 // [jlo, jend) without a block mask, else those whose mask byte is nonzero
 // (every role walks the same sequence).
-template <bool BS>
+template <int MK>
 __device__ __forceinline__ int next_block(const Tile& t, int jb) {
-  if constexpr (BS)
+  if constexpr (MK == kMaskBlocks)
     while (jb < t.jend && __ldg(t.bmrow + jb) == 0) ++jb;
   return jb;
+}
+
+// The key block of step j of the tile's walk (jbs: next_block's, with a block
+// mask).
+template <int MK>
+__device__ __forceinline__ int step_block(const Tile& t, int j, int jbs) {
+  if constexpr (MK == kMaskBlocks) return jbs;
+  if constexpr (MK == kMaskSinks) return j < t.ns ? j : t.jlo + (j - t.ns);
+  return t.jlo + j;
 }
 
 // This CTA's place in the schedule: its round-robin units (and the tiles of
@@ -330,7 +347,7 @@ struct TileIter {
 
 // The next tile of this CTA into t; false when it has none left.  Every role
 // walks the same sequence.
-template <bool DEC, bool BS>
+template <bool DEC, int MK>
 __device__ __forceinline__ bool next_tile(const FwdParams& p, const TailTable& tail,
                                           const Sched& sched, int nunits, TileIter& it, Tile& t) {
   if constexpr (DEC) {
@@ -339,13 +356,13 @@ __device__ __forceinline__ bool next_tile(const FwdParams& p, const TailTable& t
     it.u += gridDim.x;
     return true;
   } else {
-    if (BS && sched.order) {   // round it.k of the cost-sorted deal
+    if (MK == kMaskBlocks && sched.order) {   // round it.k of the cost-sorted deal
       const long long k = order_deal(it.k, gridDim.x, blockIdx.x);
       if (k >= static_cast<long long>(sched.BH) * sched.T) return false;
       ++it.k;
       int bh, m;
       order_item(sched.order, sched.BH, k, bh, m);
-      make_tile<false, BS>(p, 0, bh, m, t, sched.kvl);
+      make_tile<false, MK>(p, 0, bh, m, t, sched.kvl);
       return true;
     }
     while (it.u < sched.units) {
@@ -353,7 +370,7 @@ __device__ __forceinline__ bool next_tile(const FwdParams& p, const TailTable& t
         int bh, m;
         sched.tile(it.u, it.kt, bh, m);
         ++it.kt;
-        make_tile<false, BS>(p, 0, bh, m, t, sched.kvl);
+        make_tile<false, MK>(p, 0, bh, m, t, sched.kvl);
         return true;
       }
       it.u += gridDim.x;
@@ -363,7 +380,7 @@ __device__ __forceinline__ bool next_tile(const FwdParams& p, const TailTable& t
     const int e = tail.item[blockIdx.x][it.k];
     if (e < 0) return false;
     ++it.k;
-    make_tile<false, BS>(p, 0, tail_head(e), tail_block(e), t, sched.kvl);
+    make_tile<false, MK>(p, 0, tail_head(e), tail_block(e), t, sched.kvl);
     return true;
   }
 }
@@ -374,10 +391,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int D, bool DEC, bool FP8, bool BS>
+template <int D, bool DEC, bool FP8, int MK>
 __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ TailTable tail) {
   static_assert(!(DEC && FP8), "decode runs in bf16");
+  constexpr bool BS = MK == kMaskBlocks;
   using C = Cfg<D, FP8>;
   using Smem = FwdSmem<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
@@ -475,9 +493,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
       uint32_t q_it = 0, k_it = 0, v_it = 0;
       bool ok = true;
       TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+      for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
         {
-          const int jlo = t.jlo, nkv = t.nkv;
+          const int nkv = t.nkv;
           if (nkv == 0) continue;
           const int kvbh = t.kvbh;
           if (!mbar_wait(&sm.q_empty, (q_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
@@ -490,9 +508,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
           for (int c = 0; c < C::NCH; ++c)
             tma_load_3d(sm.q + c * CHUNK, &p.tq, &sm.q_full, C::BOX_COLS * c, t.qy, t.qz);
           ++q_it;
-          for (int j = 0, jbs = next_block<BS>(t, t.jlo); j < nkv;
-               ++j, jbs = BS ? next_block<BS>(t, jbs + 1) : jbs) {
-            const int jb = BS ? jbs : t.jlo + j;        // key block
+          for (int j = 0, jbs = next_block<MK>(t, t.jlo); j < nkv;
+               ++j, jbs = BS ? next_block<MK>(t, jbs + 1) : jbs) {
+            const int jb = step_block<MK>(t, j, jbs);   // key block
             const int st = k_it % C::STAGES;
             const uint32_t ph = (k_it / C::STAGES) & 1;
             if (!mbar_wait(&sm.k_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
@@ -552,13 +570,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
       uint32_t v_it = 0;
       bool ok = true;
       TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+      for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
         {
-          const int jlo = t.jlo, nkv = t.nkv;
+          const int nkv = t.nkv;
           const int kvbh = t.kvbh;
-          for (int j = 0, jbs = next_block<BS>(t, t.jlo); j < nkv;
-               ++j, jbs = BS ? next_block<BS>(t, jbs + 1) : jbs) {
-            const int jb = BS ? jbs : t.jlo + j;        // key block
+          for (int j = 0, jbs = next_block<MK>(t, t.jlo); j < nkv;
+               ++j, jbs = BS ? next_block<MK>(t, jbs + 1) : jbs) {
+            const int jb = step_block<MK>(t, j, jbs);   // key block
             const int st = v_it % C::STAGES;
             const uint32_t ph = (v_it / C::STAGES) & 1;
             if (!mbar_wait(&sm.v_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
@@ -597,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
       uint32_t q_it = 0, g = 0;
       bool ok = true;
       TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+      for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
         {
           const int nkv = t.nkv;
           if (nkv == 0) continue;
@@ -656,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
       uint32_t g = 0, t_it = 0;
       bool ok = true;
       TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+      for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
         {
           const int nkv = t.nkv;
           if (nkv == 0) continue;
@@ -667,6 +685,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
               issuer_fail(p.status, abort, lane, kSiteMmaV);
               ok = false;
               break;
+            }
+            if constexpr (MK == kMaskSinks) {
+              // V rows past the sequence may hold anything, and 0 NaN is NaN:
+              // zeros in their place (P is 0 there)
+              const int left = t.len - step_block<MK>(t, j, 0) * BN;
+              if (left < BN) {
+                for (int e = left * 8 + lane; e < BN * 8; e += 32)
+#pragma unroll
+                  for (int c = 0; c < C::NCH; ++c)
+                    *reinterpret_cast<uint4*>(sm.v[st] + c * CHUNK + e * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
             }
             // a tile's first P V starts a fresh O: the epilogue of the tile
             // that last used this O buffer must have read it out of tensor memory
@@ -744,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     uint32_t e_it = 0;
     bool ok = true;
     TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-    for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+    for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
       const bool row_valid = row_local < t.rows;
       const size_t row_off = static_cast<size_t>(t.out0 + row_local);
       if (t.nkv == 0) {   // no key is visible to the tile's rows: O = 0, LSE = -inf
@@ -960,9 +992,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
       return epilogue(pend.last, pend.l, pend.m_ref, pend.row_off, pend.row_valid, pend.kvbh);
     };
     TileIter it{static_cast<int>(blockIdx.x), 0, 0};
-    for (Tile t; ok && next_tile<DEC, BS>(p, tail, sched, nunits, it, t);) {
+    for (Tile t; ok && next_tile<DEC, MK>(p, tail, sched, nunits, it, t);) {
       {
-        const int len = t.len, jlo = t.jlo, nkv = t.nkv;
+        const int len = t.len, nkv = t.nkv;
         const int row = DEC ? t.qlo + row_local % p.Nq : t.qlo + row_local;   // query position
         // FP8: scores come out of the MMA in units of sq * sk
         const float q_sc = FP8 ? __ldg(p.q_scale + t.qs) : 1.f;
@@ -994,9 +1026,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         float m_ref = -INFINITY;    // reference maximum, base-2 units of S*scale
         float l = 0.f;
         bool s_next = false;        // the next block's S was seen complete (kEarlyS)
-        for (int j = 0, jbs = next_block<BS>(t, t.jlo); j < nkv;
-             ++j, jbs = BS ? next_block<BS>(t, jbs + 1) : jbs) {
-          const int jb = BS ? jbs : t.jlo + j;        // key block
+        for (int j = 0, jbs = next_block<MK>(t, t.jlo); j < nkv;
+             ++j, jbs = BS ? next_block<MK>(t, jbs + 1) : jbs) {
+          const int jb = step_block<MK>(t, j, jbs);   // key block
           const uint32_t b = kv_it % C::NSB;
           const uint32_t t_s = t_lane + C::TM_S + 128 * b;      // this block's S buffer
           if (!(kEarlyS && __all_sync(0xffffffffu, s_next)) &&
@@ -1024,14 +1056,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
           // window (above the diagonal when causal) and left of the window;
           // skipped when every key of the block is visible to every row
           const int key0 = jb * BN + NC * hf;
-          if (key0 + NC > len || key0 + NC - 1 > t.qlo + p.wr || key0 < t.qhi - p.wl) {
+          if (key0 + NC > len || key0 + NC - 1 > t.qlo + p.wr ||
+              (key0 < t.qhi - p.wl && (MK != kMaskSinks || key0 + NC > p.sinks))) {
             // visible columns [c_lo, c_hi]: before the sequence end and
-            // inside the window [row - wl, row + wr]
+            // inside the window [row - wl, row + wr]; with sinks, also the
+            // columns below them left of the window
             const int c_hi = min(len - key0 - 1, row + p.wr - key0);
             const int c_lo = row - p.wl - key0;
+            const int c_sk = MK == kMaskSinks ? p.sinks - key0 : 0;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              if (c > c_hi || c < c_lo) s[c] = -INFINITY;
+              if (c > c_hi || (c < c_lo && (MK != kMaskSinks || c >= c_sk))) s[c] = -INFINITY;
           }
           // row maximum: four chains of three-input max over s[0 .. NC)
           static_assert(NC % 8 == 0, "the max chains take 8 columns a step");
@@ -1198,10 +1233,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   }
 }
 
-template <int D, bool DEC, bool FP8 = false, bool BS = false>
+template <int D, bool DEC, bool FP8 = false, int MK = kMaskNone>
 cudaError_t launch(const FwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
   const size_t smem = smem_request(sizeof(FwdSmem<D, FP8>), max_smem);
-  cudaError_t e = cudaFuncSetAttribute(fa_fwd_kernel<D, DEC, FP8, BS>,
+  cudaError_t e = cudaFuncSetAttribute(fa_fwd_kernel<D, DEC, FP8, MK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -1216,7 +1251,7 @@ cudaError_t launch(const FwdParams& p, int num_sms, int max_smem, cudaStream_t s
     units = p.causal ? static_cast<long long>(BH) * ((T + 1) / 2) : static_cast<long long>(BH) * T;
     // (the mask planner reads the host copy as [T, T]: tiles and mask blocks
     // are both 128 rows)
-    if (p.causal || (BS && p.block_mask_host && T == p.bm_t)) {
+    if (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t)) {
       // single tiles in the tail: up to one CTA per tile
       const long long tiles = static_cast<long long>(BH) * T;
       const int g = static_cast<int>(tiles < num_sms ? tiles : num_sms);
@@ -1231,7 +1266,7 @@ cudaError_t launch(const FwdParams& p, int num_sms, int max_smem, cudaStream_t s
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  fa_fwd_kernel<D, DEC, FP8, BS><<<grid, Cfg<D, FP8>::THREADS, smem, stream>>>(p, tail);
+  fa_fwd_kernel<D, DEC, FP8, MK><<<grid, Cfg<D, FP8>::THREADS, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }
 
@@ -1279,14 +1314,24 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_consta
 cudaError_t launch_fwd(const FwdParams& p, int d, int num_sms, int max_smem, cudaStream_t stream) {
   switch (d) {
     case 64:
-      return p.block_mask ? launch<64, false, false, true>(p, num_sms, max_smem, stream)
+      return p.block_mask ? launch<64, false, false, kMaskBlocks>(p, num_sms, max_smem, stream)
                           : launch<64, false>(p, num_sms, max_smem, stream);
     case 128:
-      return p.block_mask ? launch<128, false, false, true>(p, num_sms, max_smem, stream)
+      return p.block_mask ? launch<128, false, false, kMaskBlocks>(p, num_sms, max_smem, stream)
                           : launch<128, false>(p, num_sms, max_smem, stream);
     case 256:
-      return p.block_mask ? launch<256, false, false, true>(p, num_sms, max_smem, stream)
+      return p.block_mask ? launch<256, false, false, kMaskBlocks>(p, num_sms, max_smem, stream)
                           : launch<256, false>(p, num_sms, max_smem, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_fwd_sinks(const FwdParams& p, int d, int num_sms, int max_smem,
+                             cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch<64, false, false, kMaskSinks>(p, num_sms, max_smem, stream);
+    case 128: return launch<128, false, false, kMaskSinks>(p, num_sms, max_smem, stream);
+    case 256: return launch<256, false, false, kMaskSinks>(p, num_sms, max_smem, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1295,10 +1340,10 @@ cudaError_t launch_fwd_fp8(const FwdParams& p, int d, int num_sms, int max_smem,
                            cudaStream_t stream) {
   switch (d) {
     case 128:
-      return p.block_mask ? launch<128, false, true, true>(p, num_sms, max_smem, stream)
+      return p.block_mask ? launch<128, false, true, kMaskBlocks>(p, num_sms, max_smem, stream)
                           : launch<128, false, true>(p, num_sms, max_smem, stream);
     case 256:
-      return p.block_mask ? launch<256, false, true, true>(p, num_sms, max_smem, stream)
+      return p.block_mask ? launch<256, false, true, kMaskBlocks>(p, num_sms, max_smem, stream)
                           : launch<256, false, true>(p, num_sms, max_smem, stream);
     default: return cudaErrorInvalidValue;
   }

@@ -47,6 +47,8 @@ struct FwdParams {
   // a host copy of the block mask, or nullptr; read by the launch (never by a
   // kernel) to balance the schedule
   const uint8_t* block_mask_host;
+  // the first tokens that stay visible left of the window (launch_fwd_sinks)
+  int sinks;
   // nonzero: a block mask without a host copy, whose tiles each CTA sorts
   // by cost at its start (the cost-sorted deal of fa_order.cuh)
   int cost_sorted;
@@ -75,6 +77,14 @@ struct BwdParams {
   float scale;
   float scale_log2;
   int* status;
+  // sinks: the first tokens stay visible left of the window.  The first nsb
+  // key blocks hold some; the queries past the window of such a block are cut
+  // into nfar chunks of far_rows rows, work items of their own.  Items of
+  // these blocks then leave fp32 dV, dK in sink_part [B*H_kv, nsb, nfar + 1,
+  // 2, 128, d]: the block's window item, then its chunks.  nfar = 0: the
+  // window items of these blocks run to the last query.
+  int sinks, nsb, nfar, far_rows;
+  float* sink_part;
   // block-sparse: [bm_t, bm_t] bytes, nonzero where (query block, key block)
   // is computed (blocks of 128), or nullptr
   const uint8_t* block_mask;
@@ -140,6 +150,11 @@ void plan_causal_tail(int BH, int T, int nsplit, int G, bool fwd, long long head
 void plan_mask_tail(const uint8_t* bm_host, int BH, int T, int nsplit, int G, bool fwd, int N,
                     int wl, int wr, long long head_bytes, TailTable* t);
 
+// What a forward or backward kernel's keys are limited by besides len and
+// the window: nothing, a block mask, or the window's sinks.  Instantiations of
+// their own, so that the plain kernels keep the plain walk.
+constexpr int kMaskNone = 0, kMaskBlocks = 1, kMaskSinks = 2;
+
 // Wait site recorded when the dynamic shared memory cannot hold the kernel's
 // layout at a 1024-byte aligned base.
 constexpr int kSiteSmemLayout = 99;
@@ -163,6 +178,10 @@ fa_status_t bwd_check_args(const void* q, const void* k, const void* v, const vo
 fa_status_t device_facts(int* num_sms, int* max_smem);
 
 cudaError_t launch_fwd(const FwdParams& p, int d, int num_sms, int max_smem, cudaStream_t stream);
+// The same with p.sinks first tokens visible left of the window; keys at or
+// past kv_len may hold anything.
+cudaError_t launch_fwd_sinks(const FwdParams& p, int d, int num_sms, int max_smem,
+                             cudaStream_t stream);
 cudaError_t launch_bwd_prep(const BwdParams& p, int d, cudaStream_t stream);
 // Writes p.cost_order (a block mask without a host copy; T <= kOrderMaxT).
 cudaError_t launch_bwd_order(const BwdParams& p, cudaStream_t stream);
@@ -191,11 +210,13 @@ cudaError_t launch_decode(const FwdParams& p, int d, int num_sms, int max_smem,
 cudaError_t launch_decode_combine(const FwdParams& p, int d, void* o, float* lse,
                                   cudaStream_t stream);
 cudaError_t launch_bwd_main_dt(const BwdParams& p, int d, int num_sms, int max_smem,
-                               cudaStream_t stream);
+                               cudaStream_t stream, bool sinks = false);
 // Backward main kernel for head dimension 64 (fa_bwd_d64.cu): 128-query
 // steps, dQ staged and added by bulk tensor reduce-adds through tdq, a map of
 // the [BH, Npad, 64] accumulator with a box of 32 columns x 128 rows.
 cudaError_t launch_bwd_main_d64(const BwdParams& p, int num_sms, int max_smem,
-                                cudaStream_t stream);
+                                cudaStream_t stream, bool sinks = false);
+// dK, dV of the first p.nsb key blocks from sink_part.
+cudaError_t launch_bwd_sinks_join(const BwdParams& p, int d, cudaStream_t stream);
 
 }  // namespace fa

@@ -92,6 +92,13 @@ def load():
         lib.fa_bwd_dkdv_v.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, varp, vp, sz,
                                       vp]
         lib.fa_bwd_dkdv_v.restype = i
+        lib.fa_fwd_sinks.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, varp, i, vp]
+        lib.fa_fwd_sinks.restype = i
+        lib.fa_bwd_sinks_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_bwd_sinks_workspace_bytes.restype = sz
+        lib.fa_bwd_sinks.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp,
+                                     varp, i, vp, sz, vp]
+        lib.fa_bwd_sinks.restype = i
         lib.fa_decode_splits.argtypes = [i, i, i]
         lib.fa_decode_splits.restype = i
         lib.fa_decode_workspace_bytes.argtypes = [i, i, i, i, i]
@@ -134,6 +141,7 @@ def load():
 
 EXPORTS = ("fa_fwd", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_prep", "fa_bwd_dkdv",
            "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_v", "fa_bwd_v", "fa_bwd_dkdv_v",
+           "fa_fwd_sinks", "fa_bwd_sinks_workspace_bytes", "fa_bwd_sinks",
            "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode",
            "fa_decode_paged_workspace_bytes", "fa_decode_paged", "fa_paged_append",
            "fa_pages_workspace_bytes", "fa_pages_reserve", "fa_pages_fork", "fa_pages_trim",
@@ -349,6 +357,53 @@ def fa_bwd_v(q, k, v, o, do, lse, dq, dk, dv, scale, causal=False, kv_len=None, 
     _raise(st, "fa_bwd_v")
 
 
+def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, window=None,
+                 stream=None):
+    """Calls fa_fwd_sinks: fa_fwd_v with the first `sinks` tokens visible left
+    of the window."""
+    _check_qkv("q", q)
+    B, H, N, d = q.shape
+    var = _variant(q, k, window)
+    _check_qkv("k", k, k.shape)
+    _check_qkv("v", v, k.shape)
+    _check_qkv("o", o, q.shape)
+    if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (B, H, N) \
+            or not lse.is_contiguous():
+        raise ValueError("lse: expected a contiguous fp32 CUDA tensor [B,H,N]")
+    kv_len = _check_kv_len(kv_len, B)
+    st = load().fa_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d,
+                             float(scale), int(bool(causal)), _ptr(kv_len), ctypes.byref(var),
+                             int(sinks), _stream_ptr(stream))
+    _raise(st, "fa_fwd_sinks")
+
+
+def fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, window=None, sinks=0) -> int:
+    left = -1 if window is None else int(window[0])
+    return int(load().fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, left, int(sinks)))
+
+
+def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv_len=None,
+                 window=None, workspace=None, stream=None):
+    """Calls fa_bwd_sinks; workspace of fa_bwd_sinks_workspace_bytes()."""
+    _check_qkv("q", q)
+    B, H, N, d = q.shape
+    var = _variant(q, k, window)
+    for name, t in (("o", o), ("do", do), ("dq", dq)):
+        _check_qkv(name, t, q.shape)
+    for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
+        _check_qkv(name, t, k.shape)
+    if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (B, H, N) \
+            or not lse.is_contiguous():
+        raise ValueError("lse: expected a contiguous fp32 CUDA tensor [B,H,N]")
+    kv_len = _check_kv_len(kv_len, B)
+    wp, wn = _ws(workspace)
+    st = load().fa_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                             _ptr(dk), _ptr(dv), B, H, N, d, float(scale), int(bool(causal)),
+                             _ptr(kv_len), ctypes.byref(var), int(sinks), wp, wn,
+                             _stream_ptr(stream))
+    _raise(st, "fa_bwd_sinks")
+
+
 def fa_bwd_dkdv_v(q, k, v, do, dk, dv, scale, causal=False, kv_len=None, window=None,
                   workspace=None, stream=None, block_mask=None):
     """Second backward phase for a variant: k, v, dk, dv are [B,H_kv,N,d]."""
@@ -484,14 +539,18 @@ def default_scale(d: int) -> float:
 
 
 def forward(q, k, v, scale=None, causal=False, kv_len=None, window=None, stream=None,
-            block_mask=None):
+            block_mask=None, sinks=0):
     """(O, LSE) with outputs allocated by torch on q's device.  K/V with fewer
-    heads than Q, a window or a block mask go through fa_fwd_v."""
+    heads than Q, a window or a block mask go through fa_fwd_v, sinks (first
+    tokens that stay visible left of the window) through fa_fwd_sinks."""
     B, H, N, d = q.shape
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     sc = default_scale(d) if scale is None else scale
-    if window is None and block_mask is None and k.shape == q.shape:
+    if sinks:
+        _no_block_mask(block_mask)
+        fa_fwd_sinks(q, k, v, o, lse, sc, sinks, causal, kv_len, window, stream)
+    elif window is None and block_mask is None and k.shape == q.shape:
         fa_fwd(q, k, v, o, lse, sc, causal, kv_len, stream)
     else:
         fa_fwd_v(q, k, v, o, lse, sc, causal, kv_len, window, stream, block_mask)
@@ -502,15 +561,33 @@ def workspace(B, H, N, d, device):
     return torch.empty(fa_bwd_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=device)
 
 
+def _no_block_mask(block_mask):
+    if block_mask is not None:
+        raise ValueError("sinks: not together with a block mask")
+
+
+def sinks_workspace(B, H, h_kv, N, d, device, window=None, sinks=0):
+    return torch.empty(fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, window, sinks),
+                       dtype=torch.uint8, device=device)
+
+
 def backward(q, k, v, o, lse, do, scale=None, causal=False, kv_len=None, ws=None, window=None,
-             stream=None, block_mask=None):
+             stream=None, block_mask=None, sinks=0):
     """(dQ, dK, dV) with outputs (and, if not given, the workspace) allocated by
-    torch; dK, dV are shaped like k."""
+    torch; dK, dV are shaped like k.  sinks as in forward (ws is then a
+    sinks_workspace)."""
     B, H, N, d = q.shape
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+    sc = default_scale(d) if scale is None else scale
+    if sinks:
+        _no_block_mask(block_mask)
+        if ws is None:
+            ws = sinks_workspace(B, H, k.shape[1], N, d, q.device, window, sinks)
+        fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, sc, sinks, causal, kv_len, window, ws,
+                     stream)
+        return dq, dk, dv
     if ws is None:
         ws = workspace(B, H, N, d, q.device)
-    sc = default_scale(d) if scale is None else scale
     if window is None and block_mask is None and k.shape == q.shape:
         fa_bwd(q, k, v, o, do, lse, dq, dk, dv, sc, causal, kv_len, ws, stream)
     else:

@@ -196,6 +196,32 @@ fa_status_t fa_bwd_dkdv_v(const void* q, const void* k, const void* v, const voi
                           size_t workspace_bytes, void* stream);
 
 /*
+ * Attention with a sliding window and sinks, forward and backward: the first
+ * `sinks` (>= 0) tokens stay visible left of the window, so query i sees key j
+ * when j < kv_len, j <= i + window_right (j <= i when causal), and
+ * j >= i - window_left or j < sinks.  Everything else as fa_fwd_v and
+ * fa_bwd_v (with sinks = 0, or window_left = -1, the same results), except:
+ * - a block mask is refused (FA_ERR_UNSUPPORTED);
+ * - K and V rows at or past kv_len may hold anything, NaN included (their
+ *   gradients are 0).
+ * Key blocks that hold neither sinks nor window are skipped.  dK and dV of the
+ * sinks' key blocks sum over all later queries: the backward cuts these into
+ * chunks that run on separate SMs, whose fp32 parts lie in the workspace and
+ * are added in order, so dK and dV repeat bit for bit.  workspace:
+ * fa_bwd_sinks_workspace_bytes (0 for invalid sizes), 256-byte aligned.
+ */
+fa_status_t fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                         int H, int N, int d, float scale, int causal, const int* kv_len,
+                         const fa_variant_t* variant, int sinks, void* stream);
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int h_kv, int N, int d, int window_left,
+                                    int sinks);
+fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                         const void* dO, const float* lse, void* dq, void* dk, void* dv, int B,
+                         int H, int N, int d, float scale, int causal, const int* kv_len,
+                         const fa_variant_t* variant, int sinks, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
  * Split-KV decoding: Nq new queries per head against a long key/value cache
  * (FlashDecoding, "4. FlashAttention 深度剖析" 4.8.3).  The keys of every K/V
  * head are cut into `splits` chunks that different SMs process at once; each
@@ -462,7 +488,8 @@ const char* fa_status_string(fa_status_t status);
 
 /* Library version as major*10000 + minor*100 + patch.  1.1: fa_variant_t
  * gained block_mask (a trailing member, NULL in aggregate initialisers that
- * stop before it).  1.2: fa_variant_t gained block_mask_host (the same). */
+ * stop before it).  1.2: fa_variant_t gained block_mask_host (the same).
+ * 1.3: sinks, the paged cache. */
 int fa_version(void);
 
 #ifdef __cplusplus
