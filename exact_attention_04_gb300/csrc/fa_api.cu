@@ -481,6 +481,9 @@ fa_status_t fwd_impl(const void* q, const void* k, const void* v, void* o, float
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.status = di->status;
   p.sinks = sinks;
+  p.fd_t = fa::FastDiv::of((N + 127) / 128);
+  p.fd_h = fa::FastDiv::of(H);
+  p.fd_g = fa::FastDiv::of(H / var.H_kv);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = sinks >= 0 ? fa::launch_fwd_sinks(p, d, di->num_sms, di->max_smem, s)
                                    : fa::launch_fwd(p, d, di->num_sms, di->max_smem, s);

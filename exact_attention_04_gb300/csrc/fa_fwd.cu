@@ -89,7 +89,7 @@ constexpr float kFp8Shift = 4.0f;   // log2 of the multiplier 16 = 2^(8 - slack)
 // FP8 = true: E4M3 Q and K (one byte an element, so a 128-byte swizzle row
 // holds 128 of them) and V transposed per K/V head ([d, keys]: a V block is d
 // rows of 128 keys, the K-major B operand of P V).
-template <int D, bool FP8 = false>
+template <int D, bool FP8 = false, int MK = kMaskNone>
 struct Cfg {
   static_assert(!FP8 || D >= 128, "E4M3 rows need at least 128 bytes");
   static constexpr int BOX_COLS = FP8 ? 128 : 64;    // elements in one 128-byte swizzle row
@@ -104,10 +104,14 @@ struct Cfg {
   static constexpr bool SEP = (D == 256 && !FP8);
   // NSB S buffers: block g uses columns [128*(g%NSB), +128).  NPB P buffers
   // (without SEP, P buffer b is the start of S buffer b).
-  // (E4M3 at d = 128 takes the key-half split below with two S buffers, so
-  // that its two 128-column O parts fit.)
-  static constexpr bool F8SPLIT = FP8 && D == 128;
-  static constexpr int NSB = SEP ? 1 : (F8SPLIT ? 2 : (D <= 128 ? 3 : 2));
+  // (E4M3 and sinks at d = 128 take the key-half split below with two S
+  // buffers, so that their two 128-column O parts fit.  With sinks a tile has
+  // few blocks, and the epilogue warps, the shorter masked path and the
+  // halves' overlap outweigh what the third S buffer is worth on long rows:
+  // window 255 73 us against 93, 1023 133 / 144, 2047 208 / 213, 4095 325 /
+  // 326 at the shape below.)
+  static constexpr bool SPLIT128 = D == 128 && (FP8 || MK == kMaskSinks);
+  static constexpr int NSB = SEP ? 1 : (SPLIT128 ? 2 : (D <= 128 ? 3 : 2));
   static constexpr int NPB = SEP ? 2 : NSB;
   static constexpr int PW = FP8 ? BN / 4 : BN / 2;   // columns of one block's P
   static constexpr uint32_t TM_S = 0;
@@ -124,7 +128,7 @@ struct Cfg {
   // the epilogue).  The two warps of a sub-partition never wait for each
   // other, so one computes while the other waits (for tensor memory, on a
   // barrier); elsewhere one warp a row.
-  static constexpr int NHALF = ((D == 64 && !FP8) || F8SPLIT) ? 2 : 1;
+  static constexpr int NHALF = ((D == 64 && !FP8) || SPLIT128) ? 2 : 1;
   static constexpr int OCOLS = D * NHALF;            // columns of O (its key halves)
   // EPI (with the split): four epilogue warps merge each tile's O halves,
   // divide by l, store bf16 O and LSE, off the softmax warps (whose time per
@@ -137,9 +141,9 @@ struct Cfg {
   static_assert(TM_O + OCOLS * NOB <= TM_COLS, "tensor memory budget (O)");
 };
 
-template <int D, bool FP8 = false>
+template <int D, bool FP8 = false, int MK = kMaskNone>
 struct FwdSmem {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<D, FP8, MK>;
   alignas(1024) uint8_t q[C::TILE_BYTES];
   alignas(1024) uint8_t k[C::STAGES][C::TILE_BYTES];
   alignas(1024) uint8_t v[C::STAGES][C::V_BYTES];
@@ -165,7 +169,7 @@ struct FwdSmem {
   uint64_t mma_done, pv_mma_done;
   // a block mask without a host copy: the tiles' costs, then their
   // cost-sorted order (fa_order.cuh)
-  uint32_t order[kFwdOrderMaxT];
+  uint32_t order[MK == kMaskSinks ? 1 : kFwdOrderMaxT];
   uint32_t tmem_base;
   int abort;
 };
@@ -198,9 +202,10 @@ struct Sched {
   int BH;
   const uint32_t* order;     // the cost-sorted order, or nullptr
   const int* kvl;            // kv_len staged in shared memory, or nullptr
+  const FastDiv* fd;         // sinks: division by T, else nullptr
   __device__ Sched(int BH_, int N, int causal_, int tail_heads, const uint32_t* order_,
-                   const int* kvl_)
-      : causal(causal_), BH(BH_), order(order_), kvl(kvl_) {
+                   const int* kvl_, const FastDiv* fd_)
+      : causal(causal_), BH(BH_), order(order_), kvl(kvl_), fd(fd_) {
     T = (N + BM - 1) / BM;
     P = (T + 1) / 2;
     units = (BH - tail_heads) * (causal ? P : T);
@@ -212,8 +217,8 @@ struct Sched {
   }
   __device__ void tile(int u, int k, int& bh, int& m) const {
     if (!causal) {
-      bh = u / T;
-      m = u % T;
+      bh = fd ? fd->div(u) : u / T;
+      m = u - bh * T;
     } else {
       bh = u / P;
       const int p = u % P;
@@ -273,8 +278,15 @@ __device__ __forceinline__ void make_tile(const FwdParams& p, int u, int bh, int
   if constexpr (!DEC) {
     t.qy = m * BM;
     t.qz = bh;
-    t.kvbh = kv_head_of(bh, p.H, p.H_kv);
-    t.len = seq_len(p, bh, kvl);
+    if constexpr (MK == kMaskSinks) {   // a tile of few blocks starts often: no divisions
+      const int b = p.fd_h.div(bh);
+      t.kvbh = b * p.H_kv + p.fd_g.div(bh - b * p.H);
+      t.len = p.N;
+      if (p.kv_len) t.len = max(0, min(p.N, kvl ? kvl[b] : __ldg(p.kv_len + b)));
+    } else {
+      t.kvbh = kv_head_of(bh, p.H, p.H_kv);
+      t.len = seq_len(p, bh, kvl);
+    }
     t.qlo = m * BM;
     t.qhi = m * BM + BM - 1;
     t.nkv = tile_blocks(p, m, t.len, t.jlo);
@@ -392,12 +404,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 template <int D, bool DEC, bool FP8, int MK>
-__global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, FP8, MK>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ TailTable tail) {
   static_assert(!(DEC && FP8), "decode runs in bf16");
   constexpr bool BS = MK == kMaskBlocks;
-  using C = Cfg<D, FP8>;
-  using Smem = FwdSmem<D, FP8>;
+  using C = Cfg<D, FP8, MK>;
+  using Smem = FwdSmem<D, FP8, MK>;
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
@@ -481,7 +493,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   const int BH = p.B * p.H;
   const Sched sched(BH, p.N, p.causal, DEC ? 0 : tail.heads,
                     (BS && !DEC && p.cost_sorted) ? sm.order : nullptr,
-                    (C::EPI && D == 64 && p.kv_len && p.B <= kKvlCache) ? sm.kvl : nullptr);
+                    (C::EPI && D == 64 && p.kv_len && p.B <= kKvlCache) ? sm.kvl : nullptr,
+                    MK == kMaskSinks ? &p.fd_t : nullptr);
   const int nunits = DEC ? p.B * p.H_kv * p.splits : sched.units;
 
   if (warp == 0) {
@@ -1063,10 +1076,28 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // columns below them left of the window
             const int c_hi = min(len - key0 - 1, row + p.wr - key0);
             const int c_lo = row - p.wl - key0;
-            const int c_sk = MK == kMaskSinks ? p.sinks - key0 : 0;
+            if constexpr (MK == kMaskSinks) {
+              // A bit a column, 32 columns at a time: few instructions,
+              // since a tile of a few blocks runs this path for half of them
+              // and the code is cold each time (two comparisons a column
+              // measured 145 against 136 us, skipping the chunks that all of the warp's rows
+              // see 133: H = 32, h_kv = 8, N = 8192, window 1023, 16 sinks).
+              auto below = [](int x) { return x >= 32 ? ~0u : (x <= 0 ? 0u : (1u << x) - 1u); };
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (c > c_hi || (c < c_lo && (MK != kMaskSinks || c >= c_sk))) s[c] = -INFINITY;
+              for (int w = 0; w < NC / 32; ++w) {
+                const uint32_t on = below(c_hi + 1 - 32 * w) &
+                                    (~below(c_lo - 32 * w) | below(p.sinks - key0 - 32 * w));
+                if (__any_sync(0xffffffffu, on != ~0u)) {
+#pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    if (!((on >> c) & 1u)) s[32 * w + c] = -INFINITY;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                if (c > c_hi || c < c_lo) s[c] = -INFINITY;
+            }
           }
           // row maximum: four chains of three-input max over s[0 .. NC)
           static_assert(NC % 8 == 0, "the max chains take 8 columns a step");
@@ -1235,7 +1266,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 
 template <int D, bool DEC, bool FP8 = false, int MK = kMaskNone>
 cudaError_t launch(const FwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
-  const size_t smem = smem_request(sizeof(FwdSmem<D, FP8>), max_smem);
+  const size_t smem = smem_request(sizeof(FwdSmem<D, FP8, MK>), max_smem);
   cudaError_t e = cudaFuncSetAttribute(fa_fwd_kernel<D, DEC, FP8, MK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
@@ -1266,7 +1297,7 @@ cudaError_t launch(const FwdParams& p, int num_sms, int max_smem, cudaStream_t s
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  fa_fwd_kernel<D, DEC, FP8, MK><<<grid, Cfg<D, FP8>::THREADS, smem, stream>>>(p, tail);
+  fa_fwd_kernel<D, DEC, FP8, MK><<<grid, Cfg<D, FP8, MK>::THREADS, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }
 

@@ -18,6 +18,21 @@ __host__ __device__ constexpr int status_code(int site) { return kStatusTimeout 
 // Kernels give up on any single wait after this much global time.
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;
 
+// Division of 0 <= n < 2^31 by a d >= 1 known at the launch: with l = ceil(log2
+// d) and m = ceil(2^(31 + l) / d) < 2^32, n / d = floor(n m / 2^(31 + l)),
+// since n (m d - 2^(31 + l)) < n d <= 2^(31 + l).
+struct FastDiv {
+  uint32_t mul, shift;
+  __host__ static FastDiv of(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+};
+
 struct FwdParams {
   CUtensorMap tq, tk, tv;      // bf16 [BH, N, d] viewed as 3-D (d, N, BH), box (64, 128, 1), SW128
   void* o;                     // bf16 [B, H, N, d]
@@ -47,8 +62,11 @@ struct FwdParams {
   // a host copy of the block mask, or nullptr; read by the launch (never by a
   // kernel) to balance the schedule
   const uint8_t* block_mask_host;
-  // the first tokens that stay visible left of the window (launch_fwd_sinks)
+  // the first tokens that stay visible left of the window (launch_fwd_sinks),
+  // and the divisions that a tile's place takes there: by the tiles of a
+  // head, the query heads, and the query heads of a K/V head
   int sinks;
+  FastDiv fd_t, fd_h, fd_g;
   // nonzero: a block mask without a host copy, whose tiles each CTA sorts
   // by cost at its start (the cost-sorted deal of fa_order.cuh)
   int cost_sorted;

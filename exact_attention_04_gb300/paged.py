@@ -18,7 +18,6 @@ A serving loop::
     table, ref = trim(cache, table, kv_len, ref, 4095, 4)
     table, kv_len, ref, info = fork(cache, table, kv_len, ref, parent)
 """
-import contextlib
 import ctypes
 import math
 
@@ -26,14 +25,18 @@ import torch
 
 from . import fa
 
-_NO_STREAM = contextlib.nullcontext()
+_current_device = torch.cuda.current_device
+# the current stream of a device as a raw handle; torch.cuda.current_stream()
+# takes 3 us of the about 15 that a small call costs its host
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_int32, _bf16 = torch.int32, torch.bfloat16
 
 
-def _on(stream):
-    """The context that outputs are allocated in, and the raw stream."""
-    if stream is None:
-        return _NO_STREAM, torch.cuda.current_stream().cuda_stream
-    return torch.cuda.stream(stream), stream.cuda_stream
+def _on_stream(call, stream, *args, **kw):
+    """call(...) with `stream` the current one, so that its outputs are
+    allocated for it."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 class PagedKV:
@@ -68,6 +71,7 @@ class PagedKV:
                                    self.num_pages, self.page_size, self.h_kv, self.d)
         self.ref = ctypes.byref(self.struct)
         self.scale = 1.0 / math.sqrt(self.d)
+        self._need = {}        # workspace sizes by (H) or (rows,)
 
     def empty(self, rows, max_pages):
         """(table, kv_len, ref) of a cache without tokens."""
@@ -77,7 +81,7 @@ class PagedKV:
 
 
 def _ints(name, t, shape, index):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() \
+    if t.dtype is not _int32 or t.shape != shape or not t.is_contiguous() \
             or t.get_device() != index:
         raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor {list(shape)} on the "
                          "cache's device")
@@ -85,11 +89,13 @@ def _ints(name, t, shape, index):
 
 
 def _table(cache, table):
-    if table.dim() != 2:
+    """The table's address and shape."""
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table: expected int32 [rows, max_pages]")
-    if cache.index != torch.cuda.current_device():
+    if cache.index != _current_device():
         raise ValueError("the cache is not on the current CUDA device")
-    return _ints("table", table, table.shape, cache.index), table.shape[0], table.shape[1]
+    return _ints("table", table, shape, cache.index), shape[0], shape[1]
 
 
 def _check(status, where):
@@ -97,24 +103,40 @@ def _check(status, where):
         raise fa.FAError(status, where)
 
 
-def _bytes(ws, need):
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws: expected a contiguous CUDA tensor")
-    if ws.numel() * ws.element_size() < need:
+def _bytes(ws, need, like):
+    """The address of a workspace of `need` bytes: ws, or one allocated beside
+    `like` (returned to hold it)."""
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif not ws.is_cuda or not ws.is_contiguous() or ws.device != like.device:
+        raise ValueError("ws: expected a contiguous CUDA tensor on the cache's device")
+    elif ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws: {need} bytes are needed")
-    return ws.data_ptr()
+    return ws, ws.data_ptr()
+
+
+def _pages_need(cache, rows):
+    n = cache._need.get((rows,))
+    if n is None:
+        n = cache._need[(rows,)] = fa.load().fa_pages_workspace_bytes(cache.num_pages, rows)
+    return n
+
+
+def _decode_need(cache, H):
+    n = cache._need.get(H)
+    if n is None:
+        n = cache._need[H] = fa.load().fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
+    return n
 
 
 def workspace(cache, rows=1):
     """A workspace for reserve, fork and compact of up to `rows` rows."""
-    n = fa.load().fa_pages_workspace_bytes(cache.num_pages, rows)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(_pages_need(cache, rows), dtype=torch.uint8, device=cache.device)
 
 
 def decode_workspace(cache, H):
     """A workspace for decode with H query heads."""
-    n = fa.load().fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(_decode_need(cache, H), dtype=torch.uint8, device=cache.device)
 
 
 def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=None, stream=None):
@@ -122,61 +144,65 @@ def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=
     over its pages; q [B, H, 1, d], O like q, LSE fp32 [B, H, 1].  window:
     (left, right), of which only left matters here, or None; sinks: first
     tokens that stay visible.  ws: decode_workspace(), else allocated."""
+    if stream is not None:
+        return _on_stream(decode, stream, q, cache, layer, table, kv_len, scale, window, sinks, ws)
     tp, rows, max_pages = _table(cache, table)
-    if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.shape[0] != rows or q.shape[2] != 1 \
-            or q.shape[3] != cache.d or not q.is_contiguous() or q.get_device() != cache.index:
+    index = cache.index
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != rows or shape[2] != 1 or shape[3] != cache.d \
+            or q.dtype is not _bf16 or not q.is_contiguous() or q.get_device() != index:
         raise ValueError("q: expected a contiguous bf16 CUDA tensor [rows, H, 1, d]")
-    lp = _ints("kv_len", kv_len, (rows,), cache.index)
-    H = q.shape[1]
-    lib = fa.load()
-    need = lib.fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
-    ctx, raw = _on(stream)
-    with ctx:
-        o = torch.empty_like(q)
-        lse = torch.empty((rows, H, 1), dtype=torch.float32, device=q.device)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib.fa_decode_paged(q.data_ptr(), cache.ref, layer, tp, max_pages, lp, o.data_ptr(),
-                               lse.data_ptr(), rows, H, cache.scale if scale is None else scale,
-                               -1 if window is None else int(window[0]), sinks, _bytes(ws, need),
-                               need, raw), "fa_decode_paged")
+    lp = _ints("kv_len", kv_len, shape[:1], index)
+    H = shape[1]
+    need = _decode_need(cache, H)
+    o = torch.empty_like(q)
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    ws, wp = _bytes(ws, need, q)
+    _check(fa.load().fa_decode_paged(
+        q.data_ptr(), cache.ref, layer, tp, max_pages, lp, o.data_ptr(), lse.data_ptr(), rows, H,
+        cache.scale if scale is None else scale, -1 if window is None else int(window[0]), sinks,
+        wp, need, _current_raw_stream(index)), "fa_decode_paged")
     return o, lse
 
 
 def append(k_new, v_new, cache, layer, table, start, kv_len, stream=None):
     """Writes k_new, v_new [rows, h_kv, n, d]: token t of a row to position
     start + t where that is below kv_len."""
+    if stream is not None:
+        return _on_stream(append, stream, k_new, v_new, cache, layer, table, start, kv_len)
     tp, rows, max_pages = _table(cache, table)
+    index = cache.index
+    shape = k_new.shape
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.shape != k_new.shape \
-                or t.shape[0] != rows or t.shape[1] != cache.h_kv or t.shape[3] != cache.d \
-                or not t.is_contiguous() or t.get_device() != cache.index:
+        if t.shape != shape or len(shape) != 4 or shape[0] != rows or shape[1] != cache.h_kv \
+                or shape[3] != cache.d or t.dtype is not _bf16 or not t.is_contiguous() \
+                or t.get_device() != index:
             raise ValueError(f"{name}: expected a contiguous bf16 CUDA tensor [rows, h_kv, n, d]")
-    _check(fa.load().fa_paged_append(k_new.data_ptr(), v_new.data_ptr(), cache.ref, layer, tp,
-                                     max_pages, _ints("start", start, (rows,), cache.index),
-                                     _ints("kv_len", kv_len, (rows,), cache.index), rows,
-                                     k_new.shape[2], _on(stream)[1]), "fa_paged_append")
+    _check(fa.load().fa_paged_append(
+        k_new.data_ptr(), v_new.data_ptr(), cache.ref, layer, tp, max_pages,
+        _ints("start", start, shape[:1], index), _ints("kv_len", kv_len, shape[:1], index), rows,
+        shape[2], _current_raw_stream(index)), "fa_paged_append")
 
 
 def reserve(cache, table, kv_len, ref, n_new, ws=None, stream=None):
     """(kv_len, ref, info) after every row has got the pages for n_new more
     tokens; the table is updated in place.  info = [free pages left, pages that
     were missing]."""
+    if stream is not None:
+        return _on_stream(reserve, stream, cache, table, kv_len, ref, n_new, ws)
     tp, rows, max_pages = _table(cache, table)
-    lib = fa.load()
-    need = lib.fa_pages_workspace_bytes(cache.num_pages, rows)
-    ctx, raw = _on(stream)
-    with ctx:
-        len_out, ref_out = torch.empty_like(kv_len), torch.empty_like(ref)
-        info = torch.empty(2, dtype=torch.int32, device=ref.device)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
-    _check(lib.fa_pages_reserve(tp, max_pages, cache.page_size,
-                                _ints("kv_len", kv_len, (rows,), cache.index),
-                                _ints("n_new", n_new, (rows,), cache.index),
-                                _ints("ref", ref, (cache.num_pages,), cache.index),
-                                cache.num_pages, rows, len_out.data_ptr(), ref_out.data_ptr(),
-                                info.data_ptr(), _bytes(ws, need), need, raw), "fa_pages_reserve")
+    index, num_pages = cache.index, cache.num_pages
+    lp = _ints("kv_len", kv_len, (rows,), index)
+    ap = _ints("n_new", n_new, (rows,), index)
+    rp = _ints("ref", ref, (num_pages,), index)
+    need = _pages_need(cache, rows)
+    len_out, ref_out = torch.empty_like(kv_len), torch.empty_like(ref)
+    info = torch.empty(2, dtype=_int32, device=ref.device)
+    ws, wp = _bytes(ws, need, ref)
+    _check(fa.load().fa_pages_reserve(
+        tp, max_pages, cache.page_size, lp, ap, rp, num_pages, rows, len_out.data_ptr(),
+        ref_out.data_ptr(), info.data_ptr(), wp, need, _current_raw_stream(index)),
+        "fa_pages_reserve")
     return len_out, ref_out, info
 
 
@@ -185,59 +211,60 @@ def fork(cache, table, kv_len, ref, parent, ws=None, stream=None):
     parent[r] (-1: an empty row): beams are reordered, rows forked, and rows
     that nobody continues freed.  Partly filled pages that several rows
     continue are copied.  info as of reserve."""
+    if stream is not None:
+        return _on_stream(fork, stream, cache, table, kv_len, ref, parent, ws)
     tp, rows, max_pages = _table(cache, table)
+    index = cache.index
     if parent.dim() != 1 or parent.numel() < 1:
         raise ValueError("parent: expected int32 [new rows]")
     new_rows = parent.numel()
-    lib = fa.load()
-    need = lib.fa_pages_workspace_bytes(cache.num_pages, max(rows, new_rows))
-    ctx, raw = _on(stream)
-    with ctx:
-        ints = dict(dtype=torch.int32, device=ref.device)
-        table_out = torch.empty((new_rows, max_pages), **ints)
-        len_out, ref_out = torch.empty(new_rows, **ints), torch.empty_like(ref)
-        info = torch.empty(2, **ints)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
-    _check(lib.fa_pages_fork(cache.ref, tp, max_pages,
-                             _ints("kv_len", kv_len, (rows,), cache.index),
-                             _ints("ref", ref, (cache.num_pages,), cache.index), rows,
-                             _ints("parent", parent, (new_rows,), cache.index), new_rows,
-                             table_out.data_ptr(), len_out.data_ptr(), ref_out.data_ptr(),
-                             info.data_ptr(), _bytes(ws, need), need, raw), "fa_pages_fork")
+    lp = _ints("kv_len", kv_len, (rows,), index)
+    rp = _ints("ref", ref, (cache.num_pages,), index)
+    pp = _ints("parent", parent, (new_rows,), index)
+    need = _pages_need(cache, max(rows, new_rows))
+    if new_rows == rows:
+        table_out = torch.empty_like(table)
+    else:
+        table_out = torch.empty((new_rows, max_pages), dtype=_int32, device=ref.device)
+    len_out, ref_out = torch.empty_like(parent), torch.empty_like(ref)
+    info = torch.empty(2, dtype=_int32, device=ref.device)
+    ws, wp = _bytes(ws, need, ref)
+    _check(fa.load().fa_pages_fork(
+        cache.ref, tp, max_pages, lp, rp, rows, pp, new_rows, table_out.data_ptr(),
+        len_out.data_ptr(), ref_out.data_ptr(), info.data_ptr(), wp, need,
+        _current_raw_stream(index)), "fa_pages_fork")
     return table_out, len_out, ref_out, info
 
 
 def trim(cache, table, kv_len, ref, window_left, sinks=0, stream=None):
     """(table, ref) without the pages that no later token sees under a window
     of window_left and `sinks` first tokens."""
+    if stream is not None:
+        return _on_stream(trim, stream, cache, table, kv_len, ref, window_left, sinks)
     tp, rows, max_pages = _table(cache, table)
-    ctx, raw = _on(stream)
-    with ctx:
-        table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
-    _check(fa.load().fa_pages_trim(tp, max_pages, cache.page_size,
-                                   _ints("kv_len", kv_len, (rows,), cache.index),
-                                   _ints("ref", ref, (cache.num_pages,), cache.index),
-                                   cache.num_pages, rows, window_left, sinks,
-                                   table_out.data_ptr(), ref_out.data_ptr(), raw),
-           "fa_pages_trim")
+    index, num_pages = cache.index, cache.num_pages
+    lp = _ints("kv_len", kv_len, (rows,), index)
+    rp = _ints("ref", ref, (num_pages,), index)
+    table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
+    _check(fa.load().fa_pages_trim(
+        tp, max_pages, cache.page_size, lp, rp, num_pages, rows, window_left, sinks,
+        table_out.data_ptr(), ref_out.data_ptr(), _current_raw_stream(index)), "fa_pages_trim")
     return table_out, ref_out
 
 
 def compact(cache, table, ref, ws=None, stream=None):
     """(table, ref, info) after the pages in use have moved to the front of the
     pool.  info = [pages in use, pages moved]."""
+    if stream is not None:
+        return _on_stream(compact, stream, cache, table, ref, ws)
     tp, rows, max_pages = _table(cache, table)
-    lib = fa.load()
-    need = lib.fa_pages_workspace_bytes(cache.num_pages, rows)
-    ctx, raw = _on(stream)
-    with ctx:
-        table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
-        info = torch.empty(2, dtype=torch.int32, device=ref.device)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
-    _check(lib.fa_pages_compact(cache.ref, tp, max_pages,
-                                _ints("ref", ref, (cache.num_pages,), cache.index), rows,
-                                table_out.data_ptr(), ref_out.data_ptr(), info.data_ptr(),
-                                _bytes(ws, need), need, raw), "fa_pages_compact")
+    index = cache.index
+    rp = _ints("ref", ref, (cache.num_pages,), index)
+    need = _pages_need(cache, rows)
+    table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
+    info = torch.empty(2, dtype=_int32, device=ref.device)
+    ws, wp = _bytes(ws, need, ref)
+    _check(fa.load().fa_pages_compact(
+        cache.ref, tp, max_pages, rp, rows, table_out.data_ptr(), ref_out.data_ptr(),
+        info.data_ptr(), wp, need, _current_raw_stream(index)), "fa_pages_compact")
     return table_out, ref_out, info

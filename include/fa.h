@@ -200,7 +200,7 @@ fa_status_t fa_bwd_dkdv_v(const void* q, const void* k, const void* v, const voi
  * `sinks` (>= 0) tokens stay visible left of the window, so query i sees key j
  * when j < kv_len, j <= i + window_right (j <= i when causal), and
  * j >= i - window_left or j < sinks.  Everything else as fa_fwd_v and
- * fa_bwd_v (with sinks = 0, or window_left = -1, the same results), except:
+ * fa_bwd_v (which sinks = 0 or window_left = -1 amount to), except:
  * - a block mask is refused (FA_ERR_UNSUPPORTED);
  * - K and V rows at or past kv_len may hold anything, NaN included (their
  *   gradients are 0).

@@ -173,7 +173,7 @@ def test_wrappers_refuse():
     with pytest.raises(ValueError):
         paged._table(Fake, torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError):
-        paged._bytes(torch.zeros(8, dtype=torch.uint8), 4)
+        paged._bytes(torch.zeros(8, dtype=torch.uint8), 4, None)
     q = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         fa.forward(q, q, q, window=(2, 0), sinks=1)        # not on a GPU

@@ -94,23 +94,22 @@ def test_rows_past_kv_len_may_hold_anything(d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_without_sinks_the_window_s_results(d):
-    """sinks beyond the window's reach, or no sinks through the same entry
-    points, give fa_fwd_v's and fa_bwd_v's results."""
+def test_without_sinks_the_window_alone(d):
+    """No sinks through the same entry points: the window's attention (the
+    kernels may cut a row's keys in other places than fa_fwd_v's, so both are
+    held to the definition, not to each other's bits)."""
     x = inputs(1, 4, 2, 600, d, 5)
-    plain = run(x, causal=True, window=(255, 0))
+    kw = dict(causal=True, window=(255, 0))
+    compare(x, run(x, **kw), **kw)
     B, H, N, _ = x["q"].shape
     o, lse = torch.empty_like(x["q"]), torch.empty(B, H, N, device="cuda")
     fa.fa_fwd_sinks(x["q"], x["k"], x["v"], o, lse, d ** -0.5, 0, True, None, (255, 0))
-    assert torch.equal(o, plain["o"]) and torch.equal(lse, plain["lse"])
     dq, dk, dv = torch.empty_like(o), torch.empty_like(x["k"]), torch.empty_like(x["v"])
     ws = fa.sinks_workspace(B, H, 2, N, d, "cuda", (255, 0), 0)
     fa.fa_bwd_sinks(x["q"], x["k"], x["v"], o, x["do"], lse, dq, dk, dv, d ** -0.5, 0, True, None,
                     (255, 0), ws)
     fa.fa_check()
-    assert torch.equal(dk, plain["dk"]) and torch.equal(dv, plain["dv"])
-    # dQ is summed in an order that varies: a bf16 step of the larger of two
-    assert ((dq - plain["dq"]).abs() <= 2 ** -7 * plain["dq"].abs() + 1e-5).all()
+    compare(x, dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv), **kw)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
