@@ -196,34 +196,23 @@ void bound_window(Variant* v) {
   v->wr = std::min(v->wr, fa::kUnbounded);
 }
 
-// How the backward cuts the queries that see a key block only through its
-// sinks (those past the window of the block's last key).  In blocks of 128
-// rows, `far` are left past the first block's window; a chunk is at least as
-// long as a window item (so that items stay alike) and 8 blocks, and there are
-// at most 32 chunks over all sink blocks.  No such block: the window items of
-// the sink blocks run to the last query.
-struct SinkPlan {
-  int nsb, nfar, far_rows;
-};
-
-SinkPlan plan_sinks(int N, int wl, int sinks) {
-  SinkPlan s{0, 0, 0};
-  if (sinks < 1) return s;
-  s.nsb = static_cast<int>((std::min(sinks, N) + 127ll) / 128);
+// CTAs of the backward with sinks: one an SM, fewer where all steps (blocks of
+// 128 queries, every key visible to its window's queries and the sinks to
+// all) would leave them less than four steps each.
+int sink_ctas(long long heads, int N, int wl, int sinks, int num_sms) {
   const long long T = (N + 127ll) / 128;
-  const long long far = T - (128ll + wl + 127) / 128;
-  if (far < 1) return s;
-  const long long most = std::max(1, 32 / s.nsb);
-  const long long len = std::max({(wl + 127ll) / 128 + 2, 8ll, (far + most - 1) / most});
-  s.nfar = static_cast<int>((far + len - 1) / len);
-  s.far_rows = static_cast<int>(std::min(len, T) * 128);
-  return s;
+  const long long seen = std::min(T, (wl + 127ll) / 128 + 1);
+  const long long steps = heads * T * (seen + std::min(T, (sinks + 127ll) / 128));
+  return static_cast<int>(std::max(1ll, std::min<long long>(num_sms, steps / 4)));
 }
 
-size_t sink_part_bytes(const SinkPlan& s, long long heads, int d) {
-  if (s.nfar == 0) return 0;
-  return round_up256(static_cast<size_t>(heads) * s.nsb * (s.nfar + 1) * 2 * 128 * d *
-                     sizeof(float));
+// Its share of the workspace: the cut items' rows (at most two pieces a CTA)
+// and what each CTA starts with.
+size_t sink_part_bytes(int num_sms, int d) {
+  return round_up256(static_cast<size_t>(2) * num_sms * 2 * 128 * std::min(d, 128) * sizeof(float));
+}
+size_t sink_meta_bytes(int num_sms) {
+  return round_up256(static_cast<size_t>(2) * num_sms * sizeof(int));
 }
 
 }  // namespace
@@ -640,9 +629,8 @@ fa_status_t bwd_main_impl(fa::BwdParams& p, const DeviceInfo* di, const void* q,
   p.v = v;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.cost_order && fa::launch_bwd_order(p, s) != cudaSuccess) return FA_ERR_CUDA;
-  cudaError_t e = dt ? fa::launch_bwd_main_dt(p, d, di->num_sms, di->max_smem, s, sinks)
-                     : fa::launch_bwd_main_d64(p, di->num_sms, di->max_smem, s, sinks);
-  if (e == cudaSuccess && sinks && p.nfar > 0) e = fa::launch_bwd_sinks_join(p, d, s);
+  const cudaError_t e = dt ? fa::launch_bwd_main_dt(p, d, di->num_sms, di->max_smem, s, sinks)
+                           : fa::launch_bwd_main_d64(p, di->num_sms, di->max_smem, s, sinks);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -744,12 +732,12 @@ fa_status_t fa_bwd_v(const void* q, const void* k, const void* v, const void* o,
   return r;
 }
 
-size_t fa_bwd_sinks_workspace_bytes(int B, int H, int h_kv, int N, int d, int window_left,
-                                    int sinks) {
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int N, int d) {
   const size_t base = fa_bwd_workspace_bytes(B, H, N, d);
-  if (base == 0 || h_kv < 1 || h_kv > H || H % h_kv || window_left < -1 || sinks < 0) return 0;
-  const int wl = window_left < 0 ? fa::kUnbounded : std::min(window_left, fa::kUnbounded);
-  return base + sink_part_bytes(plan_sinks(N, wl, sinks), static_cast<long long>(B) * h_kv, d);
+  if (base == 0) return 0;
+  DeviceInfo* di = device_info(nullptr);
+  const int sms = (di && di->err == cudaSuccess && di->num_sms > 0) ? di->num_sms : 152;
+  return base + sink_part_bytes(sms, d) + sink_meta_bytes(sms);
 }
 
 fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
@@ -765,9 +753,7 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
     return FA_ERR_INVALID_ARG;
   if (variant && variant->block_mask) return FA_ERR_UNSUPPORTED;
   // (0 for sizes that bwd_setup refuses)
-  if (workspace_bytes < fa_bwd_sinks_workspace_bytes(B, H, variant ? variant->h_kv : H, N, d,
-                                                     variant ? variant->window_left : -1, sinks))
-    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_bwd_sinks_workspace_bytes(B, H, N, d)) return FA_ERR_INVALID_ARG;
   fa::BwdParams p;
   DeviceInfo* di = nullptr;
   const fa_status_t st = bwd_setup(&p, &di, B, H, N, d, scale, causal, kv_len, variant, workspace,
@@ -775,13 +761,12 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   if (st != FA_OK) return st;
   p.wl = std::min(p.wl, fa::kUnbounded);
   p.wr = std::min(p.wr, fa::kUnbounded);
-  const SinkPlan plan = plan_sinks(N, p.wl, sinks);
+  char* extra = static_cast<char*>(workspace) + fa_bwd_workspace_bytes(B, H, N, d);
   p.sinks = sinks;
-  p.nsb = plan.nsb;
-  p.nfar = plan.nfar;
-  p.far_rows = plan.far_rows;
-  p.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                         fa_bwd_workspace_bytes(B, H, N, d));
+  p.sk_ctas = sink_ctas(static_cast<long long>(B) * H, N, p.wl, sinks, di->num_sms);
+  p.sk_halves = d == 256 ? 2 : 1;
+  p.sk_part = reinterpret_cast<float*>(extra);
+  p.sk_meta = reinterpret_cast<int*>(extra + sink_part_bytes(di->num_sms, d));
   p.o = o;
   p.dO = dO;
   p.lse = lse;
@@ -790,7 +775,9 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   p.dv = dv;
   fa_status_t r = bwd_prep_impl(p, d, stream);
   if (r == FA_OK) r = bwd_main_impl(p, di, q, k, v, dO, d, stream, true);
-  if (r == FA_OK) r = bwd_post_impl(p, d, stream);
+  if (r == FA_OK && fa::launch_bwd_sinks_post(p, d, static_cast<cudaStream_t>(stream)) !=
+                        cudaSuccess)
+    r = FA_ERR_CUDA;
   return r;
 }
 

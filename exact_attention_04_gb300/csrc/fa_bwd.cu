@@ -79,9 +79,8 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __grid_constant__ Bw
 
 // dQ = bf16(scale * dQ_acc) from the [BH, Npad, d] accumulator (d = 64), 8
 // elements per thread.
-__global__ void __launch_bounds__(256) bwd_post_kernel(const __grid_constant__ BwdParams p,
-                                                       long long n8) {
-  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+__device__ __forceinline__ void post_d64(const BwdParams& p, long long block, long long n8) {
+  const long long t = block * 256 + threadIdx.x;
   if (t >= n8) return;
   constexpr int D8 = 64 / 8;
   const long long row = t / D8;                       // bh * N + q
@@ -103,9 +102,8 @@ __global__ void __launch_bounds__(256) bwd_post_kernel(const __grid_constant__ B
 // reads is a coalesced 128-byte row segment; it writes 16 bf16 of query q in
 // one 32-byte store (two 16-byte stores when dQ is only 16-byte aligned).
 template <int D>
-__global__ void __launch_bounds__(256) bwd_post_t_kernel(const __grid_constant__ BwdParams p,
-                                                         long long total) {
-  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+__device__ __forceinline__ void post_t(const BwdParams& p, long long block, long long total) {
+  const long long t = block * 256 + threadIdx.x;
   if (t >= total) return;
   const int q = static_cast<int>(t % p.Npad);
   const long long rest = t / p.Npad;
@@ -129,34 +127,79 @@ __global__ void __launch_bounds__(256) bwd_post_t_kernel(const __grid_constant__
   }
 }
 
-// dV and dK of the key blocks that hold sinks: the sum of their items' fp32
-// rows, the window's first, then the far chunks in order; 8 elements a thread.
+__global__ void __launch_bounds__(256) bwd_post_kernel(const __grid_constant__ BwdParams p,
+                                                       long long n8) {
+  post_d64(p, blockIdx.x, n8);
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) bwd_sinks_join_kernel(const __grid_constant__ BwdParams p,
-                                                             long long total) {
-  const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (t >= total) return;
-  constexpr int D8 = D / 8;
-  const int c = static_cast<int>(t % D8) * 8;
-  const int r = static_cast<int>(t / D8 % 128);
-  const long long item = t / (D8 * 128);              // (K/V head, block, dV or dK)
-  const int which = static_cast<int>(item % 2);
-  const long long kn = item / 2;
-  const int n = static_cast<int>(kn % p.nsb);
-  const long long kvbh = kn / p.nsb;
+__global__ void __launch_bounds__(256) bwd_post_t_kernel(const __grid_constant__ BwdParams p,
+                                                         long long total) {
+  post_t<D>(p, blockIdx.x, total);
+}
+
+// dV and dK of the items that CTAs' shares cut (sinks): the sum of their
+// pieces' fp32 rows in the CTAs' order; 8 elements a thread.  kJoinBlocks<D>
+// blocks for the border before each CTA c but the first; the first border
+// inside an item does it.
+template <int D>
+constexpr int kJoinBlocks = 2 * 128 * (D < 128 ? D : 128) / 8 / 256;
+
+template <int D>
+__device__ __forceinline__ void sinks_join(const BwdParams& p, int block) {
+  constexpr int W = D < 128 ? D : 128, W8 = W / 8;
+  int c = block / kJoinBlocks<D> + 1;
+  if (!__ldg(p.sk_meta + 2 * c + 1)) return;
+  const int item = __ldg(p.sk_meta + 2 * c);
+  if (c > 1 && __ldg(p.sk_meta + 2 * c - 1) && __ldg(p.sk_meta + 2 * c - 2) == item) return;
+  const int e = block % kJoinBlocks<D> * 256 + threadIdx.x;   // of [dV or dK, 128, W / 8]
+  const int which = e / (128 * W8);
+  const int r = e / W8 % 128, col = e % W8 * 8;
+  const SkItems items(p);
+  int kvbh, n, h;
+  items.pool_item(item, items.plain / p.sk_ctas * p.sk_ctas, kvbh, n, h);
   const int key = n * 128 + r;
-  if (key >= p.N) return;
-  const float* src = p.sink_part + ((kn * (p.nfar + 1)) * 2 + which) * 128 * D + r * D + c;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-  for (int s = 0; s <= p.nfar; ++s, src += 2 * 128 * D) {
-    const float4 x = reinterpret_cast<const float4*>(src)[0];
-    const float4 y = reinterpret_cast<const float4*>(src)[1];
+  if (which > 1 || key >= p.N) return;
+  auto row = [&](int slot) {
+    return reinterpret_cast<const float4*>(
+        p.sk_part + ((static_cast<size_t>(slot) * 2 + which) * 128 + r) * W + col);
+  };
+  const float4* src = row(2 * c - 1);
+  float4 a = src[0], b = src[1];
+  do {
+    src = row(2 * c);
+    const float4 x = src[0], y = src[1];
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-  }
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + (kvbh * p.N + key) * D + c;
+    ++c;
+  } while (c < p.sk_ctas && __ldg(p.sk_meta + 2 * c + 1) && __ldg(p.sk_meta + 2 * c) == item);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.dk : p.dv) +
+                       (static_cast<size_t>(kvbh) * p.N + key) * D + h * W + col;
   *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
                                               pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
+
+// Both: the join's blocks first, then dQ's.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sinks_post_kernel(const __grid_constant__ BwdParams p,
+                                                             int joins, long long total) {
+  const int block = blockIdx.x;
+  if (block < joins)
+    sinks_join<D>(p, block);
+  else if constexpr (D == 64)
+    post_d64(p, block - joins, total);
+  else
+    post_t<D>(p, block - joins, total);
+}
+
+template <int D>
+cudaError_t launch_sinks_post(const BwdParams& p, cudaStream_t stream) {
+  const long long total = D == 64 ? static_cast<long long>(p.B) * p.H * p.N * D / 8
+                                  : static_cast<long long>(p.B) * p.H * (D / 16) * p.Npad;
+  const int joins = kJoinBlocks<D> * (p.sk_ctas - 1);
+  bwd_sinks_post_kernel<D>
+      <<<static_cast<unsigned>(joins + (total + 255) / 256), 256, 0, stream>>>(p, joins, total);
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -212,16 +255,13 @@ cudaError_t launch_bwd_order(const BwdParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_sinks_join(const BwdParams& p, int d, cudaStream_t stream) {
-  const long long total = static_cast<long long>(p.B) * p.H_kv * p.nsb * 2 * 128 * (d / 8);
-  const unsigned grid = static_cast<unsigned>((total + 255) / 256);
+cudaError_t launch_bwd_sinks_post(const BwdParams& p, int d, cudaStream_t stream) {
   switch (d) {
-    case 64: bwd_sinks_join_kernel<64><<<grid, 256, 0, stream>>>(p, total); break;
-    case 128: bwd_sinks_join_kernel<128><<<grid, 256, 0, stream>>>(p, total); break;
-    case 256: bwd_sinks_join_kernel<256><<<grid, 256, 0, stream>>>(p, total); break;
+    case 64: return launch_sinks_post<64>(p, stream);
+    case 128: return launch_sinks_post<128>(p, stream);
+    case 256: return launch_sinks_post<256>(p, stream);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_post(const BwdParams& p, int d, cudaStream_t stream) {

@@ -74,11 +74,10 @@ struct DtSched {
   int T, P, per_bh, units, causal, nsplit;   // units: the round-robin units
   int BH;
   const uint32_t* order;                     // the cost-sorted order, or nullptr
-  // extra: items past a head's key blocks (the far chunks of its sinks)
   __device__ DtSched(int BH_, int N, int causal_, int nsplit_, int tail_heads,
-                     const uint32_t* order_, int extra = 0)
+                     const uint32_t* order_)
       : causal(causal_), nsplit(nsplit_), BH(BH_), order(order_) {
-    T = (N + BK - 1) / BK + extra;
+    T = (N + BK - 1) / BK;
     P = (T + 1) / 2;
     per_bh = causal ? P : T;
     units = (BH - tail_heads) * per_bh * nsplit;
@@ -140,44 +139,13 @@ __device__ __forceinline__ int dt_len(const BwdParams& p, int kvbh) {
   return len;
 }
 
-// The key block and the step range of item n of a head, in steps of STEP
-// rows.  With sinks, item n may be a far chunk of one of the first nsb blocks
-// (n past the head's blocks); n becomes its block, and slot the place of its
-// dV, dK in sink_part (-1: written to dV, dK as for any block).  The window
-// item of such a block ends where the first chunk starts: at the first step
-// whose queries are all past the window of its last key.
+// Steps [i0, i1) of STEP query rows that see key block n (empty when none
+// does).  With sinks, a block that holds some is seen to the last query.
 template <int MK, int STEP>
-__device__ __forceinline__ void item_range(const BwdParams& p, int& n, int len, int& i0, int& i1,
-                                           int& slot) {
-  slot = -1;
-  if constexpr (MK == kMaskSinks) {
-    const int T = (p.N + BK - 1) / BK;
-    int c = -1;
-    if (n >= T) {
-      c = (n - T) % p.nfar;
-      n = (n - T) / p.nfar;
-    }
-    if (n < p.nsb) {
-      const int steps = (p.N + STEP - 1) / STEP;
-      int far0 = steps;
-      if (p.nfar > 0) {
-        slot = c + 1;
-        far0 = min(steps, (n * BK + BK + p.wl + STEP - 1) / STEP);
-      }
-      if (c < 0) {
-        i0 = max(0, n * BK - p.wr) / STEP;
-        i1 = far0;
-      } else {
-        const int cs = p.far_rows / STEP;
-        i0 = min(steps, far0 + c * cs);
-        i1 = c == p.nfar - 1 ? steps : min(steps, far0 + (c + 1) * cs);
-      }
-      if (n * BK >= len || i0 >= i1) i0 = i1 = 0;
-      return;
-    }
-  }
+__device__ __forceinline__ void step_range(const BwdParams& p, int n, int len, int& i0, int& i1) {
   int q_lo, q_hi;
   visible_queries(n * BK, BK, len, p.N, p.wl, p.wr, q_lo, q_hi);
+  if (MK == kMaskSinks && n * BK < p.sinks && n * BK < len) q_hi = p.N;
   if (q_hi <= q_lo) {
     i0 = i1 = 0;
     return;
@@ -186,12 +154,205 @@ __device__ __forceinline__ void item_range(const BwdParams& p, int& n, int len, 
   i1 = (q_hi + STEP - 1) / STEP;
 }
 
-// The dV (0) or dK (1) rows of an item of a sink block: [128, d] floats.
-__device__ __forceinline__ float* sink_rows(const BwdParams& p, int kvbh, int n, int slot, int d,
-                                            int which) {
-  return p.sink_part +
-         (((static_cast<size_t>(kvbh) * p.nsb + n) * (p.nfar + 1) + slot) * 2 + which) * BK * d;
+// Sinks.  The few key blocks that hold sinks are seen by every later query of
+// a whole group, many times a window's worth, and whole key blocks per CTA
+// leave the last round part-empty.  So of the items (K/V head, key block,
+// half of d) without sinks as many as fill whole rounds go round-robin (so
+// that CTAs working at the same time share Q, dO and the dQ accumulator
+// through L2); the pool of the others, those with sinks and then the last
+// part of a round, is laid end to end, an item taking its steps plus
+// kItemCost (its start-up and epilogue, in steps), and CTA c of G takes
+// [c total / G, (c + 1) total / G) of it.  A pool item within one share goes
+// to dV, dK as any item; the pieces of a cut one leave fp32 rows in sk_part,
+// slot 2c for the piece that starts past the item's first step (CTA c's
+// first) and 2c + 1 for the one that starts at it (CTA c's last), and
+// bwd_sinks_post_kernel adds them in the CTAs' order.  All of it is a
+// function of the sizes and kv_len.  H = 16, h_kv = 4, N = 16384, d = 128,
+// window 2047, 4 sinks: 700 us; whole items, the sinks' far queries as items
+// of their own, 789; all items end to end 1012 (each CTA elsewhere in the
+// sequence: the dQ accumulator falls out of L2).
+struct SkPlan {
+  int whole;                    // the round-robin items are 0 .. whole - 1
+  int j;                        // this CTA's first pool item
+  long long p0;                 // where it starts
+  long long xs, xe;             // this CTA's share of the pool
+};
+
+struct SkScratch {
+  SkPlan plan;
+  long long warp_sum[32];
+};
+
+// Shared memory for it, in the kernels with sinks.
+struct SkNothing {};
+template <int MK>
+struct SkForT {
+  using type = SkNothing;
+};
+template <>
+struct SkForT<kMaskSinks> {
+  using type = SkScratch;
+};
+template <int MK>
+using SkFor = typename SkForT<MK>::type;
+
+constexpr int kItemCost = 4;
+
+// Sum over the block and, in `before`, over the earlier threads.
+__device__ __forceinline__ long long sk_scan(long long v, long long* warp_sum, long long& before) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  long long total = 0, pre = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) pre += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before = pre + x - v;
+  return total;
 }
+
+// Steps that item (kvbh, n) takes in all.
+template <int STEP>
+__device__ __forceinline__ long long sk_steps(const BwdParams& p, int kvbh, int n, int G) {
+  int i0, i1;
+  step_range<kMaskSinks, STEP>(p, n, dt_len(p, kvbh), i0, i1);
+  return static_cast<long long>(i1 - i0) * G;
+}
+
+// The whole block; ends with a barrier.  Writes sc.plan and, for the join,
+// sk_meta[c] = {the pool item that CTA c starts in, whether its share cuts
+// it}.
+template <int STEP>
+__device__ __forceinline__ void sk_plan(const BwdParams& p, int G, SkScratch& sc) {
+  const SkItems items(p);
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int rounds = items.plain / gridDim.x;
+  const int whole = rounds * gridDim.x;
+  const int pool = items.sunk + items.plain - whole;
+  const int per = (pool + threads - 1) / threads;
+  const int lo = min(pool, tid * per), hi = min(pool, lo + per);
+  auto cost = [&](int j) {
+    int kvbh, n, h;
+    items.pool_item(j, whole, kvbh, n, h);
+    return sk_steps<STEP>(p, kvbh, n, G) + kItemCost;
+  };
+  long long sum = 0, before;
+  for (int j = lo; j < hi; ++j) sum += cost(j);
+  const long long total = sk_scan(sum, sc.warp_sum, before);
+  const long long ctas = min(static_cast<long long>(gridDim.x), total);   // no share is empty
+  const bool idle = blockIdx.x >= ctas;
+  const long long xs = idle ? 0 : total * blockIdx.x / ctas;
+  const long long xe = idle ? 0 : total * (blockIdx.x + 1) / ctas;
+  if (idle ? tid == 0 : xs >= before && xs < before + sum) {
+    int j = lo;
+    long long z = xs - before;                // how far xs lies in its item
+    if (!idle)
+      for (long long c = cost(j); z >= c; c = cost(++j)) z -= c;
+    sc.plan = SkPlan{whole, j, idle ? 0 : xs - z, xs, xe};
+    p.sk_meta[2 * blockIdx.x] = idle ? -1 : j;
+    p.sk_meta[2 * blockIdx.x + 1] = !idle && z > kItemCost;
+  }
+  __syncthreads();
+}
+
+// The dV (0) or dK (1) rows of a piece: [128, cols] floats, cols = min(d, 128).
+__device__ __forceinline__ float* sink_rows(const BwdParams& p, int slot, int cols, int which) {
+  return p.sk_part + (static_cast<size_t>(slot) * 2 + which) * BK * cols;
+}
+
+// A work item as every role sees it: steps [a, b) of its nst a query head,
+// head after head; none: a key block that no query sees (its gradients are
+// written as zeros), or with sinks the empty end of one.
+struct Item {
+  int kvbh, h, n, len;
+  int i0, i1, nst;
+  int a, b;
+  int slot;                     // of sk_part, or -1: dV and dK
+  bool zero;                    // no query sees it, and this CTA writes the zeros
+  StepMask sk;
+  __device__ __forceinline__ bool empty() const { return a >= b; }
+  __device__ __forceinline__ StepWalk walk(int bh0) const {
+    StepWalk w(i0, i1, bh0, sk);
+    if (a > 0) {                // (sinks: no block mask)
+      w.bh += a / nst;
+      w.i += a % nst;
+    }
+    return w;
+  }
+};
+
+template <int MK, int STEP>
+struct ItemWalk {
+  const BwdParams& p;
+  const TailTable& tail;
+  const DtSched& sched;
+  int G;                        // query heads per K/V head
+  DtIter it;
+  const SkScratch* sc;          // sinks: it.u is the next round-robin item, then
+  int j;                        // the pool's next item and where it starts
+  long long p0;
+  __device__ __forceinline__ ItemWalk(const BwdParams& p_, const TailTable& tail_,
+                                      const DtSched& sched_, int G_, const SkScratch* sc_)
+      : p(p_), tail(tail_), sched(sched_), G(G_), it{static_cast<int>(blockIdx.x), 0, 0},
+        sc(sc_) {
+    if constexpr (MK == kMaskSinks) {
+      j = sc->plan.j;
+      p0 = sc->plan.p0;
+    }
+  }
+  __device__ __forceinline__ bool next(Item& w) {
+    w.slot = -1;
+    if constexpr (MK == kMaskSinks) {
+      const SkItems items(p);
+      const int end = sc->plan.whole;
+      const bool whole = it.u < end;
+      if (whole) {
+        items.plain_item(it.u, w.kvbh, w.n, w.h);
+        it.u += gridDim.x;
+      } else {
+        if (p0 >= sc->plan.xe) return false;
+        items.pool_item(j++, end, w.kvbh, w.n, w.h);
+      }
+      w.len = dt_len(p, w.kvbh);
+      step_range<MK, STEP>(p, w.n, w.len, w.i0, w.i1);
+      w.nst = w.i1 - w.i0;
+      w.sk = StepMask{nullptr, 0, 1};
+      const long long steps = static_cast<long long>(w.nst) * G;
+      w.a = 0;
+      w.b = static_cast<int>(steps);
+      w.zero = steps == 0;
+      if (!whole) {
+        const long long first = p0 + kItemCost, xs = sc->plan.xs;
+        w.a = static_cast<int>(max(0ll, xs - first));
+        w.b = static_cast<int>(max(0ll, min(steps, sc->plan.xe - first)));
+        w.zero = steps == 0 && p0 >= xs;
+        if (w.a > 0)
+          w.slot = 2 * blockIdx.x;
+        else if (w.b < steps)
+          w.slot = 2 * blockIdx.x + 1;
+        p0 = first + steps;
+      }
+      return true;
+    } else {
+      if (!sched.next(tail, it, w.kvbh, w.h, w.n)) return false;
+      w.len = dt_len(p, w.kvbh);
+      step_range<MK, STEP>(p, w.n, w.len, w.i0, w.i1);
+      w.sk = StepMask{MK == kMaskBlocks ? p.block_mask + w.n : nullptr, p.bm_t, BK / STEP};
+      w.nst = count_steps(w.sk, w.i0, w.i1);
+      w.a = 0;
+      w.b = w.nst * G;
+      w.zero = w.b == 0;
+      return true;
+    }
+  }
+};
 
 // Rows [left, 128) of a tile of `chunks` 128-byte column chunks become
 // zero, by a whole warp: keys past the sequence may hold anything, and their

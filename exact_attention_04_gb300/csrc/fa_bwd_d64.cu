@@ -59,6 +59,7 @@ constexpr int kSRowWarp0 = 4;
 constexpr int kSThreads = 32 * (kSRowWarp0 + kSRowWarps);   // 20 warps
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 320, TM_DQ = 384, TM_COLS = 512;
 
+template <int MK = kMaskNone>
 struct SSmem {
   alignas(1024) uint8_t k[SCH];
   alignas(1024) uint8_t v[SCH];
@@ -78,35 +79,17 @@ struct SSmem {
   uint64_t mma_done, mma_done_b;
   uint32_t tmem_base;
   int abort;
+  SkFor<MK> sk;
 };
 
 // 227 KB of dynamic shared memory per block on sm_103a
-static_assert(sizeof(SSmem) <= 232448, "shared-memory layout exceeds the per-block limit");
+static_assert(sizeof(SSmem<kMaskSinks>) <= 232448, "shared-memory layout exceeds the per-block limit");
 
 // Column of the packed bf16 P^T / dS^T for K-step kk (16 queries) within its
 // 128-column buffer: the warp of query quarter j packs queries 32j .. 32j+31
 // over the first 16 of its own 32 columns.
 __device__ __forceinline__ constexpr uint32_t scol(int kk) {
   return static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8);
-}
-
-// The steps of the item: (query head, query block) pairs, or none.
-struct SItem {
-  int i0, i1, nsteps;
-  int slot;                             // as item_range's
-  StepMask sk;
-};
-
-// n becomes the item's key block (item_range).
-template <int MK>
-__device__ __forceinline__ SItem s_item(const BwdParams& p, int kvbh, int& n, int G) {
-  SItem w;
-  item_range<MK, SQ>(p, n, dt_len(p, kvbh), w.i0, w.i1, w.slot);
-  w.sk = StepMask{MK == kMaskBlocks ? p.block_mask + n : nullptr, p.bm_t, 1};
-  const int nst = count_steps(w.sk, w.i0, w.i1);
-  if (nst == 0) w.i1 = w.i0;
-  w.nsteps = nst * G;
-  return w;
 }
 
 template <int MK>
@@ -116,11 +99,11 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
-  if (aligned - raw + sizeof(SSmem) > dynamic_smem_size()) {
+  if (aligned - raw + sizeof(SSmem<MK>) > dynamic_smem_size()) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, status_code(kSiteSmemLayout));
     return;
   }
-  SSmem& sm = *reinterpret_cast<SSmem*>(aligned);
+  SSmem<MK>& sm = *reinterpret_cast<SSmem<MK>*>(aligned);
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   volatile int* abort = &sm.abort;
@@ -161,9 +144,13 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   const DtSched sched(p.B * p.H_kv, p.N, p.causal, 1, tail.heads,
-                      MK == kMaskBlocks ? p.cost_order : nullptr,
-                      SK ? p.nsb * p.nfar : 0);
+                      MK == kMaskBlocks ? p.cost_order : nullptr);
   const int G = p.H / p.H_kv;                     // query heads per K/V head
+  const SkScratch* SKS = nullptr;
+  if constexpr (SK) {
+    sk_plan<SQ>(p, G, sm.sk);
+    SKS = &sm.sk;
+  }
 
   // Registers: the launch gives every thread 96.  The first warpgroup
   // (producer, issuers, reduce warp) needs far fewer, and the row warps
@@ -187,10 +174,10 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         }
         uint32_t w_it = 0, g = 0;
         bool ok = true;
-        DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-        for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-          const SItem wi = s_item<MK>(p, kvbh, n, G);
-          if (wi.nsteps == 0) continue;
+        ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
+        for (Item w; ok && items.next(w);) {
+          [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
+          if (w.empty()) continue;
           if (!dlane) {
             if (!mbar_wait(&sm.kv_empty, (w_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
               record_failure(p.status, abort, kSiteProdKV);
@@ -202,8 +189,8 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
             tma_load_3d(sm.v, &p.tv, &sm.kv_full, 0, n * BK, kvbh);
             ++w_it;
           }
-          StepWalk wk(wi.i0, wi.i1, q_head_of(kvbh, 0, p.H, p.H_kv), wi.sk);
-          for (int s = 0; s < wi.nsteps; ++s, ++g, wk.next()) {
+          StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
+          for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
             const int st = g & 1;
             const uint32_t ph = ((g >> 1) & 1) ^ 1;
             const size_t roff = static_cast<size_t>(wk.bh) * p.Npad + static_cast<size_t>(wk.i) * SQ;
@@ -240,17 +227,17 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       const uint64_t dV0 = sdesc_sw128(smem_u32(sm.v), 16, 1024);
       uint32_t w_it = 0, g = 0;
       bool ok = true;
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        const SItem wi = s_item<MK>(p, kvbh, n, G);
-        if (wi.nsteps == 0) continue;
+      ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
+        if (w.empty()) continue;
         if (!mbar_wait_warp(&sm.kv_full, w_it & 1, abort, kWaitTimeoutNs)) {
           issuer_fail(p.status, abort, lane, kSiteMmaKV);
           ok = false;
           break;
         }
         if constexpr (SK) {
-          const int left = dt_len(p, kvbh) - n * BK;
+          const int left = w.len - n * BK;
           if (left < BK) {
             zero_rows(sm.k, 1, left, lane);
             zero_rows(sm.v, 1, left, lane);
@@ -258,7 +245,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
             __syncwarp();
           }
         }
-        for (int s = 0; s < wi.nsteps; ++s, ++g) {
+        for (int s = w.a; s < w.b; ++s, ++g) {
           const int st = g & 1;
           // S^T(g) into the S buffer once dV(g-1) has read P^T(g-1) out of it
           if (g > 0 && !mbar_wait_warp(&sm.dv_done, (g - 1) & 1, abort, kWaitTimeoutNs)) {
@@ -322,15 +309,15 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         issuer_fail(p.status, abort, lane, site);
         ok = false;
       };
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        const SItem wi = s_item<MK>(p, kvbh, n, G);
-        if (wi.nsteps == 0) continue;
-        for (int s = 0; s < wi.nsteps; ++s, ++g) {
+      ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
+        if (w.empty()) continue;
+        for (int s = w.a; s < w.b; ++s, ++g) {
           const int st = g & 1;
           const uint32_t ph = g & 1;
-          const bool first = (s == 0);
-          const bool last = (s + 1 == wi.nsteps);
+          const bool first = (s == w.a);
+          const bool last = (s + 1 == w.b);
           // dV += P^T dO_i
           if (!mbar_wait_warp(&sm.p_full, ph, abort, kWaitTimeoutNs)) {
             fail(kSiteMmaP);
@@ -397,11 +384,11 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         prefetch_tmap(&p.tdq);
         uint32_t g = 0;
         bool ok = true;
-        DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-        for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-          const SItem wi = s_item<MK>(p, kvbh, n, G);
-          StepWalk wk(wi.i0, wi.i1, q_head_of(kvbh, 0, p.H, p.H_kv), wi.sk);
-          for (int s = 0; s < wi.nsteps; ++s, ++g, wk.next()) {
+        ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
+        for (Item w; ok && items.next(w);) {
+          [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
+          StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
+          for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
             const int b = g & 1;
             if (!mbar_wait(&sm.stg_full[b], (g >> 1) & 1, abort, kWaitTimeoutNs)) {
               record_failure(p.status, abort, kSiteStageFull);
@@ -471,23 +458,15 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
                        31u) == 0;
     uint32_t w_it = 0, g = 0;
     bool ok = true;
-    DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-    for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-      const int len = dt_len(p, kvbh);
-      const SItem wi = s_item<MK>(p, kvbh, n, G);
+    ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
+    for (Item w; ok && items.next(w);) {
+      [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
+      const int len = w.len;
       const int key = n * BK + r;
       const size_t out_off = (static_cast<size_t>(kvbh) * p.N + key) * SD + 16 * j4;
-      if (wi.nsteps == 0) {
+      if (w.empty()) {
         // key block seen by no query: zero gradients
-        if (SK && wi.slot >= 0) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            float4* a = reinterpret_cast<float4*>(sink_rows(p, kvbh, n, wi.slot, SD, w) + r * SD +
-                                                  16 * j4);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) a[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        } else if (key < p.N) {
+        if (w.zero && key < p.N) {
           uint4* a = reinterpret_cast<uint4*>(dk_out + out_off);
           uint4* bq = reinterpret_cast<uint4*>(dv_out + out_off);
 #pragma unroll
@@ -498,8 +477,8 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         }
         continue;
       }
-      StepWalk wk(wi.i0, wi.i1, 0, wi.sk);
-      for (int s = 0; s < wi.nsteps; ++s, ++g, wk.next()) {
+      StepWalk wk = w.walk(0);
+      for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
         const int st = g & 1;
         const uint32_t ph = g & 1;
         const int q0 = wk.i * SQ;
@@ -630,10 +609,10 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_free);
-        if (SK && wi.slot >= 0) {
+        if (SK && w.slot >= 0) {
           const int at = r * SD + 16 * j4;
-          float* dvp = sink_rows(p, kvbh, n, wi.slot, SD, 0) + at;
-          float* dkp = sink_rows(p, kvbh, n, wi.slot, SD, 1) + at;
+          float* dvp = sink_rows(p, w.slot, SD, 0) + at;
+          float* dkp = sink_rows(p, w.slot, SD, 1) + at;
 #pragma unroll
           for (int t = 0; t < 16; ++t) bb[t] = __float_as_uint(__uint_as_float(bb[t]) * p.scale);
 #pragma unroll
@@ -679,17 +658,17 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
 
 template <int MK>
 cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
-  const size_t smem = smem_request(sizeof(SSmem), max_smem);
+  const size_t smem = smem_request(sizeof(SSmem<MK>), max_smem);
   cudaError_t e = cudaFuncSetAttribute(bwd_d64_kernel<MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int T = (p.N + BK - 1) / BK + (MK == kMaskSinks ? p.nsb * p.nfar : 0);
+  const int T = (p.N + BK - 1) / BK;
   const int BH = p.B * p.H_kv;
   const long long per_bh = p.causal ? (T + 1) / 2 : T;
   long long units = static_cast<long long>(BH) * per_bh;
   TailTable tail;
   tail.heads = 0;
-  if (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t)) {
+  if (MK != kMaskSinks && (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t))) {
     // single key blocks in the tail: up to one CTA per block; the tail's
     // K/V heads share their group's Q and dO through L2
     const long long blocks = static_cast<long long>(BH) * T;
@@ -702,7 +681,7 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
     if (tail.heads > 0) units = g;
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
-  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+  const int grid = MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
   bwd_d64_kernel<MK><<<grid, kSThreads, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }

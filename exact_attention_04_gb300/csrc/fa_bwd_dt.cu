@@ -90,7 +90,7 @@ struct DtCfg {
                 "tensor-memory columns overlap");
 };
 
-template <int D>
+template <int D, int MK = kMaskNone>
 struct DtSmem {
   alignas(1024) uint8_t k[DtCfg<D>::KV_BYTES];
   alignas(1024) uint8_t q[DtCfg<D>::STAGES][DtCfg<D>::Q_BYTES];
@@ -115,10 +115,11 @@ struct DtSmem {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
+  SkFor<MK> sk;
 };
 
 // 227 KB of dynamic shared memory per block on sm_103a
-static_assert(sizeof(DtSmem<128>) <= 232448 && sizeof(DtSmem<256>) <= 232448,
+static_assert(sizeof(DtSmem<128, kMaskSinks>) <= 232448 && sizeof(DtSmem<256, kMaskSinks>) <= 232448,
               "shared-memory layout exceeds the per-block limit");
 
 // MK: the launch carries a block mask or sinks (instantiations of their own,
@@ -132,11 +133,11 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
-  if (aligned - raw + sizeof(DtSmem<D>) > dynamic_smem_size()) {
+  if (aligned - raw + sizeof(DtSmem<D, MK>) > dynamic_smem_size()) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, status_code(kSiteSmemLayout));
     return;
   }
-  DtSmem<D>& sm = *reinterpret_cast<DtSmem<D>*>(aligned);
+  DtSmem<D, MK>& sm = *reinterpret_cast<DtSmem<D, MK>*>(aligned);
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   volatile int* abort = &sm.abort;
@@ -181,8 +182,13 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   const DtSched sched(p.B * p.H_kv, p.N, p.causal, C::NSPLIT, tail.heads,
-                      BS ? p.cost_order : nullptr, SK ? p.nsb * p.nfar : 0);
+                      BS ? p.cost_order : nullptr);
   const int G = p.H / p.H_kv;                     // query heads per K/V head
+  const SkScratch* SKS = nullptr;
+  if constexpr (SK) {
+    sk_plan<BQ>(p, G, sm.sk);
+    SKS = &sm.sk;
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -198,15 +204,11 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       prefetch_tmap(&p.tdo);
       uint32_t w_it = 0, g = 0;
       bool ok = true;
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
+      ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
         {
-          int i0, i1, slot;
-          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
-          const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-          const int nst = count_steps(sk, i0, i1);
-          if (nst == 0) i1 = i0;
-          if (i0 >= i1) continue;
+          if (w.empty()) continue;
           if (!dlane) {
             if (!mbar_wait(&sm.kv_empty, (w_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
               record_failure(p.status, abort, kSiteProdKV);
@@ -222,8 +224,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
             }
             ++w_it;
           }
-          StepWalk wk(i0, i1, q_head_of(kvbh, 0, p.H, p.H_kv), sk);
-          for (int s = 0; s < nst * G; ++s, wk.next()) {
+          StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
+          for (int s = w.a; s < w.b; ++s, wk.next()) {
             const int i = wk.i;
             const int bh = wk.bh;
             const int st = g % C::STAGES;
@@ -286,23 +288,18 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       const uint64_t dV0 = sdesc_sw128(smem_u32(sm.v), 16, 1024);
       uint32_t w_it = 0, g = 0;
       bool ok = true;
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
+      ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
         {
-          int i0, i1, slot;
-          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
-          const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-          const int nst = count_steps(sk, i0, i1);
-          if (nst == 0) i1 = i0;
-          if (i0 >= i1) continue;
-          const int nsteps = nst * G;
+          if (w.empty()) continue;
           if (!mbar_wait_warp(&sm.kv_full, w_it & 1, abort, kWaitTimeoutNs)) {
             issuer_fail(p.status, abort, lane, kSiteMmaKV);
             ok = false;
             break;
           }
           if constexpr (SK) {
-            const int left = dt_len(p, kvbh) - n * BK;
+            const int left = w.len - n * BK;
             if (left < BK) {
               zero_rows(sm.k, C::NCH, left, lane);
               if constexpr (!C::V_TMEM) zero_rows(sm.v, C::NCH, left, lane);
@@ -373,8 +370,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
             issuer_fail(p.status, abort, lane, kSiteMmaV);
             ok = false;
           }
-          for (int s = 0; ok && s < nsteps; ++s, ++g) {
-            ok = issue_dp(g) && (s + 1 == nsteps || issue_s(g + 1));
+          for (int s = w.a; ok && s < w.b; ++s, ++g) {
+            ok = issue_dp(g) && (s + 1 == w.b || issue_s(g + 1));
           }
           if (!ok) break;
           mma_commit_w(&sm.kv_empty);               // A's reads of K and V are done
@@ -399,25 +396,20 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
         issuer_fail(p.status, abort, lane, site);
         ok = false;
       };
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
+      ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
         // K[:, h] as the MN-major A operand of dQ^T: 64-column chunks 2h, 2h+1
         const uint64_t dKmn = sdesc_sw128(smem_u32(sm.k) + 2 * h * KCH, KCH, 1024);
         {
-          int i0, i1, slot;
-          item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
-          const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-          const int nst = count_steps(sk, i0, i1);
-          if (nst == 0) i1 = i0;
-          if (i0 >= i1) continue;
-          const int nsteps = nst * G;
-          for (int s = 0; s < nsteps; ++s, ++g) {
+          if (w.empty()) continue;
+          for (int s = w.a; s < w.b; ++s, ++g) {
             const int st = g % C::STAGES;
             const uint32_t b = g % C::NSB;          // tensor-memory S / dP buffer
             const uint32_t ph = (g / C::NSB) & 1;
             const uint32_t bs = g & 1;              // shared dS buffer
-            const bool first = (s == 0);
-            const bool last = (s + 1 == nsteps);
+            const bool first = (s == w.a);
+            const bool last = (s + 1 == w.b);
             // dV_h += P^T dO_i[:, h]
             if (!mbar_wait_warp(&sm.p_full[b], ph, abort, kWaitTimeoutNs)) {
               fail(kSiteMmaP);
@@ -491,31 +483,16 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
                        31u) == 0;
     uint32_t w_it = 0, g = 0;
     bool ok = true;
-    DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-    for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
+    ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+    for (Item w; ok && items.next(w);) {
+      [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
       {
-        const int len = dt_len(p, kvbh);
-        int i0, i1, slot;
-        item_range<MK, BQ>(p, n, len, i0, i1, slot);
-        const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-        const int nst = count_steps(sk, i0, i1);
-        if (nst == 0) i1 = i0;
+        const int len = w.len;
         const int key = n * BK + r;
         const size_t out_off = (static_cast<size_t>(kvbh) * p.N + key) * D + h * DH + 64 * hh;
-        if (i0 >= i1) {
-          if (SK && slot >= 0) {
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              float4* a = reinterpret_cast<float4*>(sink_rows(p, kvbh, n, slot, D, w) + r * D +
-                                                    h * DH + 64 * hh);
-#pragma unroll
-              for (int t = 0; t < 16; ++t) a[t] = z;
-            }
-            continue;
-          }
-          // key block entirely past the sequence: zero gradients
-          if (key < p.N) {
+        if (w.empty()) {
+          // key block seen by no query: zero gradients
+          if (w.zero && key < p.N) {
             uint4* a = reinterpret_cast<uint4*>(dk_out + out_off);
             uint4* bq = reinterpret_cast<uint4*>(dv_out + out_off);
 #pragma unroll
@@ -557,8 +534,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.v_full);
         }
-        StepWalk wk(i0, i1, 0, sk);
-        for (int s = 0; s < nst * G; ++s, ++g, wk.next()) {
+        StepWalk wk = w.walk(0);
+        for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
           const int i = wk.i;
           const int st = g % C::STAGES;
           const int q0 = i * BQ;
@@ -685,10 +662,10 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
           tmem_wait_ld();
           reg_fence<32>(a);
           reg_fence<32>(bb);
-          if (SK && slot >= 0) {
-            const size_t at = static_cast<size_t>(r) * D + h * DH + 64 * hh + 32 * c4;
-            float* dvp = sink_rows(p, kvbh, n, slot, D, 0) + at;
-            float* dkp = sink_rows(p, kvbh, n, slot, D, 1) + at;
+          if (SK && w.slot >= 0) {
+            const int at = r * DH + 64 * hh + 32 * c4;
+            float* dvp = sink_rows(p, w.slot, DH, 0) + at;
+            float* dkp = sink_rows(p, w.slot, DH, 1) + at;
 #pragma unroll
             for (int t = 0; t < 32; ++t) bb[t] = __float_as_uint(__uint_as_float(bb[t]) * p.scale);
 #pragma unroll
@@ -737,16 +714,12 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
     if (issuer) prefetch_tmap(&p.tdq);
     uint32_t g = 0;
     bool ok = true;
-    DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-    for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
+    ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+    for (Item w; ok && items.next(w);) {
+      [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
       {
-        int i0, i1, slot;
-        item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
-        const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-        const int nst = count_steps(sk, i0, i1);
-        if (nst == 0) i1 = i0;
-        StepWalk wk(i0, i1, q_head_of(kvbh, 0, p.H, p.H_kv), sk);
-        for (int s = 0; s < nst * G; ++s, ++g, wk.next()) {
+        StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
+        for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
           const int i = wk.i;
           const int bh = wk.bh;
           const uint32_t tb = g % C::NSB;
@@ -832,15 +805,11 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
       prefetch_tmap(&p.tdq);
       uint32_t g = 0;
       bool ok = true;
-      DtIter it{static_cast<int>(blockIdx.x), 0, 0};
-      for (int kvbh, h, n; ok && sched.next(tail, it, kvbh, h, n);) {
-        int i0, i1, slot;
-        item_range<MK, BQ>(p, n, dt_len(p, kvbh), i0, i1, slot);
-        const StepMask sk{BS ? p.block_mask + n : nullptr, p.bm_t, BK / BQ};
-        const int nst = count_steps(sk, i0, i1);
-        if (nst == 0) i1 = i0;
-        StepWalk wk(i0, i1, q_head_of(kvbh, 0, p.H, p.H_kv), sk);
-        for (int s = 0; s < nst * G; ++s, ++g, wk.next()) {
+      ItemWalk<MK, BQ> items(p, tail, sched, G, SKS);
+      for (Item w; ok && items.next(w);) {
+        [[maybe_unused]] const int kvbh = w.kvbh, h = w.h, n = w.n;
+        StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
+        for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
           const int st = g % C::STAGES;
           if (!mbar_wait(&sm.stg_full[st], (g / C::STAGES) & 1, abort, kWaitTimeoutNs)) {
             record_failure(p.status, abort, kSiteStageFull);
@@ -872,18 +841,18 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
 
 template <int D, int MK>
 cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
-  const size_t smem = smem_request(sizeof(DtSmem<D>), max_smem);
+  const size_t smem = smem_request(sizeof(DtSmem<D, MK>), max_smem);
   cudaError_t e = cudaFuncSetAttribute(bwd_dt_kernel<D, MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int T = (p.N + BK - 1) / BK + (MK == kMaskSinks ? p.nsb * p.nfar : 0);
+  const int T = (p.N + BK - 1) / BK;
   const int BH = p.B * p.H_kv;
   constexpr int NS = DtCfg<D>::NSPLIT;
   const long long per_bh = p.causal ? (T + 1) / 2 : T;
   long long units = static_cast<long long>(BH) * per_bh * NS;
   TailTable tail;
   tail.heads = 0;
-  if (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t)) {
+  if (MK != kMaskSinks && (p.causal || (MK == kMaskBlocks && p.block_mask_host && T == p.bm_t))) {
     // single key blocks in the tail: up to one CTA per block
     const long long blocks = static_cast<long long>(BH) * T * NS;
     const int g = static_cast<int>(blocks < num_sms ? blocks : num_sms);
@@ -896,7 +865,7 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
     if (tail.heads > 0) units = g;
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
-  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+  const int grid = MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
   bwd_dt_kernel<D, MK><<<grid, DtCfg<D>::THREADS, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }

@@ -95,14 +95,14 @@ struct BwdParams {
   float scale;
   float scale_log2;
   int* status;
-  // sinks: the first tokens stay visible left of the window.  The first nsb
-  // key blocks hold some; the queries past the window of such a block are cut
-  // into nfar chunks of far_rows rows, work items of their own.  Items of
-  // these blocks then leave fp32 dV, dK in sink_part [B*H_kv, nsb, nfar + 1,
-  // 2, 128, d]: the block's window item, then its chunks.  nfar = 0: the
-  // window items of these blocks run to the last query.
-  int sinks, nsb, nfar, far_rows;
-  float* sink_part;
+  // sinks: the first tokens stay visible left of the window.  The main
+  // kernel runs sk_ctas CTAs, some items cut between them
+  // (fa_bwd_common.cuh); sk_part [2 sk_ctas, 2, 128, min(d, 128)] takes the
+  // fp32 dV, dK of the pieces, sk_meta [sk_ctas, 2] says which these are.
+  // sk_halves: items of a key block (2 at d = 256).
+  int sinks, sk_ctas, sk_halves;
+  float* sk_part;
+  int* sk_meta;
   // block-sparse: [bm_t, bm_t] bytes, nonzero where (query block, key block)
   // is computed (blocks of 128), or nullptr
   const uint8_t* block_mask;
@@ -234,7 +234,7 @@ cudaError_t launch_bwd_main_dt(const BwdParams& p, int d, int num_sms, int max_s
 // the [BH, Npad, 64] accumulator with a box of 32 columns x 128 rows.
 cudaError_t launch_bwd_main_d64(const BwdParams& p, int num_sms, int max_smem,
                                 cudaStream_t stream, bool sinks = false);
-// dK, dV of the first p.nsb key blocks from sink_part.
-cudaError_t launch_bwd_sinks_join(const BwdParams& p, int d, cudaStream_t stream);
+// launch_bwd_post, and dK, dV of the items that the shares cut, from sk_part.
+cudaError_t launch_bwd_sinks_post(const BwdParams& p, int d, cudaStream_t stream);
 
 }  // namespace fa

@@ -54,6 +54,40 @@ __device__ __forceinline__ int q_head_of(int kvbh, int gi, int H, int H_kv) {
   return (kvbh / H_kv) * H + (kvbh % H_kv) * (H / H_kv) + gi;
 }
 
+// The backward's work items with sinks: those of the key blocks that hold some
+// (`sunk` of them) and the others (`plain`), each in the order K/V head, key
+// block, half of d.  The pool (fa_bwd_common.cuh) is the sunk ones, then the
+// plain ones from `whole` on.
+struct SkItems {
+  int nsb, rest, halves, sunk, plain;   // key blocks of a head with sinks and without
+  template <class Params>
+  __device__ __forceinline__ explicit SkItems(const Params& p) {
+    const int T = (p.N + 127) / 128;
+    nsb = min(T, p.sinks / 128 + (p.sinks % 128 != 0));
+    rest = T - nsb;
+    halves = p.sk_halves;
+    const int per = p.B * p.H_kv * halves;
+    sunk = per * nsb;
+    plain = per * rest;
+  }
+  __device__ __forceinline__ void place(int i, int blocks, int first, int& kvbh, int& n,
+                                        int& h) const {
+    const int kn = i / halves;
+    h = i - kn * halves;
+    kvbh = kn / blocks;
+    n = first + kn - kvbh * blocks;
+  }
+  __device__ __forceinline__ void plain_item(int i, int& kvbh, int& n, int& h) const {
+    place(i, rest, nsb, kvbh, n, h);
+  }
+  __device__ __forceinline__ void pool_item(int j, int whole, int& kvbh, int& n, int& h) const {
+    if (j < sunk)
+      place(j, nsb, 0, kvbh, n, h);
+    else
+      plain_item(whole + j - sunk, kvbh, n, h);
+  }
+};
+
 // The steps of a backward work item in order: query blocks [i0, i1) of the
 // group's first query head, then of the next, ...  Kept as counters so that a
 // step costs no integer division.

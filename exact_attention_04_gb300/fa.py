@@ -94,7 +94,7 @@ def load():
         lib.fa_bwd_dkdv_v.restype = i
         lib.fa_fwd_sinks.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, varp, i, vp]
         lib.fa_fwd_sinks.restype = i
-        lib.fa_bwd_sinks_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_bwd_sinks_workspace_bytes.argtypes = [i, i, i, i]
         lib.fa_bwd_sinks_workspace_bytes.restype = sz
         lib.fa_bwd_sinks.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp,
                                      varp, i, vp, sz, vp]
@@ -377,9 +377,8 @@ def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, windo
     _raise(st, "fa_fwd_sinks")
 
 
-def fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, window=None, sinks=0) -> int:
-    left = -1 if window is None else int(window[0])
-    return int(load().fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, left, int(sinks)))
+def fa_bwd_sinks_workspace_bytes(B, H, N, d) -> int:
+    return int(load().fa_bwd_sinks_workspace_bytes(B, H, N, d))
 
 
 def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv_len=None,
@@ -566,9 +565,8 @@ def _no_block_mask(block_mask):
         raise ValueError("sinks: not together with a block mask")
 
 
-def sinks_workspace(B, H, h_kv, N, d, device, window=None, sinks=0):
-    return torch.empty(fa_bwd_sinks_workspace_bytes(B, H, h_kv, N, d, window, sinks),
-                       dtype=torch.uint8, device=device)
+def sinks_workspace(B, H, N, d, device):
+    return torch.empty(fa_bwd_sinks_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=device)
 
 
 def backward(q, k, v, o, lse, do, scale=None, causal=False, kv_len=None, ws=None, window=None,
@@ -582,7 +580,7 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, kv_len=None, ws=None
     if sinks:
         _no_block_mask(block_mask)
         if ws is None:
-            ws = sinks_workspace(B, H, k.shape[1], N, d, q.device, window, sinks)
+            ws = sinks_workspace(B, H, N, d, q.device)
         fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, sc, sinks, causal, kv_len, window, ws,
                      stream)
         return dq, dk, dv

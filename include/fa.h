@@ -205,16 +205,17 @@ fa_status_t fa_bwd_dkdv_v(const void* q, const void* k, const void* v, const voi
  * - K and V rows at or past kv_len may hold anything, NaN included (their
  *   gradients are 0).
  * Key blocks that hold neither sinks nor window are skipped.  dK and dV of the
- * sinks' key blocks sum over all later queries: the backward cuts these into
- * chunks that run on separate SMs, whose fp32 parts lie in the workspace and
- * are added in order, so dK and dV repeat bit for bit.  workspace:
- * fa_bwd_sinks_workspace_bytes (0 for invalid sizes), 256-byte aligned.
+ * sinks' key blocks sum over all later queries, so the backward's steps are
+ * shared out evenly and a key block's may be cut: the fp32 pieces lie in the
+ * workspace and are added in order, so dK and dV repeat bit for bit (on the
+ * same GPU model; dQ as for fa_bwd).  workspace:
+ * fa_bwd_sinks_workspace_bytes (0 for invalid sizes), 256-byte aligned, its
+ * contents irrelevant on entry.
  */
 fa_status_t fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                          int H, int N, int d, float scale, int causal, const int* kv_len,
                          const fa_variant_t* variant, int sinks, void* stream);
-size_t fa_bwd_sinks_workspace_bytes(int B, int H, int h_kv, int N, int d, int window_left,
-                                    int sinks);
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int N, int d);
 fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
                          const void* dO, const float* lse, void* dq, void* dk, void* dv, int B,
                          int H, int N, int d, float scale, int causal, const int* kv_len,

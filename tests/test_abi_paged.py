@@ -148,14 +148,11 @@ def test_sinks_errors(lib):
         assert call(d=96) == UNSUPPORTED
         assert call(var=mask) == UNSUPPORTED
     assert bwd(ws=WS + 16) == BAD and bwd(size=100) == BAD
-    # the far chunks' parts count: what fa_bwd needs is too little
-    need = lib.fa_bwd_sinks_workspace_bytes(1, 4, 2, 4096, 64, 5, 1)
+    # the cut items' pieces count: what fa_bwd needs is too little
+    need = lib.fa_bwd_sinks_workspace_bytes(1, 4, 4096, 64)
     assert need > fa.fa_bwd_workspace_bytes(1, 4, 4096, 64)
     assert bwd(N=4096, size=need - 1) == BAD
-    assert lib.fa_bwd_sinks_workspace_bytes(1, 4, 2, 4096, 64, -1, 1) == \
-        fa.fa_bwd_workspace_bytes(1, 4, 4096, 64)
-    for bad in ((1, 4, 3, 64, 64, 5, 1), (1, 4, 2, 64, 64, -2, 1), (1, 4, 2, 64, 64, 5, -1),
-                (0, 4, 2, 64, 64, 5, 1)):
+    for bad in ((1, 4, 64, 96), (1, 4, 0, 64), (0, 4, 64, 64)):
         assert lib.fa_bwd_sinks_workspace_bytes(*bad) == 0
 
 

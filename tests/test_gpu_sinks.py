@@ -105,7 +105,7 @@ def test_without_sinks_the_window_alone(d):
     o, lse = torch.empty_like(x["q"]), torch.empty(B, H, N, device="cuda")
     fa.fa_fwd_sinks(x["q"], x["k"], x["v"], o, lse, d ** -0.5, 0, True, None, (255, 0))
     dq, dk, dv = torch.empty_like(o), torch.empty_like(x["k"]), torch.empty_like(x["v"])
-    ws = fa.sinks_workspace(B, H, 2, N, d, "cuda", (255, 0), 0)
+    ws = fa.sinks_workspace(B, H, N, d, "cuda")
     fa.fa_bwd_sinks(x["q"], x["k"], x["v"], o, x["do"], lse, dq, dk, dv, d ** -0.5, 0, True, None,
                     (255, 0), ws)
     fa.fa_check()
@@ -118,7 +118,7 @@ def test_repeats_and_ignores_the_workspace(d):
     x = inputs(1, 4, 1, 1300, d, 7)
     kw = dict(causal=True, window=(70, 0), sinks=4)
     first = run(x, **kw)
-    ws = fa.sinks_workspace(1, 4, 1, 1300, d, "cuda", (70, 0), 4)
+    ws = fa.sinks_workspace(1, 4, 1300, d, "cuda")
     for fill in (0, 255):
         ws.fill_(fill)
         o, lse = fa.forward(x["q"], x["k"], x["v"], **kw)
@@ -140,7 +140,7 @@ def test_outputs_inside_guards():
         bufs[n] = torch.full((size + 256,), float("nan"), dtype=torch.bfloat16, device="cuda")
         t[n] = bufs[n][128:128 + size].view(s)
     lse = torch.full((2, 2, 333), float("nan"), device="cuda")
-    ws = fa.sinks_workspace(2, 2, 1, 333, 128, "cuda", (20, 0), 3)
+    ws = fa.sinks_workspace(2, 2, 333, 128, "cuda")
     guarded = torch.full((ws.numel() + 512,), 255, dtype=torch.uint8, device="cuda")
     ws = guarded[256:256 + ws.numel()]
     fa.fa_fwd_sinks(x["q"], x["k"], x["v"], t["o"], lse, scale, 3, **kw)
