@@ -16,12 +16,14 @@
 // rounded to bf16 for the P V product (half a step, 2^-9 of a weight), l adds
 // the unrounded values, O stays in fp32 registers.
 //
-// Work split.  A tile is 64 token positions of one (sequence, K/V head, 16
-// query heads).  Every CTA computes the same prefix sums over kv_len and takes
+// Work split.  A tile is 64 token positions (128 at d = 64) of one (sequence,
+// K/V head, 16 query heads).  Every CTA computes the same prefix sums over kv_len and takes
 // tiles [c T / G, (c + 1) T / G) of the T there are: equal shares whatever
 // the lengths, a pure function of kv_len.  A share may end inside a (sequence,
 // head): such a part leaves its normalised O and LSE (base 2) in the
-// workspace, at most two parts a CTA, and a second kernel joins them,
+// workspace (at most two parts a CTA: slot 2c for the one that an earlier CTA
+// began, 2c + 1 for the one that it begins and does not end), and a second
+// kernel, a block per border between two shares, joins them,
 //   LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i,
 // in the order of the CTAs.  Loads run ahead across the boundary between two
 // heads or sequences.
@@ -43,8 +45,6 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpTokens = 16;                   // tokens of a warp's stage (the K of P V)
-constexpr int kTileTokens = kWarps * kWarpTokens;
 constexpr int kRows = 16;                         // query heads of a tile (M of the mma)
 
 struct DecodeParams {
@@ -57,10 +57,13 @@ struct DecodeParams {
   int max_pages, max_len;       // max_len = max_pages * page_size
   int B, H, group, row_tiles;   // group = H / h_kv, row_tiles = ceil(group / 16)
   int wl, sinks;
+  int page16;                   // the page size is a multiple of 16
   float scale_log2;
   int parts;                    // CTAs of the split kernel
   float* o_part;                // [2 parts, 16, d]
   float* lse_part;              // [2 parts, 16]
+  int2* meta;                   // [parts]: the (sequence, head) that a CTA's share starts in,
+                                // and whether it cuts it
 };
 
 // The visible tiles of a sequence: `first` tiles from position 0 (the sinks),
@@ -70,6 +73,7 @@ struct Span {
   int first, shift, tiles;
 };
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   Span s;
   int len = __ldg(p.kv_len + b);
@@ -77,11 +81,11 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   s.len = len;
   s.lo = len - 1 - p.wl > 0 ? len - 1 - p.wl : 0;
   const int send = p.sinks < s.lo ? p.sinks : s.lo;
-  const int w0 = s.lo / kTileTokens;
-  const int ns = (send + kTileTokens - 1) / kTileTokens;
+  const int w0 = s.lo / TILE;
+  const int ns = (send + TILE - 1) / TILE;
   s.first = ns < w0 ? ns : w0;
   s.shift = w0 - s.first;
-  s.tiles = len > 0 ? s.first + (len + kTileTokens - 1) / kTileTokens - w0 : 0;
+  s.tiles = len > 0 ? s.first + (len + TILE - 1) / TILE - w0 : 0;
   return s;
 }
 
@@ -92,14 +96,16 @@ struct Cursor {
   Span s;
 };
 
+template <int TILE>
 __device__ __forceinline__ void cursor_at(const DecodeParams& p, int b, int rem, Cursor& c) {
   c.b = b;
-  c.s = span_of(p, b);
+  c.s = span_of<TILE>(p, b);
   c.hr = rem / c.s.tiles;
   c.tile = rem - c.hr * c.s.tiles;
 }
 
 // The next tile; the caller knows that there is one.
+template <int TILE>
 __device__ __forceinline__ void cursor_next(const DecodeParams& p, Cursor& c) {
   if (++c.tile < c.s.tiles) return;
   c.tile = 0;
@@ -107,7 +113,7 @@ __device__ __forceinline__ void cursor_next(const DecodeParams& p, Cursor& c) {
   c.hr = 0;
   do {
     ++c.b;
-    c.s = span_of(p, c.b);
+    c.s = span_of<TILE>(p, c.b);
   } while (c.s.tiles == 0 && c.b + 1 < p.B);
 }
 
@@ -157,7 +163,7 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -169,10 +175,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 template <int D>
 struct DecodeCfg {
   static constexpr int ROW = 2 * D;                        // bytes of a token's K or V row
-  static constexpr int HALF = kWarpTokens * ROW;           // K (or V) of a stage
+  // Tokens of a warp's stage: what a stage costs besides its bytes (the page
+  // lookup, the maximum's exchange, the loop) bounds d = 64, where 32 tokens
+  // and one lookup for 16 took 87 us against 99 with 16 and one each (64 rows of 4096
+  // tokens, h_kv = 8, 537 MB).
+  static constexpr int TOK = D == 64 ? 32 : 16;
+  static constexpr int TILE = kWarps * TOK;                // tokens of a CTA's stage
+  static constexpr int HALF = TOK * ROW;                   // K (or V) of a stage
   static constexpr int STAGE = 2 * HALF;
   // 96 KB of loads in flight a CTA and two CTAs an SM (d = 256: 192 KB, one)
-  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int STAGES = 3;
   static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr bool QREG = D <= 128;                   // Q fragments in registers
   static constexpr int RED = 40;                           // floats of a reduction row (32 + pad)
@@ -194,6 +206,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = DecodeCfg<D>;
+  constexpr int TILE = C::TILE;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   DecodeSmem<D>& sm = *reinterpret_cast<DecodeSmem<D>*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -204,18 +217,32 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
   int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += span_of(p, b).tiles;
+  for (int b = b_lo; b < b_hi; ++b) mine += span_of<TILE>(p, b).tiles;
   int before;
   const int total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
   const int parts = min(p.parts, total);
   const int cta = blockIdx.x;
-  if (cta >= parts) return;
+  // sequences without a tile: O = 0, LSE = -inf
+  auto write_empty = [&]() {
+    for (int b = cta; b < p.B; b += gridDim.x) {
+      if (span_of<TILE>(p, b).tiles > 0) continue;
+      const size_t row0 = static_cast<size_t>(b) * p.H;
+      uint4* o = reinterpret_cast<uint4*>(p.o + row0 * D);
+      for (int e = threadIdx.x; e < p.H * (D / 8); e += kThreads) o[e] = make_uint4(0, 0, 0, 0);
+      for (int h = threadIdx.x; h < p.H; h += kThreads) p.lse[row0 + h] = -INFINITY;
+    }
+  };
+  if (cta >= parts) {
+    if (threadIdx.x == 0) p.meta[cta] = make_int2(-1, 0);
+    write_empty();
+    return;
+  }
   const int ta = static_cast<int>(static_cast<long long>(cta) * total / parts);
   const int tb = static_cast<int>(static_cast<long long>(cta + 1) * total / parts);
   if (ta >= before * heads && ta < (before + mine) * heads) {
     int b = b_lo, base = before * heads;
     for (;; ++b) {
-      const int n = span_of(p, b).tiles * heads;
+      const int n = span_of<TILE>(p, b).tiles * heads;
       if (ta < base + n) break;
       base += n;
     }
@@ -227,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
 
   // ---- the loading side: one tile ahead, the page of this lane's token
   Cursor next;
-  cursor_at(p, sm.start_b, sm.start_rem, next);
-  const int tok = lane & 15;
+  cursor_at<TILE>(p, sm.start_b, sm.start_rem, next);
+  const int tok = lane % C::TOK;
   int page = -1;                 // page number of the prefetched token
   long long part_off = 0;        // its slot's and head's offset
   auto look_up = [&]() {
     const int t = next.tile < next.s.first ? next.tile : next.tile + next.s.shift;
-    const int pos = t * kTileTokens + warp * kWarpTokens + tok;
+    const int pos = t * TILE + warp * C::TOK + tok;
     page = -1;
     if (pos < next.s.len && (pos >= next.s.lo || pos < p.sinks)) {
       const int j = static_cast<int>(static_cast<unsigned>(pos) /
@@ -253,26 +280,48 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
       const int slot = issued % C::STAGES;
       const bool ok = page >= 0 && page < p.pool.num_pages;
       const long long off = ok ? page * p.pool.page_stride + part_off : 0;
-      const uint32_t vis = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const uint32_t vis = __ballot_sync(0xffffffffu, ok) & (C::TOK == 32 ? ~0u : 0xffffu);
       if (lane == 0) sm.vis[warp][slot] = vis;
       if (looked < count) {
-        cursor_next(p, next);
+        cursor_next<TILE>(p, next);
         look_up();
         ++looked;
       }
       if (vis) {
         constexpr int CH = C::ROW / 16;             // 16-byte chunks of a row
         constexpr int RPI = 32 / CH;                // rows of one warp instruction
-        const uint32_t dst = ring + slot * C::STAGE;
-#pragma unroll
-        for (int r = 0; r < kWarpTokens / RPI; ++r) {
-          const int row = r * RPI + (RPI > 1 ? lane / CH : 0);
-          const int ch = lane % CH;
-          const long long ro = __shfl_sync(0xffffffffu, off, row);
+        const int sub = RPI > 1 ? lane / CH : 0, ch = lane % CH;
+        const uint32_t dst = ring + slot * C::STAGE + sub * C::ROW;
+        auto copy = [&](int row0, const __nv_bfloat16* kp, const __nv_bfloat16* vp) {
+          const int row = row0 + sub;
           const int bytes = (vis >> row) & 1u ? 16 : 0;    // 0: the row is filled with zeros
-          const uint32_t d = dst + row * C::ROW + ((ch ^ (row & 7)) << 4);
-          cp_async16(d, p.pool.k + ro + ch * 8, bytes);
-          cp_async16(d + C::HALF, p.pool.v + ro + ch * 8, bytes);
+          const uint32_t d = dst + row0 * C::ROW + ((ch ^ (row & 7)) << 4);
+          cp_async16(d, kp, bytes);
+          cp_async16(d + C::HALF, vp, bytes);
+        };
+        if (p.page16) {
+          // 16 tokens lie in one page: one lookup's offset (of any visible
+          // one) serves them, and hidden ones have their slots there as well
+          const long long stride = p.pool.token_stride;
+          const long long mine = sub * stride + ch * 8;
+#pragma unroll
+          for (int g16 = 0; g16 < C::TOK; g16 += 16) {
+            const uint32_t part = (vis >> g16) & 0xffffu;
+            const int first = part ? __ffs(part) - 1 : 0;
+            const long long base =
+                part ? __shfl_sync(0xffffffffu, off, g16 + first) - first * stride : 0;
+            const __nv_bfloat16* kp = p.pool.k + base + mine;
+            const __nv_bfloat16* vp = p.pool.v + base + mine;
+#pragma unroll
+            for (int r = 0; r < 16; r += RPI, kp += RPI * stride, vp += RPI * stride)
+              copy(g16 + r, kp, vp);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < C::TOK; r += RPI) {
+            const long long ro = __shfl_sync(0xffffffffu, off, r + sub) + ch * 8;
+            copy(r, p.pool.k + ro, p.pool.v + ro);
+          }
         }
       }
       ++issued;
@@ -284,8 +333,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
 
   // ---- the computing side
   Cursor cur;
-  cursor_at(p, sm.start_b, sm.start_rem, cur);
+  cursor_at<TILE>(p, sm.start_b, sm.start_rem, cur);
   int seg0 = ta - cur.tile;      // first tile of the current (sequence, head, row tile)
+  if (threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < ta);
   const int g = lane / 4, t4 = lane % 4;
   float acc[D / 8][4];
   float m[2], l[2];
@@ -329,48 +379,59 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
     issue();                     // into the stage that the previous tile left
     if (vis) {
       const uint32_t kb = ring + slot * C::STAGE;
-      float s[2][2][4];          // [even and odd k steps][n tile]
+      constexpr int NT = C::TOK / 8;                       // 8-token column tiles of S
+      // two tiles take two accumulators each, so that four chains of products
+      // run beside each other as with four tiles
+      constexpr int CH2 = NT == 2 ? 2 : 1;
+      float x[NT * CH2][4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int n = 0; n < NT * CH2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[a][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
       {
         const int row = (lane / 16) * 8 + (lane & 7);
         const uint32_t ka = kb + row * C::ROW;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t bf[4];
-          ldsm_x4(bf, ka + (((2 * ks + ((lane / 8) & 1)) ^ (row & 7)) << 4));
-          if constexpr (C::QREG) {
-            mma16816(s[ks & 1][0], qf[ks], bf[0], bf[1]);
-            mma16816(s[ks & 1][1], qf[ks], bf[2], bf[3]);
-          } else {
-            uint32_t af[4];
-            ldsm_x4(af, q_addr(ks));
-            mma16816(s[ks & 1][0], af, bf[0], bf[1]);
-            mma16816(s[ks & 1][1], af, bf[2], bf[3]);
+          uint32_t af[4];
+          if constexpr (!C::QREG) ldsm_x4(af, q_addr(ks));
+          const uint32_t* a4 = C::QREG ? qf[C::QREG ? ks : 0] : af;
+          const uint32_t a = ka + (((2 * ks + ((lane / 8) & 1)) ^ (row & 7)) << 4);
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            uint32_t bf[4];
+            ldsm_x4(bf, a + n * 8 * C::ROW);
+            const int o = n + (CH2 == 2 ? NT * (ks & 1) : 0);
+            mma16816(x[o], a4, bf[0], bf[1]);
+            mma16816(x[o + 1], a4, bf[2], bf[3]);
           }
         }
       }
+      if constexpr (CH2 == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] += x[NT + n][e];
+      }
       // rows g (elements 0, 1) and g + 8 (2, 3); columns 8 n + 2 t4 + {0, 1}
-      float x[2][4];
+      if (vis != (C::TOK == 32 ? ~0u : 0xffffu)) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = (vis >> (8 * n + 2 * t4 + (e & 1))) & 1u;
-          x[n][e] = on ? (s[0][n][e] + s[1][n][e]) * p.scale_log2 : -INFINITY;
-        }
-      float base[2];
+          for (int e = 0; e < 4; ++e)
+            if (!((vis >> (8 * n + 2 * t4 + (e & 1))) & 1u)) x[n][e] = -INFINITY;
+      }
+      float base[2];             // scale m, subtracted in the exponent
       bool moved = false;
       float alpha[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+        float mx = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+#pragma unroll
+        for (int n = 1; n < NT; ++n) mx = fmax3(mx, x[n][2 * r], x[n][2 * r + 1]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx *= p.scale_log2;
         const float mn = fmaxf(m[r], mx);
         alpha[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
         moved = moved || mn > m[r];
@@ -389,23 +450,31 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
         }
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[n][e] = ex2_approx(x[n][e] - base[e / 2]);
+          x[n][e] = ex2_approx(fmaf(x[n][e], p.scale_log2, -base[e / 2]));
           l[e / 2] += x[n][e];
         }
-      uint32_t pf[4] = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
-                        pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
+      uint32_t pf[NT / 2][4];
+#pragma unroll
+      for (int n = 0; n < NT / 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pf[n][e] = pack_bf16x2(x[2 * n + e / 2][2 * (e & 1)], x[2 * n + e / 2][2 * (e & 1) + 1]);
       {
         const int row = ((lane / 8) & 1) * 8 + (lane & 7);
         const uint32_t va = kb + C::HALF + row * C::ROW;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          uint32_t bf[4];
-          ldsm_x4_t(bf, va + (((2 * j + lane / 16) ^ (row & 7)) << 4));
-          mma16816(acc[2 * j], pf, bf[0], bf[1]);
-          mma16816(acc[2 * j + 1], pf, bf[2], bf[3]);
+          const uint32_t a = va + (((2 * j + lane / 16) ^ (row & 7)) << 4);
+#pragma unroll
+          for (int n = 0; n < NT / 2; ++n) {
+            uint32_t bf[4];
+            ldsm_x4_t(bf, a + n * 16 * C::ROW);
+            mma16816(acc[2 * j], pf[n], bf[0], bf[1]);
+            mma16816(acc[2 * j + 1], pf[n], bf[2], bf[3]);
+          }
         }
       }
     }
@@ -426,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
       }
     }
     const bool whole = seg0 >= ta && ends;
-    const int part = 2 * cta + (seg0 > ta ? 1 : 0);
+    const int part = 2 * cta + (seg0 < ta ? 0 : 1);
     const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
     float w[kWarps], lse2 = 0.f;
 #pragma unroll
@@ -483,102 +552,127 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
     }
     if (i + 1 < count) {
       seg0 = ta + i + 1;
-      cursor_next(p, cur);
+      cursor_next<TILE>(p, cur);
       fresh = true;
     }
   }
   cp_async_wait<0>();
+  write_empty();
 }
 
-// Joins the parts of every (sequence, head, row tile) that the split kernel
-// left in more than one, and writes O = 0, LSE = -inf for sequences without
-// tiles.  Launched as a dependent of the split kernel: the prefix sums, which
-// read kv_len alone, overlap it.
+// Joins the parts of the (sequence, head, row tile) that the border before CTA
+// blockIdx.x + 1 cuts, unless an earlier border cuts it too.
+constexpr int kJoinThreads = 512;             // at least as many as CTAs of the split kernel
+
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ int warp_sum[8];
-  __shared__ int upto;
-  __shared__ float w_sum[8];
-  __shared__ float w_acc[8][D];
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int WARPS = kJoinThreads / 32;
+  constexpr int PER = D / 32;                 // columns of a lane
+  constexpr int AHEAD = D == 256 ? 4 : 8;     // parts whose loads are in flight together
+  __shared__ int2 border;
+  __shared__ int ends;
+  __shared__ float w_max[WARPS], w_sum[WARPS];
+  __shared__ float w_acc[WARPS][D];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int heads = p.pool.h_kv * p.row_tiles;
-  const int b = blockIdx.x / heads, hr = blockIdx.x % heads;
-  const int per = (p.B + 255) / 256;
-  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
-  int mine = 0, at = 0;
-  for (int x = b_lo; x < b_hi; ++x) {
-    if (x == b) at = mine;
-    mine += span_of(p, x).tiles;
+  const int c0 = blockIdx.x;     // the CTA of the first part
+  grid_dependency_wait();
+  // thread t looks at the border before CTA c0 + 1 + t (the launch keeps parts
+  // below the threads)
+  const int c = c0 + 1 + threadIdx.x;
+  const int2 x = c < p.parts ? p.meta[c] : make_int2(-1, 0);
+  const int2 last = p.meta[c0];
+  if (threadIdx.x == 0) {
+    border = x;
+    ends = p.parts;
   }
-  int before;
-  const int total = block_scan<256>(mine, warp_sum, before) * heads;
-  if (b >= b_lo && b < b_hi) upto = before + at;
   __syncthreads();
-  const int tiles = span_of(p, b).tiles;
+  const int2 cut = border;
+  if (!cut.y || (last.y && last.x == cut.x)) return;
+  if (!x.y || x.x != cut.x) atomicMin(&ends, c);     // the first CTA that does not go on with it
+  __syncthreads();
+  const int n = ends - c0;       // parts
+  const int b = cut.x / heads, hr = cut.x % heads;
   const int kvh = hr / p.row_tiles, rt = hr - kvh * p.row_tiles;
   const int rows = min(kRows, p.group - rt * kRows);
   const size_t row0 = static_cast<size_t>(b) * p.H + kvh * p.group + rt * kRows;
-  int c0 = 0, n = 0;
-  bool second = false;           // part 0 is its CTA's second
-  if (tiles > 0) {
-    const long long parts = min(p.parts, total);
-    const long long t0 = static_cast<long long>(upto) * heads + static_cast<long long>(hr) * tiles;
-    c0 = static_cast<int>(((t0 + 1) * parts - 1) / total);
-    n = static_cast<int>(((t0 + tiles) * parts - 1) / total) - c0 + 1;
-    second = c0 * static_cast<long long>(total) / parts != t0;
-  }
-  // every CTA waits, also one with nothing to join: work behind this grid in
-  // the stream then finds the split kernel complete
-  grid_dependency_wait();
-  if (n == 1) return;            // whole in one CTA
-  // a warp takes a row, or with fewer than eight rows every k-th part of one
-  const int k = rows >= 8 ? 1 : (rows >= 3 ? 2 : (rows == 2 ? 4 : 8));
-  constexpr int PER = D / 32;
-  for (int r0 = 0; r0 < rows; r0 += 8 / k) {
-    const int row = r0 + warp / k, sub = warp % k;
-    float mx = -INFINITY, sum = 0.f, acc[PER];
+  // a warp takes a row, or with fewer rows than warps every k-th part of one
+  const int k = rows > 8 ? 1 : (rows > 4 ? 2 : (rows > 2 ? 4 : (rows == 2 ? 8 : 16)));
+  const int row = warp / k, sub = warp % k;
+  float mx = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    if (row < rows) {
-      auto slot = [&](int i) {
-        return static_cast<size_t>(2 * (c0 + i) + (i == 0 && second ? 1 : 0)) * kRows + row;
-      };
-      for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.lse_part[slot(i)]);
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  if (row < rows) {
+    auto slot = [&](int i) {
+      return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
+    };
+    for (int i0 = sub; i0 < n; i0 += AHEAD * k) {
+      float lse[AHEAD], x[AHEAD][PER];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-      for (int i = sub; i < n; i += k) {
-        const size_t s = slot(i);
-        const float w = ex2_approx(p.lse_part[s] - base);
-        sum += w;
-        const float* src = p.o_part + s * D + lane * PER;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * k;
+        lse[u] = -INFINITY;
+        if (i < n) {
+          lse[u] = p.lse_part[slot(i)];
+          const float* src = p.o_part + slot(i) * D + lane * PER;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e]);
-      }
-    }
-    if (k > 1) {
-      w_sum[warp] = sum;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) w_acc[warp][lane * PER + e] = acc[e];
-      __syncthreads();
-      if (sub == 0) {
-        for (int o = 1; o < k; ++o) {
-          sum += w_sum[warp + o];
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] += w_acc[warp + o][lane * PER + e];
+          for (int e = 0; e < PER; ++e) x[u][e] = src[e];
         }
       }
-      __syncthreads();
-    }
-    if (sub == 0 && row < rows) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + lane * PER);
+      float m = mx;
 #pragma unroll
-      for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      if (lane == 0)
-        p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+      for (int u = 0; u < AHEAD; ++u) m = fmaxf(m, lse[u]);
+      const float base = m == -INFINITY ? 0.f : m;
+      const float alpha = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
+      mx = m;
+      sum *= alpha;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] *= alpha;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (i0 + u * k < n) {
+          const float w = ex2_approx(lse[u] - base);
+          sum += w;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
+        }
+      }
     }
+  }
+  if (k > 1) {
+    if (lane == 0) {
+      w_max[warp] = mx;
+      w_sum[warp] = sum;
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) w_acc[warp][lane * PER + e] = acc[e];
+    __syncthreads();
+    if (sub == 0) {
+      float m = mx;
+      for (int o = 1; o < k; ++o) m = fmaxf(m, w_max[warp + o]);
+      const float base = m == -INFINITY ? 0.f : m;
+      const float a0 = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
+      mx = m;
+      sum *= a0;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] *= a0;
+      for (int o = 1; o < k; ++o) {
+        const float mo = w_max[warp + o];
+        const float a = mo == -INFINITY ? 0.f : ex2_approx(mo - base);
+        sum = fmaf(a, w_sum[warp + o], sum);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(a, w_acc[warp + o][lane * PER + e], acc[e]);
+      }
+    }
+  }
+  if (sub == 0 && row < rows) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0)
+      p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
   }
 }
 
@@ -591,12 +685,13 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   paged_decode_kernel<D><<<p.parts, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (p.parts < 2) return cudaSuccess;        // nothing is cut
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.pool.h_kv * p.row_tiles);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(p.parts - 1);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -604,7 +699,11 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
 }
 
 // CTAs of the split kernel: as many as are resident at once.
-int decode_parts(int d, int num_sms) { return num_sms * (d == 256 ? 1 : 2); }
+int decode_parts(int d, int num_sms) {
+  const int n = num_sms * (d == 256 ? DecodeCfg<256>::CTAS : DecodeCfg<128>::CTAS);
+  return n < kJoinThreads ? n : kJoinThreads;
+}
+static_assert(DecodeCfg<64>::CTAS == DecodeCfg<128>::CTAS, "decode_parts");
 
 size_t part_floats(int d, int num_sms) {
   return static_cast<size_t>(2) * decode_parts(d, num_sms) * kRows;
@@ -650,7 +749,8 @@ size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d) {
   int sms = 0;
   if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
   const size_t rows = fa::part_floats(d, sms);
-  return rows * d * sizeof(float) + (rows * sizeof(float) + 255) / 256 * 256;
+  return rows * d * sizeof(float) + (rows * sizeof(float) + 255) / 256 * 256 +
+         (fa::decode_parts(d, sms) * sizeof(int2) + 255) / 256 * 256;
 }
 
 fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer,
@@ -671,7 +771,8 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   p.row_tiles = (p.group + fa::kRows - 1) / fa::kRows;
   p.max_len = max_pages * p.pool.page_size;
   const long long heads = static_cast<long long>(p.pool.h_kv) * p.row_tiles;
-  const long long tiles = (p.max_len + fa::kTileTokens - 1) / fa::kTileTokens;
+  const int tile = p.pool.d == 64 ? fa::DecodeCfg<64>::TILE : fa::DecodeCfg<128>::TILE;
+  const long long tiles = (p.max_len + tile - 1ll) / tile;
   if (static_cast<long long>(B) * H >= INT_MAX || B * heads >= INT_MAX / tiles)
     return FA_ERR_INVALID_ARG;
   if (workspace_bytes < fa_decode_paged_workspace_bytes(H, p.pool.h_kv, p.pool.d))
@@ -689,10 +790,15 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   p.H = H;
   p.wl = window_left < 0 || window_left > fa::kUnbounded ? fa::kUnbounded : window_left;
   p.sinks = sinks;
+  p.page16 = p.pool.page_size % 16 == 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.parts = fa::decode_parts(p.pool.d, sms);
+  const int most = fa::decode_parts(p.pool.d, sms);
+  p.parts = B * heads * tiles < most ? static_cast<int>(B * heads * tiles) : most;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = p.o_part + fa::part_floats(p.pool.d, sms) * p.pool.d;
+  const size_t rows = fa::part_floats(p.pool.d, sms);
+  p.lse_part = p.o_part + rows * p.pool.d;
+  p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.lse_part) +
+                                   (rows * sizeof(float) + 255) / 256 * 256);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (p.pool.d) {
