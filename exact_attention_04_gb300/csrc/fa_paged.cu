@@ -686,16 +686,7 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.parts < 2) return cudaSuccess;        // nothing is cut
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.parts - 1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+  return launch_dependent(paged_join_kernel<D>, dim3(p.parts - 1), kJoinThreads, stream, p);
 }
 
 // CTAs of the split kernel: as many as are resident at once.
@@ -717,6 +708,7 @@ __global__ void __launch_bounds__(256)
                         const uint4* __restrict__ v_new, const int* __restrict__ table,
                         int max_pages, const int* __restrict__ start,
                         const int* __restrict__ kv_len, int Nq, int bh_count) {
+  grid_dependency_wait();
   constexpr int CH = D / 8;
   const unsigned e = blockIdx.x * 256u + threadIdx.x;   // the launch keeps Nq * CH below 2^31
   const int t = static_cast<int>(e / CH), ch = static_cast<int>(e % CH);
@@ -831,20 +823,14 @@ fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = static_cast<int>(bh);
   const dim3 grid(static_cast<unsigned>((vec + 255) / 256), rows < 65535 ? rows : 65535);
-  switch (pool.d) {
-    case 64:
-      fa::paged_append_kernel<64><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages, start,
-                                                       kv_len, Nq, rows);
-      break;
-    case 128:
-      fa::paged_append_kernel<128><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages,
-                                                        start, kv_len, Nq, rows);
-      break;
-    default:
-      fa::paged_append_kernel<256><<<grid, 256, 0, s>>>(pool, kn, vn, block_table, max_pages,
-                                                        start, kv_len, Nq, rows);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto launch = [&](auto kernel) {
+    return fa::launch_dependent(kernel, grid, 256, s, pool, kn, vn, block_table, max_pages, start,
+                                kv_len, Nq, rows);
+  };
+  const cudaError_t e = pool.d == 64    ? launch(fa::paged_append_kernel<64>)
+                        : pool.d == 128 ? launch(fa::paged_append_kernel<128>)
+                                        : launch(fa::paged_append_kernel<256>);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -44,6 +44,23 @@ inline fa_status_t resolve_pool(const fa_paged_kv_t* c, int layer, PagePool* out
   return FA_OK;
 }
 
+// Launches a kernel that waits for the one before it in its own code
+// (griddepcontrol.wait), so that its launch overlaps that one's run.
+template <class... Args, class... Given>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned threads,
+                             cudaStream_t stream, Given... given) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...);
+}
+
 // A block table over the pool: its width and address.
 inline bool table_ok(const int* table, int max_pages, int page_size) {
   return table && aligned_to(table, 4) && max_pages >= 1 &&
