@@ -701,13 +701,16 @@ size_t part_floats(int d, int num_sms) {
 }
 
 // New tokens into pages: a thread copies 16 bytes of K and of V.  Bound by
-// the copied bytes; every row is contiguous on both sides.
+// the copied bytes; every row is contiguous on both sides (8 rows of up to
+// 8192 tokens, h_kv = 8, d = 128: 41 us for 2 x 134 MB, 6.5 TB/s).  Launched
+// as a dependent of whatever is before it (the reservation of its pages, in a
+// serving step): it reads nothing before the wait, and nothing through the
+// read-only path, which may keep what was there when the grid started.
 template <int D>
 __global__ void __launch_bounds__(256)
-    paged_append_kernel(const __grid_constant__ PagePool pool, const uint4* __restrict__ k_new,
-                        const uint4* __restrict__ v_new, const int* __restrict__ table,
-                        int max_pages, const int* __restrict__ start,
-                        const int* __restrict__ kv_len, int Nq, int bh_count) {
+    paged_append_kernel(const __grid_constant__ PagePool pool, const uint4* k_new,
+                        const uint4* v_new, const int* table, int max_pages, const int* start,
+                        const int* kv_len, int Nq, int bh_count) {
   grid_dependency_wait();
   constexpr int CH = D / 8;
   const unsigned e = blockIdx.x * 256u + threadIdx.x;   // the launch keeps Nq * CH below 2^31
@@ -715,17 +718,17 @@ __global__ void __launch_bounds__(256)
   if (t >= Nq) return;
   for (int bh = blockIdx.y; bh < bh_count; bh += gridDim.y) {
     const int b = bh / pool.h_kv, h = bh - b * pool.h_kv;
-    const long long at = static_cast<long long>(__ldg(start + b)) + t;
-    if (at < 0 || at >= __ldg(kv_len + b)) continue;
+    const long long at = static_cast<long long>(start[b]) + t;
+    if (at < 0 || at >= kv_len[b]) continue;
     const int pos = static_cast<int>(at);
     const int j = pos / pool.page_size;
     if (j >= max_pages) continue;
-    const int page = __ldg(table + static_cast<size_t>(b) * max_pages + j);
+    const int page = table[static_cast<size_t>(b) * max_pages + j];
     if (page < 0 || page >= pool.num_pages) continue;
     const long long dst = page * pool.page_stride + h * pool.head_stride +
                           (pos - j * pool.page_size) * pool.token_stride + ch * 8;
     const size_t src = (static_cast<size_t>(bh) * Nq + t) * CH + ch;
-    const uint4 a = __ldg(k_new + src), c = __ldg(v_new + src);
+    const uint4 a = k_new[src], c = v_new[src];
     *reinterpret_cast<uint4*>(pool.k + dst) = a;
     *reinterpret_cast<uint4*>(pool.v + dst) = c;
   }

@@ -543,13 +543,17 @@ def forward(q, k, v, scale=None, causal=False, kv_len=None, window=None, stream=
     heads than Q, a window or a block mask go through fa_fwd_v, sinks (first
     tokens that stay visible left of the window) through fa_fwd_sinks."""
     B, H, N, d = q.shape
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     sc = default_scale(d) if scale is None else scale
     if sinks:
-        _no_block_mask(block_mask)
+        _check_sinks(q, block_mask)
+        with torch.cuda.stream(stream):      # None: the current one
+            o = torch.empty_like(q)
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
         fa_fwd_sinks(q, k, v, o, lse, sc, sinks, causal, kv_len, window, stream)
-    elif window is None and block_mask is None and k.shape == q.shape:
+        return o, lse
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    if window is None and block_mask is None and k.shape == q.shape:
         fa_fwd(q, k, v, o, lse, sc, causal, kv_len, stream)
     else:
         fa_fwd_v(q, k, v, o, lse, sc, causal, kv_len, window, stream, block_mask)
@@ -560,9 +564,11 @@ def workspace(B, H, N, d, device):
     return torch.empty(fa_bwd_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=device)
 
 
-def _no_block_mask(block_mask):
+def _check_sinks(q, block_mask):
     if block_mask is not None:
         raise ValueError("sinks: not together with a block mask")
+    if not q.is_cuda or q.get_device() != torch.cuda.current_device():
+        raise ValueError("q: expected a tensor on the current CUDA device")
 
 
 def sinks_workspace(B, H, N, d, device):
@@ -575,15 +581,17 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, kv_len=None, ws=None
     torch; dK, dV are shaped like k.  sinks as in forward (ws is then a
     sinks_workspace)."""
     B, H, N, d = q.shape
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
     sc = default_scale(d) if scale is None else scale
     if sinks:
-        _no_block_mask(block_mask)
-        if ws is None:
-            ws = sinks_workspace(B, H, N, d, q.device)
+        _check_sinks(q, block_mask)
+        with torch.cuda.stream(stream):
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+            if ws is None:
+                ws = sinks_workspace(B, H, N, d, q.device)
         fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, sc, sinks, causal, kv_len, window, ws,
                      stream)
         return dq, dk, dv
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
     if ws is None:
         ws = workspace(B, H, N, d, q.device)
     if window is None and block_mask is None and k.shape == q.shape:

@@ -175,4 +175,4 @@ def test_wrappers_refuse():
     with pytest.raises(ValueError):
         fa.forward(q, q, q, window=(2, 0), sinks=1)        # not on a GPU
     with pytest.raises(ValueError):
-        fa._no_block_mask(object())
+        fa._check_sinks(q, object())

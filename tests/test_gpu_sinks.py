@@ -173,3 +173,28 @@ def test_captured_and_replayed_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     compare(x, dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv), **kw)
+
+
+def test_on_a_given_stream():
+    """stream= runs there, with outputs and workspace allocated for it, while
+    the current stream allocates and overwrites what was freed."""
+    x = inputs(1, 4, 2, 900, 128, 13)
+    kw = dict(causal=True, window=(100, 0), sinks=4)
+    here = run(x, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        o, lse = fa.forward(x["q"], x["k"], x["v"], stream=s, **kw)
+        grads = fa.backward(x["q"], x["k"], x["v"], o, lse, x["do"], stream=s, **kw)
+        junk = torch.full((64 << 20,), 7, dtype=torch.uint8, device="cuda")
+        del junk
+    s.synchronize()
+    assert torch.equal(o, here["o"]) and torch.equal(lse, here["lse"])
+    assert torch.equal(grads[1], here["dk"]) and torch.equal(grads[2], here["dv"])
+
+
+def test_sinks_past_the_sequence():
+    """More sinks than tokens, at the largest count."""
+    x = inputs(1, 2, 1, 200, 64, 14, (150,))
+    kw = dict(causal=True, window=(10, 0), sinks=(1 << 31) - 1)
+    compare(x, run(x, **kw), **kw)
