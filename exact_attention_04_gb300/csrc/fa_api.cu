@@ -764,7 +764,13 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   char* extra = static_cast<char*>(workspace) + fa_bwd_workspace_bytes(B, H, N, d);
   p.sinks = sinks;
   p.sk_ctas = sink_ctas(static_cast<long long>(B) * H, N, p.wl, sinks, di->num_sms);
+  if (d == 64 && (!make_map(&p.tdk, dk, d, N, B * p.H_kv) || !make_map(&p.tdv, dv, d, N, B * p.H_kv)))
+    return FA_ERR_CUDA;
   p.sk_halves = d == 256 ? 2 : 1;
+  const int T = (N + 127) / 128, nsb = static_cast<int>(std::min<long long>(T, (sinks + 127ll) / 128));
+  p.fd_rest = fa::FastDiv::of(std::max(1, T - nsb));
+  p.fd_nsb = fa::FastDiv::of(std::max(1, nsb));
+  p.fd_hkv = fa::FastDiv::of(p.H_kv);
   p.sk_part = reinterpret_cast<float*>(extra);
   p.sk_meta = reinterpret_cast<int*>(extra + sink_part_bytes(di->num_sms, d));
   p.o = o;

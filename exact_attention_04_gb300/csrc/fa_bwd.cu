@@ -157,7 +157,7 @@ __device__ __forceinline__ void sinks_join(const BwdParams& p, int block) {
   const int r = e / W8 % 128, col = e % W8 * 8;
   const SkItems items(p);
   int kvbh, n, h;
-  items.pool_item(item, items.plain / p.sk_ctas * p.sk_ctas, kvbh, n, h);
+  items.pool_item(p, item, items.plain / p.sk_ctas * p.sk_ctas, kvbh, n, h);
   const int key = n * 128 + r;
   if (which > 1 || key >= p.N) return;
   auto row = [&](int slot) {

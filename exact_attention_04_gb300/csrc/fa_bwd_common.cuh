@@ -240,7 +240,7 @@ __device__ __forceinline__ void sk_plan(const BwdParams& p, int G, SkScratch& sc
   const int lo = min(pool, tid * per), hi = min(pool, lo + per);
   auto cost = [&](int j) {
     int kvbh, n, h;
-    items.pool_item(j, whole, kvbh, n, h);
+    items.pool_item(p, j, whole, kvbh, n, h);
     return sk_steps<STEP>(p, kvbh, n, G) + kItemCost;
   };
   long long sum = 0, before;
@@ -314,13 +314,13 @@ struct ItemWalk {
       const int end = sc->plan.whole;
       const bool whole = it.u < end;
       if (whole) {
-        items.plain_item(it.u, w.kvbh, w.n, w.h);
+        items.plain_item(p, it.u, w.kvbh, w.n, w.h);
         it.u += gridDim.x;
       } else {
         if (p0 >= sc->plan.xe) return false;
-        items.pool_item(j++, end, w.kvbh, w.n, w.h);
+        items.pool_item(p, j++, end, w.kvbh, w.n, w.h);
       }
-      w.len = dt_len(p, w.kvbh);
+      w.len = p.kv_len ? max(0, min(p.N, __ldg(p.kv_len + p.fd_hkv.div(w.kvbh)))) : p.N;
       step_range<MK, STEP>(p, w.n, w.len, w.i0, w.i1);
       w.nst = w.i1 - w.i0;
       w.sk = StepMask{nullptr, 0, 1};

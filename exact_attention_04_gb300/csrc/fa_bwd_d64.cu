@@ -61,21 +61,25 @@ constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 320, TM_DQ = 384,
 
 template <int MK = kMaskNone>
 struct SSmem {
-  alignas(1024) uint8_t k[SCH];
-  alignas(1024) uint8_t v[SCH];
+  // sinks: two K/V buffers, so that the next key block's products start
+  // while the last one's are still running
+  static constexpr int NKV = MK == kMaskSinks ? 2 : 1;
+  alignas(1024) uint8_t k[NKV][SCH];
+  alignas(1024) uint8_t v[NKV][SCH];
   alignas(1024) uint8_t q[2][SCH];
   alignas(1024) uint8_t dO[2][SCH];
   alignas(1024) uint8_t ds[2 * SCH];    // dS^T bf16: 128 keys x 128 queries, two 64-query chunks
   alignas(1024) uint8_t stage[2][2 * SCH];   // dQ fp32: two boxes of [128 rows][32 columns]
   alignas(16) float lse2[2][SQ];
   alignas(16) float delta[2][SQ];
-  uint64_t kv_full, kv_empty;
+  uint64_t kv_full[NKV], kv_empty[NKV];
   uint64_t q_full[2], q_empty[2], do_full[2], do_empty[2];
   // ds_tm: dS^T(g) is in tensor memory (dK(g) may start); ds_full: its copy
   // is in shared memory (dQ(g) may start)
   uint64_t s_full, p_full, dv_done, dp_full, ds_tm, ds_full, dk_done, dq_full, dq_free;
   uint64_t stg_full[2], stg_free[2];
   uint64_t acc_full, acc_free;
+  uint64_t out_full, out_free;     // sinks: dV, dK of a key block in ds; ds free again
   uint64_t mma_done, mma_done_b;
   uint32_t tmem_base;
   int abort;
@@ -96,6 +100,7 @@ template <int MK>
 __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_constant__ BwdParams p,
                                                                const __grid_constant__ TailTable tail) {
   constexpr bool SK = MK == kMaskSinks;
+  constexpr uint32_t NKV = SSmem<MK>::NKV;
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
@@ -110,8 +115,10 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     sm.abort = 0;
-    mbar_init(&sm.kv_full, 1);
-    mbar_init(&sm.kv_empty, 2);             // issuer A (K, V) and issuer B (K)
+    for (int b = 0; b < NKV; ++b) {
+      mbar_init(&sm.kv_full[b], 1);
+      mbar_init(&sm.kv_empty[b], 2);        // issuer A (K, V) and issuer B (K)
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 2);         // A after S^T, B after dK (the row warps are past L2)
@@ -131,6 +138,8 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
     mbar_init(&sm.dq_free, kSRowWarps);
     mbar_init(&sm.acc_full, 1);
     mbar_init(&sm.acc_free, kSRowWarps);
+    mbar_init(&sm.out_full, kSRowWarps);
+    mbar_init(&sm.out_free, 1);
     mbar_init(&sm.mma_done, 1);
     mbar_init(&sm.mma_done_b, 1);
     fence_mbar_init();
@@ -179,14 +188,15 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
           [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
           if (w.empty()) continue;
           if (!dlane) {
-            if (!mbar_wait(&sm.kv_empty, (w_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
+            const uint32_t kb = w_it % NKV;
+            if (!mbar_wait(&sm.kv_empty[kb], ((w_it / NKV) & 1) ^ 1, abort, kWaitTimeoutNs)) {
               record_failure(p.status, abort, kSiteProdKV);
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&sm.kv_full, 2 * SCH);
-            tma_load_3d(sm.k, &p.tk, &sm.kv_full, 0, n * BK, kvbh);
-            tma_load_3d(sm.v, &p.tv, &sm.kv_full, 0, n * BK, kvbh);
+            mbar_arrive_expect_tx(&sm.kv_full[kb], 2 * SCH);
+            tma_load_3d(sm.k[kb], &p.tk, &sm.kv_full[kb], 0, n * BK, kvbh);
+            tma_load_3d(sm.v[kb], &p.tv, &sm.kv_full[kb], 0, n * BK, kvbh);
             ++w_it;
           }
           StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
@@ -209,8 +219,10 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
           }
         }
         // no copy may still be landing in shared memory when the CTA exits
-        if (!dlane && w_it > 0 && !mbar_wait(&sm.kv_full, (w_it - 1) & 1, nullptr, kWaitTimeoutNs))
-          record_failure(p.status, abort, kSiteDtDrain);
+        for (uint32_t b = 0; b < NKV; ++b)
+          if (!dlane && w_it > b &&
+              !mbar_wait(&sm.kv_full[b], ((w_it - 1 - b) / NKV) & 1, nullptr, kWaitTimeoutNs))
+            record_failure(p.status, abort, kSiteDtDrain);
         for (int s = 0; s < 2; ++s) {
           if (g > static_cast<uint32_t>(s)) {
             const uint32_t nph = (g - 1 - s) / 2;
@@ -223,15 +235,16 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
     } else if (warp == 1) {
       // ------------------------------------------------------------ issuer A
       constexpr uint32_t kId = idesc_bf16_f32(BK, SQ, 0, 0);        // S^T, dP^T
-      const uint64_t dK0 = sdesc_sw128(smem_u32(sm.k), 16, 1024);
-      const uint64_t dV0 = sdesc_sw128(smem_u32(sm.v), 16, 1024);
       uint32_t w_it = 0, g = 0;
       bool ok = true;
       ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
       for (Item w; ok && items.next(w);) {
         [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
         if (w.empty()) continue;
-        if (!mbar_wait_warp(&sm.kv_full, w_it & 1, abort, kWaitTimeoutNs)) {
+        const uint32_t kb = w_it % NKV;
+        const uint64_t dK0 = sdesc_sw128(smem_u32(sm.k[kb]), 16, 1024);
+        const uint64_t dV0 = sdesc_sw128(smem_u32(sm.v[kb]), 16, 1024);
+        if (!mbar_wait_warp(&sm.kv_full[kb], (w_it / NKV) & 1, abort, kWaitTimeoutNs)) {
           issuer_fail(p.status, abort, lane, kSiteMmaKV);
           ok = false;
           break;
@@ -239,8 +252,8 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         if constexpr (SK) {
           const int left = w.len - n * BK;
           if (left < BK) {
-            zero_rows(sm.k, 1, left, lane);
-            zero_rows(sm.v, 1, left, lane);
+            zero_rows(sm.k[kb], 1, left, lane);
+            zero_rows(sm.v[kb], 1, left, lane);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
           mma_commit_w(&sm.do_empty[st]);
         }
         if (!ok) break;
-        mma_commit_w(&sm.kv_empty);                 // A's reads of K and V are done
+        mma_commit_w(&sm.kv_empty[kb]);             // A's reads of K and V are done
         ++w_it;
       }
       // every tcgen05 op issued by this thread must finish before exit
@@ -302,7 +315,6 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       // dS^T as the MN-major A operand of dQ (64-query chunks SCH apart), K as
       // its MN-major B operand
       const uint64_t dDS = sdesc_sw128(smem_u32(sm.ds), SCH, 1024);
-      const uint64_t dKmn = sdesc_sw128(smem_u32(sm.k), SCH, 1024);
       uint32_t w_it = 0, g = 0;
       bool ok = true;
       auto fail = [&](int site) {
@@ -313,6 +325,8 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       for (Item w; ok && items.next(w);) {
         [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
         if (w.empty()) continue;
+        const uint32_t kb = w_it % NKV;
+        const uint64_t dKmn = sdesc_sw128(smem_u32(sm.k[kb]), SCH, 1024);
         for (int s = w.a; s < w.b; ++s, ++g) {
           const int st = g & 1;
           const uint32_t ph = g & 1;
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
             mma_bf16_ss_w(tmem + TM_DQ, dDS + ((kk * 2048) >> 4), dKmn + ((kk * 2048) >> 4), kIdDq,
                           kk > 0 ? 1u : 0u);
           mma_commit_w(&sm.dq_full);
-          if (last) mma_commit_w(&sm.kv_empty);     // B's reads of K are done
+          if (last) mma_commit_w(&sm.kv_empty[kb]); // B's reads of K are done
         }
         if (!ok) break;
         ++w_it;
@@ -457,6 +471,10 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
     const bool st32 = ((reinterpret_cast<uintptr_t>(dk_out) | reinterpret_cast<uintptr_t>(dv_out)) &
                        31u) == 0;
     uint32_t w_it = 0, g = 0;
+    // (sinks) key blocks stored through ds, the last one perhaps still read
+    uint32_t out_it = 0;
+    bool stored = false;
+    const bool lead = SK && warp == kSRowWarp0 && lane == 0;
     bool ok = true;
     ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
     for (Item w; ok && items.next(w);) {
@@ -518,9 +536,18 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
             for (int e = 0; e < 4; ++e) pr[4 * t + e] = ex2_approx(a[e]);
           }
           if (need_mask) {      // diagonal and boundary steps only
+            if constexpr (SK) {   // short windows: half of the steps or more
+              const uint32_t on = bits_below(c_hi + 1) & ~bits_below(c_lo);
+              if (__any_sync(0xffffffffu, on != ~0u)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c < c_lo || c > c_hi) pr[c] = 0.f;
+                for (int c = 0; c < 32; ++c)
+                  if (!((on >> c) & 1u)) pr[c] = 0.f;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c < c_lo || c > c_hi) pr[c] = 0.f;
+            }
           }
           uint32_t pk[16];
 #pragma unroll
@@ -571,9 +598,22 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(&sm.ds_tm);
         // ---- the previous step's dQ (once it is complete the shared dS
         // buffer it read is free for this step's copy)
-        if (g > 0 && !drain(g - 1)) {
+        if ((SK ? s > w.a : g > 0) && !drain(g - 1)) {
           ok = false;
           break;
+        }
+        // (sinks) the last key block's dV and dK have left the buffer
+        if (SK && s == w.a && stored) {
+          stored = false;
+          if (lead) {
+            bulk_wait_group_read<0>();
+            mbar_arrive(&sm.out_free);
+          }
+          if (!warp_wait(&sm.out_free, (out_it - 1) & 1, abort)) {
+            if (lane == 0) record_failure(p.status, abort, kSiteStageFree);
+            ok = false;
+            break;
+          }
         }
         // ---- dS for dQ(g): row = key r, this quarter's 32 queries = 4 units
         // of 16 bytes in the 64-query chunk j4 / 2, XOR-swizzled by (r & 7)
@@ -609,6 +649,12 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_free);
+        // (sinks) the last step's dQ here and not in the next key block's
+        // first step: the buffer that it read serves dV and dK now
+        if (SK && !drain(g - 1)) {
+          ok = false;
+          break;
+        }
         if (SK && w.slot >= 0) {
           const int at = r * SD + 16 * j4;
           float* dvp = sink_rows(p, w.slot, SD, 0) + at;
@@ -620,6 +666,40 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
             st_global_v8(dvp + 8 * t, a + 8 * t);
             st_global_v8(dkp + 8 * t, bb + 8 * t);
           }
+        } else if constexpr (SK) {
+          // Through shared memory and two bulk tensor stores (rows past N are
+          // not written): of the threads' own stores each takes 32 lines.
+          // With the two K/V buffers, 332 us against 340 (B = 2, H = 16, N =
+          // 8192, window 1023, 4 sinks).
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int at = r * 128 + (((2 * j4 + t) ^ (r & 7)) << 4);
+            uint32_t pv[4], pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = 8 * t + 2 * e;
+              pv[e] = pack_bf16x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+              pk[e] = pack_bf16x2(__uint_as_float(bb[i]) * p.scale,
+                                  __uint_as_float(bb[i + 1]) * p.scale);
+            }
+            *reinterpret_cast<uint4*>(sm.ds + at) = make_uint4(pv[0], pv[1], pv[2], pv[3]);
+            *reinterpret_cast<uint4*>(sm.ds + SCH + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.out_full);
+          if (lead) {
+            if (!mbar_wait(&sm.out_full, out_it & 1, abort, kWaitTimeoutNs)) {
+              record_failure(p.status, abort, kSiteStageFull);
+            } else {
+              tma_store_3d(&p.tdv, sm.ds, 0, n * BK, kvbh);
+              tma_store_3d(&p.tdk, sm.ds + SCH, 0, n * BK, kvbh);
+              bulk_commit_group();
+            }
+          }
+          __syncwarp();
+          ++out_it;
+          stored = true;
         } else if (key < p.N) {
           uint32_t pv[8], pkk[8];
 #pragma unroll
@@ -645,7 +725,9 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       ++w_it;
     }
     // the last step's dQ
-    if (ok && g > 0) drain(g - 1);
+    if (!SK && ok && g > 0) drain(g - 1);
+    // every store must have landed before the CTA exits
+    if (lead) bulk_wait_group<0>();
   }
 
   tc_fence_before_sync();

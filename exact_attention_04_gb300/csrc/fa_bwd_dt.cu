@@ -577,9 +577,18 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
               for (int e = 0; e < 4; ++e) pr[4 * t + e] = ex2_approx(a[e]);
             }
             if (need_mask) {      // diagonal and boundary steps only
+              if constexpr (SK) {   // short windows: half of the steps or more
+                const uint32_t on = bits_below(c_hi + 1) & ~bits_below(c_lo);
+                if (__any_sync(0xffffffffu, on != ~0u)) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c < c_lo || c > c_hi) pr[c] = 0.f;
+                  for (int c = 0; c < 32; ++c)
+                    if (!((on >> c) & 1u)) pr[c] = 0.f;
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (c < c_lo || c > c_hi) pr[c] = 0.f;
+              }
             }
             uint32_t pk[16];
 #pragma unroll

@@ -1082,11 +1082,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, MK>::THREADS, 1)
               // and the code is cold each time (two comparisons a column
               // measured 145 against 136 us, skipping the chunks that all of the warp's rows
               // see 133: H = 32, h_kv = 8, N = 8192, window 1023, 16 sinks).
-              auto below = [](int x) { return x >= 32 ? ~0u : (x <= 0 ? 0u : (1u << x) - 1u); };
 #pragma unroll
               for (int w = 0; w < NC / 32; ++w) {
-                const uint32_t on = below(c_hi + 1 - 32 * w) &
-                                    (~below(c_lo - 32 * w) | below(p.sinks - key0 - 32 * w));
+                const uint32_t on = bits_below(c_hi + 1 - 32 * w) &
+                                    (~bits_below(c_lo - 32 * w) | bits_below(p.sinks - key0 - 32 * w));
                 if (__any_sync(0xffffffffu, on != ~0u)) {
 #pragma unroll
                   for (int c = 0; c < 32; ++c)

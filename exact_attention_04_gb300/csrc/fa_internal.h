@@ -100,7 +100,10 @@ struct BwdParams {
   // (fa_bwd_common.cuh); sk_part [2 sk_ctas, 2, 128, min(d, 128)] takes the
   // fp32 dV, dK of the pieces, sk_meta [sk_ctas, 2] says which these are.
   // sk_halves: items of a key block (2 at d = 256).
+  // The divisions: by the key blocks of a head without sinks, with, and by H_kv.
   int sinks, sk_ctas, sk_halves;
+  FastDiv fd_rest, fd_nsb, fd_hkv;
+  CUtensorMap tdk, tdv;        // d = 64: bf16 dK, dV [BHkv, N, 64], box (64, 128, 1), SW128
   float* sk_part;
   int* sk_meta;
   // block-sparse: [bm_t, bm_t] bytes, nonzero where (query block, key block)

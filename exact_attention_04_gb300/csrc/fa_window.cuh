@@ -17,6 +17,12 @@ namespace fa {
 // i +- kUnbounded never overflows an int.
 constexpr int kUnbounded = 1 << 30;
 
+// The lowest x of 32 bits (none below 1, all from 32 on): columns [0, x) of a
+// 32-column chunk as a mask.
+__device__ __forceinline__ uint32_t bits_below(int x) {
+  return x >= 32 ? ~0u : (x <= 0 ? 0u : (1u << x) - 1u);
+}
+
 // Key range [k_lo, k_hi) that query rows [r0, r0 + nrows) can see.
 __device__ __forceinline__ void visible_keys(int r0, int nrows, int len, int wl, int wr,
                                              int& k_lo, int& k_hi) {
@@ -59,32 +65,35 @@ __device__ __forceinline__ int q_head_of(int kvbh, int gi, int H, int H_kv) {
 // block, half of d.  The pool (fa_bwd_common.cuh) is the sunk ones, then the
 // plain ones from `whole` on.
 struct SkItems {
-  int nsb, rest, halves, sunk, plain;   // key blocks of a head with sinks and without
+  int nsb, rest, sunk, plain;   // key blocks of a head with sinks and without; items
   template <class Params>
   __device__ __forceinline__ explicit SkItems(const Params& p) {
     const int T = (p.N + 127) / 128;
     nsb = min(T, p.sinks / 128 + (p.sinks % 128 != 0));
     rest = T - nsb;
-    halves = p.sk_halves;
-    const int per = p.B * p.H_kv * halves;
+    const int per = p.B * p.H_kv * p.sk_halves;
     sunk = per * nsb;
     plain = per * rest;
   }
-  __device__ __forceinline__ void place(int i, int blocks, int first, int& kvbh, int& n,
-                                        int& h) const {
-    const int kn = i / halves;
-    h = i - kn * halves;
-    kvbh = kn / blocks;
-    n = first + kn - kvbh * blocks;
+  template <class Params>
+  __device__ __forceinline__ void plain_item(const Params& p, int i, int& kvbh, int& n,
+                                             int& h) const {
+    const int kn = p.sk_halves == 2 ? i >> 1 : i;
+    h = i & (p.sk_halves - 1);
+    kvbh = p.fd_rest.div(kn);
+    n = nsb + kn - kvbh * rest;
   }
-  __device__ __forceinline__ void plain_item(int i, int& kvbh, int& n, int& h) const {
-    place(i, rest, nsb, kvbh, n, h);
-  }
-  __device__ __forceinline__ void pool_item(int j, int whole, int& kvbh, int& n, int& h) const {
-    if (j < sunk)
-      place(j, nsb, 0, kvbh, n, h);
-    else
-      plain_item(whole + j - sunk, kvbh, n, h);
+  template <class Params>
+  __device__ __forceinline__ void pool_item(const Params& p, int j, int whole, int& kvbh, int& n,
+                                            int& h) const {
+    if (j >= sunk) {
+      plain_item(p, whole + j - sunk, kvbh, n, h);
+      return;
+    }
+    const int kn = p.sk_halves == 2 ? j >> 1 : j;
+    h = j & (p.sk_halves - 1);
+    kvbh = p.fd_nsb.div(kn);
+    n = kn - kvbh * nsb;
   }
 };
 
