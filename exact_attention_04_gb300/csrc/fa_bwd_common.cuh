@@ -270,17 +270,28 @@ __device__ __forceinline__ float* sink_rows(const BwdParams& p, int slot, int co
 // A work item as every role sees it: steps [a, b) of its nst a query head,
 // head after head; none: a key block that no query sees (its gradients are
 // written as zeros), or with sinks the empty end of one.
+template <int MK>
 struct Item {
+  int kvbh, h, n, len;
+  int i0, i1, nst, b;
+  StepMask sk;
+  static constexpr int a = 0, slot = -1;
+  static constexpr bool zero = true;
+  __device__ __forceinline__ bool empty() const { return b == 0; }
+  __device__ __forceinline__ StepWalk walk(int bh0) const { return StepWalk(i0, i1, bh0, sk); }
+};
+
+template <>
+struct Item<kMaskSinks> {
   int kvbh, h, n, len;
   int i0, i1, nst;
   int a, b;
   int slot;                     // of sk_part, or -1: dV and dK
   bool zero;                    // no query sees it, and this CTA writes the zeros
-  StepMask sk;
   __device__ __forceinline__ bool empty() const { return a >= b; }
   __device__ __forceinline__ StepWalk walk(int bh0) const {
-    StepWalk w(i0, i1, bh0, sk);
-    if (a > 0) {                // (sinks: no block mask)
+    StepWalk w(i0, i1, bh0);
+    if (a > 0) {
       w.bh += a / nst;
       w.i += a % nst;
     }
@@ -298,6 +309,7 @@ struct ItemWalk {
   const SkScratch* sc;          // sinks: it.u is the next round-robin item, then
   int j;                        // the pool's next item and where it starts
   long long p0;
+  bool whole;                   // the item placed last is a round-robin one
   __device__ __forceinline__ ItemWalk(const BwdParams& p_, const TailTable& tail_,
                                       const DtSched& sched_, int G_, const SkScratch* sc_)
       : p(p_), tail(tail_), sched(sched_), G(G_), it{static_cast<int>(blockIdx.x), 0, 0},
@@ -307,23 +319,34 @@ struct ItemWalk {
       p0 = sc->plan.p0;
     }
   }
-  __device__ __forceinline__ bool next(Item& w) {
-    w.slot = -1;
+  // The next item's place, false when this CTA has none left, and what it
+  // takes there.
+  __device__ __forceinline__ bool place(int& kvbh, int& h, int& n) {
     if constexpr (MK == kMaskSinks) {
       const SkItems items(p);
       const int end = sc->plan.whole;
-      const bool whole = it.u < end;
+      whole = it.u < end;
       if (whole) {
-        items.plain_item(p, it.u, w.kvbh, w.n, w.h);
+        items.plain_item(p, it.u, kvbh, n, h);
         it.u += gridDim.x;
       } else {
         if (p0 >= sc->plan.xe) return false;
-        items.pool_item(p, j++, end, w.kvbh, w.n, w.h);
+        items.pool_item(p, j++, end, kvbh, n, h);
       }
-      w.len = p.kv_len ? max(0, min(p.N, __ldg(p.kv_len + p.fd_hkv.div(w.kvbh)))) : p.N;
-      step_range<MK, STEP>(p, w.n, w.len, w.i0, w.i1);
+      return true;
+    } else {
+      return sched.next(tail, it, kvbh, h, n);
+    }
+  }
+  __device__ __forceinline__ void fill(int kvbh, int h, int n, Item<MK>& w) {
+    w.kvbh = kvbh;
+    w.h = h;
+    w.n = n;
+    if constexpr (MK == kMaskSinks) {
+      w.slot = -1;
+      w.len = p.kv_len ? max(0, min(p.N, __ldg(p.kv_len + p.fd_hkv.div(kvbh)))) : p.N;
+      step_range<MK, STEP>(p, n, w.len, w.i0, w.i1);
       w.nst = w.i1 - w.i0;
-      w.sk = StepMask{nullptr, 0, 1};
       const long long steps = static_cast<long long>(w.nst) * G;
       w.a = 0;
       w.b = static_cast<int>(steps);
@@ -339,18 +362,19 @@ struct ItemWalk {
           w.slot = 2 * blockIdx.x + 1;
         p0 = first + steps;
       }
-      return true;
     } else {
-      if (!sched.next(tail, it, w.kvbh, w.h, w.n)) return false;
-      w.len = dt_len(p, w.kvbh);
-      step_range<MK, STEP>(p, w.n, w.len, w.i0, w.i1);
-      w.sk = StepMask{MK == kMaskBlocks ? p.block_mask + w.n : nullptr, p.bm_t, BK / STEP};
+      w.len = dt_len(p, kvbh);
+      step_range<MK, STEP>(p, n, w.len, w.i0, w.i1);
+      w.sk = StepMask{MK == kMaskBlocks ? p.block_mask + n : nullptr, p.bm_t, BK / STEP};
       w.nst = count_steps(w.sk, w.i0, w.i1);
-      w.a = 0;
+      if (w.nst == 0) w.i1 = w.i0;
       w.b = w.nst * G;
-      w.zero = w.b == 0;
-      return true;
     }
+  }
+  __device__ __forceinline__ bool next(Item<MK>& w) {
+    if (!place(w.kvbh, w.h, w.n)) return false;
+    fill(w.kvbh, w.h, w.n, w);
+    return true;
   }
 };
 

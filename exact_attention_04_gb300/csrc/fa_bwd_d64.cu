@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         uint32_t w_it = 0, g = 0;
         bool ok = true;
         ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
-        for (Item w; ok && items.next(w);) {
+        for (Item<MK> w; ok && items.next(w);) {
           [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
           if (w.empty()) continue;
           if (!dlane) {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
       uint32_t w_it = 0, g = 0;
       bool ok = true;
       ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
-      for (Item w; ok && items.next(w);) {
+      for (Item<MK> w; ok && items.next(w);) {
         [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
         if (w.empty()) continue;
         const uint32_t kb = w_it % NKV;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         ok = false;
       };
       ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
-      for (Item w; ok && items.next(w);) {
+      for (Item<MK> w; ok && items.next(w);) {
         [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
         if (w.empty()) continue;
         const uint32_t kb = w_it % NKV;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
         uint32_t g = 0;
         bool ok = true;
         ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
-        for (Item w; ok && items.next(w);) {
+        for (Item<MK> w; ok && items.next(w);) {
           [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
           StepWalk wk = w.walk(q_head_of(kvbh, 0, p.H, p.H_kv));
           for (int s = w.a; s < w.b; ++s, ++g, wk.next()) {
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
     const bool lead = SK && warp == kSRowWarp0 && lane == 0;
     bool ok = true;
     ItemWalk<MK, SQ> items(p, tail, sched, G, SKS);
-    for (Item w; ok && items.next(w);) {
+    for (Item<MK> w; ok && items.next(w);) {
       [[maybe_unused]] const int kvbh = w.kvbh, n = w.n;
       const int len = w.len;
       const int key = n * BK + r;

@@ -218,7 +218,7 @@ struct Sched {
   __device__ void tile(int u, int k, int& bh, int& m) const {
     if (!causal) {
       bh = fd ? fd->div(u) : u / T;
-      m = u - bh * T;
+      m = fd ? u - bh * T : u % T;   // (u - bh T here too: 308 -> 315 us at d = 64)
     } else {
       bh = u / P;
       const int p = u % P;
