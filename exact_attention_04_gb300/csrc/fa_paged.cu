@@ -17,13 +17,14 @@
 // the unrounded values, O stays in fp32 registers.
 //
 // Work split.  A tile is 64 token positions (128 at d = 64) of one (sequence,
-// K/V head, 16 query heads).  Every CTA computes the same prefix sums over kv_len and takes
-// tiles [c T / G, (c + 1) T / G) of the T there are: equal shares whatever
-// the lengths, a pure function of kv_len.  A share may end inside a (sequence,
-// head): such a part leaves its normalised O and LSE (base 2) in the
-// workspace (at most two parts a CTA: slot 2c for the one that an earlier CTA
-// began, 2c + 1 for the one that it begins and does not end), and a second
-// kernel, a block per border between two shares, joins them,
+// K/V head, 16 query heads; 32 where a group has more than 16).  Every CTA
+// computes the same prefix sums over kv_len and takes tiles [c T / G,
+// (c + 1) T / G) of the T there are: equal shares whatever the lengths, a pure
+// function of kv_len.  A share may end inside a (sequence, head): such a part
+// leaves its normalised O and LSE (base 2) in the workspace (at most two parts
+// a CTA: slot 2c for the one that an earlier CTA began, 2c + 1 for the one
+// that it begins and does not end), and a second kernel, a block per border
+// between two shares, joins them,
 //   LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i,
 // in the order of the CTAs.  Loads run ahead across the boundary between two
 // heads or sequences.
@@ -45,7 +46,7 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;                         // query heads of a tile (M of the mma)
+constexpr int kRows = 16;                         // rows of the mma: query heads
 
 struct DecodeParams {
   PagePool pool;
@@ -55,13 +56,13 @@ struct DecodeParams {
   const int* table;             // [B, max_pages]
   const int* kv_len;            // [B]
   int max_pages, max_len;       // max_len = max_pages * page_size
-  int B, H, group, row_tiles;   // group = H / h_kv, row_tiles = ceil(group / 16)
+  int B, H, group, row_tiles;   // group = H / h_kv, row_tiles = ceil(group / (16 RT))
   int wl, sinks;
   int page16;                   // the page size is a multiple of 16
   float scale_log2;
   int parts;                    // CTAs of the split kernel
-  float* o_part;                // [2 parts, 16, d]
-  float* lse_part;              // [2 parts, 16]
+  float* o_part;                // [2 parts, 16 RT, d]
+  float* lse_part;              // [2 parts, 16 RT]
   int2* meta;                   // [parts]: the (sequence, head) that a CTA's share starts in,
                                 // and whether it cuts it
 };
@@ -172,8 +173,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, int RT = 1>
 struct DecodeCfg {
+  static constexpr int ROWS = kRows * RT;                  // query heads of a tile
   static constexpr int ROW = 2 * D;                        // bytes of a token's K or V row
   // Tokens of a warp's stage: what a stage costs besides its bytes (the page
   // lookup, the maximum's exchange, the loop) bounds d = 64, where 32 tokens
@@ -186,29 +188,30 @@ struct DecodeCfg {
   // 96 KB of loads in flight a CTA and two CTAs an SM (d = 256: 192 KB, one)
   static constexpr int STAGES = 3;
   static constexpr int CTAS = D == 256 ? 1 : 2;
-  static constexpr bool QREG = D <= 128;                   // Q fragments in registers
-  static constexpr int RED = 40;                           // floats of a reduction row (32 + pad)
+  static constexpr bool QREG = D * RT <= 128;              // Q fragments in registers
+  static constexpr int RCOLS = D * RT > 128 && D < 256 ? 16 : 32;   // columns merged at a time
+  static constexpr int RED = RCOLS + 8;                    // floats of a reduction row
 };
 
-template <int D>
+template <int D, int RT>
 struct DecodeSmem {
-  using C = DecodeCfg<D>;
+  using C = DecodeCfg<D, RT>;
   alignas(128) uint8_t ring[kWarps][C::STAGES][C::STAGE];
-  alignas(128) uint8_t q[kRows * C::ROW];
+  alignas(128) uint8_t q[C::ROWS * C::ROW];
   float red[kWarps][kRows][C::RED];
-  float ml[kWarps][kRows][2];
+  float ml[kWarps][C::ROWS][2];
   uint32_t vis[kWarps][C::STAGES];
   int warp_sum[kWarps];
   int start_b, start_rem;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
+template <int D, int RT>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using C = DecodeCfg<D>;
+  using C = DecodeCfg<D, RT>;
   constexpr int TILE = C::TILE;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  DecodeSmem<D>& sm = *reinterpret_cast<DecodeSmem<D>*>(smem_raw);
+  DecodeSmem<D, RT>& sm = *reinterpret_cast<DecodeSmem<D, RT>*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int heads = p.pool.h_kv * p.row_tiles;
   launch_dependents();
@@ -337,40 +340,43 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
   int seg0 = ta - cur.tile;      // first tile of the current (sequence, head, row tile)
   if (threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < ta);
   const int g = lane / 4, t4 = lane % 4;
-  float acc[D / 8][4];
-  float m[2], l[2];
-  uint32_t qf[C::QREG ? D / 16 : 1][4];
+  float acc[RT][D / 8][4];
+  float m[RT][2], l[RT][2];
+  uint32_t qf[RT][C::QREG ? D / 16 : 1][4];
   const uint32_t qs = smem_u32(sm.q);
-  auto q_addr = [&](int ks) {
-    const int row = lane & 15;
+  auto q_addr = [&](int t, int ks) {
+    const int row = kRows * t + (lane & 15);
     return qs + row * C::ROW + (((2 * ks + lane / 16) ^ (row & 7)) << 4);
   };
   bool fresh = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const int kvh = cur.hr / p.row_tiles, rt = cur.hr - kvh * p.row_tiles;
-    const int rows = min(kRows, p.group - rt * kRows);
-    const size_t row0 = static_cast<size_t>(cur.b) * p.H + kvh * p.group + rt * kRows;
+    const int rows = min(C::ROWS, p.group - rt * C::ROWS);
+    const size_t row0 = static_cast<size_t>(cur.b) * p.H + kvh * p.group + rt * C::ROWS;
     if (fresh) {
       fresh = false;
       // Q of the group into shared memory (rows past it zero), then registers
-      for (int e = threadIdx.x; e < kRows * (C::ROW / 16); e += kThreads) {
+      for (int e = threadIdx.x; e < C::ROWS * (C::ROW / 16); e += kThreads) {
         const int row = e / (C::ROW / 16), ch = e % (C::ROW / 16);
         uint4 x = make_uint4(0, 0, 0, 0);
         if (row < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + row) * D) + ch);
         *reinterpret_cast<uint4*>(sm.q + row * C::ROW + ((ch ^ (row & 7)) << 4)) = x;
       }
       __syncthreads();
-      if constexpr (C::QREG) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) ldsm_x4(qf[ks], q_addr(ks));
+      for (int t = 0; t < RT; ++t) {
+        if constexpr (C::QREG) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) ldsm_x4(qf[t][ks], q_addr(t, ks));
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.f;
+        m[t][0] = m[t][1] = -INFINITY;
+        l[t][0] = l[t][1] = 0.f;
       }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
     }
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();
@@ -382,86 +388,99 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
       constexpr int NT = C::TOK / 8;                       // 8-token column tiles of S
       // two tiles take two accumulators each, so that four chains of products
       // run beside each other as with four tiles
-      constexpr int CH2 = NT == 2 ? 2 : 1;
-      float x[NT * CH2][4];
+      constexpr int CH2 = NT * RT == 2 ? 2 : 1;
+      float x[RT][NT * CH2][4];
 #pragma unroll
-      for (int n = 0; n < NT * CH2; ++n)
+      for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+        for (int n = 0; n < NT * CH2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][n][e] = 0.f;
       {
         const int row = (lane / 16) * 8 + (lane & 7);
         const uint32_t ka = kb + row * C::ROW;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t af[4];
-          if constexpr (!C::QREG) ldsm_x4(af, q_addr(ks));
-          const uint32_t* a4 = C::QREG ? qf[C::QREG ? ks : 0] : af;
+          uint32_t af[RT][4];
+          if constexpr (!C::QREG) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) ldsm_x4(af[t], q_addr(t, ks));
+          }
           const uint32_t a = ka + (((2 * ks + ((lane / 8) & 1)) ^ (row & 7)) << 4);
 #pragma unroll
           for (int n = 0; n < NT; n += 2) {
             uint32_t bf[4];
             ldsm_x4(bf, a + n * 8 * C::ROW);
             const int o = n + (CH2 == 2 ? NT * (ks & 1) : 0);
-            mma16816(x[o], a4, bf[0], bf[1]);
-            mma16816(x[o + 1], a4, bf[2], bf[3]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              const uint32_t* a4 = C::QREG ? qf[t][C::QREG ? ks : 0] : af[t];
+              mma16816(x[t][o], a4, bf[0], bf[1]);
+              mma16816(x[t][o + 1], a4, bf[2], bf[3]);
+            }
           }
         }
       }
-      if constexpr (CH2 == 2) {
+      uint32_t pf[RT][NT / 2][4];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float (&y)[NT * CH2][4] = x[t];
+        if constexpr (CH2 == 2) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[n][e] += y[NT + n][e];
+        }
+        // rows g (elements 0, 1) and g + 8 (2, 3); columns 8 n + 2 t4 + {0, 1}
+        if (vis != (C::TOK == 32 ? ~0u : 0xffffu)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((vis >> (8 * n + 2 * t4 + (e & 1))) & 1u)) y[n][e] = -INFINITY;
+        }
+        float base[2];             // scale m, subtracted in the exponent
+        bool moved = false;
+        float alpha[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(y[0][2 * r], y[0][2 * r + 1]);
+#pragma unroll
+          for (int n = 1; n < NT; ++n) mx = fmax3(mx, y[n][2 * r], y[n][2 * r + 1]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mx *= p.scale_log2;
+          const float mn = fmaxf(m[t][r], mx);
+          alpha[r] = m[t][r] == -INFINITY ? 0.f : ex2_approx(m[t][r] - mn);
+          moved = moved || mn > m[t][r];
+          m[t][r] = mn;
+          base[r] = mn == -INFINITY ? 0.f : mn;
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          l[t][0] *= alpha[0];
+          l[t][1] *= alpha[1];
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            acc[t][n][0] *= alpha[0];
+            acc[t][n][1] *= alpha[0];
+            acc[t][n][2] *= alpha[1];
+            acc[t][n][3] *= alpha[1];
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[n][e] += x[NT + n][e];
-      }
-      // rows g (elements 0, 1) and g + 8 (2, 3); columns 8 n + 2 t4 + {0, 1}
-      if (vis != (C::TOK == 32 ? ~0u : 0xffffu)) {
+          for (int e = 0; e < 4; ++e) {
+            y[n][e] = ex2_approx(fmaf(y[n][e], p.scale_log2, -base[e / 2]));
+            l[t][e / 2] += y[n][e];
+          }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT / 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!((vis >> (8 * n + 2 * t4 + (e & 1))) & 1u)) x[n][e] = -INFINITY;
+            pf[t][n][e] =
+                pack_bf16x2(y[2 * n + e / 2][2 * (e & 1)], y[2 * n + e / 2][2 * (e & 1) + 1]);
       }
-      float base[2];             // scale m, subtracted in the exponent
-      bool moved = false;
-      float alpha[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
-#pragma unroll
-        for (int n = 1; n < NT; ++n) mx = fmax3(mx, x[n][2 * r], x[n][2 * r + 1]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx *= p.scale_log2;
-        const float mn = fmaxf(m[r], mx);
-        alpha[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
-        moved = moved || mn > m[r];
-        m[r] = mn;
-        base[r] = mn == -INFINITY ? 0.f : mn;
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-        l[0] *= alpha[0];
-        l[1] *= alpha[1];
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          acc[n][0] *= alpha[0];
-          acc[n][1] *= alpha[0];
-          acc[n][2] *= alpha[1];
-          acc[n][3] *= alpha[1];
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[n][e] = ex2_approx(fmaf(x[n][e], p.scale_log2, -base[e / 2]));
-          l[e / 2] += x[n][e];
-        }
-      uint32_t pf[NT / 2][4];
-#pragma unroll
-      for (int n = 0; n < NT / 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pf[n][e] = pack_bf16x2(x[2 * n + e / 2][2 * (e & 1)], x[2 * n + e / 2][2 * (e & 1) + 1]);
       {
         const int row = ((lane / 8) & 1) * 8 + (lane & 7);
         const uint32_t va = kb + C::HALF + row * C::ROW;
@@ -472,8 +491,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
           for (int n = 0; n < NT / 2; ++n) {
             uint32_t bf[4];
             ldsm_x4_t(bf, a + n * 16 * C::ROW);
-            mma16816(acc[2 * j], pf[n], bf[0], bf[1]);
-            mma16816(acc[2 * j + 1], pf[n], bf[2], bf[3]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              mma16816(acc[t][2 * j], pf[t][n], bf[0], bf[1]);
+              mma16816(acc[t][2 * j + 1], pf[t][n], bf[2], bf[3]);
+            }
           }
         }
       }
@@ -486,69 +508,82 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
     }
     // ---- the end of a (sequence, head) or of the share: merge the warps
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t4 == 0) {
-        sm.ml[warp][g + 8 * r][0] = m[r];
-        sm.ml[warp][g + 8 * r][1] = l[r];
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 1);
+        l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 2);
+        if (t4 == 0) {
+          sm.ml[warp][kRows * t + g + 8 * r][0] = m[t][r];
+          sm.ml[warp][kRows * t + g + 8 * r][1] = l[t][r];
+        }
       }
-    }
     const bool whole = seg0 >= ta && ends;
     const int part = 2 * cta + (seg0 < ta ? 0 : 1);
-    const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
-    float w[kWarps], lse2 = 0.f;
+    constexpr int PC = C::RCOLS / 8;           // columns of a thread
+    const int trow = threadIdx.x / 8, col = threadIdx.x % 8 * PC;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+    for (int t = 0; t < RT; ++t) {
+      const int row = kRows * t + trow;
+      float w[kWarps], lse2 = 0.f;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        *reinterpret_cast<float2*>(&sm.red[warp][g][8 * n + 2 * t4]) =
-            make_float2(acc[4 * c + n][0], acc[4 * c + n][1]);
-        *reinterpret_cast<float2*>(&sm.red[warp][g + 8][8 * n + 2 * t4]) =
-            make_float2(acc[4 * c + n][2], acc[4 * c + n][3]);
-      }
-      __syncthreads();
-      if (row < rows) {
-        if (c == 0) {
-          float mx = -INFINITY, sum = 0.f;
+      for (int c = 0; c < D / C::RCOLS; ++c) {
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm.ml[k][row][0]);
+        for (int n = 0; n < C::RCOLS / 8; ++n) {
+          const float* a = acc[t][C::RCOLS / 8 * c + n];
+          *reinterpret_cast<float2*>(&sm.red[warp][g][8 * n + 2 * t4]) = make_float2(a[0], a[1]);
+          *reinterpret_cast<float2*>(&sm.red[warp][g + 8][8 * n + 2 * t4]) =
+              make_float2(a[2], a[3]);
+        }
+        __syncthreads();
+        if (row < rows) {
+          if (c == 0) {
+            float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) {
-            const float mk = sm.ml[k][row][0];
-            w[k] = mk == -INFINITY ? 0.f : ex2_approx(mk - mx);
-            sum += w[k] * sm.ml[k][row][1];
+            for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm.ml[k][row][0]);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+              const float mk = sm.ml[k][row][0];
+              w[k] = mk == -INFINITY ? 0.f : ex2_approx(mk - mx);
+              sum += w[k] * sm.ml[k][row][1];
+            }
+            // a NaN sum (a NaN score) stays one
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) w[k] *= inv;
+            lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
           }
-          // a NaN sum (a NaN score) stays one
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          float y[PC];
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) w[k] *= inv;
-          lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
-        }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int e = 0; e < PC; ++e) y[e] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float4 y = *reinterpret_cast<const float4*>(&sm.red[k][row][col]);
-          x.x = fmaf(w[k], y.x, x.x);
-          x.y = fmaf(w[k], y.y, x.y);
-          x.z = fmaf(w[k], y.z, x.z);
-          x.w = fmaf(w[k], y.w, x.w);
+          for (int k = 0; k < kWarps; ++k)
+#pragma unroll
+            for (int e = 0; e < PC; e += 2) {
+              const float2 z = *reinterpret_cast<const float2*>(&sm.red[k][trow][col + e]);
+              y[e] = fmaf(w[k], z.x, y[e]);
+              y[e + 1] = fmaf(w[k], z.y, y[e + 1]);
+            }
+          const int at = C::RCOLS * c + col;
+          if (whole) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + at);
+#pragma unroll
+            for (int e = 0; e < PC; e += 2) dst[e / 2] = pack_bf16x2(y[e], y[e + 1]);
+          } else {
+            float* dst = p.o_part + (static_cast<size_t>(part) * C::ROWS + row) * D + at;
+#pragma unroll
+            for (int e = 0; e < PC; e += 2)
+              *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
+          }
         }
-        if (whole) {
-          *reinterpret_cast<uint2*>(p.o + (row0 + row) * D + 32 * c + col) =
-              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-        } else {
-          *reinterpret_cast<float4*>(p.o_part + (static_cast<size_t>(part) * kRows + row) * D +
-                                     32 * c + col) = x;
-        }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-    if (row < rows && col == 0) {
-      if (whole)
-        p.lse[row0 + row] = lse2 * 0.69314718055994531f;
-      else
-        p.lse_part[part * kRows + row] = lse2;
+      if (row < rows && col == 0) {
+        if (whole)
+          p.lse[row0 + row] = lse2 * 0.69314718055994531f;
+        else
+          p.lse_part[part * C::ROWS + row] = lse2;
+      }
     }
     if (i + 1 < count) {
       seg0 = ta + i + 1;
@@ -564,10 +599,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D>::CTAS)
 // blockIdx.x + 1 cuts, unless an earlier border cuts it too.
 constexpr int kJoinThreads = 512;             // at least as many as CTAs of the split kernel
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int WARPS = kJoinThreads / 32;
+  constexpr int ROWS = kRows * RT;
   constexpr int PER = D / 32;                 // columns of a lane
   constexpr int AHEAD = D == 256 ? 4 : 8;     // parts whose loads are in flight together
   __shared__ int2 border;
@@ -595,98 +631,102 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int n = ends - c0;       // parts
   const int b = cut.x / heads, hr = cut.x % heads;
   const int kvh = hr / p.row_tiles, rt = hr - kvh * p.row_tiles;
-  const int rows = min(kRows, p.group - rt * kRows);
-  const size_t row0 = static_cast<size_t>(b) * p.H + kvh * p.group + rt * kRows;
-  // a warp takes a row, or with fewer rows than warps every k-th part of one
+  const int rows = min(ROWS, p.group - rt * ROWS);
+  const size_t row0 = static_cast<size_t>(b) * p.H + kvh * p.group + rt * ROWS;
+  // a warp takes a row (and with more rows than warps another), or with fewer
+  // rows than warps every k-th part of one
   const int k = rows > 8 ? 1 : (rows > 4 ? 2 : (rows > 2 ? 4 : (rows == 2 ? 8 : 16)));
-  const int row = warp / k, sub = warp % k;
-  float mx = -INFINITY, sum = 0.f, acc[PER];
+  const int sub = warp % k;
+  for (int at = 0; at < (RT == 1 ? 1 : rows); at += WARPS) {   // k = 1 where it goes round
+    const int row = at + warp / k;
+    float mx = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  if (row < rows) {
-    auto slot = [&](int i) {
-      return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
-    };
-    for (int i0 = sub; i0 < n; i0 += AHEAD * k) {
-      float lse[AHEAD], x[AHEAD][PER];
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    if (row < rows) {
+      auto slot = [&](int i) {
+        return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * ROWS + row;
+      };
+      for (int i0 = sub; i0 < n; i0 += AHEAD * k) {
+        float lse[AHEAD], x[AHEAD][PER];
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int i = i0 + u * k;
-        lse[u] = -INFINITY;
-        if (i < n) {
-          lse[u] = p.lse_part[slot(i)];
-          const float* src = p.o_part + slot(i) * D + lane * PER;
+        for (int u = 0; u < AHEAD; ++u) {
+          const int i = i0 + u * k;
+          lse[u] = -INFINITY;
+          if (i < n) {
+            lse[u] = p.lse_part[slot(i)];
+            const float* src = p.o_part + slot(i) * D + lane * PER;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) x[u][e] = src[e];
+            for (int e = 0; e < PER; ++e) x[u][e] = src[e];
+          }
+        }
+        float m = mx;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) m = fmaxf(m, lse[u]);
+        const float base = m == -INFINITY ? 0.f : m;
+        const float alpha = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
+        mx = m;
+        sum *= alpha;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] *= alpha;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          if (i0 + u * k < n) {
+            const float w = ex2_approx(lse[u] - base);
+            sum += w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
+          }
         }
       }
-      float m = mx;
+    }
+    if (k > 1) {
+      if (lane == 0) {
+        w_max[warp] = mx;
+        w_sum[warp] = sum;
+      }
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) m = fmaxf(m, lse[u]);
-      const float base = m == -INFINITY ? 0.f : m;
-      const float alpha = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
-      mx = m;
-      sum *= alpha;
+      for (int e = 0; e < PER; ++e) w_acc[warp][lane * PER + e] = acc[e];
+      __syncthreads();
+      if (sub == 0) {
+        float m = mx;
+        for (int o = 1; o < k; ++o) m = fmaxf(m, w_max[warp + o]);
+        const float base = m == -INFINITY ? 0.f : m;
+        const float a0 = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
+        mx = m;
+        sum *= a0;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] *= alpha;
+        for (int e = 0; e < PER; ++e) acc[e] *= a0;
+        for (int o = 1; o < k; ++o) {
+          const float mo = w_max[warp + o];
+          const float a = mo == -INFINITY ? 0.f : ex2_approx(mo - base);
+          sum = fmaf(a, w_sum[warp + o], sum);
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        if (i0 + u * k < n) {
-          const float w = ex2_approx(lse[u] - base);
-          sum += w;
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
+          for (int e = 0; e < PER; ++e) acc[e] = fmaf(a, w_acc[warp + o][lane * PER + e], acc[e]);
         }
       }
     }
-  }
-  if (k > 1) {
-    if (lane == 0) {
-      w_max[warp] = mx;
-      w_sum[warp] = sum;
+    if (sub == 0 && row < rows) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + lane * PER);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0)
+        p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
     }
-#pragma unroll
-    for (int e = 0; e < PER; ++e) w_acc[warp][lane * PER + e] = acc[e];
-    __syncthreads();
-    if (sub == 0) {
-      float m = mx;
-      for (int o = 1; o < k; ++o) m = fmaxf(m, w_max[warp + o]);
-      const float base = m == -INFINITY ? 0.f : m;
-      const float a0 = mx == -INFINITY ? 0.f : ex2_approx(mx - base);
-      mx = m;
-      sum *= a0;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] *= a0;
-      for (int o = 1; o < k; ++o) {
-        const float mo = w_max[warp + o];
-        const float a = mo == -INFINITY ? 0.f : ex2_approx(mo - base);
-        sum = fmaf(a, w_sum[warp + o], sum);
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(a, w_acc[warp + o][lane * PER + e], acc[e]);
-      }
-    }
-  }
-  if (sub == 0 && row < rows) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + lane * PER);
-#pragma unroll
-    for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0)
-      p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
   }
 }
 
-template <int D>
+template <int D, int RT>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
-  constexpr int smem = sizeof(DecodeSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D>,
+  constexpr int smem = sizeof(DecodeSmem<D, RT>);
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D><<<p.parts, kThreads, smem, stream>>>(p);
+  paged_decode_kernel<D, RT><<<p.parts, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.parts < 2) return cudaSuccess;        // nothing is cut
-  return launch_dependent(paged_join_kernel<D>, dim3(p.parts - 1), kJoinThreads, stream, p);
+  return launch_dependent(paged_join_kernel<D, RT>, dim3(p.parts - 1), kJoinThreads, stream, p);
 }
 
 // CTAs of the split kernel: as many as are resident at once.
@@ -694,10 +734,20 @@ int decode_parts(int d, int num_sms) {
   const int n = num_sms * (d == 256 ? DecodeCfg<256>::CTAS : DecodeCfg<128>::CTAS);
   return n < kJoinThreads ? n : kJoinThreads;
 }
-static_assert(DecodeCfg<64>::CTAS == DecodeCfg<128>::CTAS, "decode_parts");
+static_assert(DecodeCfg<64>::CTAS == DecodeCfg<128>::CTAS &&
+                  2 * (sizeof(DecodeSmem<128, 2>) + 1024) <= 233472 &&
+                  2 * (sizeof(DecodeSmem<64, 2>) + 1024) <= 233472,
+              "decode_parts");
 
-size_t part_floats(int d, int num_sms) {
-  return static_cast<size_t>(2) * decode_parts(d, num_sms) * kRows;
+// 16-row tiles that a CTA takes from one pass over K and V: two where a group
+// has more than 16 heads, since a pass that reads K and V out of L2 takes its
+// time too (64 rows of 8192 tokens, h_kv = 1, one tile / two: 32 heads, d =
+// 128 89 / 64 us, d = 64 42 / 37; 64 heads 163 / 105, 70 / 56), and one at d =
+// 256, where two tiles of O are more than the registers.
+int decode_tiles(int d, int group) { return group > kRows && d < 256 ? 2 : 1; }
+
+size_t part_floats(int d, int group, int num_sms) {
+  return static_cast<size_t>(2) * decode_parts(d, num_sms) * kRows * decode_tiles(d, group);
 }
 
 // New tokens into pages: a thread copies 16 bytes of K and of V.  Bound by
@@ -743,7 +793,7 @@ size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d) {
   if (H < 1 || h_kv < 1 || H % h_kv || (d != 64 && d != 128 && d != 256)) return 0;
   int sms = 0;
   if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
-  const size_t rows = fa::part_floats(d, sms);
+  const size_t rows = fa::part_floats(d, H / h_kv, sms);
   return rows * d * sizeof(float) + (rows * sizeof(float) + 255) / 256 * 256 +
          (fa::decode_parts(d, sms) * sizeof(int2) + 255) / 256 * 256;
 }
@@ -763,7 +813,8 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   if (B < 1 || H < 1 || H % p.pool.h_kv || window_left < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f && scale <= 3.402823466e38f)) return FA_ERR_INVALID_ARG;
   p.group = H / p.pool.h_kv;
-  p.row_tiles = (p.group + fa::kRows - 1) / fa::kRows;
+  const int rt = fa::decode_tiles(p.pool.d, p.group);
+  p.row_tiles = (p.group + fa::kRows * rt - 1) / (fa::kRows * rt);
   p.max_len = max_pages * p.pool.page_size;
   const long long heads = static_cast<long long>(p.pool.h_kv) * p.row_tiles;
   const int tile = p.pool.d == 64 ? fa::DecodeCfg<64>::TILE : fa::DecodeCfg<128>::TILE;
@@ -790,16 +841,18 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   const int most = fa::decode_parts(p.pool.d, sms);
   p.parts = B * heads * tiles < most ? static_cast<int>(B * heads * tiles) : most;
   p.o_part = static_cast<float*>(workspace);
-  const size_t rows = fa::part_floats(p.pool.d, sms);
+  const size_t rows = fa::part_floats(p.pool.d, p.group, sms);
   p.lse_part = p.o_part + rows * p.pool.d;
   p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.lse_part) +
                                    (rows * sizeof(float) + 255) / 256 * 256);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (p.pool.d) {
-    case 64: e = fa::launch_decode_t<64>(p, s); break;
-    case 128: e = fa::launch_decode_t<128>(p, s); break;
-    default: e = fa::launch_decode_t<256>(p, s); break;
+    case 64: e = rt == 2 ? fa::launch_decode_t<64, 2>(p, s) : fa::launch_decode_t<64, 1>(p, s); break;
+    case 128:
+      e = rt == 2 ? fa::launch_decode_t<128, 2>(p, s) : fa::launch_decode_t<128, 1>(p, s);
+      break;
+    default: e = fa::launch_decode_t<256, 1>(p, s); break;
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -44,6 +44,9 @@ DECODE = [
     (4, 4, 256, 48, "hnd", [500, 47, 48, 49], None, 0),
     (7, 1, 64, 16, "padded", [300, 16], None, 0),          # seven heads a group
     (40, 2, 128, 32, "hnd", [515, 90], None, 0),           # more than 16 heads a group
+    (33, 1, 128, 16, "hnd", [700, 1, 64], None, 0),        # a second pass for one head
+    (64, 1, 64, 24, "nhd", [3000, 129, 0], (500, 0), 7),   # 64 heads share one K/V head
+    (34, 2, 256, 16, "hnd", [200, 65], None, 0),           # a pass a 16 heads
     (64, 1, 256, 100, "nhd", [1203, 100, 101], None, 0),
     (8, 8, 64, 16, "nhd", [2000, 100, 71, 70, 69], (69, 0), 4),
     (6, 3, 128, 24, "hnd", [1500, 64, 200, 1], (100, 0), 130),
