@@ -168,9 +168,10 @@ __device__ __forceinline__ void step_range(const BwdParams& p, int n, int len, i
 // first) and 2c + 1 for the one that starts at it (CTA c's last), and
 // bwd_sinks_post_kernel adds them in the CTAs' order.  All of it is a
 // function of the sizes and kv_len.  H = 16, h_kv = 4, N = 16384, d = 128,
-// window 2047, 4 sinks: 700 us; whole items, the sinks' far queries as items
-// of their own, 789; all items end to end 1012 (each CTA elsewhere in the
-// sequence: the dQ accumulator falls out of L2).
+// window 2047, 4 sinks: 694 us (700 when it was compared with whole items, the
+// sinks' far queries as items of their own, 789, and with all items end to
+// end, 1012: each CTA elsewhere in the sequence, and the dQ accumulator falls
+// out of L2).
 struct SkPlan {
   int whole;                    // the round-robin items are 0 .. whole - 1
   int j;                        // this CTA's first pool item

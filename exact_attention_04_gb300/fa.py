@@ -357,13 +357,24 @@ def fa_bwd_v(q, k, v, o, do, lse, dq, dk, dv, scale, causal=False, kv_len=None, 
     _raise(st, "fa_bwd_v")
 
 
+def int32_count(x) -> int:
+    """A number of tokens as a C int: one past every position stays that, one
+    below -1 stays refused."""
+    x = int(x)
+    return x if -2 < x < 0x7fffffff else (0x7fffffff if x > 0 else -2)
+
+
+def _sinks_variant(q, k, window):
+    return _variant(q, k, None if window is None else [int32_count(w) for w in window])
+
+
 def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, window=None,
                  stream=None):
     """Calls fa_fwd_sinks: fa_fwd_v with the first `sinks` tokens visible left
     of the window."""
     _check_qkv("q", q)
     B, H, N, d = q.shape
-    var = _variant(q, k, window)
+    var = _sinks_variant(q, k, window)
     _check_qkv("k", k, k.shape)
     _check_qkv("v", v, k.shape)
     _check_qkv("o", o, q.shape)
@@ -373,7 +384,7 @@ def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, windo
     kv_len = _check_kv_len(kv_len, B)
     st = load().fa_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d,
                              float(scale), int(bool(causal)), _ptr(kv_len), ctypes.byref(var),
-                             int(sinks), _stream_ptr(stream))
+                             int32_count(sinks), _stream_ptr(stream))
     _raise(st, "fa_fwd_sinks")
 
 
@@ -386,7 +397,7 @@ def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv
     """Calls fa_bwd_sinks; workspace of fa_bwd_sinks_workspace_bytes()."""
     _check_qkv("q", q)
     B, H, N, d = q.shape
-    var = _variant(q, k, window)
+    var = _sinks_variant(q, k, window)
     for name, t in (("o", o), ("do", do), ("dq", dq)):
         _check_qkv(name, t, q.shape)
     for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
@@ -398,7 +409,7 @@ def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv
     wp, wn = _ws(workspace)
     st = load().fa_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                              _ptr(dk), _ptr(dv), B, H, N, d, float(scale), int(bool(causal)),
-                             _ptr(kv_len), ctypes.byref(var), int(sinks), wp, wn,
+                             _ptr(kv_len), ctypes.byref(var), int32_count(sinks), wp, wn,
                              _stream_ptr(stream))
     _raise(st, "fa_bwd_sinks")
 

@@ -30,6 +30,7 @@ _current_device = torch.cuda.current_device
 # takes 3 us of the about 15 that a small call costs its host
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
 _int32, _bf16 = torch.int32, torch.bfloat16
+_count = fa.int32_count
 
 
 def _on_stream(call, stream, *args, **kw):
@@ -160,8 +161,8 @@ def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=
     ws, wp = _bytes(ws, need, q)
     _check(fa.load().fa_decode_paged(
         q.data_ptr(), cache.ref, layer, tp, max_pages, lp, o.data_ptr(), lse.data_ptr(), rows, H,
-        cache.scale if scale is None else scale, -1 if window is None else int(window[0]), sinks,
-        wp, need, _current_raw_stream(index)), "fa_decode_paged")
+        cache.scale if scale is None else scale, -1 if window is None else _count(window[0]),
+        _count(sinks), wp, need, _current_raw_stream(index)), "fa_decode_paged")
     return o, lse
 
 
@@ -247,8 +248,9 @@ def trim(cache, table, kv_len, ref, window_left, sinks=0, stream=None):
     rp = _ints("ref", ref, (num_pages,), index)
     table_out, ref_out = torch.empty_like(table), torch.empty_like(ref)
     _check(fa.load().fa_pages_trim(
-        tp, max_pages, cache.page_size, lp, rp, num_pages, rows, window_left, sinks,
-        table_out.data_ptr(), ref_out.data_ptr(), _current_raw_stream(index)), "fa_pages_trim")
+        tp, max_pages, cache.page_size, lp, rp, num_pages, rows, _count(window_left),
+        _count(sinks), table_out.data_ptr(), ref_out.data_ptr(), _current_raw_stream(index)),
+        "fa_pages_trim")
     return table_out, ref_out
 
 

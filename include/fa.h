@@ -335,11 +335,13 @@ fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged
  * Of a row only the first ceil(kv_len / page_size) entries count, kv_len
  * clamped to [0, max_pages * page_size]; an entry outside [0, num_pages) is no
  * page.  Fresh pages are always the free pages of lowest number, handed out
- * in the order of rows (within a row, of positions).  info: int32[2], written
- * by the call.  workspace: fa_pages_workspace_bytes(num_pages, rows) bytes
- * (rows: the larger of a call's row counts; 0 for invalid sizes), 256-byte
- * aligned, its contents irrelevant on entry; calls that may overlap on the
- * GPU need one each.
+ * in the order of rows (within a row, of positions).  No call shortens a row:
+ * pages behind a kv_len that the caller lowers keep their references, and a
+ * full page may be shared, so write into one again only where its ref is 1.
+ * info: int32[2], written by the call.  workspace:
+ * fa_pages_workspace_bytes(num_pages, rows) bytes (rows: the larger of a
+ * call's row counts; 0 for invalid sizes), 256-byte aligned, its contents
+ * irrelevant on entry; calls that may overlap on the GPU need one each.
  */
 size_t fa_pages_workspace_bytes(int num_pages, int rows);
 

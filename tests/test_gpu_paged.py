@@ -469,3 +469,104 @@ def test_calls_on_a_given_stream():
     s.synchronize()
     for a, b in zip(here, there):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,most,page", [(5, 9, 4), (700, 24, 3)])
+def test_metadata_in_place(rows, most, page):
+    """reserve, trim and compact with the outputs that may be the inputs."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, (most - 3) * page, rows)
+    pages = rows * most
+    table, kv_len, ref = R.random_cache(rng, rows, most, page, pages, lens, 0.3)
+    n_new = rng.integers(0, 3 * page, rows)
+    k, v = pools(1, pages, 1, page, 64, 3)
+    cache = paged.PagedKV(k, v)
+    table, kv_len, ref, n_new = cuda(table, kv_len, ref, n_new)
+    ws, info = paged.workspace(cache, rows), torch.zeros(2, dtype=torch.int32, device="cuda")
+    lib = fa.load()
+
+    def ptr(*tensors):
+        return [t.data_ptr() for t in tensors]
+    t1 = table.clone()
+    want = paged.reserve(cache, t1, kv_len, ref, n_new)
+    assert lib.fa_pages_reserve(*ptr(table), most, page, *ptr(kv_len, n_new, ref), pages, rows,
+                                *ptr(kv_len, ref, info, ws), ws.numel(), None) == fa.FA_OK
+    assert all(torch.equal(a, b) for a, b in zip((table, kv_len, ref, info), (t1, *want)))
+    want = paged.trim(cache, table, kv_len, ref, 2 * page, 1)
+    assert lib.fa_pages_trim(*ptr(table), most, page, *ptr(kv_len, ref), pages, rows, 2 * page, 1,
+                             *ptr(table, ref), None) == fa.FA_OK
+    assert torch.equal(table, want[0]) and torch.equal(ref, want[1])
+    k2, v2 = k.clone(), v.clone()
+    want = paged.compact(paged.PagedKV(k2, v2), table, ref)
+    assert lib.fa_pages_compact(cache.ref, *ptr(table), most, *ptr(ref), rows,
+                                *ptr(table, ref, info, ws), ws.numel(), None) == fa.FA_OK
+    assert all(torch.equal(a, b) for a, b in zip((table, ref, info), want))
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+def test_captured_maintenance():
+    """fork, trim and compact captured once and replayed over other contents."""
+    rows, most, page, pages = 6, 10, 8, 90
+    k, v = pools(2, pages, 2, page, 64, 4)
+    cache = paged.PagedKV(k, v)
+    table, kv_len, ref = cache.empty(rows, most)
+    parent = torch.zeros(rows, dtype=torch.int32, device="cuda")
+
+    def step(c):
+        t, n, r, info = paged.fork(c, table, kv_len, ref, parent)
+        t, r = paged.trim(c, t, n, r, 19, 2)
+        return (n, info) + paged.compact(c, t, r)
+    step(cache)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(cache)
+    for seed in range(5):
+        rng = np.random.default_rng(seed)
+        lens = rng.integers(0, most * page + 1, rows)
+        for t, x in zip((table, kv_len, ref),
+                        R.random_cache(rng, rows, most, page, pages, lens, 0.3)):
+            t.copy_(torch.as_tensor(x))
+        parent.copy_(torch.as_tensor(rng.integers(-1, rows, rows).astype(np.int32)))
+        x = torch.randn(k.shape, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+        k.copy_(x)
+        v.copy_(-x)
+        k2, v2 = k.clone(), v.clone()
+        want = step(paged.PagedKV(k2, v2))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+def test_two_calls_at_once():
+    """Decoding two caches on two streams, each call with a workspace of its
+    own, gives what it gives alone."""
+    args = []
+    for seed, (H, d) in enumerate(((32, 128), (40, 64))):
+        k, v = pools(1, 600, 1, 16, d, seed)
+        table = torch.randperm(600, generator=torch.Generator().manual_seed(seed))
+        table = table.to(torch.int32).cuda().view(6, 100)
+        kv_len, = cuda([1600, 3, 0, 911, 1599, 64])
+        q = torch.randn(6, H, 1, d, device="cuda").to(torch.bfloat16)
+        args.append((q, paged.PagedKV(k, v), 0, table, kv_len))
+    alone = [paged.decode(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    both = [paged.decode(*a, stream=s) for _ in range(50) for a, s in zip(args, streams)]
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(both):
+        assert torch.equal(o, alone[i % 2][0]) and torch.equal(lse, alone[i % 2][1])
+
+
+def test_a_window_past_32_bits():
+    """A window or sinks beyond every position are none, however large."""
+    k, v = pools(1, 8, 1, 16, 64, 5)
+    cache = paged.PagedKV(k, v)
+    table, kv_len, ref = cuda([[3, 1, 2, 7]], [60], [0, 1, 1, 1, 0, 0, 0, 1])
+    q = torch.randn(1, 2, 1, 64, device="cuda").to(torch.bfloat16)
+    want = paged.decode(q, cache, 0, table, kv_len)
+    for window, sinks in (((1 << 32, 0), 0), ((3, 0), 1 << 32), ((1 << 40, 0), 1 << 40)):
+        got = paged.decode(q, cache, 0, table, kv_len, window=window, sinks=sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for window, sinks in ((1 << 32, 0), (3, 1 << 32)):
+        t2, r2 = paged.trim(cache, table, kv_len, ref, window, sinks)
+        assert torch.equal(t2, table) and torch.equal(r2, ref)

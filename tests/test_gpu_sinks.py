@@ -198,3 +198,37 @@ def test_sinks_past_the_sequence():
     x = inputs(1, 2, 1, 200, 64, 14, (150,))
     kw = dict(causal=True, window=(10, 0), sinks=(1 << 31) - 1)
     compare(x, run(x, **kw), **kw)
+
+
+def test_sinks_past_32_bits():
+    q, k, v, do = (torch.randn(1, 2, 200, 64, device="cuda").to(torch.bfloat16) for _ in range(4))
+    kw = dict(causal=True, window=(20, 0))
+    o, lse = fa.forward(q, k, v, sinks=200, **kw)
+    o2, lse2 = fa.forward(q, k, v, sinks=1 << 32, **kw)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    o2, lse2 = fa.forward(q, k, v, causal=True, window=((1 << 32) + 20, 0), sinks=4)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    a = fa.backward(q, k, v, o, lse, do, sinks=200, **kw)
+    b = fa.backward(q, k, v, o, lse, do, sinks=1 << 32, **kw)
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+
+
+def test_two_backwards_at_once():
+    """On two streams, each with a workspace of its own: dK and dV as alone."""
+    args = []
+    for seed, (B, H, h_kv, N, d) in enumerate(((2, 8, 2, 1500, 128), (2, 8, 8, 1900, 64))):
+        torch.manual_seed(seed)
+        q, k, v, do = (torch.randn(B, h, N, d, device="cuda").to(torch.bfloat16)
+                       for h in (H, h_kv, h_kv, H))
+        kw = dict(causal=True, window=(200, 0), sinks=5)
+        o, lse = fa.forward(q, k, v, **kw)
+        args.append(((q, k, v, o, lse, do), kw))
+    alone = [fa.backward(*a, **kw) for a, kw in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    both = [fa.backward(*a, stream=s, **kw) for _ in range(10)
+            for (a, kw), s in zip(args, streams)]
+    torch.cuda.synchronize()
+    fa.fa_check()
+    for i, grads in enumerate(both):
+        assert torch.equal(grads[1], alone[i % 2][1]) and torch.equal(grads[2], alone[i % 2][2])
