@@ -26,8 +26,12 @@
 // that it begins and does not end), and a second kernel, a block per border
 // between two shares, joins them,
 //   LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i,
-// in the order of the CTAs.  Loads run ahead across the boundary between two
-// heads or sequences.
+// in the order of the CTAs; the blocks of an item that several borders cut
+// share its rows (one row of 16000 tokens, h_kv = 1, H = 8: 32.5 -> 11.7 us
+// against one block for all).  Loads run ahead across the boundary between two
+// heads or sequences.  Calls with few tiles take a cluster of eight CTAs for
+// each (sequence, head) instead, which joins its parts through shared memory
+// (use_clusters).
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -47,6 +51,7 @@ using namespace ptx;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;                         // rows of the mma: query heads
+constexpr int kCluster = 8;                       // CTAs of a cluster
 
 struct DecodeParams {
   PagePool pool;
@@ -205,7 +210,34 @@ struct DecodeSmem {
   int start_b, start_rem;
 };
 
-template <int D, int RT>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Shared address a of this CTA in CTA `rank` of its cluster, and loads there.
+__device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t a) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
+// CL: a cluster of CTAs takes each (sequence, head, row tile), an eighth of
+// its tiles a CTA, and joins the parts through its shared memory.
+template <int D, int RT, bool CL>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = DecodeCfg<D, RT>;
@@ -214,16 +246,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
   DecodeSmem<D, RT>& sm = *reinterpret_cast<DecodeSmem<D, RT>*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int heads = p.pool.h_kv * p.row_tiles;
-  launch_dependents();
-
-  // ---- this CTA's share of the tiles
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
-  int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += span_of<TILE>(p, b).tiles;
-  int before;
-  const int total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
-  const int parts = min(p.parts, total);
+  Cursor next;
+  int ta = 0, count;             // the share's first tile in the order of tiles, and its tiles
   const int cta = blockIdx.x;
   // sequences without a tile: O = 0, LSE = -inf
   auto write_empty = [&]() {
@@ -235,29 +259,47 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
       for (int h = threadIdx.x; h < p.H; h += kThreads) p.lse[row0 + h] = -INFINITY;
     }
   };
-  if (cta >= parts) {
-    if (threadIdx.x == 0) p.meta[cta] = make_int2(-1, 0);
-    write_empty();
-    return;
-  }
-  const int ta = static_cast<int>(static_cast<long long>(cta) * total / parts);
-  const int tb = static_cast<int>(static_cast<long long>(cta + 1) * total / parts);
-  if (ta >= before * heads && ta < (before + mine) * heads) {
-    int b = b_lo, base = before * heads;
-    for (;; ++b) {
-      const int n = span_of<TILE>(p, b).tiles * heads;
-      if (ta < base + n) break;
-      base += n;
+  if constexpr (CL) {
+    const int item = cta / kCluster, rank = cta % kCluster;
+    next.b = item / heads;
+    next.hr = item - next.b * heads;
+    next.s = span_of<TILE>(p, next.b);
+    next.tile = next.s.tiles * rank / kCluster;
+    count = next.s.tiles * (rank + 1) / kCluster - next.tile;
+  } else {
+    launch_dependents();
+    // ---- this CTA's share of the tiles
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += span_of<TILE>(p, b).tiles;
+    int before;
+    const int total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
+    const int parts = min(p.parts, total);
+    if (cta >= parts) {
+      if (threadIdx.x == 0) p.meta[cta] = make_int2(-1, 0);
+      write_empty();
+      return;
     }
-    sm.start_b = b;
-    sm.start_rem = ta - base;
+    ta = static_cast<int>(static_cast<long long>(cta) * total / parts);
+    const int tb = static_cast<int>(static_cast<long long>(cta + 1) * total / parts);
+    if (ta >= before * heads && ta < (before + mine) * heads) {
+      int b = b_lo, base = before * heads;
+      for (;; ++b) {
+        const int n = span_of<TILE>(p, b).tiles * heads;
+        if (ta < base + n) break;
+        base += n;
+      }
+      sm.start_b = b;
+      sm.start_rem = ta - base;
+    }
+    __syncthreads();
+    count = tb - ta;
+    cursor_at<TILE>(p, sm.start_b, sm.start_rem, next);
   }
-  __syncthreads();
-  const int count = tb - ta;
+  Cursor cur = next;
 
   // ---- the loading side: one tile ahead, the page of this lane's token
-  Cursor next;
-  cursor_at<TILE>(p, sm.start_b, sm.start_rem, next);
   const int tok = lane % C::TOK;
   int page = -1;                 // page number of the prefetched token
   long long part_off = 0;        // its slot's and head's offset
@@ -335,10 +377,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
   for (int i = 0; i < C::STAGES - 1; ++i) issue();
 
   // ---- the computing side
-  Cursor cur;
-  cursor_at<TILE>(p, sm.start_b, sm.start_rem, cur);
   int seg0 = ta - cur.tile;      // first tile of the current (sequence, head, row tile)
-  if (threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < ta);
+  if (!CL && threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < ta);
   const int g = lane / 4, t4 = lane % 4;
   float acc[RT][D / 8][4];
   float m[RT][2], l[RT][2];
@@ -348,6 +388,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
     const int row = kRows * t + (lane & 15);
     return qs + row * C::ROW + (((2 * ks + lane / 16) ^ (row & 7)) << 4);
   };
+  // CL: this CTA's part, where warp 0's ring was (the merge's first barrier
+  // is behind the last read of it, and no load is on its way)
+  float* const o_smem = reinterpret_cast<float*>(sm.ring[0][0]);
+  float* const lse_smem = o_smem + C::ROWS * D;
+  static_assert((C::ROWS * D + C::ROWS) * 4 <= C::STAGES * C::STAGE, "the part fits the ring");
   bool fresh = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
@@ -518,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
           sm.ml[warp][kRows * t + g + 8 * r][1] = l[t][r];
         }
       }
-    const bool whole = seg0 >= ta && ends;
+    const bool whole = !CL && seg0 >= ta && ends;
     const int part = 2 * cta + (seg0 < ta ? 0 : 1);
     constexpr int PC = C::RCOLS / 8;           // columns of a thread
     const int trow = threadIdx.x / 8, col = threadIdx.x % 8 * PC;
@@ -570,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
 #pragma unroll
             for (int e = 0; e < PC; e += 2) dst[e / 2] = pack_bf16x2(y[e], y[e + 1]);
           } else {
-            float* dst = p.o_part + (static_cast<size_t>(part) * C::ROWS + row) * D + at;
+            float* dst = CL ? o_smem + row * D + at
+                            : p.o_part + (static_cast<size_t>(part) * C::ROWS + row) * D + at;
 #pragma unroll
             for (int e = 0; e < PC; e += 2)
               *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
@@ -582,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
         if (whole)
           p.lse[row0 + row] = lse2 * 0.69314718055994531f;
         else
-          p.lse_part[part * C::ROWS + row] = lse2;
+          (CL ? lse_smem + row : p.lse_part + part * C::ROWS + row)[0] = lse2;
       }
     }
     if (i + 1 < count) {
@@ -592,11 +638,54 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
     }
   }
   cp_async_wait<0>();
-  write_empty();
+  if constexpr (CL) {
+    if (count == 0 && threadIdx.x < C::ROWS) lse_smem[threadIdx.x] = -INFINITY;
+    cluster_sync();
+    const int rank = cta % kCluster;
+    const int kvh = cur.hr / p.row_tiles, rt = cur.hr - kvh * p.row_tiles;
+    const int rows = min(C::ROWS, p.group - rt * C::ROWS);
+    const size_t row0 = static_cast<size_t>(cur.b) * p.H + kvh * p.group + rt * C::ROWS;
+    const uint32_t o_at = smem_u32(o_smem), lse_at = smem_u32(lse_smem);
+    for (int e = rank * kThreads + threadIdx.x; e < rows * (D / 4); e += kCluster * kThreads) {
+      const int row = e / (D / 4), col = e % (D / 4) * 4;
+      float lse[kCluster], mx = -INFINITY;
+      float4 x[kCluster];
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        lse[c] = cluster_load(in_cta(lse_at + row * 4, c));
+        x[c] = cluster_load4(in_cta(o_at + (row * D + col) * 4, c));
+      }
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) mx = fmaxf(mx, lse[c]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        if (lse[c] == -INFINITY) continue;      // (of a part without a tile, O was never written)
+        const float w = ex2_approx(lse[c] - base);
+        sum += w;
+        y.x = fmaf(w, x[c].x, y.x);
+        y.y = fmaf(w, x[c].y, y.y);
+        y.z = fmaf(w, x[c].z, y.z);
+        y.w = fmaf(w, x[c].w, y.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2*>(p.o + (row0 + row) * D + col) =
+          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+      if (col == 0)
+        p.lse[row0 + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    }
+    __syncwarp();
+    cluster_sync();              // no CTA leaves while its part is read
+  } else {
+    write_empty();
+  }
 }
 
 // Joins the parts of the (sequence, head, row tile) that the border before CTA
-// blockIdx.x + 1 cuts, unless an earlier border cuts it too.
+// blockIdx.x + 1 cuts; where several borders cut it, their blocks share its
+// rows.
 constexpr int kJoinThreads = 512;             // at least as many as CTAs of the split kernel
 
 template <int D, int RT>
@@ -606,39 +695,41 @@ __global__ void __launch_bounds__(kJoinThreads)
   constexpr int ROWS = kRows * RT;
   constexpr int PER = D / 32;                 // columns of a lane
   constexpr int AHEAD = D == 256 ? 4 : 8;     // parts whose loads are in flight together
-  __shared__ int2 border;
-  __shared__ int ends;
+  __shared__ int first, last;    // the borders that cut it
   __shared__ float w_max[WARPS], w_sum[WARPS];
   __shared__ float w_acc[WARPS][D];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int heads = p.pool.h_kv * p.row_tiles;
-  const int c0 = blockIdx.x;     // the CTA of the first part
+  const int c = blockIdx.x + 1;
   grid_dependency_wait();
-  // thread t looks at the border before CTA c0 + 1 + t (the launch keeps parts
-  // below the threads)
-  const int c = c0 + 1 + threadIdx.x;
-  const int2 x = c < p.parts ? p.meta[c] : make_int2(-1, 0);
-  const int2 last = p.meta[c0];
-  if (threadIdx.x == 0) {
-    border = x;
-    ends = p.parts;
+  const int2 cut = p.meta[c];
+  if (!cut.y) return;
+  if (threadIdx.x == 0) first = last = c;
+  __syncthreads();
+  if (threadIdx.x < p.parts) {   // the launch keeps parts at or below the threads
+    const int2 x = p.meta[threadIdx.x];
+    if (x.y && x.x == cut.x) {
+      atomicMin(&first, threadIdx.x);
+      atomicMax(&last, threadIdx.x);
+    }
   }
   __syncthreads();
-  const int2 cut = border;
-  if (!cut.y || (last.y && last.x == cut.x)) return;
-  if (!x.y || x.x != cut.x) atomicMin(&ends, c);     // the first CTA that does not go on with it
-  __syncthreads();
-  const int n = ends - c0;       // parts
+  const int c0 = first - 1;      // the CTA of the first part
+  const int blocks = last - c0, n = blocks + 1;   // parts
   const int b = cut.x / heads, hr = cut.x % heads;
   const int kvh = hr / p.row_tiles, rt = hr - kvh * p.row_tiles;
   const int rows = min(ROWS, p.group - rt * ROWS);
   const size_t row0 = static_cast<size_t>(b) * p.H + kvh * p.group + rt * ROWS;
+  // this block's rows: from `row_lo` every `blocks`-th
+  const int row_lo = c - first;
+  if (row_lo >= rows) return;
+  const int own = (rows - row_lo + blocks - 1) / blocks;
   // a warp takes a row (and with more rows than warps another), or with fewer
   // rows than warps every k-th part of one
-  const int k = rows > 8 ? 1 : (rows > 4 ? 2 : (rows > 2 ? 4 : (rows == 2 ? 8 : 16)));
+  const int k = own > 8 ? 1 : (own > 4 ? 2 : (own > 2 ? 4 : (own == 2 ? 8 : 16)));
   const int sub = warp % k;
-  for (int at = 0; at < (RT == 1 ? 1 : rows); at += WARPS) {   // k = 1 where it goes round
-    const int row = at + warp / k;
+  for (int at = 0; at < (RT == 1 ? 1 : own); at += WARPS) {   // k = 1 where it goes round
+    const int row = row_lo + (at + warp / k) * blocks;
     float mx = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -717,12 +808,26 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int D, int RT>
-cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_decode_t(const DecodeParams& p, bool clusters, cudaStream_t stream) {
   constexpr int smem = sizeof(DecodeSmem<D, RT>);
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, RT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto kernel = clusters ? paged_decode_kernel<D, RT, true> : paged_decode_kernel<D, RT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, RT><<<p.parts, kThreads, smem, stream>>>(p);
+  if (clusters) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.B * p.pool.h_kv * p.row_tiles * kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
+  kernel<<<p.parts, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.parts < 2) return cudaSuccess;        // nothing is cut
@@ -745,6 +850,20 @@ static_assert(DecodeCfg<64>::CTAS == DecodeCfg<128>::CTAS &&
 // 128 89 / 64 us, d = 64 42 / 37; 64 heads 163 / 105, 70 / 56), and one at d =
 // 256, where two tiles of O are more than the registers.
 int decode_tiles(int d, int group) { return group > kRows && d < 256 ? 2 : 1; }
+
+// Few tiles: a cluster an item and no join kernel.  All clusters resident at
+// once, and of the tiles that a row can see (the table's width and the window
+// bound them; kv_len is on the device) at most four a CTA, or eight where the
+// clusters fill half of the GPU: past that the shares' even split over all SMs
+// is worth more than the second kernel.  Shares / clusters, d = 128: one row,
+// h_kv = 8, of 1000 tokens 8.2 / 6.2 us, 2000 9.0 / 8.3, 4000 10.3 / 12.0;
+// four rows of 1000 10.1 / 7.4, 4000 16.4 / 13.7; one row, h_kv = 1, of 2000
+// 7.9 / 7.8, 4000 8.4 / 11.6 (and the host launches once).
+bool use_clusters(long long items, int resident, long long tiles, int tile, int wl, int sinks) {
+  const long long near = (wl + 1ll + tile - 1) / tile + 1 + (sinks + tile - 1ll) / tile;
+  const int each = 2 * items * kCluster >= resident ? 8 : 4;
+  return items * kCluster <= resident && (near < tiles ? near : tiles) <= each * kCluster;
+}
 
 size_t part_floats(int d, int group, int num_sms) {
   return static_cast<size_t>(2) * decode_parts(d, num_sms) * kRows * decode_tiles(d, group);
@@ -846,13 +965,14 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.lse_part) +
                                    (rows * sizeof(float) + 255) / 256 * 256);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool cl = fa::use_clusters(B * heads, most, tiles, tile, p.wl, sinks);
   cudaError_t e;
   switch (p.pool.d) {
-    case 64: e = rt == 2 ? fa::launch_decode_t<64, 2>(p, s) : fa::launch_decode_t<64, 1>(p, s); break;
+    case 64: e = rt == 2 ? fa::launch_decode_t<64, 2>(p, cl, s) : fa::launch_decode_t<64, 1>(p, cl, s); break;
     case 128:
-      e = rt == 2 ? fa::launch_decode_t<128, 2>(p, s) : fa::launch_decode_t<128, 1>(p, s);
+      e = rt == 2 ? fa::launch_decode_t<128, 2>(p, cl, s) : fa::launch_decode_t<128, 1>(p, cl, s);
       break;
-    default: e = fa::launch_decode_t<256, 1>(p, s); break;
+    default: e = fa::launch_decode_t<256, 1>(p, cl, s); break;
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

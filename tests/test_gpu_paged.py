@@ -162,6 +162,31 @@ def test_decode_is_a_contiguous_cache_s_and_repeats():
     R.check(r, "lse", lse2)
 
 
+@pytest.mark.parametrize("H,h_kv,d,width", [
+    (8, 2, 128, 30), (8, 2, 128, 4000), (40, 2, 64, 30), (40, 2, 64, 4000),
+    (4, 4, 256, 30), (4, 4, 256, 4000), (20, 1, 128, 250), (3, 1, 64, 4000)])
+def test_decode_of_few_tiles(H, h_kv, d, width):
+    """The same rows through a narrow and a wide table: the forms for few and
+    for many tiles a row, a row's parts joined in both."""
+    page = 16
+    lens = [min(width * page, n) for n in (4000, 1, 0, 470, 64)]
+    pages = sum(-(-n // page) for n in lens) + 3
+    table, kv_len, ref = R.random_cache(np.random.default_rng(d), 5, width, page, pages, lens)
+    table[3, 2] = -1                                     # a page that is not there
+    k, v = pools(1, pages, h_kv, page, d, 7)
+    table, kv_len = cuda(table, kv_len)
+    q = torch.randn(5, H, 1, d, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    q = q.cuda()
+    for rows in (5, 1):
+        for window, sinks in ((None, 0), ((100, 0), 3)):
+            args = (table[:rows].contiguous(), kv_len[:rows].contiguous())
+            o, lse = paged.decode(q[:rows].contiguous(), paged.PagedKV(k, v), 0, *args,
+                                  window=window, sinks=sinks)
+            r = R.decode(q[:rows], k, v, 0, *args, None, window, sinks)
+            R.check(r, "o", o)
+            R.check(r, "lse", lse)
+
+
 def test_decode_pool_larger_than_2_31_elements():
     """Offsets past 2^31 elements: the last pages of a 5 GB pool."""
     pages, h_kv, page, d = 10300, 8, 256, 128
