@@ -196,6 +196,48 @@ void bound_window(Variant* v) {
   v->wr = std::min(v->wr, fa::kUnbounded);
 }
 
+// Where no key is hidden left of the window, sinks change nothing: the kernels
+// without them, with their causal schedules, then do it (B = 2, H = 16, N =
+// 8192, d = 128, causal: forward 357 us against 410, backward 1219 / 1339), but
+// not with kv_len, past which theirs may not hold just anything.  *plain: the
+// variant for them.
+bool without_sinks(const fa_variant_t* v, int N, const int* kv_len, fa_variant_t* plain) {
+  if (kv_len || (v && (v->block_mask || (v->window_left >= 0 && v->window_left < N - 1))))
+    return false;
+  if (v) {
+    *plain = *v;
+    plain->window_left = std::min(v->window_left, -1);
+    if (v->window_right >= N - 1) plain->window_right = -1;
+  }
+  return true;
+}
+
+// Heads whose blocks the kernels with sinks take together (HeadOrder).  All
+// heads' longest blocks first would leave the CTAs most evenly loaded, but
+// what the blocks of a head share has to stay in L2 from one to the next: K
+// and V of a window's rows in the forward, Q, dO and the fp32 dQ of a group's
+// in the backward.  So a chunk is what takes 48 MB there, and 32 MB in the
+// backward, where it is at least four rounds of the CTAs all the same: fewer
+// are too uneven.  256 K/V heads of N = 2048, d = 128, window 1023: forward 212
+// us, 291 with all heads in one chunk, 244 head by head; backward 775, 1045, 794.
+// h_kv = 4, N = 16384, d = 128, window 8191 (one chunk): backward 1936, in chunks
+// of one or two heads 2150, head by head 2163.
+long long seen_rows(int N, int wl, int wr) { return std::min<long long>(N, 256ll + wl + wr); }
+
+int fwd_chunk(const Variant& v, int B, int H, int N, int d) {
+  const int G = H / v.H_kv;
+  const long long groups = std::max(1ll, 48000000ll / (seen_rows(N, v.wl, v.wr) * 4 * d));
+  return static_cast<int>(std::min(static_cast<long long>(B) * H, groups * G));
+}
+
+int bwd_chunk(const fa::BwdParams& p, int d, int num_sms) {
+  const long long row = 8ll * d * (p.H / p.H_kv);
+  const long long blocks = (p.N + 127ll) / 128 * p.sk_halves;
+  const long long heads = std::max(32000000ll / (seen_rows(p.N, p.wl, p.wr) * row),
+                                   (4ll * num_sms + blocks - 1) / blocks);
+  return static_cast<int>(std::min(static_cast<long long>(p.B) * p.H_kv, heads));
+}
+
 // CTAs of the backward with sinks: one an SM, fewer where all steps (blocks of
 // 128 queries, every key visible to its window's queries and the sinks to
 // all) would leave them less than four steps each.
@@ -461,7 +503,7 @@ fa_status_t fwd_impl(const void* q, const void* k, const void* v, void* o, float
   p.H_kv = var.H_kv;
   p.wl = var.wl;
   p.wr = var.wr;
-  p.causal = var.pair ? 1 : 0;
+  p.causal = var.pair && sinks < 0 ? 1 : 0;    // (with sinks: p.order)
   p.block_mask = var.bm;
   p.bm_t = (N + 127) / 128;
   p.block_mask_host = var.bmh;
@@ -470,7 +512,7 @@ fa_status_t fwd_impl(const void* q, const void* k, const void* v, void* o, float
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.status = di->status;
   p.sinks = sinks;
-  p.fd_t = fa::FastDiv::of((N + 127) / 128);
+  p.order = fa::HeadOrder::of(B * H, (N + 127) / 128, fwd_chunk(var, B, H, N, d));
   p.fd_h = fa::FastDiv::of(H);
   p.fd_g = fa::FastDiv::of(H / var.H_kv);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -493,6 +535,10 @@ fa_status_t fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, f
                          int H, int N, int d, float scale, int causal, const int* kv_len,
                          const fa_variant_t* variant, int sinks, void* stream) {
   if (sinks < 0) return FA_ERR_INVALID_ARG;
+  fa_variant_t plain;
+  if (without_sinks(variant, N, kv_len, &plain))
+    return fa_fwd_v(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant ? &plain : nullptr,
+                    stream);
   return fwd_impl(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant, sinks, stream);
 }
 
@@ -754,6 +800,10 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   if (variant && variant->block_mask) return FA_ERR_UNSUPPORTED;
   // (0 for sizes that bwd_setup refuses)
   if (workspace_bytes < fa_bwd_sinks_workspace_bytes(B, H, N, d)) return FA_ERR_INVALID_ARG;
+  fa_variant_t plain;
+  if (without_sinks(variant, N, kv_len, &plain))
+    return fa_bwd_v(q, k, v, o, dO, lse, dq, dk, dv, B, H, N, d, scale, causal, kv_len,
+                    variant ? &plain : nullptr, workspace, workspace_bytes, stream);
   fa::BwdParams p;
   DeviceInfo* di = nullptr;
   const fa_status_t st = bwd_setup(&p, &di, B, H, N, d, scale, causal, kv_len, variant, workspace,
@@ -768,7 +818,7 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
     return FA_ERR_CUDA;
   p.sk_halves = d == 256 ? 2 : 1;
   const int T = (N + 127) / 128, nsb = static_cast<int>(std::min<long long>(T, (sinks + 127ll) / 128));
-  p.fd_rest = fa::FastDiv::of(std::max(1, T - nsb));
+  p.order = fa::HeadOrder::of(B * p.H_kv, std::max(1, T - nsb), bwd_chunk(p, d, di->num_sms));
   p.fd_nsb = fa::FastDiv::of(std::max(1, nsb));
   p.fd_hkv = fa::FastDiv::of(p.H_kv);
   p.sk_part = reinterpret_cast<float*>(extra);

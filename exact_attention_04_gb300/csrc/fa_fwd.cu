@@ -197,28 +197,38 @@ __device__ __forceinline__ void record_failure(int* status, volatile int* abort,
 //
 // A block mask without a host copy (order != nullptr): the items go in the
 // cost-sorted turning deal of fa_order.cuh instead, from this CTA's table.
+//
+// With sinks, the tiles in HeadOrder's order from the last row block on (the
+// longest first, where the window is cut off at the first rows), and
+// every other round of CTAs from its far end, so that the CTAs' sums come out
+// even (H = 32, h_kv = 8, N = 8192, d = 128, window 1023 136 -> 127 us, window
+// 4095 332 -> 290; H = 16, N = 2519, d = 64, window 2185 37 -> 23, against one
+// head after the other).
 struct Sched {
   int T, P, units, causal;   // units: the round-robin units (tile pairs when causal)
   int BH;
   const uint32_t* order;     // the cost-sorted order, or nullptr
   const int* kvl;            // kv_len staged in shared memory, or nullptr
-  const FastDiv* fd;         // sinks: division by T, else nullptr
+  const HeadOrder* ho;       // sinks: the tiles' order, else nullptr
   __device__ Sched(int BH_, int N, int causal_, int tail_heads, const uint32_t* order_,
-                   const int* kvl_, const FastDiv* fd_)
-      : causal(causal_), BH(BH_), order(order_), kvl(kvl_), fd(fd_) {
+                   const int* kvl_, const HeadOrder* ho_)
+      : causal(causal_), BH(BH_), order(order_), kvl(kvl_), ho(ho_) {
     T = (N + BM - 1) / BM;
     P = (T + 1) / 2;
     units = (BH - tail_heads) * (causal ? P : T);
   }
   __device__ int ntiles(int u) const {
-    if (!causal) return 1;
+    if (ho || !causal) return 1;
     const int p = u % P;
     return (p == T - 1 - p) ? 1 : 2;
   }
   __device__ void tile(int u, int k, int& bh, int& m) const {
-    if (!causal) {
-      bh = fd ? fd->div(u) : u / T;
-      m = fd ? u - bh * T : u % T;   // (u - bh T here too: 308 -> 315 us at d = 64)
+    if (ho) {                  // longest first
+      ho->place(u, T, bh, m);
+      m = T - 1 - m;
+    } else if (!causal) {
+      bh = u / T;
+      m = u % T;
     } else {
       bh = u / P;
       const int p = u % P;
@@ -385,10 +395,17 @@ __device__ __forceinline__ bool next_tile(const FwdParams& p, const TailTable& t
         make_tile<false, MK>(p, 0, bh, m, t, sched.kvl);
         return true;
       }
-      it.u += gridDim.x;
+      if constexpr (MK == kMaskSinks) {   // every other round from its far end
+        const int far = 2 * static_cast<int>(gridDim.x - blockIdx.x) - 1;
+        it.u += it.k ? 2 * static_cast<int>(gridDim.x) - far : far;
+        it.k ^= 1;
+      } else {
+        it.u += gridDim.x;
+      }
       it.kt = 0;
     }
-    if (tail.heads == 0 || blockIdx.x >= kTailCtas || it.k >= kTailItems) return false;
+    if (MK == kMaskSinks || tail.heads == 0 || blockIdx.x >= kTailCtas || it.k >= kTailItems)
+      return false;
     const int e = tail.item[blockIdx.x][it.k];
     if (e < 0) return false;
     ++it.k;
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, MK>::THREADS, 1)
   const Sched sched(BH, p.N, p.causal, DEC ? 0 : tail.heads,
                     (BS && !DEC && p.cost_sorted) ? sm.order : nullptr,
                     (C::EPI && D == 64 && p.kv_len && p.B <= kKvlCache) ? sm.kvl : nullptr,
-                    MK == kMaskSinks ? &p.fd_t : nullptr);
+                    MK == kMaskSinks ? &p.order : nullptr);
   const int nunits = DEC ? p.B * p.H_kv * p.splits : sched.units;
 
   if (warp == 0) {

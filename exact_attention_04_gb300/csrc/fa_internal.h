@@ -33,6 +33,28 @@ struct FastDiv {
   }
 };
 
+// The blocks of all heads in the order in which CTAs take them with sinks:
+// `chunk` heads at a time (the last chunk may be smaller), within a chunk all
+// heads' first blocks, then all second ones.
+struct HeadOrder {
+  int chunk, last, full;         // heads of a chunk and of the last one; chunks but the last
+  FastDiv fd_items, fd_chunk, fd_last;
+  __host__ static HeadOrder of(int heads, int blocks, int most) {
+    const int n = (heads + most - 1) / most;
+    const int c = (heads + n - 1) / n;
+    const int full = (heads - 1) / c;
+    const int last = heads - full * c;
+    return HeadOrder{c, last, full, FastDiv::of(c * blocks), FastDiv::of(c), FastDiv::of(last)};
+  }
+  __device__ __forceinline__ void place(int i, int blocks, int& head, int& block) const {
+    const int k = fd_items.div(i);
+    i -= k * chunk * blocks;
+    const bool end = k == full;
+    block = end ? fd_last.div(i) : fd_chunk.div(i);
+    head = k * chunk + i - block * (end ? last : chunk);
+  }
+};
+
 struct FwdParams {
   CUtensorMap tq, tk, tv;      // bf16 [BH, N, d] viewed as 3-D (d, N, BH), box (64, 128, 1), SW128
   void* o;                     // bf16 [B, H, N, d]
@@ -63,10 +85,11 @@ struct FwdParams {
   // kernel) to balance the schedule
   const uint8_t* block_mask_host;
   // the first tokens that stay visible left of the window (launch_fwd_sinks),
-  // and the divisions that a tile's place takes there: by the tiles of a
-  // head, the query heads, and the query heads of a K/V head
+  // the order of the tiles there, and the divisions that a tile's place takes:
+  // by the query heads, and by the query heads of a K/V head
   int sinks;
-  FastDiv fd_t, fd_h, fd_g;
+  HeadOrder order;
+  FastDiv fd_h, fd_g;
   // nonzero: a block mask without a host copy, whose tiles each CTA sorts
   // by cost at its start (the cost-sorted deal of fa_order.cuh)
   int cost_sorted;
@@ -100,9 +123,11 @@ struct BwdParams {
   // (fa_bwd_common.cuh); sk_part [2 sk_ctas, 2, 128, min(d, 128)] takes the
   // fp32 dV, dK of the pieces, sk_meta [sk_ctas, 2] says which these are.
   // sk_halves: items of a key block (2 at d = 256).
-  // The divisions: by the key blocks of a head without sinks, with, and by H_kv.
+  // order: of the key blocks without sinks.  The divisions: by the key blocks
+  // of a head with sinks, and by H_kv.
   int sinks, sk_ctas, sk_halves;
-  FastDiv fd_rest, fd_nsb, fd_hkv;
+  HeadOrder order;
+  FastDiv fd_nsb, fd_hkv;
   CUtensorMap tdk, tdv;        // d = 64: bf16 dK, dV [BHkv, N, 64], box (64, 128, 1), SW128
   float* sk_part;
   int* sk_meta;

@@ -61,9 +61,10 @@ __device__ __forceinline__ int q_head_of(int kvbh, int gi, int H, int H_kv) {
 }
 
 // The backward's work items with sinks: those of the key blocks that hold some
-// (`sunk` of them) and the others (`plain`), each in the order K/V head, key
-// block, half of d.  The pool (fa_bwd_common.cuh) is the sunk ones, then the
-// plain ones from `whole` on.
+// (`sunk` of them), in the order K/V head, key block, half of d, and the others
+// (`plain`), in p.order's with the halves of d adjacent: a window's first key
+// blocks are seen by the most queries, so the longest go first.  The pool
+// (fa_bwd_common.cuh) is the sunk ones, then the plain ones from `whole` on.
 struct SkItems {
   int nsb, rest, sunk, plain;   // key blocks of a head with sinks and without; items
   template <class Params>
@@ -80,8 +81,8 @@ struct SkItems {
                                              int& h) const {
     const int kn = p.sk_halves == 2 ? i >> 1 : i;
     h = i & (p.sk_halves - 1);
-    kvbh = p.fd_rest.div(kn);
-    n = nsb + kn - kvbh * rest;
+    p.order.place(kn, rest, kvbh, n);
+    n += nsb;
   }
   template <class Params>
   __device__ __forceinline__ void pool_item(const Params& p, int j, int whole, int& kvbh, int& n,

@@ -64,6 +64,14 @@ CASES = [
     (1, 1, 1, 400, 128, False, (50, -1), 2, None),     # right side open
     (1, 2, 2, 300, 128, True, None, 4, (200,)),        # no window: sinks change nothing
     (1, 2, 2, 300, 64, True, (1 << 30, 0), 4, None),
+    (3, 20, 20, 1000, 64, True, None, 4, None),        # more tiles than CTAs, no window
+    (3, 20, 20, 1000, 64, True, None, 4, (1000, 999, 1)),
+    (2, 4, 2, 500, 128, False, (-1, 70), 4, None),     # open to the left alone
+    (2, 4, 2, 500, 128, False, (499, 1 << 30), 4, None),
+    (3, 20, 10, 1000, 128, True, (700, 0), 9, (1000, 400, 77)),   # and a wide one
+    (3, 20, 10, 1000, 64, True, (150, 0), 9, (1000, 400, 77)),
+    (2, 6, 2, 1000, 256, False, (300, 90), 140, (900, 1000)),
+    (5, 64, 64, 600, 128, True, (200, 0), 3, None),    # heads in several chunks
 ]
 
 
