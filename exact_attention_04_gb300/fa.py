@@ -364,53 +364,64 @@ def int32_count(x) -> int:
     return x if -2 < x < 0x7fffffff else (0x7fffffff if x > 0 else -2)
 
 
-def _sinks_variant(q, k, window):
-    return _variant(q, k, None if window is None else [int32_count(w) for w in window])
+def _same(name, t, shape, dtype, index):
+    """t's address; t is contiguous, of this shape and type, on device `index`.
+    (_check_qkv and _ptr in one: half of a small call is its checks.)"""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on q's device")
+    return t.data_ptr()
+
+
+def _sinks_call(q, k, v, o, lse, kv_len, window, causal, stream):
+    """What both calls with sinks check and pass: the addresses, the variant,
+    the sizes, the stream, and the device."""
+    index, shape, kshape = q.get_device(), q.shape, k.shape
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError("q: expected a tensor on the current CUDA device")
+    if len(shape) != 4:
+        raise ValueError("q: expected [B,H,N,d]")
+    B, H, N, d = shape
+    if len(kshape) != 4 or kshape[1] < 1 or kshape != (B, kshape[1], N, d) or H % kshape[1]:
+        raise ValueError(f"k: shape {tuple(kshape)} does not group the {H} query heads")
+    bf16 = torch.bfloat16
+    ptrs = (_same("q", q, shape, bf16, index), _same("k", k, kshape, bf16, index),
+            _same("v", v, kshape, bf16, index), _same("o", o, shape, bf16, index),
+            _same("lse", lse, shape[:3], torch.float32, index))
+    wl, wr = (-1, -1) if window is None else (int32_count(window[0]), int32_count(window[1]))
+    return (ptrs, FaVariant(kshape[1], wl, wr, None, None), shape,
+            None if kv_len is None else _check_kv_len(kv_len, B).data_ptr(),
+            1 if causal else 0,
+            torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream,
+            index)
 
 
 def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, window=None,
                  stream=None):
     """Calls fa_fwd_sinks: fa_fwd_v with the first `sinks` tokens visible left
     of the window."""
-    _check_qkv("q", q)
-    B, H, N, d = q.shape
-    var = _sinks_variant(q, k, window)
-    _check_qkv("k", k, k.shape)
-    _check_qkv("v", v, k.shape)
-    _check_qkv("o", o, q.shape)
-    if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (B, H, N) \
-            or not lse.is_contiguous():
-        raise ValueError("lse: expected a contiguous fp32 CUDA tensor [B,H,N]")
-    kv_len = _check_kv_len(kv_len, B)
-    st = load().fa_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d,
-                             float(scale), int(bool(causal)), _ptr(kv_len), ctypes.byref(var),
-                             int32_count(sinks), _stream_ptr(stream))
+    ptrs, var, shape, lens, causal, s, _ = _sinks_call(q, k, v, o, lse, kv_len, window, causal,
+                                                       stream)
+    st = load().fa_fwd_sinks(*ptrs, *shape, scale, causal, lens, ctypes.byref(var),
+                             int32_count(sinks), s)
     _raise(st, "fa_fwd_sinks")
 
 
 def fa_bwd_sinks_workspace_bytes(B, H, N, d) -> int:
-    return int(load().fa_bwd_sinks_workspace_bytes(B, H, N, d))
+    return load().fa_bwd_sinks_workspace_bytes(B, H, N, d)
 
 
 def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv_len=None,
                  window=None, workspace=None, stream=None):
     """Calls fa_bwd_sinks; workspace of fa_bwd_sinks_workspace_bytes()."""
-    _check_qkv("q", q)
-    B, H, N, d = q.shape
-    var = _sinks_variant(q, k, window)
-    for name, t in (("o", o), ("do", do), ("dq", dq)):
-        _check_qkv(name, t, q.shape)
-    for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
-        _check_qkv(name, t, k.shape)
-    if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (B, H, N) \
-            or not lse.is_contiguous():
-        raise ValueError("lse: expected a contiguous fp32 CUDA tensor [B,H,N]")
-    kv_len = _check_kv_len(kv_len, B)
+    (qp, kp, vp, op, lp), var, shape, lens, causal, s, index = _sinks_call(
+        q, k, v, o, lse, kv_len, window, causal, stream)
+    kshape, bf16 = k.shape, torch.bfloat16
     wp, wn = _ws(workspace)
-    st = load().fa_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
-                             _ptr(dk), _ptr(dv), B, H, N, d, float(scale), int(bool(causal)),
-                             _ptr(kv_len), ctypes.byref(var), int32_count(sinks), wp, wn,
-                             _stream_ptr(stream))
+    st = load().fa_bwd_sinks(
+        qp, kp, vp, op, _same("do", do, shape, bf16, index), lp, _same("dq", dq, shape, bf16, index),
+        _same("dk", dk, kshape, bf16, index), _same("dv", dv, kshape, bf16, index), *shape, scale,
+        causal, lens, ctypes.byref(var), int32_count(sinks), wp, wn, s)
     _raise(st, "fa_bwd_sinks")
 
 
@@ -557,10 +568,12 @@ def forward(q, k, v, scale=None, causal=False, kv_len=None, window=None, stream=
     sc = default_scale(d) if scale is None else scale
     if sinks:
         _check_sinks(q, block_mask)
-        with torch.cuda.stream(stream):      # None: the current one
-            o = torch.empty_like(q)
-            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-        fa_fwd_sinks(q, k, v, o, lse, sc, sinks, causal, kv_len, window, stream)
+        if stream is not None:               # the outputs belong to it
+            with torch.cuda.stream(stream):
+                return forward(q, k, v, sc, causal, kv_len, window, None, None, sinks)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        fa_fwd_sinks(q, k, v, o, lse, sc, sinks, causal, kv_len, window)
         return o, lse
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
@@ -595,12 +608,14 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, kv_len=None, ws=None
     sc = default_scale(d) if scale is None else scale
     if sinks:
         _check_sinks(q, block_mask)
-        with torch.cuda.stream(stream):
-            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
-            if ws is None:
-                ws = sinks_workspace(B, H, N, d, q.device)
-        fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, sc, sinks, causal, kv_len, window, ws,
-                     stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return backward(q, k, v, o, lse, do, sc, causal, kv_len, ws, window, None, None,
+                                sinks)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+        if ws is None:
+            ws = sinks_workspace(B, H, N, d, q.device)
+        fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, sc, sinks, causal, kv_len, window, ws)
         return dq, dk, dv
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
     if ws is None:
