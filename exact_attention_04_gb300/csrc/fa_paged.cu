@@ -859,10 +859,18 @@ int decode_tiles(int d, int group) { return group > kRows && d < 256 ? 2 : 1; }
 // h_kv = 8, of 1000 tokens 8.2 / 6.2 us, 2000 9.0 / 8.3, 4000 10.3 / 12.0;
 // four rows of 1000 10.1 / 7.4, 4000 16.4 / 13.7; one row, h_kv = 1, of 2000
 // 7.9 / 7.8, 4000 8.4 / 11.6 (and the host launches once).
-bool use_clusters(long long items, int resident, long long tiles, int tile, int wl, int sinks) {
-  const long long near = (wl + 1ll + tile - 1) / tile + 1 + (sinks + tile - 1ll) / tile;
+bool use_clusters(int d, int B, int h_kv, int group, int num_sms, long long positions, int left,
+                  int sinks) {
+  const int rows = kRows * decode_tiles(d, group), resident = decode_parts(d, num_sms);
+  const int tile = d == 64 ? DecodeCfg<64>::TILE : DecodeCfg<128>::TILE;
+  const long long items = static_cast<long long>(B) * h_kv * ((group + rows - 1) / rows);
+  long long tiles = (positions + tile - 1) / tile;
+  if (left >= 0) {
+    const long long near = (left + 1ll + tile - 1) / tile + 1 + (sinks + tile - 1ll) / tile;
+    tiles = near < tiles ? near : tiles;
+  }
   const int each = 2 * items * kCluster >= resident ? 8 : 4;
-  return items * kCluster <= resident && (near < tiles ? near : tiles) <= each * kCluster;
+  return items * kCluster <= resident && tiles <= each * kCluster;
 }
 
 size_t part_floats(int d, int group, int num_sms) {
@@ -917,11 +925,24 @@ size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d) {
          (fa::decode_parts(d, sms) * sizeof(int2) + 255) / 256 * 256;
 }
 
+size_t fa_decode_paged_call_bytes(const fa_paged_kv_t* cache, int max_pages, int B, int H,
+                                  int window_left, int sinks) {
+  if (!cache || cache->page_size < 1 || max_pages < 1 || B < 1 || sinks < 0) return 0;
+  const size_t all = fa_decode_paged_workspace_bytes(H, cache->h_kv, cache->d);
+  if (all == 0) return 0;
+  int sms = 0;
+  if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
+  return fa::use_clusters(cache->d, B, cache->h_kv, H / cache->h_kv, sms,
+                          static_cast<long long>(max_pages) * cache->page_size, window_left, sinks)
+             ? 0
+             : all;
+}
+
 fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer,
                             const int* block_table, int max_pages, const int* kv_len, void* o,
                             float* lse, int B, int H, float scale, int window_left, int sinks,
                             void* workspace, size_t workspace_bytes, void* stream) {
-  if (!q || !o || !lse || !kv_len || !workspace || layer < 0) return FA_ERR_INVALID_ARG;
+  if (!q || !o || !lse || !kv_len || layer < 0) return FA_ERR_INVALID_ARG;
   if (!fa::aligned_to(q, 16) || !fa::aligned_to(o, 16) || !fa::aligned_to(lse, 4) ||
       !fa::aligned_to(kv_len, 4) || !fa::aligned_to(workspace, 256))
     return FA_ERR_INVALID_ARG;
@@ -940,8 +961,8 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   const long long tiles = (p.max_len + tile - 1ll) / tile;
   if (static_cast<long long>(B) * H >= INT_MAX || B * heads >= INT_MAX / tiles)
     return FA_ERR_INVALID_ARG;
-  if (workspace_bytes < fa_decode_paged_workspace_bytes(H, p.pool.h_kv, p.pool.d))
-    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_decode_paged_call_bytes(cache, max_pages, B, H, window_left, sinks);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   int sms = 0;
   const fa_status_t ds = fa::device_facts(&sms, nullptr);
   if (ds != FA_OK) return ds;
@@ -965,7 +986,7 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.lse_part) +
                                    (rows * sizeof(float) + 255) / 256 * 256);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool cl = fa::use_clusters(B * heads, most, tiles, tile, p.wl, sinks);
+  const bool cl = need == 0;
   cudaError_t e;
   switch (p.pool.d) {
     case 64: e = rt == 2 ? fa::launch_decode_t<64, 2>(p, cl, s) : fa::launch_decode_t<64, 1>(p, cl, s); break;

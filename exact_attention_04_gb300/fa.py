@@ -113,6 +113,8 @@ def load():
         pool = ctypes.POINTER(FaPagedKV)
         lib.fa_decode_paged_workspace_bytes.argtypes = [i, i, i]
         lib.fa_decode_paged_workspace_bytes.restype = sz
+        lib.fa_decode_paged_call_bytes.argtypes = [pool, i, i, i, i, i]
+        lib.fa_decode_paged_call_bytes.restype = sz
         lib.fa_decode_paged.argtypes = [vp, pool, i, vp, i, vp, vp, vp, i, i, f, i, i, vp, sz, vp]
         lib.fa_decode_paged.restype = i
         lib.fa_paged_append.argtypes = [vp, vp, pool, i, vp, i, vp, vp, i, i, vp]
@@ -143,7 +145,7 @@ EXPORTS = ("fa_fwd", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_prep", "fa_bwd_
            "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_v", "fa_bwd_v", "fa_bwd_dkdv_v",
            "fa_fwd_sinks", "fa_bwd_sinks_workspace_bytes", "fa_bwd_sinks",
            "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode",
-           "fa_decode_paged_workspace_bytes", "fa_decode_paged", "fa_paged_append",
+           "fa_decode_paged_workspace_bytes", "fa_decode_paged_call_bytes", "fa_decode_paged", "fa_paged_append",
            "fa_pages_workspace_bytes", "fa_pages_reserve", "fa_pages_fork", "fa_pages_trim",
            "fa_pages_compact",
            "fa_fp8_quantize", "fa_fwd_fp8", "fa_selftest_wait_timeout", "fa_check",

@@ -72,7 +72,7 @@ class PagedKV:
                                    self.num_pages, self.page_size, self.h_kv, self.d)
         self.ref = ctypes.byref(self.struct)
         self.scale = 1.0 / math.sqrt(self.d)
-        self._need = {}        # workspace sizes by (H) or (rows,)
+        self._need = {}        # workspace sizes by a call's sizes
 
     def empty(self, rows, max_pages):
         """(table, kv_len, ref) of a cache without tokens."""
@@ -123,10 +123,11 @@ def _pages_need(cache, rows):
     return n
 
 
-def _decode_need(cache, H):
-    n = cache._need.get(H)
+def _call_need(cache, sizes):
+    """The workspace of a decode call of sizes (max_pages, rows, H, left, sinks)."""
+    n = cache._need.get(sizes)
     if n is None:
-        n = cache._need[H] = fa.load().fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d)
+        n = cache._need[sizes] = fa.load().fa_decode_paged_call_bytes(cache.ref, *sizes)
     return n
 
 
@@ -137,7 +138,8 @@ def workspace(cache, rows=1):
 
 def decode_workspace(cache, H):
     """A workspace for decode with H query heads."""
-    return torch.empty(_decode_need(cache, H), dtype=torch.uint8, device=cache.device)
+    return torch.empty(fa.load().fa_decode_paged_workspace_bytes(H, cache.h_kv, cache.d),
+                       dtype=torch.uint8, device=cache.device)
 
 
 def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=None, stream=None):
@@ -155,14 +157,15 @@ def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=
         raise ValueError("q: expected a contiguous bf16 CUDA tensor [rows, H, 1, d]")
     lp = _ints("kv_len", kv_len, shape[:1], index)
     H = shape[1]
-    need = _decode_need(cache, H)
+    left, sinks = -1 if window is None else _count(window[0]), _count(sinks)
+    need = _call_need(cache, (max_pages, rows, H, left, sinks))
     o = torch.empty_like(q)
     lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
-    ws, wp = _bytes(ws, need, q)
+    ws, wp = _bytes(ws, need, q) if need else (None, None)
     _check(fa.load().fa_decode_paged(
         q.data_ptr(), cache.ref, layer, tp, max_pages, lp, o.data_ptr(), lse.data_ptr(), rows, H,
-        cache.scale if scale is None else scale, -1 if window is None else _count(window[0]),
-        _count(sinks), wp, need, _current_raw_stream(index)), "fa_decode_paged")
+        cache.scale if scale is None else scale, left, sinks, wp, need,
+        _current_raw_stream(index)), "fa_decode_paged")
     return o, lse
 
 

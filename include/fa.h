@@ -307,10 +307,14 @@ typedef struct fa_paged_kv {
  * equal shares whatever the lengths; the result repeats bit for bit.
  *
  * workspace: fa_decode_paged_workspace_bytes(H, h_kv, d) bytes (0 for
- * invalid sizes), 256-byte aligned, its contents irrelevant on entry; calls
- * that may overlap on the GPU need one each.
+ * invalid sizes) serve any call; fa_decode_paged_call_bytes says what one
+ * with these sizes needs, which is 0 (and the workspace may be null) where it
+ * has few tokens to see.  256-byte aligned, its contents irrelevant on entry;
+ * calls that may overlap on the GPU need one each.
  */
 size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d);
+size_t fa_decode_paged_call_bytes(const fa_paged_kv_t* cache, int max_pages, int B, int H,
+                                  int window_left, int sinks);
 fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer,
                             const int* block_table, int max_pages, const int* kv_len, void* o,
                             float* lse, int B, int H, float scale, int window_left, int sinks,

@@ -78,9 +78,16 @@ def test_decode_errors(lib):
                dict(layer=-1), dict(layer=2), dict(most=0), dict(most=1 << 27), dict(B=0),
                dict(H=0), dict(H=6), dict(scale=0.0), dict(scale=float("nan")),
                dict(scale=float("inf")), dict(scale=-1.0), dict(left=-2), dict(sinks=-1),
-               dict(ws=0), dict(ws=WS + 16), dict(n=1000), dict(B=1 << 30)):
+               dict(ws=0, most=5000), dict(ws=WS + 16), dict(n=1000, most=5000),
+               dict(B=1 << 30)):
         assert call(**kw) == BAD, kw
     assert lib.fa_decode_paged_workspace_bytes(6, 4, 64) == 0
+    all_bytes = lib.fa_decode_paged_workspace_bytes(8, 4, 64)
+    assert all_bytes > 0
+    for args, want in (((4, 2, 8, -1, 0), 0), ((5000, 2, 8, -1, 0), all_bytes),
+                       ((5000, 2, 8, 50, 3), 0), ((4, 1000, 8, -1, 0), all_bytes),
+                       ((4, 2, 6, -1, 0), 0), ((0, 2, 8, -1, 0), 0)):
+        assert lib.fa_decode_paged_call_bytes(pool(), *args) == want, args
     assert lib.fa_decode_paged_workspace_bytes(8, 4, 80) == 0
     assert lib.fa_decode_paged_workspace_bytes(8, 4, 64) % 256 == 0
 
