@@ -196,14 +196,18 @@ void bound_window(Variant* v) {
   v->wr = std::min(v->wr, fa::kUnbounded);
 }
 
-// Where no key is hidden left of the window, sinks change nothing: the kernels
-// without them, with their causal schedules, then do it (B = 2, H = 16, N =
-// 8192, d = 128, causal: forward 357 us against 410, backward 1219 / 1339), but
-// not with kv_len, past which theirs may not hold just anything.  *plain: the
-// variant for them.
-bool without_sinks(const fa_variant_t* v, int N, const int* kv_len, fa_variant_t* plain) {
+// Where no key is hidden left of the window, sinks change nothing, and the
+// kernels without them, with their causal schedules, are faster (B = 2, H = 16,
+// N = 8192, d = 128, causal: forward 357 us against 410, backward 1219 / 1339).
+// Not with few blocks, which those with sinks spread better (H = 32, h_kv = 8, N
+// = 2048, d = 64: 30 us against 28, 125 / 82), nor with kv_len, past which the
+// others' K and V may not hold just anything.  *plain: the variant for them.
+bool without_sinks(const fa_variant_t* v, long long heads, int N, const int* kv_len,
+                   fa_variant_t* plain) {
   if (kv_len || (v && (v->block_mask || (v->window_left >= 0 && v->window_left < N - 1))))
     return false;
+  const DeviceInfo* di = device_info(nullptr);
+  if (di && di->err == cudaSuccess && heads * ((N + 127ll) / 128) < 8ll * di->num_sms) return false;
   if (v) {
     *plain = *v;
     plain->window_left = std::min(v->window_left, -1);
@@ -217,11 +221,12 @@ bool without_sinks(const fa_variant_t* v, int N, const int* kv_len, fa_variant_t
 // what the blocks of a head share has to stay in L2 from one to the next: K
 // and V of a window's rows in the forward, Q, dO and the fp32 dQ of a group's
 // in the backward.  So a chunk is what takes 48 MB there, and 32 MB in the
-// backward, where it is at least four rounds of the CTAs all the same: fewer
-// are too uneven.  256 K/V heads of N = 2048, d = 128, window 1023: forward 212
-// us, 291 with all heads in one chunk, 244 head by head; backward 775, 1045, 794.
-// h_kv = 4, N = 16384, d = 128, window 8191 (one chunk): backward 1936, in chunks
-// of one or two heads 2150, head by head 2163.
+// backward, where it is at least four rounds of the CTAs all the same under a
+// window of a quarter of the sequence or more: fewer are too uneven.  256 K/V
+// heads of N = 2048, d = 128, window 1023: forward 208 us, 291 with all heads in
+// one chunk, 244 head by head; backward 780, 1045, 794.  h_kv = 4, N = 16384, d =
+// 128, window 8191 (one chunk): backward 1945, in chunks of one or two heads
+// 2150, head by head 2163.
 long long seen_rows(int N, int wl, int wr) { return std::min<long long>(N, 256ll + wl + wr); }
 
 int fwd_chunk(const Variant& v, int B, int H, int N, int d) {
@@ -231,10 +236,10 @@ int fwd_chunk(const Variant& v, int B, int H, int N, int d) {
 }
 
 int bwd_chunk(const fa::BwdParams& p, int d, int num_sms) {
-  const long long row = 8ll * d * (p.H / p.H_kv);
+  const long long row = 8ll * d * (p.H / p.H_kv), seen = seen_rows(p.N, p.wl, p.wr);
   const long long blocks = (p.N + 127ll) / 128 * p.sk_halves;
-  const long long heads = std::max(32000000ll / (seen_rows(p.N, p.wl, p.wr) * row),
-                                   (4ll * num_sms + blocks - 1) / blocks);
+  const long long even = 4 * seen > p.N ? (4ll * num_sms + blocks - 1) / blocks : 1;
+  const long long heads = std::max(32000000ll / (seen * row), even);
   return static_cast<int>(std::min(static_cast<long long>(p.B) * p.H_kv, heads));
 }
 
@@ -536,7 +541,7 @@ fa_status_t fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, f
                          const fa_variant_t* variant, int sinks, void* stream) {
   if (sinks < 0) return FA_ERR_INVALID_ARG;
   fa_variant_t plain;
-  if (without_sinks(variant, N, kv_len, &plain))
+  if (without_sinks(variant, static_cast<long long>(B) * H, N, kv_len, &plain))
     return fa_fwd_v(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant ? &plain : nullptr,
                     stream);
   return fwd_impl(q, k, v, o, lse, B, H, N, d, scale, causal, kv_len, variant, sinks, stream);
@@ -801,7 +806,8 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   // (0 for sizes that bwd_setup refuses)
   if (workspace_bytes < fa_bwd_sinks_workspace_bytes(B, H, N, d)) return FA_ERR_INVALID_ARG;
   fa_variant_t plain;
-  if (without_sinks(variant, N, kv_len, &plain))
+  const long long kv_heads = static_cast<long long>(B) * (variant ? variant->h_kv : H);
+  if (without_sinks(variant, kv_heads, N, kv_len, &plain))
     return fa_bwd_v(q, k, v, o, dO, lse, dq, dk, dv, B, H, N, d, scale, causal, kv_len,
                     variant ? &plain : nullptr, workspace, workspace_bytes, stream);
   fa::BwdParams p;
@@ -814,10 +820,12 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   char* extra = static_cast<char*>(workspace) + fa_bwd_workspace_bytes(B, H, N, d);
   p.sinks = sinks;
   p.sk_ctas = sink_ctas(static_cast<long long>(B) * H, N, p.wl, sinks, di->num_sms);
-  if (d == 64 && (!make_map(&p.tdk, dk, d, N, B * p.H_kv) || !make_map(&p.tdv, dv, d, N, B * p.H_kv)))
+  if (d == 64 &&
+      (!make_map(&p.tdk, dk, d, N, B * p.H_kv) || !make_map(&p.tdv, dv, d, N, B * p.H_kv)))
     return FA_ERR_CUDA;
   p.sk_halves = d == 256 ? 2 : 1;
-  const int T = (N + 127) / 128, nsb = static_cast<int>(std::min<long long>(T, (sinks + 127ll) / 128));
+  const int T = (N + 127) / 128;
+  const int nsb = static_cast<int>(std::min<long long>(T, (sinks + 127ll) / 128));
   p.order = fa::HeadOrder::of(B * p.H_kv, std::max(1, T - nsb), bwd_chunk(p, d, di->num_sms));
   p.fd_nsb = fa::FastDiv::of(std::max(1, nsb));
   p.fd_hkv = fa::FastDiv::of(p.H_kv);

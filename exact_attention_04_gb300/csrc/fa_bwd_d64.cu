@@ -87,7 +87,8 @@ struct SSmem {
 };
 
 // 227 KB of dynamic shared memory per block on sm_103a
-static_assert(sizeof(SSmem<kMaskSinks>) <= 232448, "shared-memory layout exceeds the per-block limit");
+static_assert(sizeof(SSmem<kMaskSinks>) <= 232448,
+              "shared-memory layout exceeds the per-block limit");
 
 // Column of the packed bf16 P^T / dS^T for K-step kk (16 queries) within its
 // 128-column buffer: the warp of query quarter j packs queries 32j .. 32j+31
@@ -741,8 +742,9 @@ __global__ void __launch_bounds__(kSThreads, 1) bwd_d64_kernel(const __grid_cons
 template <int MK>
 cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t stream) {
   const size_t smem = smem_request(sizeof(SSmem<MK>), max_smem);
-  cudaError_t e = cudaFuncSetAttribute(bwd_d64_kernel<MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e =
+      cudaFuncSetAttribute(bwd_d64_kernel<MK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int T = (p.N + BK - 1) / BK;
   const int BH = p.B * p.H_kv;
@@ -763,7 +765,8 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
     if (tail.heads > 0) units = g;
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
-  const int grid = MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
+  const int grid =
+      MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
   bwd_d64_kernel<MK><<<grid, kSThreads, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }

@@ -119,7 +119,8 @@ struct DtSmem {
 };
 
 // 227 KB of dynamic shared memory per block on sm_103a
-static_assert(sizeof(DtSmem<128, kMaskSinks>) <= 232448 && sizeof(DtSmem<256, kMaskSinks>) <= 232448,
+static_assert(sizeof(DtSmem<128, kMaskSinks>) <= 232448 &&
+                  sizeof(DtSmem<256, kMaskSinks>) <= 232448,
               "shared-memory layout exceeds the per-block limit");
 
 // MK: the launch carries a block mask or sinks (instantiations of their own,
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
             uint32_t vr[32];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-              const uint4 x = key < (SK ? len : p.N) ? __ldg(vrow + 8 * c + t) : make_uint4(0, 0, 0, 0);
+              const uint4 x =
+                  key < (SK ? len : p.N) ? __ldg(vrow + 8 * c + t) : make_uint4(0, 0, 0, 0);
               vr[4 * t] = x.x;
               vr[4 * t + 1] = x.y;
               vr[4 * t + 2] = x.z;
@@ -555,7 +557,8 @@ __global__ void __launch_bounds__(kRegThreads, 1) bwd_dt_kernel(const __grid_con
           // [c_lo, c_hi], the queries whose window [q - wl, q + wr] holds the
           // key; none when the key is past len
           const int c_lo = key - p.wr - q0 - 32 * hh;
-          const int c_hi = (key < len) ? (SK && key < p.sinks ? 31 : key + p.wl - q0 - 32 * hh) : -1;
+          const int c_hi =
+              (key < len) ? (SK && key < p.sinks ? 31 : key + p.wl - q0 - 32 * hh) : -1;
           float pr[32];
           const uint64_t c2x2 = f2_make(c2, c2);
           {
@@ -877,7 +880,8 @@ cudaError_t launch(const BwdParams& p, int num_sms, int max_smem, cudaStream_t s
     if (tail.heads > 0) units = g;
   }
   if (tail.heads == 0) std::memset(tail.item, 0xff, sizeof(tail.item));
-  const int grid = MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
+  const int grid =
+      MK == kMaskSinks ? p.sk_ctas : static_cast<int>(units < num_sms ? units : num_sms);
   bwd_dt_kernel<D, MK><<<grid, DtCfg<D>::THREADS, smem, stream>>>(p, tail);
   return cudaGetLastError();
 }

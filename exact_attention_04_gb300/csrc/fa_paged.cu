@@ -810,7 +810,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 template <int D, int RT>
 cudaError_t launch_decode_t(const DecodeParams& p, bool clusters, cudaStream_t stream) {
   constexpr int smem = sizeof(DecodeSmem<D, RT>);
-  const auto kernel = clusters ? paged_decode_kernel<D, RT, true> : paged_decode_kernel<D, RT, false>;
+  const auto kernel =
+      clusters ? paged_decode_kernel<D, RT, true> : paged_decode_kernel<D, RT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   if (clusters) {
@@ -989,7 +990,9 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   const bool cl = need == 0;
   cudaError_t e;
   switch (p.pool.d) {
-    case 64: e = rt == 2 ? fa::launch_decode_t<64, 2>(p, cl, s) : fa::launch_decode_t<64, 1>(p, cl, s); break;
+    case 64:
+      e = rt == 2 ? fa::launch_decode_t<64, 2>(p, cl, s) : fa::launch_decode_t<64, 1>(p, cl, s);
+      break;
     case 128:
       e = rt == 2 ? fa::launch_decode_t<128, 2>(p, cl, s) : fa::launch_decode_t<128, 1>(p, cl, s);
       break;

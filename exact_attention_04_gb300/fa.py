@@ -145,7 +145,8 @@ EXPORTS = ("fa_fwd", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_prep", "fa_bwd_
            "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_v", "fa_bwd_v", "fa_bwd_dkdv_v",
            "fa_fwd_sinks", "fa_bwd_sinks_workspace_bytes", "fa_bwd_sinks",
            "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode",
-           "fa_decode_paged_workspace_bytes", "fa_decode_paged_call_bytes", "fa_decode_paged", "fa_paged_append",
+           "fa_decode_paged_workspace_bytes", "fa_decode_paged_call_bytes", "fa_decode_paged",
+           "fa_paged_append",
            "fa_pages_workspace_bytes", "fa_pages_reserve", "fa_pages_fork", "fa_pages_trim",
            "fa_pages_compact",
            "fa_fp8_quantize", "fa_fwd_fp8", "fa_selftest_wait_timeout", "fa_check",
@@ -371,7 +372,8 @@ def _same(name, t, shape, dtype, index):
     (_check_qkv and _ptr in one: half of a small call is its checks.)"""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on q's device")
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on q's "
+                         "device")
     return t.data_ptr()
 
 
@@ -421,8 +423,9 @@ def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv
     kshape, bf16 = k.shape, torch.bfloat16
     wp, wn = _ws(workspace)
     st = load().fa_bwd_sinks(
-        qp, kp, vp, op, _same("do", do, shape, bf16, index), lp, _same("dq", dq, shape, bf16, index),
-        _same("dk", dk, kshape, bf16, index), _same("dv", dv, kshape, bf16, index), *shape, scale,
+        qp, kp, vp, op, _same("do", do, shape, bf16, index), lp,
+        _same("dq", dq, shape, bf16, index), _same("dk", dk, kshape, bf16, index),
+        _same("dv", dv, kshape, bf16, index), *shape, scale,
         causal, lens, ctypes.byref(var), int32_count(sinks), wp, wn, s)
     _raise(st, "fa_bwd_sinks")
 

@@ -72,6 +72,8 @@ CASES = [
     (3, 20, 10, 1000, 64, True, (150, 0), 9, (1000, 400, 77)),
     (2, 6, 2, 1000, 256, False, (300, 90), 140, (900, 1000)),
     (5, 64, 64, 600, 128, True, (200, 0), 3, None),    # heads in several chunks
+    (5, 64, 64, 600, 128, True, None, 3, None),        # no window, many blocks
+    (5, 64, 64, 600, 64, False, (599, 40), 3, None),
 ]
 
 
