@@ -406,7 +406,7 @@ def fa_fwd_sinks(q, k, v, o, lse, scale, sinks, causal=False, kv_len=None, windo
     of the window."""
     ptrs, var, shape, lens, causal, s, _ = _sinks_call(q, k, v, o, lse, kv_len, window, causal,
                                                        stream)
-    st = load().fa_fwd_sinks(*ptrs, *shape, scale, causal, lens, ctypes.byref(var),
+    st = load().fa_fwd_sinks(*ptrs, *shape, float(scale), causal, lens, ctypes.byref(var),
                              int32_count(sinks), s)
     _raise(st, "fa_fwd_sinks")
 
@@ -425,7 +425,7 @@ def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv
     st = load().fa_bwd_sinks(
         qp, kp, vp, op, _same("do", do, shape, bf16, index), lp,
         _same("dq", dq, shape, bf16, index), _same("dk", dk, kshape, bf16, index),
-        _same("dv", dv, kshape, bf16, index), *shape, scale,
+        _same("dv", dv, kshape, bf16, index), *shape, float(scale),
         causal, lens, ctypes.byref(var), int32_count(sinks), wp, wn, s)
     _raise(st, "fa_bwd_sinks")
 
