@@ -827,6 +827,12 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   const int T = (N + 127) / 128;
   const int nsb = static_cast<int>(std::min<long long>(T, (sinks + 127ll) / 128));
   p.order = fa::HeadOrder::of(B * p.H_kv, std::max(1, T - nsb), bwd_chunk(p, d, di->num_sms));
+  // Under a wide window the key blocks get shorter all along the order, and
+  // rounds that turn even the CTAs out (H = 32, h_kv = 8, N = 8192, d = 128,
+  // window 6000: 1156 us against 1305; 4095 987 / 1047).  Where it starts again
+  // with each chunk of heads, or few blocks are shorter, they do not (N = 16384,
+  // d = 128, window 8191 in two chunks: 2128 / 1965; window 2047 695 / 688).
+  p.sk_turn = p.order.full == 0 && 4 * seen_rows(N, p.wl, p.wr) > N;
   p.fd_nsb = fa::FastDiv::of(std::max(1, nsb));
   p.fd_hkv = fa::FastDiv::of(p.H_kv);
   p.sk_part = reinterpret_cast<float*>(extra);

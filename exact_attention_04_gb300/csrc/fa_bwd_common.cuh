@@ -307,7 +307,8 @@ struct ItemWalk {
   const DtSched& sched;
   int G;                        // query heads per K/V head
   DtIter it;
-  const SkScratch* sc;          // sinks: it.u is the next round-robin item, then
+  int turn;                     // sinks: how far this CTA's place in the next round is off
+  const SkScratch* sc;          // it.u is the next round-robin item, then
   int j;                        // the pool's next item and where it starts
   long long p0;
   bool whole;                   // the item placed last is a round-robin one
@@ -316,6 +317,8 @@ struct ItemWalk {
       : p(p_), tail(tail_), sched(sched_), G(G_), it{static_cast<int>(blockIdx.x), 0, 0},
         sc(sc_) {
     if constexpr (MK == kMaskSinks) {
+      // every other round from the far end
+      turn = p.sk_turn ? static_cast<int>(gridDim.x) - 1 - 2 * static_cast<int>(blockIdx.x) : 0;
       j = sc->plan.j;
       p0 = sc->plan.p0;
     }
@@ -329,7 +332,8 @@ struct ItemWalk {
       whole = it.u < end;
       if (whole) {
         items.plain_item(p, it.u, kvbh, n, h);
-        it.u += gridDim.x;
+        it.u += static_cast<int>(gridDim.x) + turn;
+        turn = -turn;
       } else {
         if (p0 >= sc->plan.xe) return false;
         items.pool_item(p, j++, end, kvbh, n, h);

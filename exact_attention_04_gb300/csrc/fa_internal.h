@@ -122,10 +122,11 @@ struct BwdParams {
   // kernel runs sk_ctas CTAs, some items cut between them
   // (fa_bwd_common.cuh); sk_part [2 sk_ctas, 2, 128, min(d, 128)] takes the
   // fp32 dV, dK of the pieces, sk_meta [sk_ctas, 2] says which these are.
-  // sk_halves: items of a key block (2 at d = 256).
+  // sk_halves: items of a key block (2 at d = 256).  sk_turn: every other round
+  // of whole items goes from the last CTA to the first.
   // order: of the key blocks without sinks.  The divisions: by the key blocks
   // of a head with sinks, and by H_kv.
-  int sinks, sk_ctas, sk_halves;
+  int sinks, sk_ctas, sk_halves, sk_turn;
   HeadOrder order;
   FastDiv fd_nsb, fd_hkv;
   CUtensorMap tdk, tdv;        // d = 64: bf16 dK, dV [BHkv, N, 64], box (64, 128, 1), SW128
