@@ -146,7 +146,8 @@ def decode(q, cache, layer, table, kv_len, scale=None, window=None, sinks=0, ws=
     """(O, LSE): attention of each row's newest token (position kv_len - 1)
     over its pages; q [B, H, 1, d], O like q, LSE fp32 [B, H, 1].  window:
     (left, right), of which only left matters here, or None; sinks: first
-    tokens that stay visible.  ws: decode_workspace(), else allocated."""
+    tokens that stay visible.  ws: decode_workspace(), else allocated
+    where one is needed."""
     if stream is not None:
         return _on_stream(decode, stream, q, cache, layer, table, kv_len, scale, window, sinks, ws)
     tp, rows, max_pages = _table(cache, table)
