@@ -392,10 +392,11 @@ def _sinks_call(q, k, v, o, lse, kv_len, window, causal, stream):
     ptrs = (_same("q", q, shape, bf16, index), _same("k", k, kshape, bf16, index),
             _same("v", v, kshape, bf16, index), _same("o", o, shape, bf16, index),
             _same("lse", lse, shape[:3], torch.float32, index))
+    if kv_len is not None and _check_kv_len(kv_len, B).get_device() != index:
+        raise ValueError("kv_len: expected a tensor on q's device")
     wl, wr = (-1, -1) if window is None else (int32_count(window[0]), int32_count(window[1]))
     return (ptrs, FaVariant(kshape[1], wl, wr, None, None), shape,
-            None if kv_len is None else _check_kv_len(kv_len, B).data_ptr(),
-            1 if causal else 0,
+            None if kv_len is None else kv_len.data_ptr(), 1 if causal else 0,
             torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream,
             index)
 
@@ -422,6 +423,8 @@ def fa_bwd_sinks(q, k, v, o, do, lse, dq, dk, dv, scale, sinks, causal=False, kv
         q, k, v, o, lse, kv_len, window, causal, stream)
     kshape, bf16 = k.shape, torch.bfloat16
     wp, wn = _ws(workspace)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on q's device")
     st = load().fa_bwd_sinks(
         qp, kp, vp, op, _same("do", do, shape, bf16, index), lp,
         _same("dq", dq, shape, bf16, index), _same("dk", dk, kshape, bf16, index),
