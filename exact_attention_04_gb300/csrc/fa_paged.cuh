@@ -1,6 +1,7 @@
 // What the paged-cache kernels share: the pool's layout as the kernels see it
 // and the host checks of the public structure.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -24,6 +25,27 @@ inline bool aligned_to(const void* p, unsigned n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// Whether no two values of the pool share a place: taken from the smallest
+// stride up, each axis steps past everything inside it, and the whole stays
+// below 2^60 values.
+inline bool axes_apart(const fa_paged_kv_t& c) {
+  struct Axis {
+    long long stride, n;
+  };
+  Axis a[4] = {{c.layer_stride, c.num_layers},
+               {c.page_stride, c.num_pages},
+               {c.head_stride, c.h_kv},
+               {c.token_stride, c.page_size}};
+  std::sort(a, a + 4, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  long long extent = c.d;
+  for (const Axis& x : a) {
+    if (x.n == 1) continue;
+    if (x.stride < extent || x.stride > ((1ll << 60) - extent) / (x.n - 1)) return false;
+    extent += x.stride * (x.n - 1);
+  }
+  return true;
+}
+
 // The structure's own rules (see fa.h); *out is layer `layer`, or the whole
 // pool when layer < 0.
 inline fa_status_t resolve_pool(const fa_paged_kv_t* c, int layer, PagePool* out) {
@@ -37,6 +59,7 @@ inline fa_status_t resolve_pool(const fa_paged_kv_t* c, int layer, PagePool* out
   const long long st[4] = {c->layer_stride, c->page_stride, c->head_stride, c->token_stride};
   for (long long s : st)
     if (s < 0 || (s & 7)) return FA_ERR_INVALID_ARG;
+  if (!axes_apart(*c)) return FA_ERR_INVALID_ARG;
   const long long off = layer > 0 ? layer * c->layer_stride : 0;
   *out = PagePool{static_cast<__nv_bfloat16*>(c->k) + off, static_cast<__nv_bfloat16*>(c->v) + off,
                   c->layer_stride, c->page_stride, c->head_stride, c->token_stride,

@@ -40,12 +40,24 @@ def _on_stream(call, stream, *args, **kw):
         return call(*args, **kw)
 
 
+def _apart(shape, strides):
+    """Whether no two elements share a place: taken from the smallest stride
+    up, each axis steps past everything inside it."""
+    extent = 1
+    for stride, n in sorted((s, n) for s, n in zip(strides, shape) if n > 1):
+        if stride < extent:
+            return False
+        extent += stride * (n - 1)
+    return True
+
+
 class PagedKV:
     """The K and V pools: two bf16 CUDA tensors [layers, pages, h_kv,
     page_size, d] (or [pages, h_kv, page_size, d], one layer) of the same shape
     and strides, d contiguous and the other strides multiples of 8 (a
-    transposed view of [layers, pages, page_size, h_kv, d] serves as well).
-    Holds the tensors and the structure that the library reads."""
+    transposed view of [layers, pages, page_size, h_kv, d] serves as well, an
+    expanded or overlapping one is refused).  Holds the tensors and the
+    structure that the library reads."""
 
     def __init__(self, k, v):
         if k.dim() == 4:
@@ -59,9 +71,10 @@ class PagedKV:
             raise ValueError("k, v: the strides differ")
         if k.numel() == 0:
             raise ValueError("k, v: empty pools")
-        if strides[4] != 1 or any(s % 8 or (s == 0 and n > 1)
-                                  for n, s in zip(k.shape[:4], strides)):
+        if strides[4] != 1 or any(s % 8 for s in strides[:4]):
             raise ValueError("k, v: d must be contiguous and the other strides multiples of 8")
+        if not _apart(k.shape, strides):
+            raise ValueError("k, v: elements share memory (an expanded or overlapping view)")
         if k.data_ptr() % 16 or v.data_ptr() % 16:
             raise ValueError("k, v: expected 16-byte aligned pools")
         self.k, self.v = k, v

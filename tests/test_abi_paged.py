@@ -68,6 +68,40 @@ def test_pool_errors(lib, change, status):
     assert lib.fa_pages_compact(p, OK, 4, OK, 2, OK, OK, OK, WS, BIG, None) == status
 
 
+@pytest.mark.parametrize("change", [
+    dict(head_stride=0), dict(token_stride=0), dict(page_stride=0), dict(layer_stride=0),
+    dict(token_stride=56), dict(head_stride=1016), dict(page_stride=4096 - 8),
+    dict(layer_stride=50 * 4096 - 8),
+    dict(head_stride=64, token_stride=4 * 64 - 8),         # heads within a token
+    dict(page_stride=64, token_stride=50 * 64 - 8, head_stride=1 << 16),
+    dict(layer_stride=1 << 62), dict(page_stride=1 << 62), dict(layer_stride=(1 << 63) - 8)])
+def test_pools_whose_values_share_a_place(lib, change):
+    """Two pages, heads, slots or layers in one place (writing one would destroy
+    the other), and strides past every address."""
+    p = pool(**change)
+    assert lib.fa_decode_paged(OK, p, 0, OK, 4, OK, OK, OK, 2, 8, 0.1, -1, 0, WS, BIG, None) == BAD
+    assert lib.fa_paged_append(OK, OK, p, 0, OK, 4, OK, OK, 2, 1, None) == BAD
+    assert lib.fa_pages_fork(p, OK, 4, OK, OK, 2, OK, 2, OK + 8, OK + 8, OK + 8, OK, WS, BIG,
+                             None) == BAD
+    assert lib.fa_pages_compact(p, OK, 4, OK, 2, OK, OK, OK, WS, BIG, None) == BAD
+
+
+def test_which_pools_share_a_place():
+    """PagedKV's own check: views of one pool keep apart, expanded and
+    overlapping ones do not."""
+    t = torch.zeros(2, 5, 4, 16, 64)                       # layers, pages, heads, slots, d
+    both = torch.zeros(2, 5, 2, 16, 4, 64)                 # K and V of a page side by side
+    for x in (t, t.transpose(2, 3), t[:, 1::2], t[:, :, 1:3, ::4], t[:1, :1, :1, :1],
+              t.permute(1, 3, 0, 2, 4), both[:, :, 0].transpose(2, 3)):
+        assert paged._apart(x.shape, x.stride())
+    flat = torch.zeros(10000)
+    for x in (t[:, :, :1].expand(2, 5, 4, 16, 64), t[:1].expand(2, 5, 4, 16, 64),
+              flat.as_strided((1, 3, 2, 4, 64), (0, 504, 256, 64, 1)),
+              flat.as_strided((1, 1, 2, 4, 64), (0, 0, 248, 64, 1)),
+              flat.as_strided((1, 1, 1, 4, 64), (0, 0, 0, 32, 1))):
+        assert not paged._apart(x.shape, x.stride())
+
+
 def test_decode_errors(lib):
     def call(q=OK, layer=0, table=OK, most=4, kv=OK, o=OK, lse=OK, B=2, H=8, scale=0.1, left=-1,
              sinks=0, ws=WS, n=BIG, **kw):
