@@ -129,10 +129,18 @@ def _bytes(ws, need, like):
     return ws, ws.data_ptr()
 
 
+def _keep(cache, sizes, n):
+    """n, kept under `sizes`; a cache keeps 1024 of them at most."""
+    if len(cache._need) >= 1024:
+        cache._need.clear()
+    cache._need[sizes] = n
+    return n
+
+
 def _pages_need(cache, rows):
     n = cache._need.get((rows,))
     if n is None:
-        n = cache._need[(rows,)] = fa.load().fa_pages_workspace_bytes(cache.num_pages, rows)
+        n = _keep(cache, (rows,), fa.load().fa_pages_workspace_bytes(cache.num_pages, rows))
     return n
 
 
@@ -140,7 +148,7 @@ def _call_need(cache, sizes):
     """The workspace of a decode call of sizes (max_pages, rows, H, left, sinks)."""
     n = cache._need.get(sizes)
     if n is None:
-        n = cache._need[sizes] = fa.load().fa_decode_paged_call_bytes(cache.ref, *sizes)
+        n = _keep(cache, sizes, fa.load().fa_decode_paged_call_bytes(cache.ref, *sizes))
     return n
 
 

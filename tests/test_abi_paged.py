@@ -217,3 +217,15 @@ def test_wrappers_refuse():
         fa.forward(q, q, q, window=(2, 0), sinks=1)        # not on a GPU
     with pytest.raises(ValueError):
         fa._check_sinks(q, object())
+
+
+def test_a_cache_keeps_few_workspace_sizes(lib):
+    """A long-lived cache called with ever other sizes holds a bounded number
+    of them, and answers as the library does."""
+    class Fake:
+        ref, num_pages, _need = pool(), 50, {}
+    for i in range(3000):
+        sizes = (1 + i, 2, 8, i % 7 - 1, i % 5)
+        assert paged._call_need(Fake, sizes) == lib.fa_decode_paged_call_bytes(Fake.ref, *sizes)
+        assert paged._pages_need(Fake, 1 + i) == lib.fa_pages_workspace_bytes(50, 1 + i)
+        assert len(Fake._need) <= 1024
