@@ -103,11 +103,11 @@ struct Cursor {
 };
 
 template <int TILE>
-__device__ __forceinline__ void cursor_at(const DecodeParams& p, int b, int rem, Cursor& c) {
+__device__ __forceinline__ void cursor_at(const DecodeParams& p, int b, long long rem, Cursor& c) {
   c.b = b;
   c.s = span_of<TILE>(p, b);
-  c.hr = rem / c.s.tiles;
-  c.tile = rem - c.hr * c.s.tiles;
+  c.hr = static_cast<int>(rem / c.s.tiles);
+  c.tile = static_cast<int>(rem - static_cast<long long>(c.hr) * c.s.tiles);
 }
 
 // The next tile; the caller knows that there is one.
@@ -125,17 +125,18 @@ __device__ __forceinline__ void cursor_next(const DecodeParams& p, Cursor& c) {
 
 // Sum over the block of v (and the sum before this thread), through `warp_sum`.
 template <int THREADS>
-__device__ __forceinline__ int block_scan(int v, int* warp_sum, int& before) {
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sum,
+                                                long long& before) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int x = v;
+  long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sum[warp] = x;
   __syncthreads();
-  int total = 0, pre = 0;
+  long long total = 0, pre = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) pre += warp_sum[w];
@@ -206,8 +207,9 @@ struct DecodeSmem {
   float red[kWarps][kRows][C::RED];
   float ml[kWarps][C::ROWS][2];
   uint32_t vis[kWarps][C::STAGES];
-  int warp_sum[kWarps];
-  int start_b, start_rem;
+  long long warp_sum[kWarps];
+  long long start_rem;
+  int start_b;
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int heads = p.pool.h_kv * p.row_tiles;
   Cursor next;
-  int ta = 0, count;             // the share's first tile in the order of tiles, and its tiles
+  int count;                     // the share's tiles
   const int cta = blockIdx.x;
   // sequences without a tile: O = 0, LSE = -inf
   auto write_empty = [&]() {
@@ -271,22 +273,22 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
     // ---- this CTA's share of the tiles
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
-    int mine = 0;
+    long long mine = 0;          // (64 bits: 2^31 rows and heads of 2^24 tiles)
     for (int b = b_lo; b < b_hi; ++b) mine += span_of<TILE>(p, b).tiles;
-    int before;
-    const int total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
-    const int parts = min(p.parts, total);
+    long long before;
+    const long long total = block_scan<kThreads>(mine, sm.warp_sum, before) * heads;
+    const int parts = static_cast<int>(min(static_cast<long long>(p.parts), total));
     if (cta >= parts) {
       if (threadIdx.x == 0) p.meta[cta] = make_int2(-1, 0);
       write_empty();
       return;
     }
-    ta = static_cast<int>(static_cast<long long>(cta) * total / parts);
-    const int tb = static_cast<int>(static_cast<long long>(cta + 1) * total / parts);
+    const long long ta = cta * total / parts, tb = (cta + 1) * total / parts;
     if (ta >= before * heads && ta < (before + mine) * heads) {
-      int b = b_lo, base = before * heads;
+      int b = b_lo;
+      long long base = before * heads;
       for (;; ++b) {
-        const int n = span_of<TILE>(p, b).tiles * heads;
+        const long long n = static_cast<long long>(span_of<TILE>(p, b).tiles) * heads;
         if (ta < base + n) break;
         base += n;
       }
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
       sm.start_rem = ta - base;
     }
     __syncthreads();
-    count = tb - ta;
+    count = static_cast<int>(tb - ta);       // the host keeps the largest an int
     cursor_at<TILE>(p, sm.start_b, sm.start_rem, next);
   }
   Cursor cur = next;
@@ -377,8 +379,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
   for (int i = 0; i < C::STAGES - 1; ++i) issue();
 
   // ---- the computing side
-  int seg0 = ta - cur.tile;      // first tile of the current (sequence, head, row tile)
-  if (!CL && threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < ta);
+  // the first tile of the current (sequence, head, row tile), from the share's
+  // first on: negative where an earlier CTA began it
+  int seg0 = -cur.tile;
+  if (!CL && threadIdx.x == 0) p.meta[cta] = make_int2(cur.b * heads + cur.hr, seg0 < 0);
   const int g = lane / 4, t4 = lane % 4;
   float acc[RT][D / 8][4];
   float m[RT][2], l[RT][2];
@@ -563,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
           sm.ml[warp][kRows * t + g + 8 * r][1] = l[t][r];
         }
       }
-    const bool whole = !CL && seg0 >= ta && ends;
-    const int part = 2 * cta + (seg0 < ta ? 0 : 1);
+    const bool whole = !CL && seg0 >= 0 && ends;
+    const int part = 2 * cta + (seg0 < 0 ? 0 : 1);
     constexpr int PC = C::RCOLS / 8;           // columns of a thread
     const int trow = threadIdx.x / 8, col = threadIdx.x % 8 * PC;
 #pragma unroll
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, RT>::CTAS)
       }
     }
     if (i + 1 < count) {
-      seg0 = ta + i + 1;
+      seg0 = i + 1;
       cursor_next<TILE>(p, cur);
       fresh = true;
     }
@@ -960,8 +964,7 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   const long long heads = static_cast<long long>(p.pool.h_kv) * p.row_tiles;
   const int tile = p.pool.d == 64 ? fa::DecodeCfg<64>::TILE : fa::DecodeCfg<128>::TILE;
   const long long tiles = (p.max_len + tile - 1ll) / tile;
-  if (static_cast<long long>(B) * H >= INT_MAX || B * heads >= INT_MAX / tiles)
-    return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * H >= INT_MAX) return FA_ERR_INVALID_ARG;
   const size_t need = fa_decode_paged_call_bytes(cache, max_pages, B, H, window_left, sinks);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   int sms = 0;
@@ -980,6 +983,7 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   p.page16 = p.pool.page_size % 16 == 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const int most = fa::decode_parts(p.pool.d, sms);
+  if (B * heads * tiles / most >= INT_MAX) return FA_ERR_INVALID_ARG;   // a share's tiles
   p.parts = B * heads * tiles < most ? static_cast<int>(B * heads * tiles) : most;
   p.o_part = static_cast<float*>(workspace);
   const size_t rows = fa::part_floats(p.pool.d, p.group, sms);

@@ -313,6 +313,10 @@ typedef struct fa_paged_kv {
  * with these sizes needs, which is 0 (and the workspace may be null) where it
  * has few tokens to see.  256-byte aligned, its contents irrelevant on entry;
  * calls that may overlap on the GPU need one each.
+ *
+ * B * H is below 2^31 - 1.  Calls with B * H * max_pages * page_size below
+ * 2^44 are taken; wider ones may be refused (FA_ERR_INVALID_ARG), however
+ * short the rows are.
  */
 size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d);
 size_t fa_decode_paged_call_bytes(const fa_paged_kv_t* cache, int max_pages, int B, int H,

@@ -595,3 +595,26 @@ def test_a_window_past_32_bits():
     for window, sinks in ((1 << 32, 0), (3, 1 << 32)):
         t2, r2 = paged.trim(cache, table, kv_len, ref, window, sinks)
         assert torch.equal(t2, table) and torch.equal(r2, ref)
+
+
+@pytest.mark.parametrize("B,H,h_kv,d", [(64, 8, 8, 64), (40, 32, 8, 128)])
+def test_decode_through_a_very_wide_table(B, H, h_kv, d):
+    """A table that could list 2^29 tokens a row (2^31 tiles and more in all)
+    while the rows are short: the lengths count, not the width."""
+    page, most = 1 << 14, 1 << 15
+    k, v = pools(1, 3, h_kv, page, d, 11)
+    table = torch.full((B, most), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(B, device="cuda") % 3
+    table[1, :3] = torch.tensor([2, 0, 1])
+    lens = [(37 * b) % 300 for b in range(B)]
+    lens[1] = 2 * page + 77
+    kv_len, = cuda(lens)
+    q = torch.randn(B, H, 1, d, generator=torch.Generator().manual_seed(5))
+    q = q.to(torch.bfloat16).cuda()
+    cache = paged.PagedKV(k, v)
+    for window, sinks in ((None, 0), ((20000, 0), 9)):
+        o, lse = paged.decode(q, cache, 0, table, kv_len, window=window, sinks=sinks)
+        fa.fa_check()
+        r = R.decode(q, k, v, 0, table[:, :3], kv_len, None, window, sinks)
+        R.check(r, "o", o)
+        R.check(r, "lse", lse)
