@@ -871,7 +871,7 @@ bool use_clusters(int d, int B, int h_kv, int group, int num_sms, long long posi
   const long long items = static_cast<long long>(B) * h_kv * ((group + rows - 1) / rows);
   long long tiles = (positions + tile - 1) / tile;
   if (left >= 0) {
-    const long long near = (left + 1ll + tile - 1) / tile + 1 + (sinks + tile - 1ll) / tile;
+    const long long near = (left + 1ll + tile - 1) / tile + 1 + (sinks + (tile - 1ll)) / tile;
     tiles = near < tiles ? near : tiles;
   }
   const int each = 2 * items * kCluster >= resident ? 8 : 4;

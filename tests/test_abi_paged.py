@@ -229,3 +229,13 @@ def test_a_cache_keeps_few_workspace_sizes(lib):
         assert paged._call_need(Fake, sizes) == lib.fa_decode_paged_call_bytes(Fake.ref, *sizes)
         assert paged._pages_need(Fake, 1 + i) == lib.fa_pages_workspace_bytes(50, 1 + i)
         assert len(Fake._need) <= 1024
+
+
+def test_call_bytes_of_the_largest_windows(lib):
+    """A window or sinks at the largest int hide nothing: a wide table's call
+    needs the workspace that it needs without a window."""
+    top = (1 << 31) - 1
+    all_bytes = lib.fa_decode_paged_workspace_bytes(8, 4, 64)
+    for left, sinks in ((-1, 0), (top, 0), (0, top), (top, top), (top, top - 100), (50, top - 1)):
+        assert lib.fa_decode_paged_call_bytes(pool(), 5000, 2, 8, left, sinks) == all_bytes
+        assert lib.fa_decode_paged_call_bytes(pool(), 4, 2, 8, left, sinks) == 0
