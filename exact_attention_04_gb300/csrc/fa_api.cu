@@ -163,7 +163,8 @@ size_t round_up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The variant as the kernels see it: K/V heads, and the window folded with
 // causal into the bounds wl, wr (key j visible to query i iff
-// i - wl <= j <= i + wr), unbounded sides as fa::kUnbounded.  `pair` is true
+// i - wl <= j <= i + wr), unbounded sides, and those past every position, as
+// fa::kUnbounded (so that i +- them stays an int).  `pair` is true
 // for plain causal attention (no block mask), where the schedule pairs long
 // and short tiles.  bm: the block mask or nullptr.
 struct Variant {
@@ -180,20 +181,13 @@ fa_status_t resolve_variant(const fa_variant_t* var, int H, int causal, Variant*
   if (h_kv < 1 || h_kv > H || H % h_kv != 0 || left < -1 || right < -1)
     return FA_ERR_INVALID_ARG;
   out->H_kv = h_kv;
-  out->wl = left < 0 ? fa::kUnbounded : left;
-  out->wr = right < 0 ? fa::kUnbounded : right;
+  out->wl = left < 0 ? fa::kUnbounded : std::min(left, fa::kUnbounded);
+  out->wr = right < 0 ? fa::kUnbounded : std::min(right, fa::kUnbounded);
   if (causal && out->wr > 0) out->wr = 0;
   out->bm = var ? var->block_mask : nullptr;
   out->bmh = out->bm ? var->block_mask_host : nullptr;
   out->pair = causal && left < 0 && !out->bm;
   return FA_OK;
-}
-
-// A window side past every position is unbounded (so that i +- it stays an
-// int in the kernels).
-void bound_window(Variant* v) {
-  v->wl = std::min(v->wl, fa::kUnbounded);
-  v->wr = std::min(v->wr, fa::kUnbounded);
 }
 
 // Where no key is hidden left of the window, sinks change nothing, and the
@@ -486,10 +480,7 @@ fa_status_t fwd_impl(const void* q, const void* k, const void* v, void* o, float
   Variant var;
   const fa_status_t vs = resolve_variant(variant, H, causal, &var);
   if (vs != FA_OK) return vs;
-  if (sinks >= 0) {
-    if (var.bm) return FA_ERR_UNSUPPORTED;
-    bound_window(&var);
-  }
+  if (sinks >= 0 && var.bm) return FA_ERR_UNSUPPORTED;
   DeviceInfo* di = device_info(nullptr);
   if (!di || di->err != cudaSuccess) return FA_ERR_CUDA;
   if (!di->supported) return FA_ERR_UNSUPPORTED;
@@ -815,8 +806,6 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   const fa_status_t st = bwd_setup(&p, &di, B, H, N, d, scale, causal, kv_len, variant, workspace,
                                    workspace_bytes);
   if (st != FA_OK) return st;
-  p.wl = std::min(p.wl, fa::kUnbounded);
-  p.wr = std::min(p.wr, fa::kUnbounded);
   char* extra = static_cast<char*>(workspace) + fa_bwd_workspace_bytes(B, H, N, d);
   p.sinks = sinks;
   p.sk_ctas = sink_ctas(static_cast<long long>(B) * H, N, p.wl, sinks, di->num_sms);

@@ -148,3 +148,28 @@ def test_window_of_one_key_is_exact(d):
     assert np.abs(P.f64(lse) - s_ii).max() <= 1e-5
     assert dq.float().abs().max().item() <= 1e-3
     assert dk.float().abs().max().item() <= 1e-3
+
+
+@pytest.mark.parametrize("window", [((1 << 31) - 1, (1 << 31) - 1), ((1 << 31) - 1, 40),
+                                    (33, (1 << 31) - 1), (1 << 30, (1 << 31) - 200)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_largest_windows_are_open(d, window):
+    """A window side at the largest int is the unbounded side: forward,
+    backward, decode and the E4M3 forward, bit for bit."""
+    open_window = tuple(-1 if w >= 1 << 30 else w for w in window)
+    g = torch.Generator().manual_seed(d)
+    q, do = (torch.randn(2, 4, 300, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    k, v = (torch.randn(2, 2, 300, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    kv_len = torch.tensor([300, 131], dtype=torch.int32, device="cuda")
+    q1 = q[:, :, :1].contiguous()
+
+    def all_of(w):
+        o, lse = fa.forward(q, k, v, kv_len=kv_len, window=w)
+        _, dk, dv = fa.backward(q, k, v, o, lse, do, kv_len=kv_len, window=w)
+        out = [o, lse, dk, dv, *fa.decode(q1, k, v, causal=True, kv_len=kv_len, window=w)]
+        if d >= 128:
+            out += fa.forward_fp8(q, k, v, kv_len=kv_len, window=w)[:2]
+        fa.fa_check()
+        return out
+    for a, b in zip(all_of(window), all_of(open_window)):
+        assert torch.equal(a, b)
