@@ -308,6 +308,18 @@ def _check_block_mask(bm, N):
     return bm.data_ptr(), None if host is None else host.data_ptr()
 
 
+def int32_count(x) -> int:
+    """A number of tokens as a C int: one past every position stays that, one
+    below -1 stays refused."""
+    x = int(x)
+    return x if -2 < x < 0x7fffffff else (0x7fffffff if x > 0 else -2)
+
+
+def _window(window):
+    """(left, right) as C ints, -1 unbounded."""
+    return (-1, -1) if window is None else (int32_count(window[0]), int32_count(window[1]))
+
+
 def _variant(q, k, window, block_mask=None):
     """fa_variant_t for K/V of k's head count, the (left, right) window and a
     block mask."""
@@ -315,8 +327,7 @@ def _variant(q, k, window, block_mask=None):
     if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d) or k.shape[1] < 1 \
             or H % k.shape[1]:
         raise ValueError(f"k: shape {tuple(k.shape)} does not group the {H} query heads")
-    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    return FaVariant(int(k.shape[1]), wl, wr, *_check_block_mask(block_mask, N))
+    return FaVariant(int(k.shape[1]), *_window(window), *_check_block_mask(block_mask, N))
 
 
 def fa_fwd_v(q, k, v, o, lse, scale, causal=False, kv_len=None, window=None, stream=None,
@@ -360,13 +371,6 @@ def fa_bwd_v(q, k, v, o, do, lse, dq, dk, dv, scale, causal=False, kv_len=None, 
     _raise(st, "fa_bwd_v")
 
 
-def int32_count(x) -> int:
-    """A number of tokens as a C int: one past every position stays that, one
-    below -1 stays refused."""
-    x = int(x)
-    return x if -2 < x < 0x7fffffff else (0x7fffffff if x > 0 else -2)
-
-
 def _same(name, t, shape, dtype, index):
     """t's address; t is contiguous, of this shape and type, on device `index`.
     (_check_qkv and _ptr in one: half of a small call is its checks.)"""
@@ -394,8 +398,7 @@ def _sinks_call(q, k, v, o, lse, kv_len, window, causal, stream):
             _same("lse", lse, shape[:3], torch.float32, index))
     if kv_len is not None and _check_kv_len(kv_len, B).get_device() != index:
         raise ValueError("kv_len: expected a tensor on q's device")
-    wl, wr = (-1, -1) if window is None else (int32_count(window[0]), int32_count(window[1]))
-    return (ptrs, FaVariant(kshape[1], wl, wr, None, None), shape,
+    return (ptrs, FaVariant(kshape[1], *_window(window), None, None), shape,
             None if kv_len is None else kv_len.data_ptr(), 1 if causal else 0,
             torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream,
             index)
@@ -473,8 +476,7 @@ def fa_decode(q, k, v, o, lse, scale, causal=False, kv_len=None, window=None, sp
             or not lse.is_contiguous():
         raise ValueError("lse: expected a contiguous fp32 CUDA tensor [B,H,Nq]")
     kv_len = _check_kv_len(kv_len, B)
-    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    var = FaVariant(int(Hkv), wl, wr)
+    var = FaVariant(int(Hkv), *_window(window))
     wp, wn = _ws(workspace)
     _raise(load().fa_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, d,
                             float(scale), int(bool(causal)), _ptr(kv_len), ctypes.byref(var),
@@ -530,8 +532,7 @@ def fa_fwd_fp8(buf, o, lse, scale, causal=False, kv_len=None, window=None, strea
     if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (B, H, N):
         raise ValueError("lse: expected fp32 CUDA tensor [B,H,N]")
     kv_len = _check_kv_len(kv_len, B)
-    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    var = FaVariant(int(Hkv), wl, wr, *_check_block_mask(block_mask, N))
+    var = FaVariant(int(Hkv), *_window(window), *_check_block_mask(block_mask, N))
     _raise(load().fa_fwd_fp8(_ptr(buf["q8"]), _ptr(buf["q_scale"]), _ptr(buf["k8"]),
                              _ptr(buf["k_scale"]), _ptr(buf["v8t"]), _ptr(buf["v_scale"]),
                              _ptr(o), _ptr(lse), B, H, N, d, float(scale), int(bool(causal)),

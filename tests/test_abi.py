@@ -273,3 +273,14 @@ def test_noalloc_backward_reports_fa_bwd_status_codes(lib):
         assert a == b, (c, a, b)
         assert a != fa.FA_OK
     assert both(B=1, H=1, N=131072, d=128)[1] == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("window,want", [
+    (None, (-1, -1)), ((-1, 7), (-1, 7)), ((1 << 32, 0), ((1 << 31) - 1, 0)),
+    ((5, (1 << 32) + 3), (5, (1 << 31) - 1)), ((-(1 << 32), 1 << 40), (-2, (1 << 31) - 1))])
+def test_a_window_past_32_bits_does_not_wrap(window, want):
+    """In the variant that every call with a window passes."""
+    import torch
+    q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64)
+    var = fa._variant(q, k, window)
+    assert (var.window_left, var.window_right) == want
