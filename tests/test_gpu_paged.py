@@ -618,3 +618,76 @@ def test_decode_through_a_very_wide_table(B, H, h_kv, d):
         r = R.decode(q, k, v, 0, table[:, :3], kv_len, None, window, sinks)
         R.check(r, "o", o)
         R.check(r, "lse", lse)
+
+
+@pytest.mark.parametrize("window,sinks", [
+    (((1 << 31) - 1, -1), 9), (((1 << 30) + 1, -1), 9), ((1 << 30, -1), 0),
+    (((1 << 31) - 1, -1), (1 << 31) - 1)])
+def test_decode_under_the_largest_windows(window, sinks):
+    """Windows at and past every position, over rows whose parts are joined."""
+    lens, page = [20000, 3], 8
+    table, kv_len, _ = cuda(*R.random_cache(np.random.default_rng(1), 2, 2500, page, 2510, lens))
+    k, v = pools(1, 2510, 1, page, 128, 9)
+    cache = paged.PagedKV(k, v)
+    assert fa.load().fa_decode_paged_call_bytes(cache.ref, 2500, 2, 2, window[0], sinks) > 0
+    q = torch.randn(2, 2, 1, 128, generator=torch.Generator().manual_seed(3))
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = paged.decode(q, cache, 0, table, kv_len, window=window, sinks=sinks)
+    fa.fa_check()
+    r = R.decode(q, k, v, 0, table, kv_len, None, window, sinks)
+    R.check(r, "o", o)
+    R.check(r, "lse", lse)
+
+
+@pytest.mark.parametrize("rows,most,page,pages", [
+    (50, 40, 3, 3000),        # several CTAs of the cluster, a page a thread at most
+    (300, 60, 2, 20000),      # several pages a thread
+    (3000, 4, 5, 12000),      # and rows in several CTAs
+])
+def test_metadata_of_large_pools(rows, most, page, pages):
+    """reserve, trim and compact over pools that all CTAs of the cluster share,
+    against the plain implementation, the moved pages' contents included."""
+    rng = np.random.default_rng(pages)
+    lens = rng.integers(0, (most - 1) * page + 1, rows)
+    table, kv_len, ref = R.random_cache(rng, rows, most, page, pages, lens, 0.2, 0.05)
+    want = R.Cache(table, kv_len, ref, page)
+    k, v = pools(1, pages, 1, page, 64, 3)
+    expect = [k.clone(), v.clone()]
+    cache = paged.PagedKV(k, v)
+    n_new = rng.integers(-1, page + 2, rows)
+    table, kv_len, ref, n_new = cuda(table, kv_len, ref, n_new)
+    kv_len, ref, got = paged.reserve(cache, table, kv_len, ref, n_new)
+    assert got.tolist() == want.reserve(n_new.tolist())
+    assert table.tolist() == want.table and kv_len.tolist() == want.len
+    assert ref.tolist() == want.ref
+    want.trim(page, 1)
+    table, ref = paged.trim(cache, table, kv_len, ref, page, 1)
+    assert table.tolist() == want.table and ref.tolist() == want.ref
+    info, moves = want.compact()
+    assert len(moves) > 50
+    src, dst = (torch.tensor([m[i] for m in moves]) for i in (0, 1))
+    for pool in expect:
+        pool[:, dst] = pool[:, src]
+    table, ref, got = paged.compact(cache, table, ref)
+    assert table.tolist() == want.table and ref.tolist() == want.ref and got.tolist() == info
+    assert torch.equal(k, expect[0]) and torch.equal(v, expect[1])
+
+
+@pytest.mark.parametrize("spare", [0, 1, 900, 2500])
+def test_reserve_of_many_rows_that_runs_out(spare):
+    """More rows than one CTA has threads, the pages running out inside a later
+    CTA's."""
+    rng = np.random.default_rng(spare)
+    rows, most, page = 5000, 3, 2
+    lens = rng.integers(0, 4, rows)
+    pages = int(sum(-(-n // page) for n in lens)) + spare
+    table, kv_len, ref = R.random_cache(rng, rows, most, page, pages, lens)
+    want = R.Cache(table, kv_len, ref, page)
+    n_new = rng.integers(0, 4, rows)
+    info = want.reserve(n_new)
+    assert info[1] > 0
+    cache = paged.PagedKV(*pools(1, pages, 1, page, 64, 0))
+    table, kv_len, ref, n_new = cuda(table, kv_len, ref, n_new)
+    new_len, new_ref, got = paged.reserve(cache, table, kv_len, ref, n_new)
+    assert table.tolist() == want.table and new_len.tolist() == want.len
+    assert new_ref.tolist() == want.ref and got.tolist() == info

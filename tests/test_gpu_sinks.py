@@ -242,3 +242,23 @@ def test_two_backwards_at_once():
     fa.fa_check()
     for i, grads in enumerate(both):
         assert torch.equal(grads[1], alone[i % 2][1]) and torch.equal(grads[2], alone[i % 2][2])
+
+
+@pytest.mark.parametrize("B,H,h_kv,N,d,window,sinks,kv", [
+    # (K/V heads times key blocks without sinks, twice that at d = 256, against
+    # two rounds of 152 CTAs)
+    (3, 16, 16, 1000, 64, (700, 0), 9, None),              # 336: the second round turned
+    (3, 16, 16, 1000, 128, (700, 0), 9, (1000, 800, 977)),
+    (2, 12, 12, 1000, 256, (700, 0), 9, None),             # 168 blocks, 336 items
+    (4, 32, 16, 1500, 64, (90, 0), 4, None),               # 704, short windows: not turned
+    (4, 32, 16, 1500, 128, (90, 0), 4, (1500, 1499, 700, 3)),
+    (2, 24, 12, 2000, 256, (60, 0), 200, (2000, 1777)),    # 336 blocks behind two of sinks
+    (1, 2, 1, 4500, 128, (1000, 0), 4, None),              # a long row, one K/V head
+    (1, 2, 1, 4500, 64, (3000, 0), 130, None),
+])
+def test_several_rounds_under_a_window(B, H, h_kv, N, d, window, sinks, kv):
+    """The backward's whole rounds of items, the turned ones among them, beside
+    the pool of cut ones."""
+    x = inputs(B, H, h_kv, N, d, N + d + sinks + 1, kv)
+    kw = dict(causal=True, window=window, sinks=sinks)
+    compare(x, run(x, **kw), **kw)
