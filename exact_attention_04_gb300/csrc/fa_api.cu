@@ -636,12 +636,11 @@ fa_status_t bwd_check_args(const void* q, const void* k, const void* v, const vo
 
 namespace fa {
 
-fa_status_t device_facts(int* num_sms, int* max_smem) {
+fa_status_t device_facts(int* num_sms) {
   DeviceInfo* di = device_info(nullptr);
   if (!di || di->err != cudaSuccess) return FA_ERR_CUDA;
   if (!di->supported) return FA_ERR_UNSUPPORTED;
   if (num_sms) *num_sms = di->num_sms;
-  if (max_smem) *max_smem = di->max_smem;
   return FA_OK;
 }
 

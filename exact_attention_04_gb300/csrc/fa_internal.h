@@ -220,9 +220,10 @@ fa_status_t bwd_check_args(const void* q, const void* k, const void* v, const vo
                            const void* dv, int B, int H, int N, int d, float scale,
                            int causal, const int* kv_len, size_t workspace_bytes);
 
-// The current device's SM count, for the entry points outside fa_api.cu:
-// FA_ERR_CUDA or FA_ERR_UNSUPPORTED as every entry point reports them.
-fa_status_t device_facts(int* num_sms, int* max_smem);
+// The current device's SM count (num_sms may be null), for the entry points
+// outside fa_api.cu: FA_ERR_CUDA or FA_ERR_UNSUPPORTED as every entry point
+// reports them.
+fa_status_t device_facts(int* num_sms);
 
 cudaError_t launch_fwd(const FwdParams& p, int d, int num_sms, int max_smem, cudaStream_t stream);
 // The same with p.sinks first tokens visible left of the window; keys at or

@@ -212,17 +212,6 @@ struct DecodeSmem {
   int start_b;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
-// Shared address a of this CTA in CTA `rank` of its cluster, and loads there.
-__device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ float cluster_load(uint32_t a) {
   float x;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
@@ -924,7 +913,7 @@ extern "C" {
 size_t fa_decode_paged_workspace_bytes(int H, int h_kv, int d) {
   if (H < 1 || h_kv < 1 || H % h_kv || (d != 64 && d != 128 && d != 256)) return 0;
   int sms = 0;
-  if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
+  if (fa::device_facts(&sms) != FA_OK) sms = 152;
   const size_t rows = fa::part_floats(d, H / h_kv, sms);
   return rows * d * sizeof(float) + (rows * sizeof(float) + 255) / 256 * 256 +
          (fa::decode_parts(d, sms) * sizeof(int2) + 255) / 256 * 256;
@@ -936,7 +925,7 @@ size_t fa_decode_paged_call_bytes(const fa_paged_kv_t* cache, int max_pages, int
   const size_t all = fa_decode_paged_workspace_bytes(H, cache->h_kv, cache->d);
   if (all == 0) return 0;
   int sms = 0;
-  if (fa::device_facts(&sms, nullptr) != FA_OK) sms = 152;
+  if (fa::device_facts(&sms) != FA_OK) sms = 152;
   return fa::use_clusters(cache->d, B, cache->h_kv, H / cache->h_kv, sms,
                           static_cast<long long>(max_pages) * cache->page_size, window_left, sinks)
              ? 0
@@ -968,7 +957,7 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
   const size_t need = fa_decode_paged_call_bytes(cache, max_pages, B, H, window_left, sinks);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   int sms = 0;
-  const fa_status_t ds = fa::device_facts(&sms, nullptr);
+  const fa_status_t ds = fa::device_facts(&sms);
   if (ds != FA_OK) return ds;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
@@ -1020,7 +1009,7 @@ fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged
   const long long bh = static_cast<long long>(B) * pool.h_kv;
   const long long vec = static_cast<long long>(Nq) * (pool.d / 8);
   if (vec >= INT_MAX - 256 || bh >= INT_MAX) return FA_ERR_INVALID_ARG;
-  const fa_status_t ds = fa::device_facts(nullptr, nullptr);
+  const fa_status_t ds = fa::device_facts(nullptr);
   if (ds != FA_OK) return ds;
   const uint4* kn = static_cast<const uint4*>(k_new);
   const uint4* vn = static_cast<const uint4*>(v_new);

@@ -67,6 +67,19 @@ inline fa_status_t resolve_pool(const fa_paged_kv_t* c, int layer, PagePool* out
   return FA_OK;
 }
 
+// All threads of a cluster meet; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// The shared address a of this CTA in CTA `rank` of its cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
 // Launches a kernel that waits for the one before it in its own code
 // (griddepcontrol.wait), so that its launch overlaps that one's run.
 template <class... Args, class... Given>

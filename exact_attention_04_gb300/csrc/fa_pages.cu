@@ -37,16 +37,12 @@ constexpr int kCluster = 8;
 constexpr int kMetaThreads = 1024;
 constexpr int kMeta = kCluster * kMetaThreads;
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 __device__ __forceinline__ int remote_load(const int* p, int cta) {
-  uint32_t a;
   int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];"
+               : "=r"(v)
+               : "r"(in_cta(smem_u32(p), cta))
+               : "memory");
   return v;
 }
 
@@ -595,7 +591,7 @@ fa_status_t fa_pages_reserve(int* block_table, int max_pages, int page_size, con
       static_cast<long long>(rows) * max_pages >= INT_MAX)
     return FA_ERR_INVALID_ARG;
   if (workspace_bytes < fa_pages_workspace_bytes(num_pages, rows)) return FA_ERR_INVALID_ARG;
-  const fa_status_t ds = fa::device_facts(nullptr, nullptr);
+  const fa_status_t ds = fa::device_facts(nullptr);
   if (ds != FA_OK) return ds;
   fa::Regions w{static_cast<char*>(workspace)};
   int* off = w.take(rows);
@@ -624,7 +620,7 @@ fa_status_t fa_pages_fork(const fa_paged_kv_t* cache, const int* block_table, in
   const int most = rows > new_rows ? rows : new_rows;
   if (workspace_bytes < fa_pages_workspace_bytes(p.pool.num_pages, most)) return FA_ERR_INVALID_ARG;
   int sms = 0;
-  const fa_status_t ds = fa::device_facts(&sms, nullptr);
+  const fa_status_t ds = fa::device_facts(&sms);
   if (ds != FA_OK) return ds;
   p.table = block_table;
   p.max_pages = max_pages;
@@ -672,7 +668,7 @@ fa_status_t fa_pages_trim(const int* block_table, int max_pages, int page_size,
   if (num_pages < 1 || rows < 1 || rows > fa::kMaxRows || window_left < 0 || sinks < 0)
     return FA_ERR_INVALID_ARG;
   int sms = 0;
-  const fa_status_t ds = fa::device_facts(&sms, nullptr);
+  const fa_status_t ds = fa::device_facts(&sms);
   if (ds != FA_OK) return ds;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const fa::TrimParams p{block_table, max_pages, page_size, num_pages, rows, kv_len,
@@ -710,7 +706,7 @@ fa_status_t fa_pages_compact(const fa_paged_kv_t* cache, const int* block_table,
   if (rows < 1 || rows > fa::kMaxRows) return FA_ERR_INVALID_ARG;
   if (workspace_bytes < fa_pages_workspace_bytes(p.pool.num_pages, rows)) return FA_ERR_INVALID_ARG;
   int sms = 0;
-  const fa_status_t ds = fa::device_facts(&sms, nullptr);
+  const fa_status_t ds = fa::device_facts(&sms);
   if (ds != FA_OK) return ds;
   p.table = block_table;
   p.max_pages = max_pages;

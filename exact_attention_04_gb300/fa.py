@@ -600,8 +600,6 @@ def workspace(B, H, N, d, device):
 def _check_sinks(q, block_mask):
     if block_mask is not None:
         raise ValueError("sinks: not together with a block mask")
-    if not q.is_cuda or q.get_device() != torch.cuda.current_device():
-        raise ValueError("q: expected a tensor on the current CUDA device")
 
 
 def sinks_workspace(B, H, N, d, device):
