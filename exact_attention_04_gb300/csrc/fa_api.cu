@@ -192,10 +192,11 @@ fa_status_t resolve_variant(const fa_variant_t* var, int H, int causal, Variant*
 
 // Where no key is hidden left of the window, sinks change nothing, and the
 // kernels without them, with their causal schedules, are faster (B = 2, H = 16,
-// N = 8192, d = 128, causal: forward 357 us against 410, backward 1219 / 1339).
-// Not with few blocks, which those with sinks spread better (H = 32, h_kv = 8, N
-// = 2048, d = 64: 30 us against 28, 125 / 82), nor with kv_len, past which the
-// others' K and V may not hold just anything.  *plain: the variant for them.
+// N = 8192, d = 128, causal: forward 356 us against 404, backward 1209 / 1329).
+// Not with few blocks, whose backward those with sinks spread better (H = 32,
+// h_kv = 8, N = 2048, d = 64: backward 127 us against 84, forward 30 / 28), nor
+// with kv_len, past which the others' K and V may not hold just anything.
+// *plain: the variant for them.
 bool without_sinks(const fa_variant_t* v, long long heads, int N, const int* kv_len,
                    fa_variant_t* plain) {
   if (kv_len || (v && (v->block_mask || (v->window_left >= 0 && v->window_left < N - 1))))
@@ -217,10 +218,10 @@ bool without_sinks(const fa_variant_t* v, long long heads, int N, const int* kv_
 // in the backward.  So a chunk is what takes 48 MB there, and 32 MB in the
 // backward, where it is at least four rounds of the CTAs all the same under a
 // window of a quarter of the sequence or more: fewer are too uneven.  256 K/V
-// heads of N = 2048, d = 128, window 1023: forward 208 us, 291 with all heads in
-// one chunk, 244 head by head; backward 780, 1045, 794.  h_kv = 4, N = 16384, d =
-// 128, window 8191 (one chunk): backward 1945, in chunks of one or two heads
-// 2150, head by head 2163.
+// heads of N = 2048, d = 128, window 1023: forward 209 us, 279 with all heads in
+// one chunk, 225 head by head; backward 783, 1038, 782.  h_kv = 4, N = 16384, d =
+// 128, window 8191 (one chunk): backward 1838, in chunks of two heads 1964, head
+// by head 2162.
 long long seen_rows(int N, int wl, int wr) { return std::min<long long>(N, 256ll + wl + wr); }
 
 int fwd_chunk(const Variant& v, int B, int H, int N, int d) {
@@ -817,9 +818,11 @@ fa_status_t fa_bwd_sinks(const void* q, const void* k, const void* v, const void
   p.order = fa::HeadOrder::of(B * p.H_kv, std::max(1, T - nsb), bwd_chunk(p, d, di->num_sms));
   // Under a wide window the key blocks get shorter all along the order, and
   // rounds that turn even the CTAs out (H = 32, h_kv = 8, N = 8192, d = 128,
-  // window 6000: 1156 us against 1305; 4095 987 / 1047).  Where it starts again
-  // with each chunk of heads, or few blocks are shorter, they do not (N = 16384,
-  // d = 128, window 8191 in two chunks: 2128 / 1965; window 2047 695 / 688).
+  // window 6000: 1156 us against 1306; 4095 989 / 1050).  Few shorter blocks
+  // gain nothing (N = 16384, d = 128, h_kv = 4, window 2047: 688 / 687), and
+  // where the order starts again with each chunk of heads it is mixed (window
+  // 8191 in chunks of two heads 2128 / 1965; h_kv = 8, in chunks of four 3730 /
+  // 3886): such orders are left as they are.
   p.sk_turn = p.order.full == 0 && 4 * seen_rows(N, p.wl, p.wr) > N;
   p.fd_nsb = fa::FastDiv::of(std::max(1, nsb));
   p.fd_hkv = fa::FastDiv::of(p.H_kv);

@@ -108,8 +108,8 @@ struct Cfg {
   // buffers, so that their two 128-column O parts fit.  With sinks a tile has
   // few blocks, and the epilogue warps, the shorter masked path and the
   // halves' overlap outweigh what the third S buffer is worth on long rows:
-  // window 255 73 us against 93, 1023 133 / 144, 2047 208 / 213, 4095 325 /
-  // 326 at the shape below.)
+  // H = 32, h_kv = 8, N = 8192, 16 sinks, window 255 71 us against 85, 1023
+  // 126 / 144, 2047 189 / 213, 4095 289 / 320.)
   static constexpr bool SPLIT128 = D == 128 && (FP8 || MK == kMaskSinks);
   static constexpr int NSB = SEP ? 1 : (SPLIT128 ? 2 : (D <= 128 ? 3 : 2));
   static constexpr int NPB = SEP ? 2 : NSB;
@@ -201,8 +201,8 @@ __device__ __forceinline__ void record_failure(int* status, volatile int* abort,
 // With sinks, the tiles in HeadOrder's order from the last row block on (the
 // longest first, where the window is cut off at the first rows), and
 // every other round of CTAs from its far end, so that the CTAs' sums come out
-// even (H = 32, h_kv = 8, N = 8192, d = 128, window 1023 136 -> 127 us, window
-// 4095 332 -> 290; H = 16, N = 2519, d = 64, window 2185 37 -> 23, against one
+// even (H = 32, h_kv = 8, N = 8192, d = 128, window 1023 136 -> 126 us, window
+// 4095 332 -> 289; H = 16, N = 2519, d = 64, window 2185 37 -> 23, against one
 // head after the other).
 struct Sched {
   int T, P, units, causal;   // units: the round-robin units (tile pairs when causal)
@@ -925,11 +925,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, MK>::THREADS, 1)
     const float c2 = p.scale_log2;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o);
     uint32_t kv_it = 0, e_it = 0;                       // e_it: tiles with key blocks
-    // kEarlyS: one warp a row (d = 128, 256) tests for the next block's S
-    // while its P store lands, and skips the wait when it is there (1 % on
-    // the causal d = 128 forward).  With the key-half split (bf16 d = 64,
-    // E4M3 d = 128), where the two warps of a row cover each other's waits,
-    // it measured 1-5 % slower.
+    // kEarlyS: one warp a row (d = 256, and d = 128 without sinks) tests for
+    // the next block's S while its P store lands, and skips the wait when it
+    // is there (1 % on the causal d = 128 forward).  With the key-half split
+    // (bf16 d = 64, E4M3 d = 128, sinks at d = 128), where the two warps of a
+    // row cover each other's waits, it measured 1-5 % slower (bf16 d = 64 and
+    // E4M3; with sinks it was not measured).
     constexpr bool kEarlyS = !C::EPI;
     bool ok = true;
     // The epilogue of a tile (O / l into bf16 O, and LSE): run once the next
@@ -1096,9 +1097,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, MK>::THREADS, 1)
             if constexpr (MK == kMaskSinks) {
               // A bit a column, 32 columns at a time: few instructions,
               // since a tile of a few blocks runs this path for half of them
-              // and the code is cold each time (two comparisons a column
-              // measured 145 against 136 us, skipping the chunks that all of the warp's rows
-              // see 133: H = 32, h_kv = 8, N = 8192, window 1023, 16 sinks).
+              // and the code is cold each time (H = 32, h_kv = 8, N = 8192,
+              // window 1023, 16 sinks, one head after the other: two comparisons
+              // a column 145 us, this 136, skipping the chunks that all of the
+              // warp's rows see 133).
 #pragma unroll
               for (int w = 0; w < NC / 32; ++w) {
                 const uint32_t on = bits_below(c_hi + 1 - 32 * w) &

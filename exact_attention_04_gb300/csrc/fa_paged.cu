@@ -13,8 +13,8 @@
 //   s_j = scale q.k_j,  m = max s_j,  l = sum exp(s_j - m),
 //   O = sum exp(s_j - m) v_j / l,  LSE = m + ln l
 // over the visible keys, in one pass with the running m and l (fp32); P is
-// rounded to bf16 for the P V product (half a step, 2^-9 of a weight), l adds
-// the unrounded values, O stays in fp32 registers.
+// rounded to bf16 for the P V product (half a step, at most 2^-8 of a weight),
+// l adds the unrounded values, O stays in fp32 registers.
 //
 // Work split.  A tile is 64 token positions (128 at d = 64) of one (sequence,
 // K/V head, 16 query heads; 32 where a group has more than 16).  Every CTA
@@ -849,8 +849,8 @@ int decode_tiles(int d, int group) { return group > kRows && d < 256 ? 2 : 1; }
 // once, and of the tiles that a row can see (the table's width and the window
 // bound them; kv_len is on the device) at most four a CTA, or eight where the
 // clusters fill half of the GPU: past that the shares' even split over all SMs
-// is worth more than the second kernel.  Shares / clusters, d = 128: one row,
-// h_kv = 8, of 1000 tokens 8.2 / 6.2 us, 2000 9.0 / 8.3, 4000 10.3 / 12.0;
+// is worth more than the second kernel.  Shares / clusters, d = 128, ten calls
+// a graph over rows that L2 holds: one row, h_kv = 8, of 1000 tokens 8.2 / 6.2 us, 2000 9.0 / 8.3, 4000 10.3 / 12.0;
 // four rows of 1000 10.1 / 7.4, 4000 16.4 / 13.7; one row, h_kv = 1, of 2000
 // 7.9 / 7.8, 4000 8.4 / 11.6 (and the host launches once).
 bool use_clusters(int d, int B, int h_kv, int group, int num_sms, long long positions, int left,

@@ -267,7 +267,8 @@ fa_status_t fa_decode(const void* q, const void* k, const void* v, void* o, floa
  * smallest stride up, each axis steps past everything inside it (the stride
  * of an axis of one may be anything, 0 included).  Offsets
  * are 64-bit: a pool may be larger than 2^31 elements.  k and v are 16-byte
- * aligned; d is 64, 128 or 256; page_size >= 1; num_pages < 2^31.
+ * aligned; d is 64, 128 or 256; page_size >= 1; num_pages and
+ * num_layers * h_kv are below 2^31.
  *
  * A row of the block table (int32 [rows, max_pages], row-major) lists a
  * sequence's pages: token position x sits in slot x % page_size of page
@@ -331,7 +332,7 @@ fa_status_t fa_decode_paged(const void* q, const fa_paged_kv_t* cache, int layer
  * [B, h_kv, Nq, d], and token t of row b goes to position start[b] + t if
  * that is at least 0 and below kv_len[b] (both int32[B]; kv_len as
  * fa_pages_reserve returned it).  Other tokens, and tokens whose page does
- * not exist, are not written.
+ * not exist, are not written.  B * h_kv is below 2^31 - 1, Nq up to 2^25.
  */
 fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged_kv_t* cache,
                             int layer, const int* block_table, int max_pages, const int* start,
@@ -352,6 +353,8 @@ fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged
  * fa_pages_workspace_bytes(num_pages, rows) bytes (rows: the larger of a
  * call's row counts; 0 for invalid sizes), 256-byte aligned, its contents
  * irrelevant on entry; calls that may overlap on the GPU need one each.
+ * A call takes up to 2^24 rows; fa_pages_reserve also wants rows * max_pages
+ * below 2^31 - 1.
  */
 size_t fa_pages_workspace_bytes(int num_pages, int rows);
 
