@@ -850,9 +850,10 @@ int decode_tiles(int d, int group) { return group > kRows && d < 256 ? 2 : 1; }
 // bound them; kv_len is on the device) at most four a CTA, or eight where the
 // clusters fill half of the GPU: past that the shares' even split over all SMs
 // is worth more than the second kernel.  Shares / clusters, d = 128, ten calls
-// a graph over rows that L2 holds: one row, h_kv = 8, of 1000 tokens 8.2 / 6.2 us, 2000 9.0 / 8.3, 4000 10.3 / 12.0;
-// four rows of 1000 10.1 / 7.4, 4000 16.4 / 13.7; one row, h_kv = 1, of 2000
-// 7.9 / 7.8, 4000 8.4 / 11.6 (and the host launches once).
+// a graph over rows that L2 holds: one row, h_kv = 8, of 1000 tokens 8.2 / 6.2
+// us, 2000 9.0 / 8.3, 4000 10.3 / 12.0; four rows of 1000 10.1 / 7.4, 4000 16.4
+// / 13.7; one row, h_kv = 1, of 2000 7.9 / 7.8, 4000 8.4 / 11.6 (and the host
+// launches once).
 bool use_clusters(int d, int B, int h_kv, int group, int num_sms, long long positions, int left,
                   int sinks) {
   const int rows = kRows * decode_tiles(d, group), resident = decode_parts(d, num_sms);

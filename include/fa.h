@@ -265,8 +265,8 @@ fa_status_t fa_decode(const void* q, const void* k, const void* v, void* o, floa
  * 8, so [pages, h_kv, page_size, d], [pages, page_size, h_kv, d] and views of
  * a larger pool all serve.  No two elements share a place: taken from the
  * smallest stride up, each axis steps past everything inside it (the stride
- * of an axis of one may be anything, 0 included).  Offsets
- * are 64-bit: a pool may be larger than 2^31 elements.  k and v are 16-byte
+ * of an axis of one may be any multiple of 8, 0 included).  Offsets are
+ * 64-bit: a pool may be larger than 2^31 elements.  k and v are 16-byte
  * aligned; d is 64, 128 or 256; page_size >= 1; num_pages and
  * num_layers * h_kv are below 2^31.
  *
