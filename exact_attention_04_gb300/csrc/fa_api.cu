@@ -16,6 +16,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_strided.cuh"
 #include "fa_window.cuh"
 
 // Written by kernels that gave up waiting; read and cleared by fa_check.
@@ -444,7 +445,7 @@ void plan_mask_tail(const uint8_t* bm_host, int BH, int T, int nsplit, int G, bo
 
 extern "C" {
 
-int fa_version(void) { return 1 * 10000 + 3 * 100 + 0; }
+int fa_version(void) { return 1 * 10000 + 4 * 100 + 0; }
 
 const char* fa_status_string(fa_status_t s) {
   switch (s) {
@@ -643,6 +644,34 @@ fa_status_t device_facts(int* num_sms) {
   if (!di->supported) return FA_ERR_UNSUPPORTED;
   if (num_sms) *num_sms = di->num_sms;
   return FA_OK;
+}
+
+fa_status_t device_facts(int* num_sms, int* max_smem, int** status) {
+  const fa_status_t s = device_facts(num_sms);
+  if (s != FA_OK) return s;
+  const DeviceInfo* di = device_info(nullptr);
+  *max_smem = di->max_smem;
+  *status = di->status;
+  return FA_OK;
+}
+
+bool make_map_4d(CUtensorMap* m, const void* base, int d, const long long* n, const long long* s,
+                 const int* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), 0, 0, 0};
+  cuuint64_t strides[3];
+  cuuint32_t boxes[4] = {64, 0, 0, 0};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(n[i]);
+    strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? s[i] : d) * 2;
+    boxes[i + 1] = static_cast<cuuint32_t>(box[i]);
+  }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace fa

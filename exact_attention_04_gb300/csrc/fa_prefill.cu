@@ -1,0 +1,1397 @@
+// Attention of a chunk of new tokens per row over the paged cache.
+//
+// Work: a tile is up to 128 query rows - the heads of one K/V head's group
+// times as many tokens of one row of the batch as fit - against the tiles of
+// up to 128 keys that any of them sees.  The lengths are on the device, so a
+// first kernel of one block lists the pieces (tile, range of key tiles): whole
+// tiles where there are many, and ranges where few tiles would leave SMs idle
+// (see plan_kernel).  The main kernel is persistent and takes the next piece
+// from a counter, K/V heads innermost, so that the tiles that run at the same
+// time share their keys through L2; a cut tile's pieces leave fp32 partial
+// outputs and log-sum-exps that a third kernel joins.  What a piece computes
+// does not depend on who takes it or when: results repeat bit for bit.
+//
+// Main kernel, one CTA per SM, roles by warp:
+//   0        producer: takes pieces, looks pages up, loads Q, K (and V for d <=
+//            128) by TMA.  A key tile is whole pages (page_size <= 128: as many
+//            as fit, a box a page; else up to 128 slots of one page).  A page
+//            that does not exist is a box outside the pool: TMA fills in
+//            zeros, and a bit mask of the tile's keys hides them.
+//   1        S = Q K^T on tcgen05 into tensor memory, running ahead
+//   2        O += P V, P from tensor memory
+//   3..      softmax: a row of the tile a thread; with d <= 128 two warps share
+//            a row, each over half of every tile's keys with a maximum, sum
+//            and O of its own
+//   then 4   epilogue: merge the halves, divide, store O and LSE
+//   last     (d = 256) V producer
+// The recurrence and its roundings are those of the forward (fa_fwd.cu): S in
+// base-2 units, a reference maximum that moves only when a block exceeds it by
+// 2^24, P rounded to bf16 for the product and summed unrounded.
+#include <climits>
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "fa_paged.cuh"
+#include "fa_strided.cuh"
+#include "fa_window.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace ptx;
+
+constexpr int BM = 128;
+constexpr int BN = 128;
+constexpr int CHUNK = 128 * 128;   // bytes of 128 rows x 64 columns
+constexpr float kRescaleSlack = 24.0f;
+constexpr int kPlanThreads = 1024;
+constexpr int kMostRounds = 4;     // pieces of a cut call: at most so many a CTA, by its sum
+constexpr int kItems = 4;          // pieces announced ahead
+constexpr int kRing = 8;           // key tiles whose masks are kept
+
+// A piece as the plan lists it, for every unit (K/V head, part of its group).
+struct Entry {
+  int row, n0, ntok;   // batch row; first token (its place on the token axis), tokens
+  int pos0, len;       // position of the first token; the row's keys
+  int s0, s1;          // key tiles of the tile's walk
+  int slot;            // partial output (times units + unit), or -1
+};
+
+struct JoinEntry {
+  int batch, n0, ntok, slot0, pieces, pad[3];
+};
+
+struct Counters {
+  unsigned items;      // pieces times units
+  unsigned next;       // the next one to take
+  int joins, most;     // cut tiles; most pieces of one
+};
+
+struct PrefillParams {
+  CUtensorMap tq, tk, tv;
+  __nv_bfloat16* o;
+  long long ob, oh, ot;            // strides of o
+  float* lse;                      // [batch, H, N]
+  const int* table;
+  const int* start;
+  const int* kv_len;
+  const int* offsets;              // nullptr: padded rows
+  int B, H, N, h_kv;
+  int group, gh, parts, units;     // query heads of a K/V head, of a tile; tiles a group; units
+  int tpt;                         // tokens of a tile
+  FastDiv fd_units, fd_parts, fd_gh, fd_tn;
+  int max_pages, num_pages, page_size;
+  int ppt, tpp, kt;                // pages of a key tile (0: tpp tiles a page), keys of one
+  FastDiv fd_kt, fd_ps, fd_tpp;
+  int wl, wr, sinks, causal;
+  float scale_log2;
+  int* status;
+  Counters* counters;
+  int* row_tiles;                  // [B + 1] tiles before a row (offsets)
+  Entry* entries;
+  JoinEntry* joins;
+  int cap_entries, cap_slots;      // (slots: times units)
+  int slot_rows;
+  float* o_part;
+  float* lse_part;
+  int grid;
+};
+
+// What a row's tokens are and see.
+struct Row {
+  int n0, ntok;        // its tokens on the token axis
+  int start, len;
+};
+
+__device__ __forceinline__ Row row_at(const PrefillParams& p, int b) {
+  Row r;
+  int end;
+  row_tokens(p.offsets, b, p.N, r.n0, end);
+  r.ntok = end - r.n0;
+  // (positions and window sides stay within 2^30, so that sums fit)
+  r.start = min(max(p.start[b], -kUnbounded), kUnbounded - 1);
+  r.len = min(max(p.kv_len[b], 0), p.max_pages * p.page_size);
+  return r;
+}
+
+__device__ __forceinline__ int key_tile(const PrefillParams& p, int x) {
+  if (p.ppt) return p.fd_kt.div(x);
+  const int page = p.fd_ps.div(x);
+  return page * p.tpp + ((x - page * p.page_size) >> 7);
+}
+
+// The position of a key tile's first key.
+__device__ __forceinline__ int tile_pos(const PrefillParams& p, int j) {
+  if (p.ppt) return j * p.kt;
+  const int page = p.fd_tpp.div(j);
+  return page * p.page_size + (j - page * p.tpp) * BN;
+}
+
+// Keys [lo, hi) of the tokens at positions pos0 .. pos0 + ntok - 1 (left of lo:
+// the sinks).
+__device__ __forceinline__ void tile_keys(const PrefillParams& p, int pos0, int ntok, int len,
+                                          int& lo, int& hi) {
+  long long last = static_cast<long long>(pos0) + ntok - 1;
+  if (p.causal) last = last < len ? last : len - 1;   // tokens at or past len are not there
+  if (p.causal && pos0 >= len) last = -1ll - kUnbounded;
+  const long long h = last + p.wr + 1;
+  hi = p.wr >= kUnbounded && !p.causal ? len : static_cast<int>(h < 0 ? 0 : (h > len ? len : h));
+  const long long l = static_cast<long long>(pos0) - p.wl;
+  lo = static_cast<int>(l < 0 ? 0 : (l > hi ? hi : l));
+}
+
+// The tile's walk: `ns` key tiles of sinks from 0, then from jlo; returns their
+// number.
+__device__ __forceinline__ int tile_walk(const PrefillParams& p, int pos0, int ntok, int len,
+                                         int& jlo, int& ns) {
+  int lo, hi;
+  tile_keys(p, pos0, ntok, len, lo, hi);
+  const int first = min(p.sinks, hi);
+  ns = first > 0 ? key_tile(p, first - 1) + 1 : 0;
+  jlo = 0;
+  if (hi <= lo) return ns;
+  jlo = key_tile(p, lo);
+  ns = min(ns, jlo);
+  return ns + key_tile(p, hi - 1) + 1 - jlo;
+}
+
+// ---------------------------------------------------------------- the plan
+
+// Exclusive prefix sum over the block; total to every thread.
+__device__ __forceinline__ int block_scan(int x, int* sm, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) sm[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int w = sm[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    sm[lane] = w;
+  }
+  __syncthreads();
+  total = sm[kPlanThreads / 32 - 1];
+  return v - x + (warp ? sm[warp - 1] : 0);
+}
+
+// Tile i of the call: rows in order, in a row the last tokens (under causality
+// the most keys) first.
+__device__ __forceinline__ void plan_tile(const PrefillParams& p, int i, Entry& e, int& n) {
+  int b, k, tiles;
+  if (p.offsets) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) / 2;
+      if (p.row_tiles[m] <= i)
+        lo = m;
+      else
+        hi = m;
+    }
+    b = lo;
+    k = i - p.row_tiles[b];
+    tiles = p.row_tiles[b + 1] - p.row_tiles[b];
+  } else {
+    tiles = (p.N + p.tpt - 1) / p.tpt;
+    b = p.fd_tn.div(i);
+    k = i - b * tiles;
+  }
+  const Row r = row_at(p, b);
+  const int t0 = (tiles - 1 - k) * p.tpt;
+  e.row = b;
+  e.n0 = r.n0 + t0;
+  e.ntok = min(p.tpt, r.ntok - t0);
+  e.pos0 = r.start + t0;
+  e.len = r.len;
+  int jlo, ns;
+  n = tile_walk(p, e.pos0, e.ntok, e.len, jlo, ns);
+}
+
+// Lists the pieces.  With W key tiles to walk over all units, cutting the
+// walks into pieces of at most W / (k CTAs) tiles, k = 1 .. kMostRounds, or not
+// at all: whichever ends first by the estimate below.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
+  __shared__ int sm[32];
+  __shared__ unsigned long long sum[1 + kMostRounds];
+  __shared__ int most, cut, slots, joins, join_most;
+  launch_dependents();
+  grid_dependency_wait();
+  const int tid = threadIdx.x;
+  if (tid <= kMostRounds) sum[tid] = 0;
+  if (tid == 0) most = slots = joins = join_most = 0;
+  // tiles of the rows
+  int tiles;
+  if (p.offsets) {
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < p.B) {
+        int begin, end;
+        row_tokens(p.offsets, b, p.N, begin, end);
+        n = (end - begin + p.tpt - 1) / p.tpt;
+      }
+      int total;
+      const int at = before + block_scan(n, sm, total);
+      if (b < p.B) p.row_tiles[b] = at;
+      before += total;
+    }
+    if (tid == 0) p.row_tiles[p.B] = before;
+    // (offsets that do not rise may name a token twice: what is past the
+    // list's room is left out)
+    tiles = before;
+  } else {
+    tiles = p.B * ((p.N + p.tpt - 1) / p.tpt);
+  }
+  __syncthreads();
+  // the walks' sum, and the longest
+  unsigned long long s = 0;
+  int longest = 0;
+  Entry e;
+  int n = 0;
+  const bool once = tiles <= kPlanThreads;
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    plan_tile(p, i, e, n);
+    s += n;
+    longest = max(longest, n);
+  }
+  if (s) atomicAdd(&sum[0], s);
+  if (longest) atomicMax(&most, longest);
+  __syncthreads();
+  const unsigned long long W = sum[0] * p.units;
+  int P[kMostRounds];
+#pragma unroll
+  for (int k = 0; k < kMostRounds; ++k) {
+    const unsigned long long share = static_cast<unsigned long long>(p.grid) * (k + 1);
+    const unsigned long long x = (W + share - 1) / share;
+    P[k] = x > INT_MAX ? INT_MAX : (x ? static_cast<int>(x) : 1);
+  }
+  if (most > P[kMostRounds - 1]) {       // something to cut
+    unsigned c[kMostRounds] = {};
+    for (int i = tid; i < tiles; i += kPlanThreads) {
+      if (!once) plan_tile(p, i, e, n);
+#pragma unroll
+      for (int k = 0; k < kMostRounds; ++k) c[k] += n > P[k] ? (n + P[k] - 1) / P[k] : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < kMostRounds; ++k)
+      if (c[k]) atomicAdd(&sum[1 + k], static_cast<unsigned long long>(c[k]));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // key tiles that a CTA walks to the end: a piece costs one more, a cut one
+    // two, the join about six
+    const auto end_of = [&](double pieces, double len, double extra) {
+      const double rounds = ceil(pieces / p.grid) * (len + extra);
+      const double even = (static_cast<double>(W) + pieces * extra) / p.grid + len;
+      return rounds < even ? rounds : even;
+    };
+    double best = end_of(static_cast<double>(tiles) * p.units, most, 1.0);
+    cut = INT_MAX;
+    if (most > P[kMostRounds - 1]) {
+      for (int k = 0; k < kMostRounds; ++k) {
+        const double t =
+            end_of(static_cast<double>(sum[1 + k]) * p.units, min(P[k], most), 2.0) + 6.0;
+        if (most > P[k] && t < best) {
+          best = t;
+          cut = P[k];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  int before = 0;
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int c = 0;
+    if (i < tiles) {
+      if (!once) plan_tile(p, i, e, n);
+      c = n > cut ? (n + cut - 1) / cut : 1;
+    }
+    int total;
+    const int at = before + block_scan(c, sm, total);
+    if (c > 0 && at + c <= p.cap_entries) {
+      int slot = -1;
+      if (c > 1) {
+        slot = atomicAdd(&slots, c);
+        if (slot + c <= p.cap_slots) {
+          JoinEntry j = {p.offsets ? 0 : e.row, e.n0, e.ntok, slot, c, {0, 0, 0}};
+          p.joins[atomicAdd(&joins, 1)] = j;
+          atomicMax(&join_most, c);
+        } else {                           // (never: cap_slots holds every cut)
+          slot = -1;
+        }
+      }
+      for (int k = 0; k < c; ++k) {
+        e.s0 = static_cast<int>(static_cast<long long>(n) * k / c);
+        e.s1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / c);
+        e.slot = slot < 0 ? -1 : slot + k;
+        p.entries[at + k] = e;
+      }
+    }
+    before += total;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    Counters c;
+    c.items = static_cast<unsigned>(min(before, p.cap_entries)) * p.units;
+    c.next = p.grid;
+    c.joins = joins;
+    c.most = join_most;
+    *p.counters = c;
+  }
+}
+
+// ---------------------------------------------------------------- the main kernel
+
+template <int D>
+struct Cfg {
+  static constexpr int NCH = D / 64;
+  static constexpr int TILE_BYTES = NCH * CHUNK;
+  static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 1);
+  // d = 256: O takes 256 columns of tensor memory, P buffers of their own let
+  // the one S buffer be refilled once the softmax has loaded it, and V comes
+  // from a warp of its own, since one stage a ring is all that fits.
+  static constexpr bool SEP = D == 256;
+  static constexpr int NHALF = D <= 128 ? 2 : 1;
+  static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
+  static constexpr int NPB = SEP ? 2 : NSB;
+  static constexpr uint32_t TM_S = 0;
+  static constexpr uint32_t TM_P = SEP ? 128 * NSB : TM_S;
+  static constexpr uint32_t P_STRIDE = SEP ? 64 : 128;
+  static constexpr uint32_t TM_O = SEP ? TM_P + 64 * NPB : 128 * NSB;
+  static constexpr int OCOLS = D * NHALF;
+  static constexpr uint32_t TM_COLS = 512;
+  static_assert(TM_O + OCOLS <= TM_COLS, "tensor memory budget");
+  static constexpr int EPI_WARP0 = 3 + 4 * NHALF;
+  static constexpr int WARPS = EPI_WARP0 + 4 + (SEP ? 1 : 0);
+  static constexpr int THREADS = 32 * WARPS;
+  // a tile's mask slot is free again before the producer reaches the tile
+  // kRing further on: S of tile g - STAGES is done when K of tile g is loaded,
+  // so the softmax has read the mask of g - STAGES - NSB (before it lets go of
+  // the S buffer)
+  static_assert(STAGES + NSB <= kRing, "mask ring");
+};
+
+// A piece as the roles see it.
+struct alignas(16) Item {
+  int n0, ntok, pos0, len;      // n0 < 0: no more pieces
+  int s0, nst, slot, jlo;
+  int ns, rlo, rhi, batch;      // [rlo, rhi): the keys that the row's tokens see, beside the sinks
+  int kvh, h0, nh, row;
+};
+
+struct alignas(16) KeyMask {
+  uint32_t word[4];             // keys that exist
+  int pos, pad[3];              // position of the first
+};
+
+template <int D>
+struct Smem {
+  using C = Cfg<D>;
+  alignas(1024) uint8_t q[C::TILE_BYTES];
+  alignas(1024) uint8_t k[C::STAGES][C::TILE_BYTES];
+  alignas(1024) uint8_t v[C::STAGES][C::TILE_BYTES];
+  Item item[kItems];
+  KeyMask mask[kRing];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[C::STAGES], k_empty[C::STAGES];
+  uint64_t v_full[C::STAGES], v_empty[C::STAGES];
+  uint64_t s_full[C::NSB], s_free[C::NSB];
+  uint64_t p_full[C::NPB * C::NHALF];
+  uint64_t pv_done[C::NPB];
+  uint64_t o_free, o_done, stats_full;
+  uint64_t mma_done, pv_mma_done;
+  float ostat[2 * C::NHALF][BM];
+  uint32_t tmem_base;
+  int abort;
+};
+
+enum Site {
+  kSiteItem = 41, kSiteItemSlot, kSiteQ, kSiteK, kSiteV, kSiteMmaQ, kSiteMmaK, kSiteMmaS,
+  kSiteMmaP, kSiteMmaV, kSiteMmaO, kSiteSmS, kSiteSmP, kSiteSmO, kSiteEpi, kSiteDrain
+};
+
+__device__ __forceinline__ void fail(int* status, volatile int* abort, int site) {
+  if ((threadIdx.x & 31) == 0) {
+    atomicCAS(status, 0, status_code(site));
+    *abort = 1;
+  }
+}
+
+// 4-D tiled load global -> shared.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// The next announced piece; false at the end, or after a wait that gave up.
+template <class S>
+__device__ __forceinline__ bool next_item(S& sm, uint32_t& k, Item& t, int* status) {
+  const uint32_t b = k % kItems;
+  if (!mbar_wait_warp(&sm.item_full[b], (k / kItems) & 1, &sm.abort, kWaitTimeoutNs)) {
+    fail(status, &sm.abort, kSiteItem);
+    return false;
+  }
+  t = sm.item[b];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.item_empty[b]);
+  ++k;
+  return t.n0 >= 0;
+}
+
+// The key tile of step j of the walk.
+__device__ __forceinline__ int step_tile(const Item& t, int j) {
+  const int s = t.s0 + j;
+  return s < t.ns ? s : t.jlo + (s - t.ns);
+}
+
+// Looks up the pages of key tiles, one a lane.
+struct Pages {
+  const PrefillParams& p;
+  const int* row;
+  int len;
+  // page m of key tile j, or -1
+  __device__ __forceinline__ int at(int j, int m) const {
+    const int i = p.ppt ? j * p.ppt + m : p.fd_tpp.div(j);
+    if (m >= (p.ppt ? p.ppt : 1) || i >= p.max_pages) return -1;
+    if (static_cast<long long>(i) * p.page_size >= len) return -1;
+    const int page = row[i];
+    return page >= 0 && page < p.num_pages ? page : -1;
+  }
+};
+
+// Loads one key tile of K or V: a box a page and 64 columns.  page: this
+// lane's (Pages::at(j, lane)).
+template <int D>
+__device__ __forceinline__ void load_tile(const PrefillParams& p, const Pages& pages, int j,
+                                          int page, int head, uint8_t* dst, const CUtensorMap* map,
+                                          uint64_t* bar) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_arrive_expect_tx(bar, p.kt * (D * 2));
+  __syncwarp();
+  if (p.ppt) {
+    for (int m = lane; m < p.ppt; m += 32) {
+      if (m >= 32) page = pages.at(j, m);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_4d(dst + c * CHUNK + m * p.page_size * 128, map, bar, 64 * c, 0, head,
+                    page < 0 ? p.num_pages : page);
+    }
+  } else if (lane < D / 64) {
+    const int slot0 = (j - p.fd_tpp.div(j) * p.tpp) * BN;
+    tma_load_4d(dst + lane * CHUNK, map, bar, 64 * lane, slot0, head,
+                page < 0 ? p.num_pages : page);
+  }
+  __syncwarp();
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    prefill_kernel(const __grid_constant__ PrefillParams p) {
+  using C = Cfg<D>;
+  using S = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
+  const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
+  if (aligned - raw + sizeof(S) > dynamic_smem_size()) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, status_code(kSiteSmemLayout));
+    return;
+  }
+  S& sm = *reinterpret_cast<S*>(aligned);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* abort = &sm.abort;
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], C::WARPS - 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int b = 0; b < C::NSB; ++b) {
+      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.s_free[b], 4);
+    }
+    for (int b = 0; b < C::NPB; ++b) {
+      for (int h = 0; h < C::NHALF; ++h) mbar_init(&sm.p_full[b * C::NHALF + h], 4);
+      mbar_init(&sm.pv_done[b], 1);
+    }
+    mbar_init(&sm.o_free, 4);
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.stats_full, 32 * 4 * C::NHALF);
+    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.pv_mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, C::TM_COLS);
+    tmem_relinquish();
+  }
+  // Rows of V that no load writes (a tile of fewer than 128 keys): zeros, since
+  // P is 0 there and 0 NaN is NaN.
+  if (p.kt < BN) {
+    for (int s = 0; s < C::STAGES; ++s)
+      for (int c = 0; c < C::NCH; ++c)
+        for (int e = p.kt * 8 + threadIdx.x; e < BN * 8; e += C::THREADS)
+          *reinterpret_cast<uint4*>(sm.v[s] + c * CHUNK + e * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sm.tmem_base;
+  // (every warp: the waits on barriers are bounded, this one is not)
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&p.tq);
+      prefetch_tmap(&p.tk);
+      prefetch_tmap(&p.tv);
+    }
+    const uint32_t items = *reinterpret_cast<volatile unsigned*>(&p.counters->items);
+    uint32_t i = blockIdx.x, q_it = 0, g = 0, v_it = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const uint32_t b = k % kItems;
+      Item t;
+      uint32_t next = 0;
+      if (i < items) {
+        if (lane == 0) next = atomicAdd(&p.counters->next, 1u);   // (used after this piece)
+        const int e = p.fd_units.div(i), u = static_cast<int>(i) - e * p.units;
+        const Entry en = p.entries[e];
+        const Row r = row_at(p, en.row);
+        t.n0 = en.n0;
+        t.ntok = en.ntok;
+        t.pos0 = en.pos0;
+        t.len = en.len;
+        t.s0 = en.s0;
+        t.nst = en.s1 - en.s0;
+        t.slot = en.slot < 0 ? -1 : en.slot * p.units + u;
+        tile_walk(p, en.pos0, en.ntok, en.len, t.jlo, t.ns);
+        tile_keys(p, r.start, r.ntok, r.len, t.rlo, t.rhi);
+        t.batch = p.offsets ? 0 : en.row;
+        t.kvh = p.fd_parts.div(u);
+        const int part = u - t.kvh * p.parts;
+        t.h0 = t.kvh * p.group + part * p.gh;
+        t.nh = min(p.gh, p.group - part * p.gh);
+        t.row = en.row;
+      } else {
+        t.n0 = -1;
+        t.nst = 0;
+      }
+      if (!mbar_wait_warp(&sm.item_empty[b], ((k / kItems) & 1) ^ 1, abort, kWaitTimeoutNs)) {
+        fail(p.status, abort, kSiteItemSlot);
+        break;
+      }
+      if (lane == 0) {
+        sm.item[b] = t;
+        mbar_arrive(&sm.item_full[b]);
+      }
+      if (t.n0 < 0) break;
+      const Pages pages{p, p.table + static_cast<long long>(t.row) * p.max_pages, t.len};
+      int page = t.nst > 0 ? pages.at(step_tile(t, 0), lane) : -1;
+      for (int j = 0; j < t.nst; ++j, ++g) {
+        const int jt = step_tile(t, j);
+        const int page_next = j + 1 < t.nst ? pages.at(step_tile(t, j + 1), lane) : -1;
+        const int st = g % C::STAGES;
+        const uint32_t ph = (g / C::STAGES) & 1;
+        if (!mbar_wait_warp(&sm.k_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteK);
+          ok = false;
+          break;
+        }
+        // which keys exist, and the first one's position
+        {
+          KeyMask& km = sm.mask[g % kRing];
+          if (p.ppt) {
+            uint32_t have[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int m = 32 * w + lane;
+              const int pg = w == 0 ? page : (32 * w < p.ppt ? pages.at(jt, m) : -1);
+              have[w] = __ballot_sync(0xffffffffu, pg >= 0);
+            }
+            if (lane < 4) {
+              uint32_t word = 0;
+              if (p.ppt <= 32 && have[0] == bits_below(p.ppt)) {
+                word = bits_below(p.kt - 32 * lane);
+              } else {
+                for (int x = 0; x < 32; ++x) {
+                  const int m = p.fd_ps.div(32 * lane + x);
+                  const uint32_t w = m < 32 ? have[0] : (m < 64 ? have[1] : (m < 96 ? have[2] : have[3]));
+                  if (m < p.ppt && ((w >> (m & 31)) & 1u)) word |= 1u << x;
+                }
+              }
+              km.word[lane] = word;
+            }
+          } else {
+            const int pg = __shfl_sync(0xffffffffu, page, 0);
+            page = pg;
+            const int pj = p.fd_tpp.div(jt), slot0 = (jt - pj * p.tpp) * BN;
+            if (lane < 4)
+              km.word[lane] = pg < 0 ? 0u : bits_below(p.page_size - slot0 - 32 * lane);
+          }
+          if (lane == 0) km.pos = tile_pos(p, jt);
+          __syncwarp();
+        }
+        load_tile<D>(p, pages, jt, page, t.kvh, sm.k[st], &p.tk, &sm.k_full[st]);
+        if (j == 0) {
+          // Q after the first keys: its buffer is free only when the piece
+          // before has no more products to issue
+          if (!mbar_wait_warp(&sm.q_empty, (q_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteQ);
+            ++g;                               // (K of this tile is in flight)
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.q_full, p.gh * p.tpt * (D * 2));
+#pragma unroll
+            for (int c = 0; c < C::NCH; ++c)
+              tma_load_4d(sm.q + c * CHUNK, &p.tq, &sm.q_full, 64 * c, t.h0, t.n0, t.batch);
+          }
+          __syncwarp();
+          ++q_it;
+        }
+        if constexpr (!C::SEP) {
+          if (!mbar_wait_warp(&sm.v_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteV);
+            ++g;
+            ok = false;
+            break;
+          }
+          load_tile<D>(p, pages, jt, page, t.kvh, sm.v[st], &p.tv, &sm.v_full[st]);
+          ++v_it;
+        }
+        page = page_next;
+      }
+      i = __shfl_sync(0xffffffffu, next, 0);
+    }
+    // no copy may still be landing when the CTA exits
+    if (q_it > 0 && !mbar_wait_warp(&sm.q_full, (q_it - 1) & 1, nullptr, kWaitTimeoutNs))
+      fail(p.status, abort, kSiteDrain);
+    for (int s = 0; s < C::STAGES; ++s) {
+      if (g > static_cast<uint32_t>(s) &&
+          !mbar_wait_warp(&sm.k_full[s], ((g - 1 - s) / C::STAGES) & 1, nullptr, kWaitTimeoutNs))
+        fail(p.status, abort, kSiteDrain);
+      if (v_it > static_cast<uint32_t>(s) &&
+          !mbar_wait_warp(&sm.v_full[s], ((v_it - 1 - s) / C::STAGES) & 1, nullptr, kWaitTimeoutNs))
+        fail(p.status, abort, kSiteDrain);
+    }
+  } else if (C::SEP && warp == C::WARPS - 1) {
+    // ------------------------------------------------------------ V producer (d = 256)
+    uint32_t k = 0, v_it = 0;
+    bool ok = true;
+    for (Item t; ok && next_item(sm, k, t, p.status);) {
+      const Pages pages{p, p.table + static_cast<long long>(t.row) * p.max_pages, t.len};
+      int page = t.nst > 0 ? pages.at(step_tile(t, 0), lane) : -1;
+      for (int j = 0; j < t.nst; ++j) {
+        const int jt = step_tile(t, j);
+        const int page_next = j + 1 < t.nst ? pages.at(step_tile(t, j + 1), lane) : -1;
+        const int st = v_it % C::STAGES;
+        if (!mbar_wait_warp(&sm.v_empty[st], ((v_it / C::STAGES) & 1) ^ 1, abort,
+                            kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteV);
+          ok = false;
+          break;
+        }
+        if (!p.ppt) page = __shfl_sync(0xffffffffu, page, 0);
+        load_tile<D>(p, pages, jt, page, t.kvh, sm.v[st], &p.tv, &sm.v_full[st]);
+        ++v_it;
+        page = page_next;
+      }
+    }
+    for (int s = 0; s < C::STAGES; ++s)
+      if (v_it > static_cast<uint32_t>(s) &&
+          !mbar_wait_warp(&sm.v_full[s], ((v_it - 1 - s) / C::STAGES) & 1, nullptr, kWaitTimeoutNs))
+        fail(p.status, abort, kSiteDrain);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, 0, 0);
+    const uint64_t dq0 = sdesc_sw128(smem_u32(sm.q), 16, 1024);
+    uint32_t k = 0, q_it = 0, g = 0;
+    bool ok = true;
+    for (Item t; ok && next_item(sm, k, t, p.status);) {
+      for (int j = 0; j < t.nst; ++j, ++g) {
+        const uint32_t b = g % C::NSB;
+        if (j == 0) {
+          if (!mbar_wait_warp(&sm.q_full, q_it & 1, abort, kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteMmaQ);
+            ok = false;
+            break;
+          }
+          ++q_it;
+        }
+        if (g >= static_cast<uint32_t>(C::NSB) &&
+            !mbar_wait_warp(C::SEP ? &sm.s_free[b] : &sm.pv_done[b], ((g / C::NSB) & 1) ^ 1, abort,
+                            kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteMmaS);
+          ok = false;
+          break;
+        }
+        const int st = g % C::STAGES;
+        if (!mbar_wait_warp(&sm.k_full[st], (g / C::STAGES) & 1, abort, kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteMmaK);
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint64_t dk0 = sdesc_sw128(smem_u32(sm.k[st]), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < C::NCH * 4; ++kk) {
+          const uint32_t off = (kk / 4) * CHUNK + (kk % 4) * 32;
+          mma_bf16_ss_w(tmem + C::TM_S + 128 * b, dq0 + (off >> 4), dk0 + (off >> 4), kIdescS,
+                        kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(&sm.k_empty[st]);
+        mma_commit_w(&sm.s_full[b]);
+        if (j == t.nst - 1) mma_commit_w(&sm.q_empty);
+      }
+    }
+    // every product issued by this thread must finish before exit
+    mma_commit_w(&sm.mma_done);
+    if (!mbar_wait_warp(&sm.mma_done, 0, nullptr, kWaitTimeoutNs))
+      fail(p.status, abort, kSiteDrain);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ P V issuer
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, 0, 1);
+    uint32_t k = 0, g = 0, o_it = 0;
+    bool ok = true;
+    for (Item t; ok && next_item(sm, k, t, p.status);) {
+      for (int j = 0; j < t.nst; ++j, ++g) {
+        const uint32_t b = g % C::NPB;
+        const int st = g % C::STAGES;
+        if (!mbar_wait_warp(&sm.v_full[st], (g / C::STAGES) & 1, abort, kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteMmaV);
+          ok = false;
+          break;
+        }
+        // slots that no token of the row sees may hold anything, and 0 NaN is
+        // NaN: zeros in their place
+        const int pos = tile_pos(p, step_tile(t, j));
+        if (pos + p.kt > t.rhi || (pos < t.rlo && pos + p.kt > p.sinks)) {
+          for (int e = lane; e < p.kt * 8; e += 32) {
+            const int x = pos + e / 8;
+            if (x >= t.rhi || (x < t.rlo && x >= p.sinks)) {
+#pragma unroll
+              for (int c = 0; c < C::NCH; ++c)
+                *reinterpret_cast<uint4*>(sm.v[st] + c * CHUNK + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (j == 0) {
+          if (!mbar_wait_warp(&sm.o_free, (o_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteMmaO);
+            ok = false;
+            break;
+          }
+          ++o_it;
+        }
+        const uint64_t dv0 = sdesc_sw128(smem_u32(sm.v[st]), BN * 128, 1024);
+#pragma unroll
+        for (int h = 0; h < C::NHALF; ++h) {
+          if (!mbar_wait_warp(&sm.p_full[b * C::NHALF + h], (g / C::NPB) & 1, abort,
+                              kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteMmaP);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          constexpr int KH = BN / 16 / C::NHALF;
+#pragma unroll
+          for (int kk = 0; kk < KH; ++kk)
+            mma_bf16_ts_w(tmem + C::TM_O + D * h,
+                          tmem + C::TM_P + C::P_STRIDE * b + (BN / C::NHALF) * h + kk * 8,
+                          dv0 + static_cast<uint64_t>(((h * KH + kk) * 16 * 128) >> 4), kIdescPV,
+                          (j == 0 && kk == 0) ? 0u : 1u);
+        }
+        if (!ok) break;
+        mma_commit_w(&sm.v_empty[st]);
+        mma_commit_w(&sm.pv_done[b]);
+        if (j == t.nst - 1) mma_commit_w(&sm.o_done);
+      }
+    }
+    mma_commit_w(&sm.pv_mma_done);
+    if (!mbar_wait_warp(&sm.pv_mma_done, 0, nullptr, kWaitTimeoutNs))
+      fail(p.status, abort, kSiteDrain);
+  } else if (warp >= C::EPI_WARP0) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;           // the thread's row of the tile
+    const int tr = p.fd_gh.div(r), hr = r - tr * p.gh;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const bool st32 = ((reinterpret_cast<uintptr_t>(p.o) | (p.ob * 2) | (p.oh * 2) | (p.ot * 2)) & 31) == 0;
+    uint32_t k = 0, e_it = 0;
+    for (Item t; next_item(sm, k, t, p.status);) {
+      const bool valid = tr < t.ntok && hr < t.nh;
+      __nv_bfloat16* out = p.o + t.batch * p.ob + (t.h0 + hr) * p.oh + (t.n0 + tr) * p.ot;
+      float* lse = p.lse + (static_cast<long long>(t.batch) * p.H + t.h0 + hr) * p.N + t.n0 + tr;
+      const long long part = static_cast<long long>(t.slot) * p.slot_rows + r;
+      if (t.nst == 0) {                          // nothing to see: O = 0, LSE = -inf
+        if (valid) {
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+          *lse = -INFINITY;
+        }
+        continue;
+      }
+      const uint32_t ph = e_it & 1;
+      ++e_it;
+      if (!mbar_wait_warp(&sm.stats_full, ph, abort, kWaitTimeoutNs) ||
+          !mbar_wait_warp(&sm.o_done, ph, abort, kWaitTimeoutNs)) {
+        fail(p.status, abort, kSiteEpi);
+        break;
+      }
+      tc_fence_after_sync();
+      // the halves against the larger maximum: O = sum_h a_h O_h / sum_h a_h l_h
+      float a[C::NHALF], m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int h = 0; h < C::NHALF; ++h) m = fmaxf(m, sm.ostat[C::NHALF + h][r]);
+#pragma unroll
+      for (int h = 0; h < C::NHALF; ++h) {
+        const float mh = sm.ostat[C::NHALF + h][r];
+        a[h] = mh == -INFINITY ? 0.f : ex2_approx(mh - m);
+        l += a[h] * sm.ostat[h][r];
+      }
+      // (a sum that is not a number stays one)
+      const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      const float lse_row = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+      for (int h = 0; h < C::NHALF; ++h) a[h] *= inv_l;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t orr[C::NHALF][32];
+#pragma unroll
+        for (int h = 0; h < C::NHALF; ++h) tmem_ld_x32(t_lane + C::TM_O + D * h + 32 * c, orr[h]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < C::NHALF; ++h) reg_fence<32>(orr[h]);
+        if (c == D / 32 - 1) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.o_free);
+        }
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          o[e] = __uint_as_float(orr[0][e]) * a[0];
+#pragma unroll
+          for (int h = 1; h < C::NHALF; ++h) o[e] = fmaf(__uint_as_float(orr[h][e]), a[h], o[e]);
+        }
+        if (!valid) continue;
+        if (t.slot >= 0) {
+          float* dst = p.o_part + part * D + 32 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t r8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r8[e] = __float_as_uint(o[8 * i + e]);
+            st_global_v8(dst + 8 * i, r8);
+          }
+        } else {
+          __nv_bfloat16* dst = out + 32 * c;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              pk8[e] = pack_bf16x2(o[16 * i + 2 * e], o[16 * i + 2 * e + 1]);
+            if (st32) {
+              st_global_v8(dst + 16 * i, pk8);
+            } else {
+              uint4* d4 = reinterpret_cast<uint4*>(dst + 16 * i);
+              d4[0] = make_uint4(pk8[0], pk8[1], pk8[2], pk8[3]);
+              d4[1] = make_uint4(pk8[4], pk8[5], pk8[6], pk8[7]);
+            }
+          }
+        }
+      }
+      if (valid) {
+        if (t.slot >= 0)
+          p.lse_part[part] = lse_row;
+        else
+          *lse = lse_row;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;
+    const int hf = (warp - 3) >> 2;
+    constexpr int NC = BN / C::NHALF;            // keys of a tile that this warp takes
+    const int r = quarter * 32 + lane;
+    const int tr = p.fd_gh.div(r);
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t t_o = t_lane + C::TM_O + D * hf;
+    const float c2 = p.scale_log2;
+    uint32_t k = 0, kv_it = 0, e_it = 0;
+    bool ok = true;
+    for (Item t; ok && next_item(sm, k, t, p.status);) {
+      if (t.nst == 0) continue;
+      // this row sees keys [.., hi] from lo on or below the sinks (a row behind
+      // the tile's last counts as that one)
+      const auto last_key = [&](int pos) {
+        if (p.causal && pos >= t.len) return -1;
+        const long long h = static_cast<long long>(pos) + p.wr;
+        return static_cast<int>(h < t.len - 1 ? (h < -1 ? -1 : h) : t.len - 1);
+      };
+      const int pos = t.pos0 + min(tr, t.ntok - 1), pos_last = t.pos0 + t.ntok - 1;
+      const int hi = last_key(pos), lo = max(pos, p.wl) - p.wl;
+      // what every row of the tile sees
+      const int all_hi = min(last_key(t.pos0), last_key(pos_last));
+      const int all_lo = max(pos_last, p.wl) - p.wl;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < t.nst; ++j) {
+        const uint32_t b = kv_it % C::NSB;
+        const uint32_t t_s = t_lane + C::TM_S + 128 * b;
+        if (!mbar_wait_warp(&sm.s_full[b], (kv_it / C::NSB) & 1, abort, kWaitTimeoutNs)) {
+          fail(p.status, abort, kSiteSmS);
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t sr[NC];
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) tmem_ld_x32(t_s + NC * hf + 32 * c, sr + 32 * c);
+        const KeyMask& km = sm.mask[kv_it % kRing];
+        uint32_t word[NC / 32], whole = ~0u;
+#pragma unroll
+        for (int w = 0; w < NC / 32; ++w) {
+          word[w] = km.word[NC / 32 * hf + w];
+          whole &= word[w];
+        }
+        const int key0 = km.pos + NC * hf;
+        tmem_wait_ld();
+        reg_fence<NC>(sr);
+        if constexpr (C::SEP) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free[b]);
+        }
+        float s[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sr[c]);
+        if (whole != ~0u || key0 + NC - 1 > all_hi || (key0 < all_lo && key0 + NC > p.sinks)) {
+          const int c_hi = hi - key0, c_lo = lo - key0;
+#pragma unroll
+          for (int w = 0; w < NC / 32; ++w) {
+            const uint32_t on = word[w] & bits_below(c_hi + 1 - 32 * w) &
+                                (~bits_below(c_lo - 32 * w) | bits_below(p.sinks - key0 - 32 * w));
+            if (__any_sync(0xffffffffu, on != ~0u)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((on >> c) & 1u)) s[32 * w + c] = -INFINITY;
+            }
+          }
+        }
+        float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+        for (int c = 4; c + 8 <= NC; c += 8) {
+          mx0 = fmax3(mx0, s[c], s[c + 1]);
+          mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+          mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+          mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+        }
+        mx0 = fmax3(mx0, s[NC - 4], s[NC - 3]);
+        mx1 = fmax3(mx1, s[NC - 2], s[NC - 1]);
+        const float m_blk = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (m_ref == -INFINITY) {
+          if (m_blk != -INFINITY) {
+            alpha = 0.f;
+            m_ref = m_blk;
+          }
+        } else if (m_blk > m_ref + kRescaleSlack) {
+          alpha = ex2_approx(m_ref - m_blk);
+          m_ref = m_blk;
+          rescale = true;
+        }
+        const float base = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t c2x2 = f2_make(c2, c2), nbx2 = f2_make(-base, -base);
+        uint64_t rsa = f2_make(0.f, 0.f), rsb = f2_make(0.f, 0.f);
+        uint32_t pk[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC / 2; c += 2) {
+          float a0, a1, a2, a3;
+          f2_split(f2_fma(f2_make(s[2 * c], s[2 * c + 1]), c2x2, nbx2), a0, a1);
+          f2_split(f2_fma(f2_make(s[2 * c + 2], s[2 * c + 3]), c2x2, nbx2), a2, a3);
+          const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+          const float p2 = ex2_approx(a2), p3 = ex2_approx(a3);
+          rsa = f2_add(rsa, f2_make(p0, p1));
+          rsb = f2_add(rsb, f2_make(p2, p3));
+          pk[c] = pack_bf16x2(p0, p1);
+          pk[c + 1] = pack_bf16x2(p2, p3);
+        }
+        float rs0, rs1, rs2, rs3;
+        f2_split(rsa, rs0, rs1);
+        f2_split(rsb, rs2, rs3);
+        l = l * alpha + ((rs0 + rs1) + (rs2 + rs3));
+        const uint32_t pb = kv_it % C::NPB;
+        if constexpr (C::SEP) {
+          if (kv_it >= static_cast<uint32_t>(C::NPB) &&
+              !mbar_wait_warp(&sm.pv_done[pb], ((kv_it / C::NPB) & 1) ^ 1, abort,
+                              kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteSmP);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+        }
+        const uint32_t t_p = t_lane + C::TM_P + C::P_STRIDE * pb + NC * hf;
+        tmem_st_x32(t_p, pk);
+        if constexpr (NC == 128) tmem_st_x32(t_p + 32, pk + 32);
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O holds every earlier product before it is scaled
+          const uint32_t prev = kv_it - 1;
+          if (!mbar_wait_warp(&sm.pv_done[prev % C::NPB], (prev / C::NPB) & 1, abort,
+                              kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteSmO);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t a2 = f2_make(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t orr[32];
+            tmem_ld_x32(t_o + 32 * c, orr);
+            tmem_wait_ld();
+            reg_fence<32>(orr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_split(f2_mul(f2_make(__uint_as_float(orr[2 * i]), __uint_as_float(orr[2 * i + 1])), a2), x0, x1);
+              orr[2 * i] = __float_as_uint(x0);
+              orr[2 * i + 1] = __float_as_uint(x1);
+            }
+            tmem_st_x32(t_o + 32 * c, orr);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[pb * C::NHALF + hf]);
+        ++kv_it;
+      }
+      if (!ok) break;
+      // hand the rows' sums and maxima over, once the epilogue of the piece
+      // before has read its own
+      ++e_it;
+      if (!mbar_wait_warp(&sm.o_free, ((e_it - 1) & 1) ^ 1, abort, kWaitTimeoutNs)) {
+        fail(p.status, abort, kSiteEpi);
+        break;
+      }
+      sm.ostat[hf][r] = l;
+      sm.ostat[C::NHALF + hf][r] = m_ref;
+      mbar_arrive(&sm.stats_full);
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- the join
+
+// Cut tiles: per row LSE = log sum_s exp(LSE_s) and O = sum_s exp(LSE_s - LSE)
+// O_s, pieces in order.  Few pieces: a warp a row; many: a block a row, its
+// warps every fourth piece each.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefillParams p) {
+  grid_dependency_wait();
+  constexpr int PER = D / 32, W = 4;
+  __shared__ float sm_o[W][D];
+  __shared__ float sm_w[W];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Counters c = *p.counters;
+  const bool wide = c.most > 8;
+  const long long rows = static_cast<long long>(c.joins) * p.units * p.slot_rows;
+  const long long step = wide ? 1 : W;
+  for (long long x0 = blockIdx.x * step; x0 < rows; x0 += gridDim.x * step) {
+    const long long x = wide ? x0 : x0 + warp;
+    JoinEntry j = {};
+    int u = 0, r = 0, tr = 0, h = 0;
+    bool valid = x < rows;
+    if (valid) {
+      const long long item = x / p.slot_rows;
+      r = static_cast<int>(x - item * p.slot_rows);
+      const int e = static_cast<int>(item / p.units);
+      u = static_cast<int>(item - static_cast<long long>(e) * p.units);
+      j = p.joins[e];
+      tr = p.fd_gh.div(r);
+      const int kvh = p.fd_parts.div(u), pt = u - kvh * p.parts;
+      h = kvh * p.group + pt * p.gh + (r - tr * p.gh);
+      valid = tr < j.ntok && r - tr * p.gh < min(p.gh, p.group - pt * p.gh);
+    }
+    if (!wide && !valid) continue;
+    if (wide && !valid) continue;       // (the whole block)
+    const auto at = [&](int s) {
+      return (static_cast<long long>(j.slot0 + s) * p.units + u) * p.slot_rows + r;
+    };
+    // the largest LSE (a NaN stays in the sums below)
+    float m = -INFINITY;
+    for (int s = lane; s < j.pieces; s += 32) m = fmaxf(m, p.lse_part[at(s)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[PER], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int s = wide ? warp : 0; s < j.pieces; s += wide ? W : 1) {
+      const float w = expf(p.lse_part[at(s)] - base);
+      const float* src = p.o_part + at(s) * D + lane * PER;
+      sum += w;
+      if constexpr (PER == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src + i);
+          acc[i] = fmaf(w, v.x, acc[i]);
+          acc[i + 1] = fmaf(w, v.y, acc[i + 1]);
+          acc[i + 2] = fmaf(w, v.z, acc[i + 2]);
+          acc[i + 3] = fmaf(w, v.w, acc[i + 3]);
+        }
+      }
+    }
+    if (wide) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sm_o[warp][lane * PER + i] = acc[i];
+      if (lane == 0) sm_w[warp] = sum;
+      __syncthreads();
+      if (warp > 0) continue;
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        sum += sm_w[w];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += sm_o[w][lane * PER + i];
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long tok = j.n0 + tr;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + j.batch * p.ob + h * p.oh + tok * p.ot +
+                                                lane * PER);
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i)
+      dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0)
+      p.lse[(static_cast<long long>(j.batch) * p.H + h) * p.N + tok] =
+          sum == 0.f ? -INFINITY : base + logf(sum);
+  }
+}
+
+// ---------------------------------------------------------------- the host's side
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Everything that the sizes determine; false for sizes that no call takes.
+struct Shape {
+  int group, gh, parts, units, tpt, slot_rows;
+  long long tiles, entries, slots;       // (slots: of all units)
+};
+
+bool shape_of(int B, int H, int N, int h_kv, bool packed, int num_sms, Shape* s) {
+  if (B < 1 || H < 1 || N < 1 || h_kv < 1 || H % h_kv || N >= kMaxPositions) return false;
+  s->group = H / h_kv;
+  s->parts = (s->group + BM - 1) / BM;
+  s->gh = (s->group + s->parts - 1) / s->parts;
+  s->units = h_kv * s->parts;
+  s->tpt = BM / s->gh;
+  s->slot_rows = s->gh * (N < s->tpt ? N : s->tpt);
+  s->tiles = packed ? N / s->tpt + static_cast<long long>(B)
+                    : static_cast<long long>(B) * ((N + s->tpt - 1) / s->tpt);
+  const long long cut = 2ll * kMostRounds * num_sms / s->units + 1;
+  s->entries = s->tiles + cut;
+  s->slots = cut * s->units;
+  return s->entries * s->units < INT_MAX - 4096 && static_cast<long long>(B) * H < INT_MAX &&
+         (packed || static_cast<long long>(B) * N < INT_MAX);
+}
+
+struct Layout {
+  size_t rows, entries, joins, o_part, lse_part, total;
+};
+
+Layout layout_of(const Shape& s, int B, int d) {
+  Layout l;
+  l.rows = 256;
+  l.entries = l.rows + up256((static_cast<size_t>(B) + 1) * sizeof(int));
+  l.joins = l.entries + up256(static_cast<size_t>(s.entries) * sizeof(Entry));
+  l.o_part = l.joins + up256(static_cast<size_t>(s.slots / s.units) * sizeof(JoinEntry));
+  const size_t rows = static_cast<size_t>(s.slots) * s.slot_rows;
+  l.lse_part = l.o_part + up256(rows * d * sizeof(float));
+  l.total = l.lse_part + up256(rows * sizeof(float));
+  return l;
+}
+
+template <int D>
+cudaError_t launch(PrefillParams& p, int max_smem, cudaStream_t stream) {
+  const size_t smem = smem_request(sizeof(Smem<D>), max_smem);
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess) e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, stream, p);
+  if (e == cudaSuccess) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(Cfg<D>::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prefill_kernel<D>, p);
+  }
+  if (e == cudaSuccess) e = launch_dependent(join_kernel<D>, dim3(p.grid * 8), 128, stream, p);
+  return e;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+size_t fa_prefill_paged_workspace_bytes(int B, int H, int N, int h_kv, int d, int packed) {
+  int sms = 0;
+  if (fa::device_facts(&sms) != FA_OK) sms = 152;
+  fa::Shape s;
+  if ((d != 64 && d != 128 && d != 256) || !fa::shape_of(B, H, N, h_kv, packed != 0, sms, &s))
+    return 0;
+  return fa::layout_of(s, B, d).total;
+}
+
+fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, int layer,
+                             const int* block_table, int max_pages, const int* start,
+                             const int* kv_len, const int* offsets, const fa_strided_t* o,
+                             float* lse, int B, int H, int N, float scale, int causal,
+                             int window_left, int window_right, int sinks, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!lse || !start || !kv_len || layer < 0) return FA_ERR_INVALID_ARG;
+  if (!fa::aligned_to(lse, 4) || !fa::aligned_to(start, 4) || !fa::aligned_to(kv_len, 4) ||
+      !fa::aligned_to(offsets, 4) || !workspace || !fa::aligned_to(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  fa::PagePool pool;
+  const fa_status_t ps = fa::resolve_pool(cache, layer, &pool);
+  if (ps != FA_OK) return ps;
+  if (!fa::table_ok(block_table, max_pages, pool.page_size)) return FA_ERR_INVALID_ARG;
+  if (window_left < -1 || window_right < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f && scale <= 3.402823466e38f)) return FA_ERR_INVALID_ARG;
+  int sms = 0, max_smem = 0;
+  int* status = nullptr;
+  fa::Shape s;
+  // (the sizes are checked before the device is asked)
+  if (!fa::shape_of(B, H, N, pool.h_kv, offsets != nullptr, 1, &s)) return FA_ERR_INVALID_ARG;
+  const int batch = offsets ? 1 : B;
+  if (!fa::strided_ok(q, batch, H, N, pool.d, true) ||
+      !fa::strided_ok(o, batch, H, N, pool.d, true))
+    return FA_ERR_INVALID_ARG;
+  const fa_status_t ds = fa::device_facts(&sms, &max_smem, &status);
+  if (ds != FA_OK) return ds;
+  if (!fa::shape_of(B, H, N, pool.h_kv, offsets != nullptr, sms, &s)) return FA_ERR_INVALID_ARG;
+  const fa::Layout l = fa::layout_of(s, B, pool.d);
+  if (workspace_bytes < l.total) return FA_ERR_INVALID_ARG;
+  fa::PrefillParams p = {};
+  const long long qd[3] = {H, N, batch};
+  const long long qs[3] = {q->head_stride, q->token_stride, q->batch_stride};
+  const int qb[3] = {s.gh, s.tpt, 1};
+  const long long kd[3] = {pool.page_size, pool.h_kv, pool.num_pages};
+  const long long ks[3] = {pool.token_stride, pool.head_stride, pool.page_stride};
+  const int kb[3] = {pool.page_size < fa::BM ? pool.page_size : fa::BM, 1, 1};
+  if (!fa::make_map_4d(&p.tq, q->p, pool.d, qd, qs, qb) ||
+      !fa::make_map_4d(&p.tk, pool.k, pool.d, kd, ks, kb) ||
+      !fa::make_map_4d(&p.tv, pool.v, pool.d, kd, ks, kb))
+    return FA_ERR_CUDA;
+  p.o = static_cast<__nv_bfloat16*>(o->p);
+  p.ob = batch > 1 ? o->batch_stride : 0;
+  p.oh = H > 1 ? o->head_stride : 0;
+  p.ot = N > 1 ? o->token_stride : 0;
+  p.lse = lse;
+  p.table = block_table;
+  p.start = start;
+  p.kv_len = kv_len;
+  p.offsets = offsets;
+  p.B = B;
+  p.H = H;
+  p.N = N;
+  p.h_kv = pool.h_kv;
+  p.group = s.group;
+  p.gh = s.gh;
+  p.parts = s.parts;
+  p.units = s.units;
+  p.tpt = s.tpt;
+  p.fd_units = fa::FastDiv::of(s.units);
+  p.fd_parts = fa::FastDiv::of(s.parts);
+  p.fd_gh = fa::FastDiv::of(s.gh);
+  p.fd_tn = fa::FastDiv::of((N + s.tpt - 1) / s.tpt);
+  p.max_pages = max_pages;
+  p.num_pages = pool.num_pages;
+  p.page_size = pool.page_size;
+  p.ppt = pool.page_size <= fa::BN ? fa::BN / pool.page_size : 0;
+  p.tpp = (pool.page_size + fa::BN - 1) / fa::BN;
+  p.kt = p.ppt ? p.ppt * pool.page_size : fa::BN;
+  p.fd_kt = fa::FastDiv::of(p.kt);
+  p.fd_ps = fa::FastDiv::of(pool.page_size);
+  p.fd_tpp = fa::FastDiv::of(p.tpp);
+  p.causal = causal != 0;
+  p.wl = window_left < 0 || window_left > fa::kUnbounded ? fa::kUnbounded : window_left;
+  p.wr = window_right < 0 || window_right > fa::kUnbounded ? fa::kUnbounded : window_right;
+  if (p.causal && p.wr > 0) p.wr = 0;
+  p.sinks = sinks;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.status = status;
+  char* ws = static_cast<char*>(workspace);
+  p.counters = reinterpret_cast<fa::Counters*>(ws);
+  p.row_tiles = reinterpret_cast<int*>(ws + l.rows);
+  p.entries = reinterpret_cast<fa::Entry*>(ws + l.entries);
+  p.joins = reinterpret_cast<fa::JoinEntry*>(ws + l.joins);
+  p.o_part = reinterpret_cast<float*>(ws + l.o_part);
+  p.lse_part = reinterpret_cast<float*>(ws + l.lse_part);
+  p.cap_entries = static_cast<int>(s.entries);
+  p.cap_slots = static_cast<int>(s.slots / s.units);
+  p.slot_rows = s.slot_rows;
+  p.grid = sms;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pool.d == 64    ? fa::launch<64>(p, max_smem, st)
+                        : pool.d == 128 ? fa::launch<128>(p, max_smem, st)
+                                        : fa::launch<256>(p, max_smem, st);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -42,6 +42,21 @@ class FaPagedKV(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int)]
 
 
+class FaStrided(ctypes.Structure):
+    """fa_strided_t: a tensor's address and its batch, head and token strides
+    in elements."""
+    _fields_ = [("p", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong)]
+
+
+class FaRotary(ctypes.Structure):
+    """fa_rotary_t: the pairs' angles per position (device pointer), the factor
+    of a turned vector, the values turned and how they pair (rope.Rotary fills
+    one)."""
+    _fields_ = [("turns", ctypes.c_void_p), ("magnitude", ctypes.c_float),
+                ("dims", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
 class BlockMask:
     """A block mask on the device together with its host copy.  Any function
     taking block_mask= accepts one in place of the CUDA tensor; the library
@@ -129,6 +144,17 @@ def load():
         lib.fa_pages_trim.restype = i
         lib.fa_pages_compact.argtypes = [pool, vp, i, vp, i, vp, vp, vp, vp, sz, vp]
         lib.fa_pages_compact.restype = i
+        view, rotary = ctypes.POINTER(FaStrided), ctypes.POINTER(FaRotary)
+        lib.fa_rotate.argtypes = [view, view, i, view, view, i, i, i, i, vp, vp, rotary, i, vp]
+        lib.fa_rotate.restype = i
+        lib.fa_paged_append_rotated.argtypes = [view, view, i, view, view, pool, i, vp, i, vp, vp,
+                                                vp, i, i, rotary, vp]
+        lib.fa_paged_append_rotated.restype = i
+        lib.fa_prefill_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        lib.fa_prefill_paged_workspace_bytes.restype = sz
+        lib.fa_prefill_paged.argtypes = [view, pool, i, vp, i, vp, vp, vp, view, vp, i, i, i, f, i,
+                                         i, i, i, vp, sz, vp]
+        lib.fa_prefill_paged.restype = i
         lib.fa_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
         lib.fa_selftest_wait_timeout.restype = i
         lib.fa_check.argtypes = [vp]
@@ -149,6 +175,8 @@ EXPORTS = ("fa_fwd", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_prep", "fa_bwd_
            "fa_paged_append",
            "fa_pages_workspace_bytes", "fa_pages_reserve", "fa_pages_fork", "fa_pages_trim",
            "fa_pages_compact",
+           "fa_rotate", "fa_paged_append_rotated", "fa_prefill_paged_workspace_bytes",
+           "fa_prefill_paged",
            "fa_fp8_quantize", "fa_fwd_fp8", "fa_selftest_wait_timeout", "fa_check",
            "fa_status_string", "fa_version")
 

@@ -15,6 +15,16 @@ A serving loop::
         append(k_new, v_new, cache, layer, table, kv_len, new_len)
         o, lse = decode(q, cache, layer, table, new_len, window=(4095, 0), sinks=4)
     kv_len = new_len
+
+and with prompts, or several tokens a row, turned and in one pass each (rows
+one after the other in a batch of one, or padded)::
+
+    for layer in range(cache.num_layers):
+        q = append_rotated(q, k_new, v_new, cache, layer, table, kv_len, new_len, rotary, offsets)
+        o, lse = prefill(q, cache, layer, table, kv_len, new_len, offsets)
+
+Keeping the cache::
+
     table, ref = trim(cache, table, kv_len, ref, 4095, 4)
     table, kv_len, ref, info = fork(cache, table, kv_len, ref, parent)
 """
@@ -23,7 +33,7 @@ import math
 
 import torch
 
-from . import fa
+from . import fa, rope
 
 _current_device = torch.cuda.current_device
 # the current stream of a device as a raw handle; torch.cuda.current_stream()
@@ -208,6 +218,93 @@ def append(k_new, v_new, cache, layer, table, start, kv_len, stream=None):
         k_new.data_ptr(), v_new.data_ptr(), cache.ref, layer, tp, max_pages,
         _ints("start", start, shape[:1], index), _ints("kv_len", kv_len, shape[:1], index), rows,
         shape[2], _current_raw_stream(index)), "fa_paged_append")
+
+
+def _rows(cache, table, t, offsets):
+    """(the table's address, rows, its width, the offsets' address) of a call
+    whose queries or keys are t [B, H, N, d]."""
+    tp, rows, max_pages = _table(cache, table)
+    if t.dim() != 4 or t.shape[0] != (rows if offsets is None else 1) or t.shape[3] != cache.d:
+        raise ValueError("expected [rows, H, N, d], or with offsets [1, H, N, d]")
+    return tp, rows, max_pages, rope.ints("offsets", offsets, (rows + 1,), cache.index)
+
+
+def append_rotated(q, k_new, v_new, cache, layer, table, start, kv_len, rotary, offsets=None,
+                   inplace=False, stream=None):
+    """q turned by its tokens' positions, after the turned k_new and v_new have
+    been written into the pages.  q [rows, H, N, d] (or None), k_new, v_new
+    [rows, h_kv, N, d], any strides: row r's token t is at position start[r] +
+    t.  With offsets (int32 [rows + 1]) they are [1, heads, N, d], and row r
+    has the tokens offsets[r] .. offsets[r + 1] - 1; q's other tokens are not
+    turned (and unset where q is not turned in place).  Keys and values are
+    written as append does."""
+    if stream is not None:
+        return _on_stream(append_rotated, stream, q, k_new, v_new, cache, layer, table, start,
+                          kv_len, rotary, offsets, inplace)
+    tp, rows, max_pages, op = _rows(cache, table, k_new, offsets)
+    index = cache.index
+    if rotary.index != index or rotary.d != cache.d:
+        raise ValueError(f"rotary: made for d = {rotary.d} on device {rotary.index}")
+    shape = k_new.shape
+    if shape[1] != cache.h_kv:
+        raise ValueError("k_new: expected the cache's K/V heads")
+    H, qo, qs, qos = 0, None, None, None
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q: expected [B, H, N, d]")
+        H = q.shape[1]
+        qs = rope.view("q", q, (shape[0], H, shape[2], cache.d), index)
+        qo = q if inplace else rope.empty_like(q)
+        qos = rope.view("q", qo, q.shape, index)
+    _check(fa.load().fa_paged_append_rotated(
+        qs, qos, H, rope.view("k_new", k_new, shape, index), rope.view("v_new", v_new, shape, index),
+        cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
+        _ints("kv_len", kv_len, (rows,), index), op, rows, shape[2], rotary.ref,
+        _current_raw_stream(index)), "fa_paged_append_rotated")
+    return qo
+
+
+def prefill_workspace(cache, rows, H, N, packed=False):
+    """A workspace for prefill of up to N tokens (a row, or with offsets all
+    rows) and H query heads."""
+    return torch.empty(fa.load().fa_prefill_paged_workspace_bytes(
+        rows, H, N, cache.h_kv, cache.d, int(packed)), dtype=torch.uint8, device=cache.device)
+
+
+def prefill(q, cache, layer, table, start, kv_len, offsets=None, scale=None, causal=True,
+            window=None, sinks=0, ws=None, stream=None):
+    """(O, LSE): attention of each row's new tokens, at positions start + t,
+    over its pages, which hold their keys already.  q [rows, H, N, d], or with
+    offsets (int32 [rows + 1]) [1, H, N, d], row r's tokens offsets[r] ..
+    offsets[r + 1] - 1; any strides.  O like q, LSE fp32 without d.  causal: a
+    token sees keys up to itself (one at or past kv_len none); window (left,
+    right) and sinks as in decode; causal=False without a window sees all of
+    kv_len, an encoder's states for instance.  A token that sees nothing gets O
+    = 0, LSE = -inf; tokens of no row are unset.  ws: prefill_workspace(), else
+    allocated."""
+    if stream is not None:
+        return _on_stream(prefill, stream, q, cache, layer, table, start, kv_len, offsets, scale,
+                          causal, window, sinks, ws)
+    tp, rows, max_pages, op = _rows(cache, table, q, offsets)
+    index = cache.index
+    B, H, N, d = shape = q.shape
+    sizes = ("prefill", rows, H, N, op is not None)
+    need = cache._need.get(sizes)
+    if need is None:
+        need = _keep(cache, sizes, fa.load().fa_prefill_paged_workspace_bytes(
+            rows, H, N, cache.h_kv, d, int(op is not None)))
+    qs = rope.view("q", q, shape, index)
+    o = rope.empty_like(q)
+    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    ws, wp = _bytes(ws, need, q)
+    left, right = fa._window(window)
+    _check(fa.load().fa_prefill_paged(
+        qs, cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
+        _ints("kv_len", kv_len, (rows,), index), op, rope.view("o", o, shape, index),
+        lse.data_ptr(), rows, H, N, cache.scale if scale is None else scale, 1 if causal else 0,
+        left, right, _count(sinks), wp, ws.numel() * ws.element_size(),
+        _current_raw_stream(index)), "fa_prefill_paged")
+    return o, lse
 
 
 def reserve(cache, table, kv_len, ref, n_new, ws=None, stream=None):

@@ -339,6 +339,107 @@ fa_status_t fa_paged_append(const void* k_new, const void* v_new, const fa_paged
                             const int* kv_len, int B, int Nq, void* stream);
 
 /*
+ * A bf16 tensor [B, H, N, d] seen through strides: element (b, h, t, c) is
+ * p[b batch_stride + h head_stride + t token_stride + c].  p is 16-byte
+ * aligned; the strides count elements and are multiples of 8 (that of an axis
+ * of one does not count), so that [B, H, N, d], [B, N, H, d] and a slice of a
+ * fused projection all serve.  No two elements of a written tensor, nor of a
+ * chunk's q, share a place.  Offsets are 64-bit.
+ */
+typedef struct fa_strided {
+  void* p;
+  long long batch_stride;
+  long long head_stride;
+  long long token_stride;
+} fa_strided_t;
+
+/*
+ * Rotary positions.  The first `dims` values of a head (even, at most d) are
+ * dims/2 pairs: values i and i + dims/2, or 2i and 2i + 1 when interleaved.
+ * The token at position x has its pair i turned by the angle
+ * 2 pi x turns[i] / 2^64, that is (a, b) becomes
+ *   m (a cos - b sin),  m (a sin + b cos)   with m = magnitude;
+ * values from dims on stay as they are.  turns: device memory, dims/2 values,
+ * 8-byte aligned: a pair's angle per position as a fraction of a turn (modulo
+ * one) times 2^64, which makes the angle exact to 2^-32 turns at any
+ * position.  Sums are fp32; results are rounded to bf16 once.
+ */
+typedef struct fa_rotary {
+  const unsigned long long* turns;
+  float magnitude;
+  int dims;
+  int interleaved;
+} fa_rotary_t;
+
+/*
+ * Turns queries [B, H, N, d] and keys [B, h_kv, N, d] (h_kv = 0: none, k and
+ * k_out ignored) in one pass.  Token t of batch entry b is at position
+ * pos[b N + t] (int32[B, N]), or start[b] + t (int32[B]), or t where both are
+ * NULL; both together are refused.  back != 0 turns by the negative angle:
+ * the gradients of q_out and k_out to those of q and k (the transpose of a
+ * turn; the magnitude is the same).  An output is its input (turned in place)
+ * or apart from every input.  d is 64, 128 or 256; B * N is below 2^31 - 1 and
+ * H + h_kv below 2^16.
+ */
+fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
+                      const fa_strided_t* k, const fa_strided_t* k_out, int h_kv, int B, int N,
+                      int d, const int* start, const int* pos, const fa_rotary_t* rotary, int back,
+                      void* stream);
+
+/*
+ * New tokens, turned, into the pages of one layer.  Rows are padded or packed:
+ * - offsets NULL: q is [B, H, N, d], k_new and v_new are [B, h_kv, N, d], and
+ *   row b has N tokens;
+ * - offsets int32[B + 1], rising: q is [1, H, N, d], k_new and v_new are [1,
+ *   h_kv, N, d], and row b has the tokens offsets[b] .. offsets[b + 1] - 1 of
+ *   the N.  Tokens of no row are neither read nor written.
+ * Token t of row b is at position start[b] + t.  q_out (q or apart from it)
+ * gets every token's queries turned; the turned keys and the values go into
+ * the token's page as fa_paged_append says (positions from 0 and below
+ * kv_len[b], pages that exist).  H = 0: no queries, q and q_out ignored.
+ * N is below 2^30, B * N (padded) below 2^31 - 1, H + 2 h_kv below 2^16.
+ */
+fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q_out, int H,
+                                    const fa_strided_t* k_new, const fa_strided_t* v_new,
+                                    const fa_paged_kv_t* cache, int layer, const int* block_table,
+                                    int max_pages, const int* start, const int* kv_len,
+                                    const int* offsets, int B, int N, const fa_rotary_t* rotary,
+                                    void* stream);
+
+/*
+ * Attention of a chunk of new tokens per row over the paged cache, which holds
+ * their keys and values already.  q, o: [B, H, N, d], or with offsets
+ * (int32[B + 1], rising) [1, H, N, d] whose tokens offsets[b] ..
+ * offsets[b + 1] - 1 are row b's; lse: fp32, contiguous, the same without d.
+ * Token t of row b is at position x = start[b] + t and sees key j when j <
+ * kv_len[b] (clamped to [0, max_pages * page_size]), its page exists, and
+ * - causal: j <= x, and the token itself is there, x < kv_len[b] (a token at
+ *   or past kv_len sees nothing, so padded rows may end early);
+ * - window sides other than -1: j <= x + window_right, and j >= x -
+ *   window_left or j < sinks.
+ * causal = 0 without a window is attention to another sequence's states
+ * (cross attention), of which start says nothing.  A token that sees no key
+ * gets O = 0, LSE = -inf; tokens of no row are left as they were.  Query head
+ * h reads K/V head h / (H / h_kv), any group size.  Slots that no token of
+ * their row sees may hold anything, NaN included.  The GPU divides the work
+ * from the lengths, along the keys too where rows are few; results repeat bit
+ * for bit (on the same GPU model).
+ *
+ * workspace: fa_prefill_paged_workspace_bytes (packed != 0: with offsets; 0
+ * for sizes that no call takes), 256-byte aligned, its contents irrelevant on
+ * entry; calls that may overlap on the GPU need one each.  N is below 2^30,
+ * B * N (padded) and B * H below 2^31 - 1, and so is the number of 128-row
+ * tiles over all K/V heads.
+ */
+size_t fa_prefill_paged_workspace_bytes(int B, int H, int N, int h_kv, int d, int packed);
+fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, int layer,
+                             const int* block_table, int max_pages, const int* start,
+                             const int* kv_len, const int* offsets, const fa_strided_t* o,
+                             float* lse, int B, int H, int N, float scale, int causal,
+                             int window_left, int window_right, int sinks, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * Pages of a cache: reserving, forking, freeing, compacting.
  *
  * ref: int32[num_pages], for each page the number of table entries that hold
@@ -505,7 +606,8 @@ const char* fa_status_string(fa_status_t status);
 /* Library version as major*10000 + minor*100 + patch.  1.1: fa_variant_t
  * gained block_mask (a trailing member, NULL in aggregate initialisers that
  * stop before it).  1.2: fa_variant_t gained block_mask_host (the same).
- * 1.3: sinks, the paged cache. */
+ * 1.3: sinks, the paged cache.  1.4: rotary positions, chunks of new tokens
+ * over the paged cache. */
 int fa_version(void);
 
 #ifdef __cplusplus
