@@ -12,8 +12,7 @@
 // does not depend on who takes it or when: results repeat bit for bit.
 //
 // Main kernel, one CTA per SM, roles by warp:
-//   0        producer: takes pieces, looks pages up, loads Q, K (and V for d <=
-//            128) by TMA.  A key tile is whole pages (page_size <= 128: as many
+//   0        producer: takes pieces, looks pages up, loads Q and K by TMA.  A key tile is whole pages (page_size <= 128: as many
 //            as fit, a box a page; else up to 128 slots of one page).  A page
 //            that does not exist is a box outside the pool: TMA fills in
 //            zeros, and a bit mask of the tile's keys hides them.
@@ -23,7 +22,7 @@
 //            a row, each over half of every tile's keys with a maximum, sum
 //            and O of its own
 //   then 4   epilogue: merge the halves, divide, store O and LSE
-//   last     (d = 256) V producer
+//   last     V producer
 // The recurrence and its roundings are those of the forward (fa_fwd.cu): S in
 // base-2 units, a reference maximum that moves only when a block exceeds it by
 // 2^24, P rounded to bf16 for the product and summed unrounded.
@@ -48,17 +47,20 @@ constexpr int BM = 128;
 constexpr int BN = 128;
 constexpr int CHUNK = 128 * 128;   // bytes of 128 rows x 64 columns
 constexpr float kRescaleSlack = 24.0f;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kPlanRows = 1024;    // rows whose tiles the plan counts in shared memory
 constexpr int kMostRounds = 4;     // pieces of a cut call: at most so many a CTA, by its sum
 constexpr int kItems = 4;          // pieces announced ahead
 constexpr int kRing = 8;           // key tiles whose masks are kept
 
 // A piece as the plan lists it, for every unit (K/V head, part of its group).
-struct Entry {
-  int row, n0, ntok;   // batch row; first token (its place on the token axis), tokens
-  int pos0, len;       // position of the first token; the row's keys
-  int s0, s1;          // key tiles of the tile's walk
-  int slot;            // partial output (times units + unit), or -1
+struct alignas(16) Entry {
+  int row, n0, ntok, pos0;   // batch row; the tile's first token on the token axis, tokens,
+                             // position of the first
+  int len, s0, s1, slot;     // the row's keys; key tiles of the walk; partial output (times
+                             // units + unit), or -1
+  int jlo, ns, rlo, rhi;     // the walk: ns tiles of sinks, then from jlo on; [rlo, rhi): the
+                             // keys that the row's tokens see, beside the sinks
 };
 
 struct JoinEntry {
@@ -173,36 +175,35 @@ __device__ __forceinline__ int block_scan(int x, int* sm, int& total) {
   __syncthreads();
   if (lane == 31) sm[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int w = sm[lane];
+  int before = 0;
+  total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    sm[lane] = w;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const int y = sm[w];
+    if (w < warp) before += y;
+    total += y;
   }
-  __syncthreads();
-  total = sm[kPlanThreads / 32 - 1];
-  return v - x + (warp ? sm[warp - 1] : 0);
+  return v - x + before;
 }
 
 // Tile i of the call: rows in order, in a row the last tokens (under causality
 // the most keys) first.
-__device__ __forceinline__ void plan_tile(const PrefillParams& p, int i, Entry& e, int& n) {
+// rows: the tiles before each row.
+__device__ __forceinline__ void plan_tile(const PrefillParams& p, const int* rows, int i, Entry& e,
+                                          int& n) {
   int b, k, tiles;
   if (p.offsets) {
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int m = (lo + hi) / 2;
-      if (p.row_tiles[m] <= i)
+      if (rows[m] <= i)
         lo = m;
       else
         hi = m;
     }
     b = lo;
-    k = i - p.row_tiles[b];
-    tiles = p.row_tiles[b + 1] - p.row_tiles[b];
+    k = i - rows[b];
+    tiles = rows[b + 1] - rows[b];
   } else {
     tiles = (p.N + p.tpt - 1) / p.tpt;
     b = p.fd_tn.div(i);
@@ -215,24 +216,31 @@ __device__ __forceinline__ void plan_tile(const PrefillParams& p, int i, Entry& 
   e.ntok = min(p.tpt, r.ntok - t0);
   e.pos0 = r.start + t0;
   e.len = r.len;
-  int jlo, ns;
-  n = tile_walk(p, e.pos0, e.ntok, e.len, jlo, ns);
+  n = tile_walk(p, e.pos0, e.ntok, e.len, e.jlo, e.ns);
+  tile_keys(p, r.start, r.ntok, r.len, e.rlo, e.rhi);
 }
 
 // Lists the pieces.  With W key tiles to walk over all units, cutting the
-// walks into pieces of at most W / (k CTAs) tiles, k = 1 .. kMostRounds, or not
-// at all: whichever ends first by the estimate below.
+// walks into equal pieces of at most W / (k CTAs) tiles, k = 1 ..
+// kMostRounds, or not at all: whichever ends first by the estimate below.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
-  __shared__ int sm[32];
-  __shared__ unsigned long long sum[1 + kMostRounds];
+  __shared__ int sm[kPlanThreads / 32];
+  __shared__ int sm_rows[kPlanRows + 1];
+  __shared__ unsigned long long sum;
   __shared__ int most, cut, slots, joins, join_most;
+  __shared__ int most_of[kMostRounds], pieces_of[kMostRounds], longest_of[kMostRounds];
   launch_dependents();
   grid_dependency_wait();
-  const int tid = threadIdx.x;
-  if (tid <= kMostRounds) sum[tid] = 0;
-  if (tid == 0) most = slots = joins = join_most = 0;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < kMostRounds) pieces_of[tid] = longest_of[tid] = 0;
+  if (tid == 0) {
+    sum = 0;
+    most = slots = joins = join_most = 0;
+    cut = INT_MAX;
+  }
   // tiles of the rows
   int tiles;
+  int* rows = p.B <= kPlanRows ? sm_rows : p.row_tiles;
   if (p.offsets) {
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
@@ -245,10 +253,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       }
       int total;
       const int at = before + block_scan(n, sm, total);
-      if (b < p.B) p.row_tiles[b] = at;
+      if (b < p.B) rows[b] = at;
       before += total;
     }
-    if (tid == 0) p.row_tiles[p.B] = before;
+    if (tid == 0) rows[p.B] = before;
     // (offsets that do not rise may name a token twice: what is past the
     // list's room is left out)
     tiles = before;
@@ -258,66 +266,80 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __syncthreads();
   // the walks' sum, and the longest
   unsigned long long s = 0;
-  int longest = 0;
+  int longest = 0, n = 0;
   Entry e;
-  int n = 0;
   const bool once = tiles <= kPlanThreads;
   for (int i = tid; i < tiles; i += kPlanThreads) {
-    plan_tile(p, i, e, n);
+    plan_tile(p, rows, i, e, n);
     s += n;
     longest = max(longest, n);
   }
-  if (s) atomicAdd(&sum[0], s);
-  if (longest) atomicMax(&most, longest);
-  __syncthreads();
-  const unsigned long long W = sum[0] * p.units;
-  int P[kMostRounds];
+  longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
-  for (int k = 0; k < kMostRounds; ++k) {
-    const unsigned long long share = static_cast<unsigned long long>(p.grid) * (k + 1);
-    const unsigned long long x = (W + share - 1) / share;
-    P[k] = x > INT_MAX ? INT_MAX : (x ? static_cast<int>(x) : 1);
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) {
+    atomicAdd(&sum, s);
+    atomicMax(&most, longest);
   }
-  if (most > P[kMostRounds - 1]) {       // something to cut
-    unsigned c[kMostRounds] = {};
+  __syncthreads();
+  const float W = static_cast<float>(sum) * p.units;   // (of an estimate)
+  if (tid < kMostRounds) {
+    // (rounded up, so that the cut tiles' pieces are never more than there is room for)
+    const unsigned long long all = sum * p.units, share = p.grid * (tid + 1ull);
+    const unsigned long long x = (all + share - 1) / share;
+    most_of[tid] = x > INT_MAX ? INT_MAX : (x ? static_cast<int>(x) : 1);
+  }
+  __syncthreads();
+  const bool some = most > most_of[kMostRounds - 1];   // something to cut
+  if (some) {
+    int P[kMostRounds], c[kMostRounds] = {}, len[kMostRounds] = {};
+#pragma unroll
+    for (int k = 0; k < kMostRounds; ++k) P[k] = most_of[k];
     for (int i = tid; i < tiles; i += kPlanThreads) {
-      if (!once) plan_tile(p, i, e, n);
+      if (!once) plan_tile(p, rows, i, e, n);
 #pragma unroll
-      for (int k = 0; k < kMostRounds; ++k) c[k] += n > P[k] ? (n + P[k] - 1) / P[k] : 1;
-    }
-#pragma unroll
-    for (int k = 0; k < kMostRounds; ++k)
-      if (c[k]) atomicAdd(&sum[1 + k], static_cast<unsigned long long>(c[k]));
-  }
-  __syncthreads();
-  if (tid == 0) {
-    // key tiles that a CTA walks to the end: a piece costs one more, a cut one
-    // two, the join about six
-    const auto end_of = [&](double pieces, double len, double extra) {
-      const double rounds = ceil(pieces / p.grid) * (len + extra);
-      const double even = (static_cast<double>(W) + pieces * extra) / p.grid + len;
-      return rounds < even ? rounds : even;
-    };
-    double best = end_of(static_cast<double>(tiles) * p.units, most, 1.0);
-    cut = INT_MAX;
-    if (most > P[kMostRounds - 1]) {
       for (int k = 0; k < kMostRounds; ++k) {
-        const double t =
-            end_of(static_cast<double>(sum[1 + k]) * p.units, min(P[k], most), 2.0) + 6.0;
-        if (most > P[k] && t < best) {
-          best = t;
-          cut = P[k];
-        }
+        const int pieces = n > P[k] ? (n + P[k] - 1) / P[k] : 1;
+        c[k] += pieces;
+        len[k] = max(len[k], (n + pieces - 1) / pieces);
       }
     }
+#pragma unroll
+    for (int k = 0; k < kMostRounds; ++k) {
+      const int a = __reduce_add_sync(0xffffffffu, c[k]);
+      const int b = __reduce_max_sync(0xffffffffu, len[k]);
+      if (lane == 0) {
+        atomicAdd(&pieces_of[k], a);
+        atomicMax(&longest_of[k], b);
+      }
+    }
+    __syncthreads();
+    if (tid < 32) {
+      // key tiles that a CTA walks to the end: a piece costs one more, a cut
+      // one two, the join about six
+      const int k = tid - 1;                           // lane 0: no cuts
+      float end = INFINITY;
+      if (k < kMostRounds && (k < 0 || most > most_of[k])) {
+        const float pieces = static_cast<float>(k < 0 ? tiles : pieces_of[k]) * p.units;
+        const float length = k < 0 ? most : longest_of[k], extra = k < 0 ? 1.f : 2.f;
+        const float rounds = ceilf(pieces / p.grid) * (length + extra);
+        const float even = (W + pieces * extra) / p.grid + length;
+        end = fminf(rounds, even) + (k < 0 ? 0.f : 6.f);
+      }
+      float best = end;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      const int first = __ffs(__ballot_sync(0xffffffffu, end == best)) - 1;
+      if (tid == 0 && first > 0) cut = most_of[first - 1];
+    }
+    __syncthreads();
   }
-  __syncthreads();
   int before = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int c = 0;
     if (i < tiles) {
-      if (!once) plan_tile(p, i, e, n);
+      if (!once) plan_tile(p, rows, i, e, n);
       c = n > cut ? (n + cut - 1) / cut : 1;
     }
     int total;
@@ -361,9 +383,8 @@ struct Cfg {
   static constexpr int NCH = D / 64;
   static constexpr int TILE_BYTES = NCH * CHUNK;
   static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 1);
-  // d = 256: O takes 256 columns of tensor memory, P buffers of their own let
-  // the one S buffer be refilled once the softmax has loaded it, and V comes
-  // from a warp of its own, since one stage a ring is all that fits.
+  // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
+  // let the one S buffer be refilled once the softmax has loaded it.
   static constexpr bool SEP = D == 256;
   static constexpr int NHALF = D <= 128 ? 2 : 1;
   static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
@@ -376,13 +397,13 @@ struct Cfg {
   static constexpr uint32_t TM_COLS = 512;
   static_assert(TM_O + OCOLS <= TM_COLS, "tensor memory budget");
   static constexpr int EPI_WARP0 = 3 + 4 * NHALF;
-  static constexpr int WARPS = EPI_WARP0 + 4 + (SEP ? 1 : 0);
+  static constexpr int WARPS = EPI_WARP0 + 4 + 1;
   static constexpr int THREADS = 32 * WARPS;
   // a tile's mask slot is free again before the producer reaches the tile
-  // kRing further on: S of tile g - STAGES is done when K of tile g is loaded,
-  // so the softmax has read the mask of g - STAGES - NSB (before it lets go of
-  // the S buffer)
-  static_assert(STAGES + NSB <= kRing, "mask ring");
+  // kRing further on: it writes tile g's mask once K of tile g - 1 is on its
+  // way, when S of g - 1 - STAGES is done, so that the softmax has read the
+  // mask of g - 1 - STAGES - NSB (before it lets go of the S buffer)
+  static_assert(1 + STAGES + NSB <= kRing, "mask ring");
 };
 
 // A piece as the roles see it.
@@ -463,44 +484,54 @@ __device__ __forceinline__ int step_tile(const Item& t, int j) {
   return s < t.ns ? s : t.jlo + (s - t.ns);
 }
 
-// Looks up the pages of key tiles, one a lane.
-struct Pages {
+// The boxes of a key tile, one of 64 columns a page (page_size <= 128) or one
+// of 64 columns: box x is columns 64 (x % NCH) of page x / NCH.  A lane issues
+// the boxes lane, lane + 32, ..
+template <int D>
+struct Boxes {
+  static constexpr int NCH = D / 64;
   const PrefillParams& p;
-  const int* row;
-  int len;
-  // page m of key tile j, or -1
-  __device__ __forceinline__ int at(int j, int m) const {
-    const int i = p.ppt ? j * p.ppt + m : p.fd_tpp.div(j);
-    if (m >= (p.ppt ? p.ppt : 1) || i >= p.max_pages) return -1;
-    if (static_cast<long long>(i) * p.page_size >= len) return -1;
-    const int page = row[i];
-    return page >= 0 && page < p.num_pages ? page : -1;
+  const int* row;              // the row's pages
+  int len, head;
+  int count;                   // boxes of a tile
+  __device__ Boxes(const PrefillParams& p_, const Item& t)
+      : p(p_), row(p_.table + static_cast<long long>(t.row) * p_.max_pages), len(t.len),
+        head(t.kvh), count((p_.ppt ? p_.ppt : 1) * NCH) {}
+  // the page of box x of key tile j, or num_pages (outside the pool) for none
+  __device__ __forceinline__ int page(int j, int x) const {
+    const int i = p.ppt ? j * p.ppt + x / NCH : p.fd_tpp.div(j);
+    if (x >= count || i >= p.max_pages || static_cast<long long>(i) * p.page_size >= len)
+      return p.num_pages;
+    const unsigned page = row[i];
+    return min(page, static_cast<unsigned>(p.num_pages));
+  }
+  // first: page(j, lane)
+  __device__ __forceinline__ void load(int j, int first, uint8_t* dst, const CUtensorMap* map,
+                                       uint64_t* bar) const {
+    const int slot0 = p.ppt ? 0 : (j - p.fd_tpp.div(j) * p.tpp) * BN;
+    for (int x = threadIdx.x & 31; x < count; x += 32) {
+      if (x >= 32) first = page(j, x);
+      const int m = x / NCH, c = x % NCH;
+      tma_load_4d(dst + c * CHUNK + m * p.page_size * 128, map, bar, 64 * c, slot0, head, first);
+    }
   }
 };
 
-// Loads one key tile of K or V: a box a page and 64 columns.  page: this
-// lane's (Pages::at(j, lane)).
+// A key tile's mask where pages may be missing, or its boxes are more than the
+// lanes.
 template <int D>
-__device__ __forceinline__ void load_tile(const PrefillParams& p, const Pages& pages, int j,
-                                          int page, int head, uint8_t* dst, const CUtensorMap* map,
-                                          uint64_t* bar) {
+__device__ __noinline__ void key_words(const PrefillParams& p, const Boxes<D>& boxes, int j,
+                                       KeyMask& km) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) mbar_arrive_expect_tx(bar, p.kt * (D * 2));
-  __syncwarp();
-  if (p.ppt) {
-    for (int m = lane; m < p.ppt; m += 32) {
-      if (m >= 32) page = pages.at(j, m);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_4d(dst + c * CHUNK + m * p.page_size * 128, map, bar, 64 * c, 0, head,
-                    page < 0 ? p.num_pages : page);
-    }
-  } else if (lane < D / 64) {
-    const int slot0 = (j - p.fd_tpp.div(j) * p.tpp) * BN;
-    tma_load_4d(dst + lane * CHUNK, map, bar, 64 * lane, slot0, head,
-                page < 0 ? p.num_pages : page);
+  for (int w = 0; w < 4; ++w) {
+    const int x = 32 * w + lane;               // the lane's key of the tile
+    const int m = p.ppt ? p.fd_ps.div(x) : 0;
+    bool on = p.ppt ? x < p.kt
+                    : x < p.page_size - (j - p.fd_tpp.div(j) * p.tpp) * BN;
+    on = on && boxes.page(j, m * Boxes<D>::NCH) < p.num_pages;
+    const uint32_t word = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) km.word[w] = word;
   }
-  __syncwarp();
 }
 
 template <int D>
@@ -575,8 +606,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       prefetch_tmap(&p.tk);
       prefetch_tmap(&p.tv);
     }
-    const uint32_t items = *reinterpret_cast<volatile unsigned*>(&p.counters->items);
-    uint32_t i = blockIdx.x, q_it = 0, g = 0, v_it = 0;
+    const uint32_t items = p.counters->items;
+    uint32_t i = blockIdx.x, q_it = 0, g = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const uint32_t b = k % kItems;
@@ -586,7 +617,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (lane == 0) next = atomicAdd(&p.counters->next, 1u);   // (used after this piece)
         const int e = p.fd_units.div(i), u = static_cast<int>(i) - e * p.units;
         const Entry en = p.entries[e];
-        const Row r = row_at(p, en.row);
         t.n0 = en.n0;
         t.ntok = en.ntok;
         t.pos0 = en.pos0;
@@ -594,8 +624,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         t.s0 = en.s0;
         t.nst = en.s1 - en.s0;
         t.slot = en.slot < 0 ? -1 : en.slot * p.units + u;
-        tile_walk(p, en.pos0, en.ntok, en.len, t.jlo, t.ns);
-        tile_keys(p, r.start, r.ntok, r.len, t.rlo, t.rhi);
+        t.jlo = en.jlo;
+        t.ns = en.ns;
+        t.rlo = en.rlo;
+        t.rhi = en.rhi;
         t.batch = p.offsets ? 0 : en.row;
         t.kvh = p.fd_parts.div(u);
         const int part = u - t.kvh * p.parts;
@@ -615,53 +647,34 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         mbar_arrive(&sm.item_full[b]);
       }
       if (t.n0 < 0) break;
-      const Pages pages{p, p.table + static_cast<long long>(t.row) * p.max_pages, t.len};
-      int page = t.nst > 0 ? pages.at(step_tile(t, 0), lane) : -1;
+      const Boxes<D> boxes(p, t);
+      int ahead = t.nst > 0 ? boxes.page(step_tile(t, 0), lane) : 0;
       for (int j = 0; j < t.nst; ++j, ++g) {
         const int jt = step_tile(t, j);
-        const int page_next = j + 1 < t.nst ? pages.at(step_tile(t, j + 1), lane) : -1;
+        const int page = ahead;
+        if (j + 1 < t.nst) ahead = boxes.page(step_tile(t, j + 1), lane);
+        // which keys exist, and the first one's position
+        KeyMask& km = sm.mask[g % kRing];
+        const bool all = boxes.count <= 32 &&
+                         __all_sync(0xffffffffu, lane >= boxes.count || page < p.num_pages);
+        if (all) {
+          const int keys =
+              p.ppt ? p.kt : p.page_size - (jt - p.fd_tpp.div(jt) * p.tpp) * BN;
+          if (lane < 4) km.word[lane] = bits_below(keys - 32 * lane);
+        } else {
+          key_words<D>(p, boxes, jt, km);
+        }
+        if (lane == 0) km.pos = tile_pos(p, jt);
+        __syncwarp();
         const int st = g % C::STAGES;
-        const uint32_t ph = (g / C::STAGES) & 1;
-        if (!mbar_wait_warp(&sm.k_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
+        if (!mbar_wait_warp(&sm.k_empty[st], ((g / C::STAGES) & 1) ^ 1, abort, kWaitTimeoutNs)) {
           fail(p.status, abort, kSiteK);
           ok = false;
           break;
         }
-        // which keys exist, and the first one's position
-        {
-          KeyMask& km = sm.mask[g % kRing];
-          if (p.ppt) {
-            uint32_t have[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int m = 32 * w + lane;
-              const int pg = w == 0 ? page : (32 * w < p.ppt ? pages.at(jt, m) : -1);
-              have[w] = __ballot_sync(0xffffffffu, pg >= 0);
-            }
-            if (lane < 4) {
-              uint32_t word = 0;
-              if (p.ppt <= 32 && have[0] == bits_below(p.ppt)) {
-                word = bits_below(p.kt - 32 * lane);
-              } else {
-                for (int x = 0; x < 32; ++x) {
-                  const int m = p.fd_ps.div(32 * lane + x);
-                  const uint32_t w = m < 32 ? have[0] : (m < 64 ? have[1] : (m < 96 ? have[2] : have[3]));
-                  if (m < p.ppt && ((w >> (m & 31)) & 1u)) word |= 1u << x;
-                }
-              }
-              km.word[lane] = word;
-            }
-          } else {
-            const int pg = __shfl_sync(0xffffffffu, page, 0);
-            page = pg;
-            const int pj = p.fd_tpp.div(jt), slot0 = (jt - pj * p.tpp) * BN;
-            if (lane < 4)
-              km.word[lane] = pg < 0 ? 0u : bits_below(p.page_size - slot0 - 32 * lane);
-          }
-          if (lane == 0) km.pos = tile_pos(p, jt);
-          __syncwarp();
-        }
-        load_tile<D>(p, pages, jt, page, t.kvh, sm.k[st], &p.tk, &sm.k_full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[st], p.kt * (D * 2));
+        boxes.load(jt, page, sm.k[st], &p.tk, &sm.k_full[st]);
+        __syncwarp();
         if (j == 0) {
           // Q after the first keys: its buffer is free only when the piece
           // before has no more products to issue
@@ -671,26 +684,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             ok = false;
             break;
           }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.q_full, p.gh * p.tpt * (D * 2));
-#pragma unroll
-            for (int c = 0; c < C::NCH; ++c)
-              tma_load_4d(sm.q + c * CHUNK, &p.tq, &sm.q_full, 64 * c, t.h0, t.n0, t.batch);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, p.gh * p.tpt * (D * 2));
+          if (lane < C::NCH)
+            tma_load_4d(sm.q + lane * CHUNK, &p.tq, &sm.q_full, 64 * lane, t.h0, t.n0, t.batch);
           __syncwarp();
           ++q_it;
         }
-        if constexpr (!C::SEP) {
-          if (!mbar_wait_warp(&sm.v_empty[st], ph ^ 1, abort, kWaitTimeoutNs)) {
-            fail(p.status, abort, kSiteV);
-            ++g;
-            ok = false;
-            break;
-          }
-          load_tile<D>(p, pages, jt, page, t.kvh, sm.v[st], &p.tv, &sm.v_full[st]);
-          ++v_it;
-        }
-        page = page_next;
       }
       i = __shfl_sync(0xffffffffu, next, 0);
     }
@@ -701,20 +700,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (g > static_cast<uint32_t>(s) &&
           !mbar_wait_warp(&sm.k_full[s], ((g - 1 - s) / C::STAGES) & 1, nullptr, kWaitTimeoutNs))
         fail(p.status, abort, kSiteDrain);
-      if (v_it > static_cast<uint32_t>(s) &&
-          !mbar_wait_warp(&sm.v_full[s], ((v_it - 1 - s) / C::STAGES) & 1, nullptr, kWaitTimeoutNs))
-        fail(p.status, abort, kSiteDrain);
     }
-  } else if (C::SEP && warp == C::WARPS - 1) {
-    // ------------------------------------------------------------ V producer (d = 256)
+  } else if (warp == C::WARPS - 1) {
+    // ------------------------------------------------------------ V producer
     uint32_t k = 0, v_it = 0;
     bool ok = true;
     for (Item t; ok && next_item(sm, k, t, p.status);) {
-      const Pages pages{p, p.table + static_cast<long long>(t.row) * p.max_pages, t.len};
-      int page = t.nst > 0 ? pages.at(step_tile(t, 0), lane) : -1;
-      for (int j = 0; j < t.nst; ++j) {
+      const Boxes<D> boxes(p, t);
+      int ahead = t.nst > 0 ? boxes.page(step_tile(t, 0), lane) : 0;
+      for (int j = 0; j < t.nst; ++j, ++v_it) {
         const int jt = step_tile(t, j);
-        const int page_next = j + 1 < t.nst ? pages.at(step_tile(t, j + 1), lane) : -1;
+        const int page = ahead;
+        if (j + 1 < t.nst) ahead = boxes.page(step_tile(t, j + 1), lane);
         const int st = v_it % C::STAGES;
         if (!mbar_wait_warp(&sm.v_empty[st], ((v_it / C::STAGES) & 1) ^ 1, abort,
                             kWaitTimeoutNs)) {
@@ -722,10 +719,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           ok = false;
           break;
         }
-        if (!p.ppt) page = __shfl_sync(0xffffffffu, page, 0);
-        load_tile<D>(p, pages, jt, page, t.kvh, sm.v[st], &p.tv, &sm.v_full[st]);
-        ++v_it;
-        page = page_next;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[st], p.kt * (D * 2));
+        boxes.load(jt, page, sm.v[st], &p.tv, &sm.v_full[st]);
+        __syncwarp();
       }
     }
     for (int s = 0; s < C::STAGES; ++s)
