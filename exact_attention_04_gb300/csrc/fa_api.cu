@@ -655,23 +655,38 @@ fa_status_t device_facts(int* num_sms, int* max_smem, int** status) {
   return FA_OK;
 }
 
-bool make_map_4d(CUtensorMap* m, const void* base, int d, const long long* n, const long long* s,
-                 const int* box) {
+namespace {
+
+// (cols, n[0], ..) through strides s, `rank` - 1 of them; a box of 64 columns.
+bool make_map_nd(CUtensorMap* m, const void* base, int rank, int cols, const long long* n,
+                 const long long* s, const int* box) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), 0, 0, 0};
-  cuuint64_t strides[3];
-  cuuint32_t boxes[4] = {64, 0, 0, 0};
-  for (int i = 0; i < 3; ++i) {
+  cuuint64_t dims[5] = {static_cast<cuuint64_t>(cols)};
+  cuuint64_t strides[4];
+  cuuint32_t boxes[5] = {64};
+  for (int i = 0; i < rank - 1; ++i) {
     dims[i + 1] = static_cast<cuuint64_t>(n[i]);
-    strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? s[i] : d) * 2;
+    strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? s[i] : cols) * 2;   // (one: any)
     boxes[i + 1] = static_cast<cuuint32_t>(box[i]);
   }
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides,
+             boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool make_map_4d(CUtensorMap* m, const void* base, int d, const long long* n, const long long* s,
+                 const int* box) {
+  return make_map_nd(m, base, 4, d, n, s, box);
+}
+
+bool make_map_5d(CUtensorMap* m, const void* base, const long long* n, const long long* s,
+                 const int* box) {
+  return make_map_nd(m, base, 5, 64, n, s, box);
 }
 
 }  // namespace fa

@@ -88,6 +88,8 @@ struct PrefillParams {
   FastDiv fd_units, fd_parts, fd_gh, fd_tn;
   int max_pages, num_pages, page_size;
   int ppt, tpp, kt;                // pages of a key tile (0: tpp tiles a page), keys of one
+  int groups, eights;              // eights of slots from page to page in tk, tv, and in all; or 0
+  uint32_t chunk16, group16;       // of a tile: from 64 columns to 64, from 8 keys to 8 (16 B)
   FastDiv fd_kt, fd_ps, fd_tpp;
   int wl, wr, sinks, causal;
   float scale_log2;
@@ -414,11 +416,6 @@ struct alignas(16) Item {
   int kvh, h0, nh, row;
 };
 
-struct alignas(16) KeyMask {
-  uint32_t word[4];             // keys that exist
-  int pos, pad[3];              // position of the first
-};
-
 template <int D>
 struct Smem {
   using C = Cfg<D>;
@@ -426,7 +423,7 @@ struct Smem {
   alignas(1024) uint8_t k[C::STAGES][C::TILE_BYTES];
   alignas(1024) uint8_t v[C::STAGES][C::TILE_BYTES];
   Item item[kItems];
-  KeyMask mask[kRing];
+  alignas(16) uint32_t mask[kRing][4];    // a key tile's keys that exist
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full, q_empty;
   uint64_t k_full[C::STAGES], k_empty[C::STAGES];
@@ -463,6 +460,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(c4)
+      : "memory");
+}
+
 // The next announced piece; false at the end, or after a wait that gave up.
 template <class S>
 __device__ __forceinline__ bool next_item(S& sm, uint32_t& k, Item& t, int* status) {
@@ -478,41 +485,83 @@ __device__ __forceinline__ bool next_item(S& sm, uint32_t& k, Item& t, int* stat
   return t.n0 >= 0;
 }
 
-// The key tile of step j of the walk.
-__device__ __forceinline__ int step_tile(const Item& t, int j) {
-  const int s = t.s0 + j;
-  return s < t.ns ? s : t.jlo + (s - t.ns);
-}
+// The key tiles of a piece, one after the other.
+struct Walk {
+  int s, j;                    // step of the tile's walk, key tile
+  __device__ explicit Walk(const Item& t) : s(t.s0), j(s < t.ns ? s : t.jlo + (s - t.ns)) {}
+  __device__ __forceinline__ void next(const Item& t) { j = ++s == t.ns ? t.jlo : j + 1; }
+};
 
-// The boxes of a key tile, one of 64 columns a page (page_size <= 128) or one
-// of 64 columns: box x is columns 64 (x % NCH) of page x / NCH.  A lane issues
-// the boxes lane, lane + 32, ..
+// A place in a ring of N barriers.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The boxes of a key tile.  Whole groups of eight slots (p.groups): a box a
+// page, which lands as [group][64 columns][slot].  Else a box a page (or 128
+// slots of one) and 64 columns, which lands as [64 columns][slot]; box x is
+// columns 64 (x % each) of page x / each.  A lane issues the boxes lane, lane +
+// 32, ..  A page's number is asked for a tile ahead and not looked at before:
+// the producer is the kernel's pace maker, and a look costs it the load's
+// 700 cycles.
 template <int D>
 struct Boxes {
-  static constexpr int NCH = D / 64;
   const PrefillParams& p;
   const int* row;              // the row's pages
-  int len, head;
-  int count;                   // boxes of a tile
+  int head;
+  int pages;                   // of the row
+  int each, count;             // boxes of a page, of a tile
+  int m, to;                   // this lane's (first) page of a tile, and where it lands
   __device__ Boxes(const PrefillParams& p_, const Item& t)
-      : p(p_), row(p_.table + static_cast<long long>(t.row) * p_.max_pages), len(t.len),
-        head(t.kvh), count((p_.ppt ? p_.ppt : 1) * NCH) {}
-  // the page of box x of key tile j, or num_pages (outside the pool) for none
-  __device__ __forceinline__ int page(int j, int x) const {
-    const int i = p.ppt ? j * p.ppt + x / NCH : p.fd_tpp.div(j);
-    if (x >= count || i >= p.max_pages || static_cast<long long>(i) * p.page_size >= len)
-      return p.num_pages;
-    const unsigned page = row[i];
-    return min(page, static_cast<unsigned>(p.num_pages));
+      : p(p_), row(p_.table + static_cast<long long>(t.row) * p_.max_pages), head(t.kvh),
+        each(p_.groups ? 1 : D / 64) {
+    pages = min(p.max_pages, (t.len + p.page_size - 1) / p.page_size);
+    count = (p.ppt ? p.ppt : 1) * each;
+    m = (threadIdx.x & 31) / each;
+    to = place(threadIdx.x & 31);
   }
-  // first: page(j, lane)
+  __device__ __forceinline__ int place(int x) const {
+    return p.groups ? x * p.page_size * (D * 2)
+                    : x % (D / 64) * CHUNK + x / (D / 64) * p.page_size * 128;
+  }
+  // the tile's first slot in its page
+  __device__ __forceinline__ int slot0(int j) const {
+    return p.ppt ? 0 : (j - p.fd_tpp.div(j) * p.tpp) * BN;
+  }
+  // the table's entry of page m of key tile j, -1 where there is none
+  __device__ __forceinline__ int entry(int j, int m) const {
+    const int i = p.ppt ? j * p.ppt + m : p.fd_tpp.div(j);
+    return i < pages ? row[i] : -1;
+  }
+  __device__ __forceinline__ bool exists(int entry) const {
+    return static_cast<unsigned>(entry) < static_cast<unsigned>(p.num_pages);
+  }
+  __device__ __forceinline__ void box(int x, int entry, int slot0, uint8_t* dst,
+                                      const CUtensorMap* map, uint64_t* bar) const {
+    // a page that does not exist lies outside the pool
+    if (p.groups)
+      tma_load_5d(dst, map, bar, 0, 0, 0,
+                  exists(entry) ? entry * p.groups + slot0 / 8 : p.eights, head);
+    else
+      tma_load_4d(dst, map, bar, 64 * (x % (D / 64)), slot0, head,
+                  exists(entry) ? entry : p.num_pages);
+  }
+  // first: entry(j, m)
   __device__ __forceinline__ void load(int j, int first, uint8_t* dst, const CUtensorMap* map,
                                        uint64_t* bar) const {
-    const int slot0 = p.ppt ? 0 : (j - p.fd_tpp.div(j) * p.tpp) * BN;
-    for (int x = threadIdx.x & 31; x < count; x += 32) {
-      if (x >= 32) first = page(j, x);
-      const int m = x / NCH, c = x % NCH;
-      tma_load_4d(dst + c * CHUNK + m * p.page_size * 128, map, bar, 64 * c, slot0, head, first);
+    const int lane = threadIdx.x & 31;
+    if (lane < count) box(lane, first, slot0(j), dst + to, map, bar);
+    if (count > 32) {
+      for (int x = lane + 32; x < count; x += 32)
+        box(x, entry(j, x / each), slot0(j), dst + place(x), map, bar);
     }
   }
 };
@@ -520,18 +569,24 @@ struct Boxes {
 // A key tile's mask where pages may be missing, or its boxes are more than the
 // lanes.
 template <int D>
-__device__ __noinline__ void key_words(const PrefillParams& p, const Boxes<D>& boxes, int j,
-                                       KeyMask& km) {
+__device__ __forceinline__ void key_words(const PrefillParams& p, const Boxes<D>& boxes, int j,
+                                          uint32_t* words) {
   const int lane = threadIdx.x & 31;
   for (int w = 0; w < 4; ++w) {
     const int x = 32 * w + lane;               // the lane's key of the tile
     const int m = p.ppt ? p.fd_ps.div(x) : 0;
     bool on = p.ppt ? x < p.kt
                     : x < p.page_size - (j - p.fd_tpp.div(j) * p.tpp) * BN;
-    on = on && boxes.page(j, m * Boxes<D>::NCH) < p.num_pages;
+    on = on && boxes.exists(boxes.entry(j, m));
     const uint32_t word = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) km.word[w] = word;
+    if (lane == 0) words[w] = word;
   }
+}
+
+// 16 bytes (part e % 8 of key e / 8, whatever the swizzle's order) of the 64
+// columns c of a tile.
+__device__ __forceinline__ uint4& v_part(const PrefillParams& p, uint8_t* tile, int c, int e) {
+  return *reinterpret_cast<uint4*>(tile + 16 * (c * p.chunk16 + (e >> 6) * p.group16 + (e & 63)));
 }
 
 template <int D>
@@ -589,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     for (int s = 0; s < C::STAGES; ++s)
       for (int c = 0; c < C::NCH; ++c)
         for (int e = p.kt * 8 + threadIdx.x; e < BN * 8; e += C::THREADS)
-          *reinterpret_cast<uint4*>(sm.v[s] + c * CHUNK + e * 16) = make_uint4(0, 0, 0, 0);
+          v_part(p, sm.v[s], c, e) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
   tc_fence_before_sync();
@@ -607,7 +662,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       prefetch_tmap(&p.tv);
     }
     const uint32_t items = p.counters->items;
-    uint32_t i = blockIdx.x, q_it = 0, g = 0;
+    uint32_t i = blockIdx.x, q_it = 0, g = 0, whole = 0;   // whole: masks that hide nothing
+    Ring<C::STAGES> st;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const uint32_t b = k % kItems;
@@ -648,39 +704,40 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (t.n0 < 0) break;
       const Boxes<D> boxes(p, t);
-      int ahead = t.nst > 0 ? boxes.page(step_tile(t, 0), lane) : 0;
-      for (int j = 0; j < t.nst; ++j, ++g) {
-        const int jt = step_tile(t, j);
-        const int page = ahead;
-        if (j + 1 < t.nst) ahead = boxes.page(step_tile(t, j + 1), lane);
-        // which keys exist, and the first one's position
-        KeyMask& km = sm.mask[g % kRing];
-        const bool all = boxes.count <= 32 &&
-                         __all_sync(0xffffffffu, lane >= boxes.count || page < p.num_pages);
-        if (all) {
-          const int keys =
-              p.ppt ? p.kt : p.page_size - (jt - p.fd_tpp.div(jt) * p.tpp) * BN;
-          if (lane < 4) km.word[lane] = bits_below(keys - 32 * lane);
+      Walk walk(t);
+      int ahead = t.nst > 0 ? boxes.entry(walk.j, boxes.m) : 0;
+      for (int j = 0; j < t.nst; ++j) {
+        const int jt = walk.j, page = ahead;
+        walk.next(t);
+        if (j + 1 < t.nst) ahead = boxes.entry(walk.j, boxes.m);
+        // which keys exist: mostly all, as the mask's slot says already
+        const int slot = g % kRing;
+        const int keys = p.ppt ? p.kt : p.page_size - boxes.slot0(jt);
+        if (boxes.count <= 32 && keys >= p.kt &&
+            __all_sync(0xffffffffu, lane >= boxes.count || boxes.exists(page))) {
+          if (!(whole >> slot & 1u)) {
+            if (lane < 4) sm.mask[slot][lane] = bits_below(p.kt - 32 * lane);
+            whole |= 1u << slot;
+          }
         } else {
-          key_words<D>(p, boxes, jt, km);
+          key_words(p, boxes, jt, sm.mask[slot]);
+          whole &= ~(1u << slot);
         }
-        if (lane == 0) km.pos = tile_pos(p, jt);
-        __syncwarp();
-        const int st = g % C::STAGES;
-        if (!mbar_wait_warp(&sm.k_empty[st], ((g / C::STAGES) & 1) ^ 1, abort, kWaitTimeoutNs)) {
+        if (!mbar_wait_warp(&sm.k_empty[st.at], st.phase ^ 1, abort, kWaitTimeoutNs)) {
           fail(p.status, abort, kSiteK);
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[st], p.kt * (D * 2));
-        boxes.load(jt, page, sm.k[st], &p.tk, &sm.k_full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[st.at], p.kt * (D * 2));
+        boxes.load(jt, page, sm.k[st.at], &p.tk, &sm.k_full[st.at]);
         __syncwarp();
+        ++g;
+        st.next();
         if (j == 0) {
           // Q after the first keys: its buffer is free only when the piece
           // before has no more products to issue
           if (!mbar_wait_warp(&sm.q_empty, (q_it & 1) ^ 1, abort, kWaitTimeoutNs)) {
             fail(p.status, abort, kSiteQ);
-            ++g;                               // (K of this tile is in flight)
             ok = false;
             break;
           }
@@ -704,24 +761,26 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   } else if (warp == C::WARPS - 1) {
     // ------------------------------------------------------------ V producer
     uint32_t k = 0, v_it = 0;
+    Ring<C::STAGES> st;
     bool ok = true;
     for (Item t; ok && next_item(sm, k, t, p.status);) {
       const Boxes<D> boxes(p, t);
-      int ahead = t.nst > 0 ? boxes.page(step_tile(t, 0), lane) : 0;
-      for (int j = 0; j < t.nst; ++j, ++v_it) {
-        const int jt = step_tile(t, j);
-        const int page = ahead;
-        if (j + 1 < t.nst) ahead = boxes.page(step_tile(t, j + 1), lane);
-        const int st = v_it % C::STAGES;
-        if (!mbar_wait_warp(&sm.v_empty[st], ((v_it / C::STAGES) & 1) ^ 1, abort,
-                            kWaitTimeoutNs)) {
+      Walk walk(t);
+      int ahead = t.nst > 0 ? boxes.entry(walk.j, boxes.m) : 0;
+      for (int j = 0; j < t.nst; ++j) {
+        const int jt = walk.j, page = ahead;
+        walk.next(t);
+        if (j + 1 < t.nst) ahead = boxes.entry(walk.j, boxes.m);
+        if (!mbar_wait_warp(&sm.v_empty[st.at], st.phase ^ 1, abort, kWaitTimeoutNs)) {
           fail(p.status, abort, kSiteV);
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[st], p.kt * (D * 2));
-        boxes.load(jt, page, sm.v[st], &p.tv, &sm.v_full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[st.at], p.kt * (D * 2));
+        boxes.load(jt, page, sm.v[st.at], &p.tv, &sm.v_full[st.at]);
         __syncwarp();
+        ++v_it;
+        st.next();
       }
     }
     for (int s = 0; s < C::STAGES; ++s)
@@ -759,13 +818,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           break;
         }
         tc_fence_after_sync();
-        const uint64_t dk0 = sdesc_sw128(smem_u32(sm.k[st]), 16, 1024);
+        const uint64_t dk0 = sdesc_sw128(smem_u32(sm.k[st]), 16, p.group16 * 16);
 #pragma unroll
-        for (int kk = 0; kk < C::NCH * 4; ++kk) {
-          const uint32_t off = (kk / 4) * CHUNK + (kk % 4) * 32;
-          mma_bf16_ss_w(tmem + C::TM_S + 128 * b, dq0 + (off >> 4), dk0 + (off >> 4), kIdescS,
-                        kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < C::NCH * 4; ++kk)
+          mma_bf16_ss_w(tmem + C::TM_S + 128 * b, dq0 + ((kk / 4) * CHUNK + (kk % 4) * 32) / 16,
+                        dk0 + ((kk / 4) * p.chunk16 + (kk % 4) * 2), kIdescS, kk > 0 ? 1u : 0u);
         mma_commit_w(&sm.k_empty[st]);
         mma_commit_w(&sm.s_full[b]);
         if (j == t.nst - 1) mma_commit_w(&sm.q_empty);
@@ -781,7 +838,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     uint32_t k = 0, g = 0, o_it = 0;
     bool ok = true;
     for (Item t; ok && next_item(sm, k, t, p.status);) {
-      for (int j = 0; j < t.nst; ++j, ++g) {
+      // the tiles that may hold keys which no token of the row sees
+      const int edge_hi = key_tile(p, t.rhi), edge_lo = key_tile(p, t.rlo);
+      Walk walk(t);
+      for (int j = 0; j < t.nst; ++j, ++g, walk.next(t)) {
         const uint32_t b = g % C::NPB;
         const int st = g % C::STAGES;
         if (!mbar_wait_warp(&sm.v_full[st], (g / C::STAGES) & 1, abort, kWaitTimeoutNs)) {
@@ -791,14 +851,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         // slots that no token of the row sees may hold anything, and 0 NaN is
         // NaN: zeros in their place
-        const int pos = tile_pos(p, step_tile(t, j));
-        if (pos + p.kt > t.rhi || (pos < t.rlo && pos + p.kt > p.sinks)) {
+        if (walk.j >= edge_hi || (walk.j <= edge_lo && t.rlo > 0)) {
+          const int pos = tile_pos(p, walk.j);
           for (int e = lane; e < p.kt * 8; e += 32) {
             const int x = pos + e / 8;
             if (x >= t.rhi || (x < t.rlo && x >= p.sinks)) {
 #pragma unroll
               for (int c = 0; c < C::NCH; ++c)
-                *reinterpret_cast<uint4*>(sm.v[st] + c * CHUNK + e * 16) = make_uint4(0, 0, 0, 0);
+                v_part(p, sm.v[st], c, e) = make_uint4(0, 0, 0, 0);
             }
           }
           fence_proxy_async_smem();
@@ -812,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
           ++o_it;
         }
-        const uint64_t dv0 = sdesc_sw128(smem_u32(sm.v[st]), BN * 128, 1024);
+        const uint64_t dv0 = sdesc_sw128(smem_u32(sm.v[st]), p.chunk16 * 16, p.group16 * 16);
 #pragma unroll
         for (int h = 0; h < C::NHALF; ++h) {
           if (!mbar_wait_warp(&sm.p_full[b * C::NHALF + h], (g / C::NPB) & 1, abort,
@@ -827,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int kk = 0; kk < KH; ++kk)
             mma_bf16_ts_w(tmem + C::TM_O + D * h,
                           tmem + C::TM_P + C::P_STRIDE * b + (BN / C::NHALF) * h + kk * 8,
-                          dv0 + static_cast<uint64_t>(((h * KH + kk) * 16 * 128) >> 4), kIdescPV,
+                          dv0 + (h * KH + kk) * 2 * p.group16, kIdescPV,
                           (j == 0 && kk == 0) ? 0u : 1u);
         }
         if (!ok) break;
@@ -961,11 +1021,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       };
       const int pos = t.pos0 + min(tr, t.ntok - 1), pos_last = t.pos0 + t.ntok - 1;
       const int hi = last_key(pos), lo = max(pos, p.wl) - p.wl;
-      // what every row of the tile sees
-      const int all_hi = min(last_key(t.pos0), last_key(pos_last));
+      // the tiles in between have nothing that some row does not see
+      const int edge_hi = key_tile(p, min(last_key(t.pos0), last_key(pos_last)) + 1);
       const int all_lo = max(pos_last, p.wl) - p.wl;
+      const int edge_lo = all_lo > 0 ? key_tile(p, min(all_lo, t.len)) : -1;
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < t.nst; ++j) {
+      Walk walk(t);
+      for (int j = 0; j < t.nst; ++j, walk.next(t)) {
         const uint32_t b = kv_it % C::NSB;
         const uint32_t t_s = t_lane + C::TM_S + 128 * b;
         if (!mbar_wait_warp(&sm.s_full[b], (kv_it / C::NSB) & 1, abort, kWaitTimeoutNs)) {
@@ -977,14 +1039,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint32_t sr[NC];
 #pragma unroll
         for (int c = 0; c < NC / 32; ++c) tmem_ld_x32(t_s + NC * hf + 32 * c, sr + 32 * c);
-        const KeyMask& km = sm.mask[kv_it % kRing];
         uint32_t word[NC / 32], whole = ~0u;
 #pragma unroll
         for (int w = 0; w < NC / 32; ++w) {
-          word[w] = km.word[NC / 32 * hf + w];
+          word[w] = sm.mask[kv_it % kRing][NC / 32 * hf + w];
           whole &= word[w];
         }
-        const int key0 = km.pos + NC * hf;
         tmem_wait_ld();
         reg_fence<NC>(sr);
         if constexpr (C::SEP) {
@@ -995,7 +1055,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         float s[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sr[c]);
-        if (whole != ~0u || key0 + NC - 1 > all_hi || (key0 < all_lo && key0 + NC > p.sinks)) {
+        if (whole != ~0u || walk.j >= edge_hi || walk.j <= edge_lo) {
+          const int key0 = tile_pos(p, walk.j) + NC * hf;
           const int c_hi = hi - key0, c_lo = lo - key0;
 #pragma unroll
           for (int w = 0; w < NC / 32; ++w) {
@@ -1327,13 +1388,38 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   const long long qd[3] = {H, N, batch};
   const long long qs[3] = {q->head_stride, q->token_stride, q->batch_stride};
   const int qb[3] = {s.gh, s.tpt, 1};
-  const long long kd[3] = {pool.page_size, pool.h_kv, pool.num_pages};
-  const long long ks[3] = {pool.token_stride, pool.head_stride, pool.page_stride};
-  const int kb[3] = {pool.page_size < fa::BM ? pool.page_size : fa::BM, 1, 1};
-  if (!fa::make_map_4d(&p.tq, q->p, pool.d, qd, qs, qb) ||
-      !fa::make_map_4d(&p.tk, pool.k, pool.d, kd, ks, kb) ||
-      !fa::make_map_4d(&p.tv, pool.v, pool.d, kd, ks, kb))
-    return FA_ERR_CUDA;
+  // Pages of whole eights whose step is whole eights too may come in one box
+  // each, with the keys' eights outermost: a copy holds its warp for some 56
+  // cycles, and tiles of few slots a page take many.  Where a page is more than
+  // 8 KB a head, boxes of 64 columns land sooner (whole / by 64 columns, N =
+  // 8192: d = 128, H = 32, h_kv = 8, pages of 8 1044 / 1482 us, 16 842 / 1063, 32
+  // 768 / 839, 64 771 / 737; d = 256, H = 16, h_kv = 4, 8 889 / 1861, 16 866 /
+  // 1003, 32 878 / 784).
+  const long long eight = 8 * pool.token_stride;
+  const long long step = pool.num_pages > 1 ? pool.page_stride / eight : pool.page_size / 8;
+  const long long last = (pool.num_pages - 1) * step + pool.page_size / 8;   // eights in all
+  const bool grouped = pool.page_size % 8 == 0 && pool.page_size * pool.d <= 4096 &&
+                       (pool.num_pages == 1 || pool.page_stride % eight == 0) && last < INT_MAX;
+  const int slots = pool.page_size < fa::BN ? pool.page_size : fa::BN;
+  if (grouped) {
+    const long long gd[4] = {8, pool.d / 64, last, pool.h_kv};
+    const long long gs[4] = {pool.token_stride, 64, eight, pool.head_stride};
+    const int gb[4] = {8, pool.d / 64, slots / 8, 1};
+    if (!fa::make_map_5d(&p.tk, pool.k, gd, gs, gb) || !fa::make_map_5d(&p.tv, pool.v, gd, gs, gb))
+      return FA_ERR_CUDA;
+  } else {
+    const long long kd[3] = {pool.page_size, pool.h_kv, pool.num_pages};
+    const long long ks[3] = {pool.token_stride, pool.head_stride, pool.page_stride};
+    const int kb[3] = {slots, 1, 1};
+    if (!fa::make_map_4d(&p.tk, pool.k, pool.d, kd, ks, kb) ||
+        !fa::make_map_4d(&p.tv, pool.v, pool.d, kd, ks, kb))
+      return FA_ERR_CUDA;
+  }
+  if (!fa::make_map_4d(&p.tq, q->p, pool.d, qd, qs, qb)) return FA_ERR_CUDA;
+  p.groups = grouped ? static_cast<int>(step) : 0;
+  p.eights = static_cast<int>(grouped ? last : 0);
+  p.chunk16 = grouped ? 64 : fa::CHUNK / 16;
+  p.group16 = grouped ? pool.d : 64;
   p.o = static_cast<__nv_bfloat16*>(o->p);
   p.ob = batch > 1 ? o->batch_stride : 0;
   p.oh = H > 1 ? o->head_stride : 0;

@@ -21,6 +21,9 @@ fa_status_t device_facts(int* num_sms, int* max_smem, int** status);
 // axis, 128-byte swizzle, zeros outside.
 bool make_map_4d(CUtensorMap* m, const void* base, int d, const long long* n, const long long* s,
                  const int* box);
+// The same of 64 columns (64, n[0], .., n[3]).
+bool make_map_5d(CUtensorMap* m, const void* base, const long long* n, const long long* s,
+                 const int* box);
 
 // A public fa_strided_t over [B, H, N, d]: 16-byte aligned, strides that are
 // multiples of 8 and reach less than 2^60 values; written tensors also have no
