@@ -89,7 +89,6 @@ struct PrefillParams {
   int max_pages, num_pages, page_size;
   int ppt, tpp, kt;                // pages of a key tile (0: tpp tiles a page), keys of one
   int groups, eights;              // eights of slots from page to page in tk, tv, and in all; or 0
-  uint32_t chunk16, group16;       // of a tile: from 64 columns to 64, from 8 keys to 8 (16 B)
   FastDiv fd_kt, fd_ps, fd_tpp;
   int wl, wr, sinks, causal;
   float scale_log2;
@@ -380,10 +379,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- the main kernel
 
-template <int D>
+// GROUPED: how the boxes of a key tile land (Boxes).
+template <int D, bool GROUPED>
 struct Cfg {
   static constexpr int NCH = D / 64;
   static constexpr int TILE_BYTES = NCH * CHUNK;
+  // of a K or V tile, in 16 bytes: from 64 columns to 64, from 8 keys to 8
+  static constexpr uint32_t CHUNK16 = GROUPED ? 64 : CHUNK / 16, GROUP16 = GROUPED ? D : 64;
   static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 1);
   // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
   // let the one S buffer be refilled once the softmax has loaded it.
@@ -416,9 +418,8 @@ struct alignas(16) Item {
   int kvh, h0, nh, row;
 };
 
-template <int D>
+template <class C>
 struct Smem {
-  using C = Cfg<D>;
   alignas(1024) uint8_t q[C::TILE_BYTES];
   alignas(1024) uint8_t k[C::STAGES][C::TILE_BYTES];
   alignas(1024) uint8_t v[C::STAGES][C::TILE_BYTES];
@@ -505,32 +506,32 @@ struct Ring {
   }
 };
 
-// The boxes of a key tile.  Whole groups of eight slots (p.groups): a box a
+// The boxes of a key tile.  Whole groups of eight slots (GROUPED): a box a
 // page, which lands as [group][64 columns][slot].  Else a box a page (or 128
 // slots of one) and 64 columns, which lands as [64 columns][slot]; box x is
-// columns 64 (x % each) of page x / each.  A lane issues the boxes lane, lane +
+// columns 64 (x % EACH) of page x / EACH.  A lane issues the boxes lane, lane +
 // 32, ..  A page's number is asked for a tile ahead and not looked at before:
 // the producer is the kernel's pace maker, and a look costs it the load's
 // 700 cycles.
-template <int D>
+template <int D, bool GROUPED>
 struct Boxes {
+  static constexpr int EACH = GROUPED ? 1 : D / 64;   // boxes of a page
   const PrefillParams& p;
   const int* row;              // the row's pages
   int head;
   int pages;                   // of the row
-  int each, count;             // boxes of a page, of a tile
+  int count;                   // boxes of a tile
   int m, to;                   // this lane's (first) page of a tile, and where it lands
   __device__ Boxes(const PrefillParams& p_, const Item& t)
-      : p(p_), row(p_.table + static_cast<long long>(t.row) * p_.max_pages), head(t.kvh),
-        each(p_.groups ? 1 : D / 64) {
+      : p(p_), row(p_.table + static_cast<long long>(t.row) * p_.max_pages), head(t.kvh) {
     pages = min(p.max_pages, (t.len + p.page_size - 1) / p.page_size);
-    count = (p.ppt ? p.ppt : 1) * each;
-    m = (threadIdx.x & 31) / each;
+    count = (p.ppt ? p.ppt : 1) * EACH;
+    m = (threadIdx.x & 31) / EACH;
     to = place(threadIdx.x & 31);
   }
   __device__ __forceinline__ int place(int x) const {
-    return p.groups ? x * p.page_size * (D * 2)
-                    : x % (D / 64) * CHUNK + x / (D / 64) * p.page_size * 128;
+    return GROUPED ? x * p.page_size * (D * 2)
+                   : x % (D / 64) * CHUNK + x / (D / 64) * p.page_size * 128;
   }
   // the tile's first slot in its page
   __device__ __forceinline__ int slot0(int j) const {
@@ -547,7 +548,7 @@ struct Boxes {
   __device__ __forceinline__ void box(int x, int entry, int slot0, uint8_t* dst,
                                       const CUtensorMap* map, uint64_t* bar) const {
     // a page that does not exist lies outside the pool
-    if (p.groups)
+    if constexpr (GROUPED)
       tma_load_5d(dst, map, bar, 0, 0, 0,
                   exists(entry) ? entry * p.groups + slot0 / 8 : p.eights, head);
     else
@@ -561,15 +562,15 @@ struct Boxes {
     if (lane < count) box(lane, first, slot0(j), dst + to, map, bar);
     if (count > 32) {
       for (int x = lane + 32; x < count; x += 32)
-        box(x, entry(j, x / each), slot0(j), dst + place(x), map, bar);
+        box(x, entry(j, x / EACH), slot0(j), dst + place(x), map, bar);
     }
   }
 };
 
 // A key tile's mask where pages may be missing, or its boxes are more than the
 // lanes.
-template <int D>
-__device__ __forceinline__ void key_words(const PrefillParams& p, const Boxes<D>& boxes, int j,
+template <class B>
+__device__ __forceinline__ void key_words(const PrefillParams& p, const B& boxes, int j,
                                           uint32_t* words) {
   const int lane = threadIdx.x & 31;
   for (int w = 0; w < 4; ++w) {
@@ -585,15 +586,16 @@ __device__ __forceinline__ void key_words(const PrefillParams& p, const Boxes<D>
 
 // 16 bytes (part e % 8 of key e / 8, whatever the swizzle's order) of the 64
 // columns c of a tile.
-__device__ __forceinline__ uint4& v_part(const PrefillParams& p, uint8_t* tile, int c, int e) {
-  return *reinterpret_cast<uint4*>(tile + 16 * (c * p.chunk16 + (e >> 6) * p.group16 + (e & 63)));
+template <class C>
+__device__ __forceinline__ uint4& v_part(uint8_t* tile, int c, int e) {
+  return *reinterpret_cast<uint4*>(tile + 16 * (c * C::CHUNK16 + (e >> 6) * C::GROUP16 + (e & 63)));
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, bool GROUPED>
+__global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillParams p) {
-  using C = Cfg<D>;
-  using S = Smem<D>;
+  using C = Cfg<D, GROUPED>;
+  using S = Smem<C>;
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t aligned = (raw + 1023) & ~static_cast<uintptr_t>(1023);
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     for (int s = 0; s < C::STAGES; ++s)
       for (int c = 0; c < C::NCH; ++c)
         for (int e = p.kt * 8 + threadIdx.x; e < BN * 8; e += C::THREADS)
-          v_part(p, sm.v[s], c, e) = make_uint4(0, 0, 0, 0);
+          v_part<C>(sm.v[s], c, e) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
   tc_fence_before_sync();
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         mbar_arrive(&sm.item_full[b]);
       }
       if (t.n0 < 0) break;
-      const Boxes<D> boxes(p, t);
+      const Boxes<D, GROUPED> boxes(p, t);
       Walk walk(t);
       int ahead = t.nst > 0 ? boxes.entry(walk.j, boxes.m) : 0;
       for (int j = 0; j < t.nst; ++j) {
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     Ring<C::STAGES> st;
     bool ok = true;
     for (Item t; ok && next_item(sm, k, t, p.status);) {
-      const Boxes<D> boxes(p, t);
+      const Boxes<D, GROUPED> boxes(p, t);
       Walk walk(t);
       int ahead = t.nst > 0 ? boxes.entry(walk.j, boxes.m) : 0;
       for (int j = 0; j < t.nst; ++j) {
@@ -818,11 +820,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           break;
         }
         tc_fence_after_sync();
-        const uint64_t dk0 = sdesc_sw128(smem_u32(sm.k[st]), 16, p.group16 * 16);
+        const uint64_t dk0 = sdesc_sw128(smem_u32(sm.k[st]), 16, C::GROUP16 * 16);
 #pragma unroll
         for (int kk = 0; kk < C::NCH * 4; ++kk)
           mma_bf16_ss_w(tmem + C::TM_S + 128 * b, dq0 + ((kk / 4) * CHUNK + (kk % 4) * 32) / 16,
-                        dk0 + ((kk / 4) * p.chunk16 + (kk % 4) * 2), kIdescS, kk > 0 ? 1u : 0u);
+                        dk0 + ((kk / 4) * C::CHUNK16 + (kk % 4) * 2), kIdescS, kk > 0 ? 1u : 0u);
         mma_commit_w(&sm.k_empty[st]);
         mma_commit_w(&sm.s_full[b]);
         if (j == t.nst - 1) mma_commit_w(&sm.q_empty);
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (x >= t.rhi || (x < t.rlo && x >= p.sinks)) {
 #pragma unroll
               for (int c = 0; c < C::NCH; ++c)
-                v_part(p, sm.v[st], c, e) = make_uint4(0, 0, 0, 0);
+                v_part<C>(sm.v[st], c, e) = make_uint4(0, 0, 0, 0);
             }
           }
           fence_proxy_async_smem();
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
           ++o_it;
         }
-        const uint64_t dv0 = sdesc_sw128(smem_u32(sm.v[st]), p.chunk16 * 16, p.group16 * 16);
+        const uint64_t dv0 = sdesc_sw128(smem_u32(sm.v[st]), C::CHUNK16 * 16, C::GROUP16 * 16);
 #pragma unroll
         for (int h = 0; h < C::NHALF; ++h) {
           if (!mbar_wait_warp(&sm.p_full[b * C::NHALF + h], (g / C::NPB) & 1, abort,
@@ -887,7 +889,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int kk = 0; kk < KH; ++kk)
             mma_bf16_ts_w(tmem + C::TM_O + D * h,
                           tmem + C::TM_P + C::P_STRIDE * b + (BN / C::NHALF) * h + kk * 8,
-                          dv0 + (h * KH + kk) * 2 * p.group16, kIdescPV,
+                          dv0 + (h * KH + kk) * 2 * C::GROUP16, kIdescPV,
                           (j == 0 && kk == 0) ? 0u : 1u);
         }
         if (!ok) break;
@@ -1317,10 +1319,12 @@ Layout layout_of(const Shape& s, int B, int d) {
   return l;
 }
 
-template <int D>
-cudaError_t launch(PrefillParams& p, int max_smem, cudaStream_t stream) {
-  const size_t smem = smem_request(sizeof(Smem<D>), max_smem);
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D, bool GROUPED>
+cudaError_t launch_main(PrefillParams& p, int max_smem, cudaStream_t stream) {
+  using C = Cfg<D, GROUPED>;
+  const size_t smem = smem_request(sizeof(Smem<C>), max_smem);
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, GROUPED>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e == cudaSuccess) e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, stream, p);
   if (e == cudaSuccess) {
@@ -1329,15 +1333,22 @@ cudaError_t launch(PrefillParams& p, int max_smem, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
-    cfg.blockDim = dim3(Cfg<D>::THREADS);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefill_kernel<D>, p);
+    e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, GROUPED>, p);
   }
   if (e == cudaSuccess) e = launch_dependent(join_kernel<D>, dim3(p.grid * 8), 128, stream, p);
   return e;
+}
+
+template <int D>
+cudaError_t launch(PrefillParams& p, int max_smem, cudaStream_t stream) {
+  if constexpr (D > 64)
+    if (p.groups) return launch_main<D, true>(p, max_smem, stream);
+  return launch_main<D, false>(p, max_smem, stream);
 }
 
 }  // namespace
@@ -1398,7 +1409,7 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   const long long eight = 8 * pool.token_stride;
   const long long step = pool.num_pages > 1 ? pool.page_stride / eight : pool.page_size / 8;
   const long long last = (pool.num_pages - 1) * step + pool.page_size / 8;   // eights in all
-  const bool grouped = pool.page_size % 8 == 0 && pool.page_size * pool.d <= 4096 &&
+  const bool grouped = pool.d > 64 && pool.page_size % 8 == 0 && pool.page_size * pool.d <= 4096 &&
                        (pool.num_pages == 1 || pool.page_stride % eight == 0) && last < INT_MAX;
   const int slots = pool.page_size < fa::BN ? pool.page_size : fa::BN;
   if (grouped) {
@@ -1418,8 +1429,6 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   if (!fa::make_map_4d(&p.tq, q->p, pool.d, qd, qs, qb)) return FA_ERR_CUDA;
   p.groups = grouped ? static_cast<int>(step) : 0;
   p.eights = static_cast<int>(grouped ? last : 0);
-  p.chunk16 = grouped ? 64 : fa::CHUNK / 16;
-  p.group16 = grouped ? pool.d : 64;
   p.o = static_cast<__nv_bfloat16*>(o->p);
   p.ob = batch > 1 ? o->batch_stride : 0;
   p.oh = H > 1 ? o->head_stride : 0;
