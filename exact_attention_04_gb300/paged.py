@@ -254,8 +254,7 @@ def append_rotated(q, k_new, v_new, cache, layer, table, start, kv_len, rotary, 
             raise ValueError("q: expected [B, H, N, d]")
         H = q.shape[1]
         qs = rope.view("q", q, (shape[0], H, shape[2], cache.d), index)
-        qo = q if inplace else rope.empty_like(q)
-        qos = rope.view("q", qo, q.shape, index)
+        qo, qos = (q, qs) if inplace else rope.out_like(q)
     _check(fa.load().fa_paged_append_rotated(
         qs, qos, H, rope.view("k_new", k_new, shape, index), rope.view("v_new", v_new, shape, index),
         cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
@@ -294,16 +293,15 @@ def prefill(q, cache, layer, table, start, kv_len, offsets=None, scale=None, cau
         need = _keep(cache, sizes, fa.load().fa_prefill_paged_workspace_bytes(
             rows, H, N, cache.h_kv, d, int(op is not None)))
     qs = rope.view("q", q, shape, index)
-    o = rope.empty_like(q)
+    o, os = rope.out_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     ws, wp = _bytes(ws, need, q)
     left, right = fa._window(window)
     _check(fa.load().fa_prefill_paged(
         qs, cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
-        _ints("kv_len", kv_len, (rows,), index), op, rope.view("o", o, shape, index),
-        lse.data_ptr(), rows, H, N, cache.scale if scale is None else scale, 1 if causal else 0,
-        left, right, _count(sinks), wp, ws.numel() * ws.element_size(),
-        _current_raw_stream(index)), "fa_prefill_paged")
+        _ints("kv_len", kv_len, (rows,), index), op, os, lse.data_ptr(), rows, H, N,
+        cache.scale if scale is None else scale, 1 if causal else 0, left, right,
+        _count(sinks) if sinks else 0, wp, need, _current_raw_stream(index)), "fa_prefill_paged")
     return o, lse
 
 

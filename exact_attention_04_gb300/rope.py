@@ -11,7 +11,8 @@ turns q and k in one pass, ``rotate_back`` takes their gradients back::
     dq, dk = rope.rotate_back(dq, dk, rotary)
 
 Tensors are bf16 [B, H, N, d] with any strides that are multiples of 8
-([B, N, H, d] seen through transpose(1, 2), slices of a fused projection).
+([B, N, H, d] seen through transpose(1, 2), slices of a fused projection);
+results are dense, and laid out like a dense input.
 Nothing synchronises or copies to the host after the Rotary is made.
 paged.append_rotated is the same turn on the way into the paged cache.
 """
@@ -26,6 +27,8 @@ from . import fa
 
 _current_device = torch.cuda.current_device
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_bf16, _int32, _strided = torch.bfloat16, torch.int32, fa.FaStrided
+_load = fa.load
 
 
 def frequencies(dims, base=10000.0, scaling=None):
@@ -122,30 +125,31 @@ class Rotary:
 
 def view(name, t, shape, index):
     """The fa_strided_t of a bf16 tensor of this shape on device `index`."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != index:
+    if t.dtype is not _bf16 or t.shape != shape or t.get_device() != index:
         raise ValueError(f"{name}: expected a bf16 CUDA tensor {list(shape)} on the current device")
     b, h, n, c = t.stride()
-    if (c != 1 and shape[3] > 1) or t.data_ptr() % 16:
-        raise ValueError(f"{name}: d must be contiguous and the tensor 16-byte aligned")
-    for s, size in ((b, shape[0]), (h, shape[1]), (n, shape[2])):
-        if s % 8 and size > 1:
-            raise ValueError(f"{name}: strides must be multiples of 8")
-    return fa.FaStrided(t.data_ptr(), b, h, n)
+    p = t.data_ptr()
+    if (c | p & 15 | (b | h | n) & 7) != 1:        # not d contiguous, 16 bytes, eights
+        if (c != 1 and shape[3] > 1) or p % 16:
+            raise ValueError(f"{name}: d must be contiguous and the tensor 16-byte aligned")
+        for s, size in ((b, shape[0]), (h, shape[1]), (n, shape[2])):
+            if s % 8 and size > 1:
+                raise ValueError(f"{name}: strides must be multiples of 8")
+    return _strided(p, b, h, n)
 
 
-def empty_like(t):
-    """A tensor of t's shape, dense: tokens outside heads where t has them so."""
-    B, H, N, d = t.shape
-    if t.stride(1) < t.stride(2):
-        return torch.empty((B, N, H, d), dtype=t.dtype, device=t.device).transpose(1, 2)
-    return torch.empty((B, H, N, d), dtype=t.dtype, device=t.device)
+def out_like(t):
+    """(a tensor like t, dense, its fa_strided_t)."""
+    o = torch.empty_like(t)
+    b, h, n, _ = o.stride()
+    return o, _strided(o.data_ptr(), b, h, n)
 
 
 def ints(name, t, shape, index):
     """The address of a contiguous int32 tensor, None for None."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index \
+    if t.dtype is not _int32 or t.shape != shape or t.get_device() != index \
             or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor {list(shape)} on the "
                          "current device")
@@ -154,9 +158,10 @@ def ints(name, t, shape, index):
 
 def device_of(q, rotary):
     index = q.get_device()
-    if q.dim() != 4 or index < 0 or index != _current_device():
+    shape = q.shape
+    if len(shape) != 4 or index < 0 or index != _current_device():
         raise ValueError("q: expected a tensor [B, H, N, d] on the current CUDA device")
-    if rotary is not None and (rotary.index != index or rotary.d != q.shape[3]):
+    if rotary.index != index or rotary.d != shape[3]:
         raise ValueError(f"rotary: made for d = {rotary.d} on device {rotary.index}")
     return index
 
@@ -167,19 +172,18 @@ def _call(q, k, rotary, start, pos, inplace, back, stream):
             return _call(q, k, rotary, start, pos, inplace, back, None)
     index = device_of(q, rotary)
     B, H, N, d = shape = q.shape
-    h_kv = 0
-    qo, ko, ks, kos = q if inplace else empty_like(q), None, None, None
+    qs = view("q", q, shape, index)
+    qo, qos = (q, qs) if inplace else out_like(q)
+    h_kv, ko, ks, kos = 0, None, None, None
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k: expected a tensor [B, H_kv, N, d]")
         h_kv = k.shape[1]
         ks = view("k", k, (B, h_kv, N, d), index)
-        ko = k if inplace else empty_like(k)
-        kos = view("k", ko, ko.shape, index)
-    status = fa.load().fa_rotate(
-        view("q", q, shape, index), view("q", qo, shape, index), H, ks, kos, h_kv, B, N, d,
-        ints("start", start, (B,), index), ints("pos", pos, (B, N), index), rotary.ref, int(back),
-        _current_raw_stream(index))
+        ko, kos = (k, ks) if inplace else out_like(k)
+    status = _load().fa_rotate(
+        qs, qos, H, ks, kos, h_kv, B, N, d, ints("start", start, (B,), index),
+        ints("pos", pos, (B, N), index), rotary.ref, back, _current_raw_stream(index))
     if status:
         raise fa.FAError(status, "fa_rotate")
     return qo, ko
@@ -189,9 +193,9 @@ def rotate(q, k, rotary, start=None, pos=None, inplace=False, stream=None):
     """(q, k) turned; q [B, H, N, d], k [B, H_kv, N, d] or None.  Token t is at
     position t, start[b] + t (start: int32 [B]) or pos[b, t] (int32 [B, N]).
     inplace: q and k themselves."""
-    return _call(q, k, rotary, start, pos, inplace, False, stream)
+    return _call(q, k, rotary, start, pos, inplace, 0, stream)
 
 
 def rotate_back(dq, dk, rotary, start=None, pos=None, inplace=False, stream=None):
     """The gradients (dq, dk) of the turned q and k as those of q and k."""
-    return _call(dq, dk, rotary, start, pos, inplace, True, stream)
+    return _call(dq, dk, rotary, start, pos, inplace, 1, stream)

@@ -214,8 +214,16 @@ def test_wrappers_refuse_what_is_not_on_the_gpu():
         rope.view("q", x.transpose(2, 3).contiguous().transpose(2, 3), x.shape, -1)
     v = rope.view("q", x.transpose(1, 2).contiguous().transpose(1, 2), x.shape, -1)
     assert (v.batch_stride, v.head_stride, v.token_stride) == (384, 64, 128)
-    assert rope.empty_like(x.transpose(1, 2).contiguous().transpose(1, 2)).stride() == \
-        (384, 64, 128, 1)
+    o, v = rope.out_like(x.transpose(1, 2).contiguous().transpose(1, 2))
+    assert o.stride() == (384, 64, 128, 1) and v.p == o.data_ptr()
+    assert (v.batch_stride, v.head_stride, v.token_stride) == (384, 64, 128)
+    wide = torch.zeros(1, 3, 4, 72, dtype=torch.bfloat16)[:, :, :2, :64].transpose(1, 2)
+    assert rope.view("q", wide, wide.shape, -1).token_stride == 288
+    o, _ = rope.out_like(wide)
+    assert o.transpose(1, 2).is_contiguous() or o.is_contiguous()
+    with pytest.raises(ValueError):
+        rope.view("q", torch.zeros(2, 2, 3 * 64 + 4, dtype=torch.bfloat16)[:, :, :192].view(
+            2, 2, 3, 64), (2, 2, 3, 64), -1)
     with pytest.raises(ValueError):
         rope.ints("pos", torch.zeros(3), (3,), -1)
     assert rope.ints("pos", None, (3,), -1) is None
