@@ -49,6 +49,7 @@ constexpr int CHUNK = 128 * 128;   // bytes of 128 rows x 64 columns
 constexpr float kRescaleSlack = 24.0f;
 constexpr int kPlanThreads = 256;
 constexpr int kPlanRows = 1024;    // rows whose tiles the plan counts in shared memory
+constexpr float kJoinTiles = 2.f;  // what joining takes, in key tiles
 constexpr int kMostRounds = 4;     // pieces of a cut call: at most so many a CTA, by its sum
 constexpr int kItems = 4;          // pieces announced ahead
 constexpr int kRing = 8;           // key tiles whose masks are kept
@@ -222,8 +223,10 @@ __device__ __forceinline__ void plan_tile(const PrefillParams& p, const int* row
 }
 
 // Lists the pieces.  With W key tiles to walk over all units, cutting the
-// walks into equal pieces of at most W / (k CTAs) tiles, k = 1 ..
-// kMostRounds, or not at all: whichever ends first by the estimate below.
+// walks into equal pieces of about W / (k CTAs) tiles, k = 1 .. kMostRounds, or
+// not at all: whichever ends first by the estimate below.  The code runs once,
+// from instruction caches that hold none of it, so it is kept short: three
+// passes over the tiles through one loop body.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
   __shared__ int sm[kPlanThreads / 32];
   __shared__ int sm_rows[kPlanRows + 1];
@@ -265,106 +268,116 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     tiles = p.B * ((p.N + p.tpt - 1) / p.tpt);
   }
   __syncthreads();
-  // the walks' sum, and the longest
-  unsigned long long s = 0;
-  int longest = 0, n = 0;
+  const bool once = tiles <= kPlanThreads;   // a tile a thread: looked at once
+  int n = 0, before = 0;
   Entry e;
-  const bool once = tiles <= kPlanThreads;
-  for (int i = tid; i < tiles; i += kPlanThreads) {
-    plan_tile(p, rows, i, e, n);
-    s += n;
-    longest = max(longest, n);
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) {
-    atomicAdd(&sum, s);
-    atomicMax(&most, longest);
-  }
-  __syncthreads();
-  const float W = static_cast<float>(sum) * p.units;   // (of an estimate)
-  if (tid < kMostRounds) {
-    // (rounded up, so that the cut tiles' pieces are never more than there is room for)
-    const unsigned long long all = sum * p.units, share = p.grid * (tid + 1ull);
-    const unsigned long long x = (all + share - 1) / share;
-    most_of[tid] = x > INT_MAX ? INT_MAX : (x ? static_cast<int>(x) : 1);
-  }
-  __syncthreads();
-  const bool some = most > most_of[kMostRounds - 1];   // something to cut
-  if (some) {
-    int P[kMostRounds], c[kMostRounds] = {}, len[kMostRounds] = {};
-#pragma unroll
-    for (int k = 0; k < kMostRounds; ++k) P[k] = most_of[k];
-    for (int i = tid; i < tiles; i += kPlanThreads) {
-      if (!once) plan_tile(p, rows, i, e, n);
-#pragma unroll
-      for (int k = 0; k < kMostRounds; ++k) {
-        const int pieces = n > P[k] ? (n + P[k] - 1) / P[k] : 1;
-        c[k] += pieces;
-        len[k] = max(len[k], (n + pieces - 1) / pieces);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kMostRounds; ++k) {
-      const int a = __reduce_add_sync(0xffffffffu, c[k]);
-      const int b = __reduce_max_sync(0xffffffffu, len[k]);
-      if (lane == 0) {
-        atomicAdd(&pieces_of[k], a);
-        atomicMax(&longest_of[k], b);
-      }
-    }
-    __syncthreads();
-    if (tid < 32) {
-      // key tiles that a CTA walks to the end: a piece costs one more, a cut
-      // one two, the join about six
-      const int k = tid - 1;                           // lane 0: no cuts
-      float end = INFINITY;
-      if (k < kMostRounds && (k < 0 || most > most_of[k])) {
-        const float pieces = static_cast<float>(k < 0 ? tiles : pieces_of[k]) * p.units;
-        const float length = k < 0 ? most : longest_of[k], extra = k < 0 ? 1.f : 2.f;
-        const float rounds = ceilf(pieces / p.grid) * (length + extra);
-        const float even = (W + pieces * extra) / p.grid + length;
-        end = fminf(rounds, even) + (k < 0 ? 0.f : 6.f);
-      }
-      float best = end;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
-      const int first = __ffs(__ballot_sync(0xffffffffu, end == best)) - 1;
-      if (tid == 0 && first > 0) cut = most_of[first - 1];
-    }
-    __syncthreads();
-  }
-  int before = 0;
-  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    int c = 0;
-    if (i < tiles) {
-      if (!once) plan_tile(p, rows, i, e, n);
-      c = n > cut ? (n + cut - 1) / cut : 1;
-    }
-    int total;
-    const int at = before + block_scan(c, sm, total);
-    if (c > 0 && at + c <= p.cap_entries) {
-      int slot = -1;
-      if (c > 1) {
-        slot = atomicAdd(&slots, c);
-        if (slot + c <= p.cap_slots) {
-          JoinEntry j = {p.offsets ? 0 : e.row, e.n0, e.ntok, slot, c, {0, 0, 0}};
-          p.joins[atomicAdd(&joins, 1)] = j;
-          atomicMax(&join_most, c);
-        } else {                           // (never: cap_slots holds every cut)
-          slot = -1;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {     // the sum; the cuts; the list
+    unsigned long long s = 0;
+    int longest = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+      const bool in = i0 + tid < tiles;
+      if (in && (pass == 0 || !once)) plan_tile(p, rows, i0 + tid, e, n);
+      if (pass == 0) {
+        if (in) {
+          s += n;
+          longest = max(longest, n);
+        }
+      } else if (pass == 1) {
+#pragma unroll 1
+        for (int k = 0; k < kMostRounds; ++k) {
+          // (an estimate: quotients in fp32)
+          const float c = fmaxf(ceilf(__fdividef(n, most_of[k])), 1.f);
+          const int a = __reduce_add_sync(0xffffffffu, in ? static_cast<int>(c) : 0);
+          const int b = __reduce_max_sync(
+              0xffffffffu, in ? static_cast<int>(ceilf(__fdividef(n, c))) : 0);
+          if (lane == 0) {
+            atomicAdd(&pieces_of[k], a);
+            atomicMax(&longest_of[k], b);
+          }
+        }
+      } else {
+        const int c = !in ? 0 : (n > cut ? (n + cut - 1) / cut : 1);
+        int total;
+        const int at = before + block_scan(c, sm, total);
+        before += total;
+        int slot = -1;
+        const bool room = c > 0 && at + c <= p.cap_entries;
+        if (room && c > 1) {
+          slot = atomicAdd(&slots, c);
+          if (slot + c <= p.cap_slots) {
+            JoinEntry j = {p.offsets ? 0 : e.row, e.n0, e.ntok, slot, c, {0, 0, 0}};
+            p.joins[atomicAdd(&joins, 1)] = j;
+            atomicMax(&join_most, c);
+          } else {                           // (never: cap_slots holds every cut)
+            slot = -1;
+          }
+        }
+        // the first n % c pieces have a key tile more; a tile's thread writes a
+        // few pieces, its warp many
+        const auto put = [&](Entry x, int n, int c, int k, int slot, int at) {
+          const int each = n / c, more = n - each * c;
+          x.s0 = k * each + min(k, more);
+          x.s1 = x.s0 + each + (k < more);
+          x.slot = slot < 0 ? -1 : slot + k;
+          p.entries[at + k] = x;
+        };
+        constexpr int OWN = 6;
+        if (room && c <= OWN) {
+#pragma unroll 1
+          for (int k = 0; k < c; ++k) put(e, n, c, k, slot, at);
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, room && c > OWN); m; m &= m - 1) {
+          const int l = __ffs(m) - 1;
+          const auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
+          const Entry x = {from(e.row), from(e.n0), from(e.ntok), from(e.pos0), from(e.len), 0, 0,
+                           0, from(e.jlo), from(e.ns), from(e.rlo), from(e.rhi)};
+          const int xn = from(n), xc = from(c), xs = from(slot), xa = from(at);
+          for (int k = lane; k < xc; k += 32) put(x, xn, xc, k, xs, xa);
         }
       }
-      for (int k = 0; k < c; ++k) {
-        e.s0 = static_cast<int>(static_cast<long long>(n) * k / c);
-        e.s1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / c);
-        e.slot = slot < 0 ? -1 : slot + k;
-        p.entries[at + k] = e;
-      }
     }
-    before += total;
+    if (pass == 0) {
+      longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) {
+        atomicAdd(&sum, s);
+        atomicMax(&most, longest);
+      }
+      __syncthreads();
+      if (tid < kMostRounds) {
+        // (never less than the share, so that there is room for the cut tiles'
+        // pieces, which are at most twice their key tiles by this)
+        const float x = static_cast<float>(sum) * p.units / (p.grid * (tid + 1)) * 1.000001f + 1.f;
+        most_of[tid] = x < 2e9f ? static_cast<int>(x) : INT_MAX;
+      }
+      __syncthreads();
+      if (most <= most_of[kMostRounds - 1]) ++pass;      // nothing to cut
+    } else if (pass == 1) {
+      __syncthreads();
+      if (tid < 32) {
+        // key tiles that a CTA walks to the end: a piece costs one more, a cut
+        // one two, the joins kJoinTiles
+        const int k = tid - 1;                           // lane 0: no cuts
+        float end = INFINITY;
+        if (k < kMostRounds && (k < 0 || most > most_of[k])) {
+          const float W = static_cast<float>(sum) * p.units;
+          const float pieces = static_cast<float>(k < 0 ? tiles : pieces_of[k]) * p.units;
+          const float length = k < 0 ? most : longest_of[k], extra = k < 0 ? 1.f : 2.f;
+          const float rounds = ceilf(pieces / p.grid) * (length + extra);
+          const float even = (W + pieces * extra) / p.grid + length;
+          end = fminf(rounds, even) + (k < 0 ? 0.f : kJoinTiles);
+        }
+        float best = end;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const int first = __ffs(__ballot_sync(0xffffffffu, end == best)) - 1;
+        if (tid == 0 && first > 0) cut = most_of[first - 1];
+      }
+      __syncthreads();
+    }
   }
   __syncthreads();
   if (tid == 0) {
@@ -438,6 +451,10 @@ struct Smem {
   uint32_t tmem_base;
   int abort;
 };
+
+static_assert(sizeof(Smem<Cfg<64, false>>) <= 232448 && sizeof(Smem<Cfg<128, true>>) <= 232448 &&
+                  sizeof(Smem<Cfg<256, true>>) <= 232448,
+              "shared memory of a block");
 
 enum Site {
   kSiteItem = 41, kSiteItemSlot, kSiteQ, kSiteK, kSiteV, kSiteMmaQ, kSiteMmaK, kSiteMmaS,
@@ -671,10 +688,10 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
       const uint32_t b = k % kItems;
       Item t;
       uint32_t next = 0;
+      const int e = p.fd_units.div(i), u = static_cast<int>(i) - e * p.units;
       if (i < items) {
-        if (lane == 0) next = atomicAdd(&p.counters->next, 1u);   // (used after this piece)
-        const int e = p.fd_units.div(i), u = static_cast<int>(i) - e * p.units;
         const Entry en = p.entries[e];
+        if (lane == 0) next = atomicAdd(&p.counters->next, 1u);   // (used after this piece)
         t.n0 = en.n0;
         t.ntok = en.ntok;
         t.pos0 = en.pos0;
@@ -1186,93 +1203,128 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
 // ---------------------------------------------------------------- the join
 
 // Cut tiles: per row LSE = log sum_s exp(LSE_s) and O = sum_s exp(LSE_s - LSE)
-// O_s, pieces in order.  Few pieces: a warp a row; many: a block a row, its
-// warps every fourth piece each.
+// O_s, pieces in order.  Few pieces: eight rows a warp, whose loads are in
+// flight together (64 tiles of 128 rows in two pieces, 8 heads, d = 128: 67 MB in
+// TJOIN us); many: a block a row, its warps every fourth piece each.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefillParams p) {
   grid_dependency_wait();
-  constexpr int PER = D / 32, W = 4;
+  constexpr int PER = D / 32, V = PER == 2 ? 2 : 4, W = 4, ROWS = 8, FEW = 8;
   __shared__ float sm_o[W][D];
   __shared__ float sm_w[W];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Counters c = *p.counters;
-  const bool wide = c.most > 8;
-  const long long rows = static_cast<long long>(c.joins) * p.units * p.slot_rows;
-  const long long step = wide ? 1 : W;
-  for (long long x0 = blockIdx.x * step; x0 < rows; x0 += gridDim.x * step) {
-    const long long x = wide ? x0 : x0 + warp;
-    JoinEntry j = {};
-    int u = 0, r = 0, tr = 0, h = 0;
-    bool valid = x < rows;
-    if (valid) {
-      const long long item = x / p.slot_rows;
-      r = static_cast<int>(x - item * p.slot_rows);
-      const int e = static_cast<int>(item / p.units);
-      u = static_cast<int>(item - static_cast<long long>(e) * p.units);
-      j = p.joins[e];
-      tr = p.fd_gh.div(r);
-      const int kvh = p.fd_parts.div(u), pt = u - kvh * p.parts;
-      h = kvh * p.group + pt * p.gh + (r - tr * p.gh);
-      valid = tr < j.ntok && r - tr * p.gh < min(p.gh, p.group - pt * p.gh);
-    }
-    if (!wide && !valid) continue;
-    if (wide && !valid) continue;       // (the whole block)
-    const auto at = [&](int s) {
-      return (static_cast<long long>(j.slot0 + s) * p.units + u) * p.slot_rows + r;
+  const bool wide = c.most > FEW;
+  const int per = wide ? 1 : ROWS;                       // rows of a warp (or block)
+  const int groups = (p.slot_rows + per - 1) / per;      // of a tile and unit
+  const long long total = static_cast<long long>(c.joins) * p.units * groups;
+  const long long step = wide ? gridDim.x : gridDim.x * W;
+  for (long long x = wide ? blockIdx.x : blockIdx.x * W + warp; x < total; x += step) {
+    const int item = static_cast<int>(x / groups);       // (joins times units: below 2^31)
+    const int r0 = static_cast<int>(x - static_cast<long long>(item) * groups) * per;
+    const int je = p.fd_units.div(item), u = item - je * p.units;
+    const JoinEntry j = p.joins[je];
+    const int kvh = p.fd_parts.div(u), pt = u - kvh * p.parts;
+    const int nh = min(p.gh, p.group - pt * p.gh), h0 = kvh * p.group + pt * p.gh;
+    // row r of piece s
+    const auto at = [&](int s, int r) {
+      return ((j.slot0 + s) * static_cast<long long>(p.units) + u) * p.slot_rows +
+             min(r, p.slot_rows - 1);
     };
-    // the largest LSE (a NaN stays in the sums below)
+    const auto load = [&](int s, int r, float* v) {
+      const float* src = p.o_part + at(s, r) * D + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; i += V) {
+        if constexpr (V == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + i);
+          v[i] = y.x;
+          v[i + 1] = y.y;
+        } else {
+          const float4 y = *reinterpret_cast<const float4*>(src + i);
+          v[i] = y.x;
+          v[i + 1] = y.y;
+          v[i + 2] = y.z;
+          v[i + 3] = y.w;
+        }
+      }
+    };
+    const auto store = [&](int r, const float* acc, float lse) {
+      const int tr = p.fd_gh.div(r), h = r - tr * p.gh;
+      if (r >= p.slot_rows || tr >= j.ntok || h >= nh) return;
+      const long long tok = j.n0 + tr;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + j.batch * p.ob + (h0 + h) * p.oh +
+                                                  tok * p.ot + lane * PER);
+#pragma unroll
+      for (int i = 0; i < PER / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+      if (lane == 0)
+        p.lse[(static_cast<long long>(j.batch) * p.H + h0 + h) * p.N + tok] = lse;
+    };
+    if (!wide) {
+      // weights: lane l has row l % 8's pieces l / 8 and l / 8 + 4
+      const int r = r0 + lane % ROWS, s = lane / ROWS;
+      const float a = s < j.pieces ? p.lse_part[at(s, r)] : -INFINITY;
+      const float b = s + 4 < j.pieces ? p.lse_part[at(s + 4, r)] : -INFINITY;
+      float m = fmaxf(a, b);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      const float base = m == -INFINITY ? 0.f : m;
+      // (a NaN stays one: the sum is taken over the values themselves)
+      float wa = expf(a - base), wb = expf(b - base);
+      float sum = wa + wb;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse = sum == 0.f ? -INFINITY : base + logf(sum);
+      wa *= inv;
+      wb *= inv;
+      float acc[ROWS][PER] = {};
+#pragma unroll 1
+      for (int s = 0; s < j.pieces; ++s) {
+        float v[ROWS][PER];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) load(s, r0 + i, v[i]);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          const float w = __shfl_sync(0xffffffffu, s < 4 ? wa : wb, (s & 3) * ROWS + i);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[i][e] = fmaf(w, v[i][e], acc[i][e]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) store(r0 + i, acc[i], __shfl_sync(0xffffffffu, lse, i));
+      continue;
+    }
     float m = -INFINITY;
-    for (int s = lane; s < j.pieces; s += 32) m = fmaxf(m, p.lse_part[at(s)]);
+    for (int s = lane; s < j.pieces; s += 32) m = fmaxf(m, p.lse_part[at(s, r0)]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
-    float acc[PER], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    float acc[PER] = {}, sum = 0.f;
 #pragma unroll 4
-    for (int s = wide ? warp : 0; s < j.pieces; s += wide ? W : 1) {
-      const float w = expf(p.lse_part[at(s)] - base);
-      const float* src = p.o_part + at(s) * D + lane * PER;
+    for (int s = warp; s < j.pieces; s += W) {
+      float v[PER];
+      load(s, r0, v);
+      const float w = expf(p.lse_part[at(s, r0)] - base);
       sum += w;
-      if constexpr (PER == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      } else {
 #pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src + i);
-          acc[i] = fmaf(w, v.x, acc[i]);
-          acc[i + 1] = fmaf(w, v.y, acc[i + 1]);
-          acc[i + 2] = fmaf(w, v.z, acc[i + 2]);
-          acc[i + 3] = fmaf(w, v.w, acc[i + 3]);
-        }
-      }
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, v[i], acc[i]);
     }
-    if (wide) {
-      __syncthreads();
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sm_o[warp][lane * PER + i] = acc[i];
-      if (lane == 0) sm_w[warp] = sum;
-      __syncthreads();
-      if (warp > 0) continue;
+    for (int i = 0; i < PER; ++i) sm_o[warp][lane * PER + i] = acc[i];
+    if (lane == 0) sm_w[warp] = sum;
+    __syncthreads();
+    if (warp > 0) continue;
 #pragma unroll
-      for (int w = 1; w < W; ++w) {
-        sum += sm_w[w];
+    for (int w = 1; w < W; ++w) {
+      sum += sm_w[w];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] += sm_o[w][lane * PER + i];
-      }
+      for (int i = 0; i < PER; ++i) acc[i] += sm_o[w][lane * PER + i];
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long tok = j.n0 + tr;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + j.batch * p.ob + h * p.oh + tok * p.ot +
-                                                lane * PER);
 #pragma unroll
-    for (int i = 0; i < PER / 2; ++i)
-      dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0)
-      p.lse[(static_cast<long long>(j.batch) * p.H + h) * p.N + tok] =
-          sum == 0.f ? -INFINITY : base + logf(sum);
+    for (int i = 0; i < PER; ++i) acc[i] *= inv;
+    store(r0, acc, sum == 0.f ? -INFINITY : base + logf(sum));
   }
 }
 
