@@ -5,8 +5,8 @@
 //
 // Bound by memory: each value is read and written once.  A lane owns 16
 // bytes of a head, a warp 32 / (d / 8) tokens, and sine and cosine of a lane's
-// pairs serve all the heads that the warp walks, in steps of kUnroll heads
-// whose loads are in flight together.  The other half of a pair comes from the
+// pairs serve all the heads that the warp walks, kUnroll heads at a time, the
+// next ones' loads in flight meanwhile.  The other half of a pair comes from the
 // lane that owns it (shuffles; where P is no multiple of 8, through shared
 // memory), so the turn may be in place.
 #include <climits>
@@ -64,15 +64,18 @@ struct RotParams {
   int B, max_pages;
 };
 
-// The row of packed token i: the last one that begins at or before i.
+// The row of packed token i, the last one that begins at or before it, by a
+// whole warp: 32 borders a look, so that few of the memory's latencies follow
+// one another.  (Offsets that do not rise give some row.)
 __device__ __forceinline__ int row_of(const int* offsets, int B, int i) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) / 2;
-    if (offsets[m] <= i)
-      lo = m;
-    else
-      hi = m;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = B;
+  while (len > 1) {
+    const int step = (len + 31) / 32, at = lane * step;
+    const bool here = at < len && offsets[lo + at] <= i;
+    const int n = max(__popc(__ballot_sync(0xffffffffu, here)), 1) - 1;
+    lo += n * step;
+    len = min(step, len - n * step);
   }
   return lo;
 }
@@ -137,47 +140,62 @@ __global__ void __launch_bounds__(kWarps * 32)
   const long long tok = (static_cast<long long>(blockIdx.x) * kWarps + warp) * TPW + lane / LPR;
   bool there = tok < p.tokens;
   int b = 0, n = there ? static_cast<int>(tok) : 0, at = 0, limit = 0;
-  if (PAGED && p.offsets) {
-    // (tokens behind the last row are no row's)
-    there = there && n >= p.offsets[0] && n < p.offsets[p.B];
-    if (there) {
-      b = row_of(p.offsets, p.B, n);
-      at = n - p.offsets[b];
-    }
-  } else {
+  const bool packed = PAGED && p.offsets;
+  if (!packed) {
     b = p.fd_n.div(n);
     n -= b * p.N;
     at = n;
   }
-  long long where;                       // the position
+  // The lane's values of the heads of the walk: queries, keys, (paged) values.
+  // The first heads are asked for before the token's row and position are
+  // known, and each group before the one in hand is turned.
+  const int bt = packed ? 0 : b;               // the batch entry of the token's address
+  const __nv_bfloat16* x[3] = {p.t[0].x + bt * p.t[0].xb + n * p.t[0].xt + 8 * ch,
+                               p.t[1].x + bt * p.t[1].xb + n * p.t[1].xt + 8 * ch,
+                               p.v + bt * p.vb + n * p.vt + 8 * ch};
+  const int hq = p.t[0].heads, hk = p.t[1].heads;
+  const int h0 = blockIdx.y * p.chunk, h1 = min(h0 + p.chunk, p.heads);
+  const auto load = [&](int h, uint4* v) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = h + u;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (there && i < h1) {
+        const __nv_bfloat16* from = i < hq ? x[0] + i * p.t[0].xh
+                                    : !PAGED || i < hq + hk
+                                        ? x[1] + (i - hq) * p.t[1].xh
+                                        : x[2] + (i - hq - hk) * p.vh;
+        v[u] = *reinterpret_cast<const uint4*>(from);
+      }
+    }
+  };
+  uint4 v[kUnroll];
+  load(h0, v);
+  unsigned long long turns[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int e = NC * ch + i;           // a pair (neighbours) or a value
+    const int pair = PAIRS != kNeighbours && e >= p.half ? e - p.half : e;
+    turns[i] = pair < p.half ? p.turns[pair] : 0;
+  }
+  if (packed) {
+    // the warp's first token's row; the other tokens' rows follow it
+    const int first = static_cast<int>(
+        min((static_cast<long long>(blockIdx.x) * kWarps + warp) * TPW, p.tokens - 1ll));
+    b = row_of(p.offsets, p.B, first);
+    // (tokens before the first row and behind the last are no row's)
+    there = there && n >= p.offsets[0] && n < p.offsets[p.B];
+    if (there) {
+      while (b + 1 < p.B && p.offsets[b + 1] <= n) ++b;
+      at = n - p.offsets[b];
+    }
+  }
+  long long where = 0;                   // the position
   if (there) {
     where = p.pos ? p.pos[static_cast<long long>(b) * p.N + n]
                   : (p.start ? static_cast<long long>(p.start[b]) : 0) + at;
     if constexpr (PAGED) limit = p.kv_len[b];
-  } else {
-    where = 0;
   }
-  const int bt = PAGED && p.offsets ? 0 : b;   // the batch entry of the token's address
-  float c[NC], s[NC];
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int e = NC * ch + i;           // a pair (neighbours) or a value
-    const bool second = PAIRS != kNeighbours && e >= p.half;
-    const int pair = second ? e - p.half : e;
-    c[i] = 1.f;
-    s[i] = 0.f;
-    if (pair < p.half) {
-      rotary_angle(p.turns[pair], where, p.magnitude, s[i], c[i]);
-      if ((p.back != 0) != (PAIRS != kNeighbours && !second)) s[i] = -s[i];
-    }
-  }
-  // halves: the other value of a pair lies `shift` lanes on
-  const int shift = PAIRS != kHalves ? 0 : (8 * ch < p.half ? p.half / 8 : (8 * ch < 2 * p.half ? -(p.half / 8) : 0));
-  const bool turned = 8 * ch < 2 * p.half;
-  const bool write = there && (turned || p.copy);
-  int h0 = blockIdx.y * p.chunk;
-  const int h1 = min(h0 + p.chunk, p.heads);
-  int first = 0;
   // where a token's keys and values go
   long long slot = -1;
   if constexpr (PAGED) {
@@ -191,48 +209,70 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
     }
   }
+  float c[NC], s[NC];
+  const bool turned = 8 * ch < 2 * p.half;
+  // halves: the other value of a pair lies `shift` lanes on
+  const int shift =
+      PAIRS != kHalves || !turned ? 0 : (8 * ch < p.half ? p.half / 8 : -(p.half / 8));
+  if constexpr (PAIRS == kHalves) {
+    // both lanes of a pair have the same eight angles: each takes four
+    const int mine = shift < 0 ? 4 : 0;
+    float sc[8];
 #pragma unroll
-  for (int k = 0; k < (PAGED ? 3 : 2); ++k) {   // queries, keys, (paged) values
-    const int heads = p.t[k == 2 ? 1 : k].heads;
-    const __nv_bfloat16* x;
-    long long xh, yh;
-    __nv_bfloat16* y;
-    bool out, need;
-    if (k == 2) {
-      x = p.v + bt * p.vb + n * p.vt + 8 * ch;
-      xh = p.vh;
-    } else {
-      x = p.t[k].x + bt * p.t[k].xb + n * p.t[k].xt + 8 * ch;
-      xh = p.t[k].xh;
-    }
-    if (PAGED && k > 0) {
-      y = (k == 1 ? p.pool.k : p.pool.v) + slot;
-      yh = p.pool.head_stride;
-      out = slot >= 0;
-    } else {
-      y = p.t[k].y + bt * p.t[k].yb + n * p.t[k].yt + 8 * ch;
-      yh = p.t[k].yh;
-      out = write;
-    }
-    need = out;
-    for (int h = max(h0 - first, 0); h < min(h1 - first, heads); h += kUnroll) {
-      const int end = min(h1 - first, heads);
-      uint4 v[kUnroll];
+    for (int i = 0; i < 4; ++i)
+      rotary_angle(shift < 0 ? turns[i + 4] : turns[i], where, p.magnitude, sc[2 * i],
+                   sc[2 * i + 1]);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (need && h + u < end) v[u] = *reinterpret_cast<const uint4*>(x + (h + u) * xh);
+    for (int i = 0; i < 4; ++i) {
+      const float so = __shfl_sync(0xffffffffu, sc[2 * i], lane + shift);
+      const float co = __shfl_sync(0xffffffffu, sc[2 * i + 1], lane + shift);
+      s[i] = mine ? so : sc[2 * i];
+      c[i] = mine ? co : sc[2 * i + 1];
+      s[i + 4] = mine ? sc[2 * i] : so;
+      c[i + 4] = mine ? sc[2 * i + 1] : co;
+    }
+    // the first half's values take the other's times -sin, back the other way
+    const bool minus = (p.back != 0) == (shift < 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = minus ? -s[i] : s[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int e = NC * ch + i;
+      const bool second = PAIRS != kNeighbours && e >= p.half;
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if ((second ? e - p.half : e) < p.half) {
+        rotary_angle(turns[i], where, p.magnitude, s[i], c[i]);
+        if ((p.back != 0) != (PAIRS != kNeighbours && !second)) s[i] = -s[i];
       }
+    }
+  }
+  const bool write = there && (turned || p.copy);
+  __nv_bfloat16* const yq = p.t[0].y + bt * p.t[0].yb + n * p.t[0].yt + 8 * ch;
+  __nv_bfloat16* const yk =
+      PAGED ? p.pool.k + slot : p.t[1].y + bt * p.t[1].yb + n * p.t[1].yt + 8 * ch;
+  const long long ykh = PAGED ? p.pool.head_stride : p.t[1].yh;
+#pragma unroll 1
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 next[kUnroll];
+    if (h + kUnroll < h1) load(h + kUnroll, next);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (k < 2) {
-          const uint4 r = turn<D, PAIRS>(v[u], c, s, shift, p.half, row_sm, ch);
-          if (turned) v[u] = r;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = h + u;
+      const uint4 r = turn<D, PAIRS>(v[u], c, s, shift, p.half, row_sm, ch);
+      if (i < h1) {
+        if (i < hq) {
+          if (write) *reinterpret_cast<uint4*>(yq + i * p.t[0].yh) = turned ? r : v[u];
+        } else if (!PAGED || i < hq + hk) {
+          if (PAGED ? slot >= 0 : write)
+            *reinterpret_cast<uint4*>(yk + (i - hq) * ykh) = turned ? r : v[u];
+        } else if (slot >= 0) {
+          *reinterpret_cast<uint4*>(p.pool.v + slot + (i - hq - hk) * p.pool.head_stride) = v[u];
         }
-        if (out && h + u < end) *reinterpret_cast<uint4*>(y + (h + u) * yh) = v[u];
       }
+      v[u] = next[u];
     }
-    first += heads;
   }
 }
 
