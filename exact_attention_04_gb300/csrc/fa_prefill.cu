@@ -116,7 +116,7 @@ __device__ __forceinline__ Row row_at(const PrefillParams& p, int b) {
   int end;
   row_tokens(p.offsets, b, p.N, r.n0, end);
   r.ntok = end - r.n0;
-  // (positions and window sides stay within 2^30, so that sums fit)
+  // (every token's position is an int: starts within 2^30, N below)
   r.start = min(max(p.start[b], -kUnbounded), kUnbounded - 1);
   r.len = min(max(p.kv_len[b], 0), p.max_pages * p.page_size);
   return r;
@@ -143,7 +143,7 @@ __device__ __forceinline__ void tile_keys(const PrefillParams& p, int pos0, int 
   if (p.causal) last = last < len ? last : len - 1;   // tokens at or past len are not there
   if (p.causal && pos0 >= len) last = -1ll - kUnbounded;
   const long long h = last + p.wr + 1;
-  hi = p.wr >= kUnbounded && !p.causal ? len : static_cast<int>(h < 0 ? 0 : (h > len ? len : h));
+  hi = static_cast<int>(h < 0 ? 0 : (h > len ? len : h));
   const long long l = static_cast<long long>(pos0) - p.wl;
   lo = static_cast<int>(l < 0 ? 0 : (l > hi ? hi : l));
 }
@@ -166,22 +166,23 @@ __device__ __forceinline__ int tile_walk(const PrefillParams& p, int pos0, int n
 // ---------------------------------------------------------------- the plan
 
 // Exclusive prefix sum over the block; total to every thread.
-__device__ __forceinline__ int block_scan(int x, int* sm, int& total) {
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T* sm, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
+  T v = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();
   if (lane == 31) sm[warp] = v;
   __syncthreads();
-  int before = 0;
+  T before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const int y = sm[w];
+    const T y = sm[w];
     if (w < warp) before += y;
     total += y;
   }
@@ -229,6 +230,7 @@ __device__ __forceinline__ void plan_tile(const PrefillParams& p, const int* row
 // passes over the tiles through one loop body.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
   __shared__ int sm[kPlanThreads / 32];
+  __shared__ long long sm_long[kPlanThreads / 32];
   __shared__ int sm_rows[kPlanRows + 1];
   __shared__ unsigned long long sum;
   __shared__ int most, cut, slots, joins, join_most;
@@ -246,24 +248,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   int tiles;
   int* rows = p.B <= kPlanRows ? sm_rows : p.row_tiles;
   if (p.offsets) {
-    int before = 0;
+    // (offsets that do not rise may name a token again and again: what is past
+    // the list's room is left out)
+    long long before = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
       const int b = b0 + tid;
-      int n = 0;
+      long long n = 0, total;
       if (b < p.B) {
         int begin, end;
         row_tokens(p.offsets, b, p.N, begin, end);
         n = (end - begin + p.tpt - 1) / p.tpt;
       }
-      int total;
-      const int at = before + block_scan(n, sm, total);
-      if (b < p.B) rows[b] = at;
+      const long long at = before + block_scan(n, sm_long, total);
+      if (b < p.B) rows[b] = static_cast<int>(min(at, static_cast<long long>(p.cap_entries)));
       before += total;
     }
-    if (tid == 0) rows[p.B] = before;
-    // (offsets that do not rise may name a token twice: what is past the
-    // list's room is left out)
-    tiles = before;
+    tiles = static_cast<int>(min(before, static_cast<long long>(p.cap_entries)));
+    if (tid == 0) rows[p.B] = tiles;
   } else {
     tiles = p.B * ((p.N + p.tpt - 1) / p.tpt);
   }
@@ -1513,9 +1514,9 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   p.fd_ps = fa::FastDiv::of(pool.page_size);
   p.fd_tpp = fa::FastDiv::of(p.tpp);
   p.causal = causal != 0;
-  p.wl = window_left < 0 || window_left > fa::kUnbounded ? fa::kUnbounded : window_left;
-  p.wr = window_right < 0 || window_right > fa::kUnbounded ? fa::kUnbounded : window_right;
-  if (p.causal && p.wr > 0) p.wr = 0;
+  // (an unbounded side reaches past every position)
+  p.wl = window_left < 0 ? INT_MAX : window_left;
+  p.wr = p.causal ? 0 : (window_right < 0 ? INT_MAX : window_right);
   p.sinks = sinks;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.status = status;

@@ -79,7 +79,8 @@ def frequencies(dims, base=10000.0, scaling=None):
     return w / factor * ramp + w * (1 - ramp), magnitude
 
 
-_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
+# 2^160 turns of one radian
+_RADIAN = int(2 ** 160 / (2 * Fraction("3.14159265358979323846264338327950288419716939937510582")))
 
 
 def turns_of(freqs):
@@ -87,8 +88,11 @@ def turns_of(freqs):
     freqs = np.asarray(freqs, dtype=np.float64)
     if not np.isfinite(freqs).all():
         raise ValueError("freqs: expected finite angles")
-    return np.array([math.floor(Fraction(float(w)) / _TWO_PI * 2 ** 64) % 2 ** 64 for w in freqs],
-                    dtype=np.uint64)
+    turns = []
+    for w in freqs.tolist():
+        n, d = w.as_integer_ratio()                   # d: a power of two
+        turns.append((n * _RADIAN >> 96 + d.bit_length() - 1) % 2 ** 64)
+    return np.array(turns, dtype=np.uint64)
 
 
 class Rotary:

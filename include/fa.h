@@ -411,8 +411,9 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
  * their keys and values already.  q, o: [B, H, N, d], or with offsets
  * (int32[B + 1], rising) [1, H, N, d] whose tokens offsets[b] ..
  * offsets[b + 1] - 1 are row b's; lse: fp32, contiguous, the same without d.
- * Token t of row b is at position x = start[b] + t and sees key j when j <
- * kv_len[b] (clamped to [0, max_pages * page_size]), its page exists, and
+ * Token t of row b is at position x = start[b] + t (a start outside [-2^30,
+ * 2^30) counts as the nearest) and sees key j when j < kv_len[b] (clamped to
+ * [0, max_pages * page_size]), its page exists, and
  * - causal: j <= x, and the token itself is there, x < kv_len[b] (a token at
  *   or past kv_len sees nothing, so padded rows may end early);
  * - window sides other than -1: j <= x + window_right, and j >= x -
@@ -421,7 +422,9 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
  * (cross attention), of which start says nothing.  A token that sees no key
  * gets O = 0, LSE = -inf; tokens of no row are left as they were.  Query head
  * h reads K/V head h / (H / h_kv), any group size.  Slots that no token of
- * their row sees may hold anything, NaN included.  The GPU divides the work
+ * their row sees may hold anything, NaN included (a value that is not finite
+ * in a slot that one of the row's tokens sees may reach others of them).  The
+ * GPU divides the work
  * from the lengths, along the keys too where rows are few; results repeat bit
  * for bit (on the same GPU model).
  *

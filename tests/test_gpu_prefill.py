@@ -310,6 +310,46 @@ def test_offsets_that_are_none():
     fa.fa_check()
 
 
+def test_offsets_that_name_tokens_2_31_times():
+    """More tiles than an int counts, by offsets that rise and fall: within the
+    buffers, and the first row right."""
+    H, d, page, T, B = 128, 64, 16, 1 << 17, 1 << 16
+    table, start, kv_len, pages = rows_of([0], [20], page)
+    k, v = pools(1, pages, 1, page, d, 1)
+    q = torch.zeros(1, T, H, d, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    q[:, :, :20] = queries(1, H, 20, d, "nhd")
+    offsets, = cuda([0, 20] + [0, T] * ((B - 2) // 2) + [0])
+    assert offsets.numel() == B + 1
+    lens = kv_len.expand(B).contiguous()
+    o, lse = paged.prefill(q, paged.PagedKV(k, v), 0, table[:, :2].expand(B, -1).contiguous(),
+                           torch.zeros_like(lens), lens, offsets)
+    fa.fa_check()
+    r = P.prefill(q[:, :, :20], k, v, 0, table[:, :2], start, kv_len, [0, 20])
+    R.check(r, "o", o[:, :, :20])
+
+
+def test_far_starts():
+    """Without a window a start says nothing of what a token sees, next to 2^30
+    and beyond either; under one it counts as documented."""
+    have, new = [300, 40], [30, 30]
+    table, start, kv_len, pages = rows_of(have, new, 16)
+    k, v = pools(1, pages, 1, 16, 64, 1)
+    q = queries(2, 2, 30, 64, "hnd")
+    cache = paged.PagedKV(k, v)
+    r = P.prefill(q, k, v, 0, table, start, kv_len, causal=False)
+    for far in ([0, -5], [(1 << 30) - 1, (1 << 30) - 7], [1 << 30, (1 << 31) - 1],
+                [-(1 << 31), -(1 << 30)]):
+        o, lse = paged.prefill(q, cache, 0, table, cuda(far)[0], kv_len, causal=False)
+        check(r, o, lse)
+    for far, window in (([(1 << 30) - 3, (1 << 30) - 100], ((1 << 30) - 90, -1)),
+                        ([-200, -20], (-1, 210)), ([-(1 << 30), -30], (-1, (1 << 30) + 50)),
+                        ([(1 << 30) - 1, 700], ((1 << 31) - 2, 0))):
+        far, = cuda(far)
+        kw = dict(causal=False, window=window, sinks=3)
+        o, lse = paged.prefill(q, cache, 0, table, far, kv_len, **kw)
+        check(P.prefill(q, k, v, 0, table, far, kv_len, **kw), o, lse)
+
+
 def test_captured_and_replayed():
     """A captured call follows the lengths, the table and the queries."""
     H, h_kv, d, page, rows, n = 8, 2, 128, 16, 3, 20
