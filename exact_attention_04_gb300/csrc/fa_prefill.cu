@@ -12,20 +12,32 @@
 // does not depend on who takes it or when: results repeat bit for bit.
 //
 // Main kernel, one CTA per SM, roles by warp:
-//   0        producer: takes pieces, looks pages up, loads Q and K by TMA.  A key tile is whole pages (page_size <= 128: as many
-//            as fit, a box a page; else up to 128 slots of one page).  A page
-//            that does not exist is a box outside the pool: TMA fills in
-//            zeros, and a bit mask of the tile's keys hides them.
+//   0        producer: takes pieces, looks pages up, loads Q and K by TMA.  A key
+//            tile is whole pages (page_size <= 128: as many as fit; else up to
+//            128 slots of one).  A page that does not exist is a box outside the
+//            pool: TMA fills in zeros, and a bit mask of the tile's keys hides
+//            them.
 //   1        S = Q K^T on tcgen05 into tensor memory, running ahead
 //   2        O += P V, P from tensor memory
 //   3..      softmax: a row of the tile a thread; with d <= 128 two warps share
 //            a row, each over half of every tile's keys with a maximum, sum
 //            and O of its own
 //   then 4   epilogue: merge the halves, divide, store O and LSE
-//   last     V producer
+//   last     V producer (K and V from one warp: N = 8192, d = 128, pages of 16
+//            1086 us against 752, of 128 783 against 760)
 // The recurrence and its roundings are those of the forward (fa_fwd.cu): S in
 // base-2 units, a reference maximum that moves only when a block exceeds it by
-// 2^24, P rounded to bf16 for the product and summed unrounded.
+// 2^24, P rounded to bf16 for the product (half a step, 2^-8 of a weight) and
+// summed unrounded.
+//
+// What bounds it.  Many query rows: the softmax's instructions and the tensor
+// pipe, as in the forward (H = 32, h_kv = 8, N = 8192, d = 128, not causal, pages
+// of 16 and of 128: 714 and 717 us, 0.80 of the bf16 peak, the forward over
+// contiguous K and V 672; d = 256, H = 16, h_kv = 4: 692 and 676 against 667; d =
+// 64, B = 2, H = 16: 709 and 597 against 590, where the producers' eight copies a
+// tile of 16-token pages are the pace).  Few rows: HBM (32 rows of 4 tokens after
+// 8192, H = 32, h_kv = 8, d = 128: 1077 MB in 165 us, 0.96 of the copy bandwidth).
+// Short calls: the chain plan (4 us), first loads (4), a tile or two, and join (3).
 #include <climits>
 #include <cmath>
 
@@ -404,6 +416,8 @@ struct Cfg {
   // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
   // let the one S buffer be refilled once the softmax has loaded it.
   static constexpr bool SEP = D == 256;
+  // key halves a warp, as the forward's kernels for few key blocks a tile have
+  // them (d = 256: one warp a row, since two O parts would not fit)
   static constexpr int NHALF = D <= 128 ? 2 : 1;
   static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int NPB = SEP ? 2 : NSB;
@@ -1204,9 +1218,12 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
 // ---------------------------------------------------------------- the join
 
 // Cut tiles: per row LSE = log sum_s exp(LSE_s) and O = sum_s exp(LSE_s - LSE)
-// O_s, pieces in order.  Few pieces: eight rows a warp, whose loads are in
-// flight together (64 tiles of 128 rows in two pieces, 8 heads, d = 128: 67 MB in
-// TJOIN us); many: a block a row, its warps every fourth piece each.
+// O_s, pieces in order.  Bound by L2's and HBM's latency.  Few pieces: eight
+// rows a warp, whose loads are in flight together (64 tiles of 128 rows in two
+// pieces, 8 heads, d = 128: 67 MB in 22 us with cold caches; a row a warp took 24
+// us more); many: a block a row, its warps every fourth piece each.  A kernel of
+// its own: the last CTA to finish a tile joining it ran cold code on one SM (one
+// row of 5 tokens after 1000 17 us a call, 40 so).
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefillParams p) {
   grid_dependency_wait();
