@@ -416,8 +416,8 @@ struct Cfg {
   // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
   // let the one S buffer be refilled once the softmax has loaded it.
   static constexpr bool SEP = D == 256;
-  // key halves a warp, as the forward's kernels for few key blocks a tile have
-  // them (d = 256: one warp a row, since two O parts would not fit)
+  // key halves a warp (d = 128, N = 8192: 713 us; one warp a row, with three S
+  // buffers, 848.  d = 256: one warp a row, since two O parts would not fit)
   static constexpr int NHALF = D <= 128 ? 2 : 1;
   static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int NPB = SEP ? 2 : NSB;
