@@ -64,6 +64,11 @@ constexpr int kPlanRows = 1024;    // rows whose tiles the plan counts in shared
 constexpr float kJoinTiles = 2.f;  // what joining takes, in key tiles
 constexpr int kMostRounds = 4;     // pieces of a cut call: at most so many a CTA, by its sum
 constexpr int kItems = 4;          // pieces announced ahead
+constexpr int kMostTail = 8;       // pieces of a tile behind the last whole round
+// What a cut tile's piece takes beside its own key tiles (2 / 6 / 9: 512 tokens
+// after 16000, d = 256, H = 16, h_kv = 4 218 / 164 / 168 us, d = 64, H = 16 90 / 75
+// / 79; two chunks of 512 beside fourteen single tokens 95 / 95 / 110).
+constexpr float kCutTiles = 6.f;
 constexpr int kRing = 8;           // key tiles whose masks are kept
 
 // A piece as the plan lists it, for every unit (K/V head, part of its group).
@@ -236,8 +241,10 @@ __device__ __forceinline__ void plan_tile(const PrefillParams& p, const int* row
 }
 
 // Lists the pieces.  With W key tiles to walk over all units, cutting the
-// walks into equal pieces of about W / (k CTAs) tiles, k = 1 .. kMostRounds, or
-// not at all: whichever ends first by the estimate below.  The code runs once,
+// walks into equal pieces of about W / (k CTAs) tiles, k = 1 .. kMostRounds; or,
+// where the walks are about alike, those behind the last whole round of tiles
+// over the CTAs into 2 .. kMostTail pieces; or not at all: whichever ends first
+// by the estimate below.  The code runs once,
 // from instruction caches that hold none of it, so it is kept short: three
 // passes over the tiles through one loop body.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ long long sm_long[kPlanThreads / 32];
   __shared__ int sm_rows[kPlanRows + 1];
   __shared__ unsigned long long sum;
-  __shared__ int most, cut, slots, joins, join_most;
+  __shared__ int most, cut, cut_from, slots, joins, join_most;
   __shared__ int most_of[kMostRounds], pieces_of[kMostRounds], longest_of[kMostRounds];
   launch_dependents();
   grid_dependency_wait();
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (tid < kMostRounds) pieces_of[tid] = longest_of[tid] = 0;
   if (tid == 0) {
     sum = 0;
-    most = slots = joins = join_most = 0;
+    most = cut_from = slots = joins = join_most = 0;
     cut = INT_MAX;
   }
   // tiles of the rows
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           }
         }
       } else {
-        const int c = !in ? 0 : (n > cut ? (n + cut - 1) / cut : 1);
+        const int c = !in ? 0 : (n > cut && i0 + tid >= cut_from ? (n + cut - 1) / cut : 1);
         int total;
         const int at = before + block_scan(c, sm, total);
         before += total;
@@ -371,23 +378,42 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     } else if (pass == 1) {
       __syncthreads();
       if (tid < 32) {
-        // key tiles that a CTA walks to the end: a piece costs one more, a cut
-        // one two, the joins kJoinTiles
-        const int k = tid - 1;                           // lane 0: no cuts
-        float end = INFINITY;
-        if (k < kMostRounds && (k < 0 || most > most_of[k])) {
-          const float W = static_cast<float>(sum) * p.units;
-          const float pieces = static_cast<float>(k < 0 ? tiles : pieces_of[k]) * p.units;
-          const float length = k < 0 ? most : longest_of[k], extra = k < 0 ? 1.f : 2.f;
-          const float rounds = ceilf(pieces / p.grid) * (length + extra);
-          const float even = (W + pieces * extra) / p.grid + length;
-          end = fminf(rounds, even) + (k < 0 ? 0.f : kJoinTiles);
+        // key tiles that a CTA walks to the end: a whole tile costs one more, a
+        // piece kCutTiles, the joins kJoinTiles.  Lane 0: no cuts; then the
+        // kMostRounds cuts of all; then the tails.
+        const float W = static_cast<float>(sum) * p.units, longest = most;
+        const int k = lane - 1, c = lane - kMostRounds + 1;
+        int from = 0, limit = INT_MAX;
+        float whole = 0.f, pieces = static_cast<float>(tiles) * p.units, length = longest,
+              rest = W, extra = 1.f;
+        bool can = k < 0;
+        if (k >= 0 && k < kMostRounds) {
+          limit = most_of[k];
+          can = most > limit;
+          pieces = static_cast<float>(pieces_of[k]) * p.units;
+          length = longest_of[k];
+        } else if (k >= kMostRounds && c <= kMostTail) {
+          const int rounds = static_cast<int>(pieces / p.grid);
+          from = static_cast<int>(static_cast<long long>(rounds) * p.grid / p.units);
+          limit = (most + c - 1) / c;
+          can = rounds > 0 && limit < most && W * 1.1f > longest * pieces;
+          pieces = static_cast<float>(tiles - from) * p.units * c;
+          length = limit;
+          rest = W - W / tiles * from;
+          whole = rounds * (longest + 1.f);
         }
+        if (k >= 0) extra = kCutTiles;
+        const float even = (rest + pieces * extra) / p.grid + length;
+        float end = whole + fminf(ceilf(pieces / p.grid) * (length + extra), even);
+        if (k >= 0) end += kJoinTiles + 0.5f * pieces / p.grid;   // (its parts' bytes)
+        if (!can) end = INFINITY;
         float best = end;
 #pragma unroll
         for (int o = 16; o; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
-        const int first = __ffs(__ballot_sync(0xffffffffu, end == best)) - 1;
-        if (tid == 0 && first > 0) cut = most_of[first - 1];
+        if (lane == __ffs(__ballot_sync(0xffffffffu, end == best)) - 1) {
+          cut = limit;
+          cut_from = from;
+        }
       }
       __syncthreads();
     }
@@ -404,6 +430,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- the main kernel
+
+static_assert(kMostTail <= 2 * kMostRounds, "room for a tail's pieces");
 
 // GROUPED: how the boxes of a key tile land (Boxes).
 template <int D, bool GROUPED>
@@ -1366,7 +1394,7 @@ bool shape_of(int B, int H, int N, int h_kv, bool packed, int num_sms, Shape* s)
   s->slot_rows = s->gh * (N < s->tpt ? N : s->tpt);
   s->tiles = packed ? N / s->tpt + static_cast<long long>(B)
                     : static_cast<long long>(B) * ((N + s->tpt - 1) / s->tpt);
-  const long long cut = 2ll * kMostRounds * num_sms / s->units + 1;
+  const long long cut = 2ll * kMostRounds * num_sms / s->units + kMostTail + 1;
   s->entries = s->tiles + cut;
   s->slots = cut * s->units;
   return s->entries * s->units < INT_MAX - 4096 && static_cast<long long>(B) * H < INT_MAX &&
