@@ -245,6 +245,32 @@ def test_a_whole_prompt_is_forward_s(d):
         at += n
 
 
+@pytest.mark.parametrize("H,h_kv,N,d,page,new", [
+    (32, 8, 8192, 128, 16, 2048), (32, 8, 5000, 128, 128, 1024), (16, 16, 6000, 64, 16, 2500),
+    (16, 4, 4096, 256, 32, 4096), (16, 4, 9000, 256, 64, 512), (8, 1, 20000, 128, 24, 300)])
+def test_large_chunks_are_forward_s(H, h_kv, N, d, page, new):
+    """Chunks of many tiles, whole and cut in either way, against the forward
+    of the whole sequence: both within their bounds of the exact output, whose
+    sum over weights times |v| is the forward's of |v|."""
+    q, k, v = (randn(1, h, N, d, seed=s) for s, h in ((1, H), (2, h_kv), (3, h_kv)))
+    most = -(-N // page)
+    pool = torch.zeros(2, 1, most, h_kv, page, d, dtype=torch.bfloat16, device="cuda")
+    order = torch.randperm(most, generator=torch.Generator().manual_seed(0)).cuda()
+    for i, t in enumerate((k, v)):
+        padded = torch.zeros(1, h_kv, most * page, d, dtype=torch.bfloat16, device="cuda")
+        padded[:, :, :N] = t
+        pool[i, 0, order] = padded.view(h_kv, most, page, d).transpose(0, 1)
+    table, start, kv_len = order.to(torch.int32)[None], *cuda([N - new], [N])
+    cache = paged.PagedKV(pool[0], pool[1])
+    o, lse = paged.prefill(q[:, :, N - new:], cache, 0, table, start, kv_len)
+    fa.fa_check()
+    want, want_lse = (t[:, :, N - new:] for t in fa.forward(q, k, v, causal=True))
+    mean = fa.forward(q, k, v.abs(), causal=True)[0][:, :, N - new:].float() * 1.02
+    bound = 2.02 * ((R.BF16 + R.F32) * mean + R.BF16 * want.float().abs()) + R.TINY
+    assert ((o.float() - want.float()).abs() <= bound).all()
+    assert (lse - want_lse).abs().max() <= 2e-4
+
+
 def test_scale_and_streams():
     table, start, kv_len, pages = rows_of([100, 3], [40, 7], 16)
     k, v = pools(1, pages, 2, 16, 64, 1)
