@@ -144,7 +144,8 @@ def load():
         lib.fa_pages_trim.restype = i
         lib.fa_pages_compact.argtypes = [pool, vp, i, vp, i, vp, vp, vp, vp, sz, vp]
         lib.fa_pages_compact.restype = i
-        view, rotary = ctypes.POINTER(FaStrided), ctypes.POINTER(FaRotary)
+        # fa_strided_t and fa_rotary_t by address (rope.view packs the former)
+        view = rotary = vp
         lib.fa_rotate.argtypes = [view, view, i, view, view, i, i, i, i, vp, vp, rotary, i, vp]
         lib.fa_rotate.restype = i
         lib.fa_paged_append_rotated.argtypes = [view, view, i, view, view, pool, i, vp, i, vp, vp,

@@ -39,7 +39,8 @@ _current_device = torch.cuda.current_device
 # the current stream of a device as a raw handle; torch.cuda.current_stream()
 # takes 3 us of the about 15 that a small call costs its host
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
-_int32, _bf16 = torch.int32, torch.bfloat16
+_int32, _bf16, _fp32, _uint8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+_empty = torch.empty
 _count = fa.int32_count
 
 
@@ -220,13 +221,16 @@ def append(k_new, v_new, cache, layer, table, start, kv_len, stream=None):
         shape[2], _current_raw_stream(index)), "fa_paged_append")
 
 
-def _rows(cache, table, t, offsets):
+def _rows(cache, table, shape, offsets):
     """(the table's address, rows, its width, the offsets' address) of a call
-    whose queries or keys are t [B, H, N, d]."""
+    whose queries or keys are [B, H, N, d]."""
     tp, rows, max_pages = _table(cache, table)
-    if t.dim() != 4 or t.shape[0] != (rows if offsets is None else 1) or t.shape[3] != cache.d:
-        raise ValueError("expected [rows, H, N, d], or with offsets [1, H, N, d]")
-    return tp, rows, max_pages, rope.ints("offsets", offsets, (rows + 1,), cache.index)
+    if offsets is None:
+        if len(shape) == 4 and shape[0] == rows and shape[3] == cache.d:
+            return tp, rows, max_pages, None
+    elif len(shape) == 4 and shape[0] == 1 and shape[3] == cache.d:
+        return tp, rows, max_pages, _ints("offsets", offsets, (rows + 1,), cache.index)
+    raise ValueError("expected [rows, H, N, d], or with offsets [1, H, N, d]")
 
 
 def append_rotated(q, k_new, v_new, cache, layer, table, start, kv_len, rotary, offsets=None,
@@ -241,24 +245,25 @@ def append_rotated(q, k_new, v_new, cache, layer, table, start, kv_len, rotary, 
     if stream is not None:
         return _on_stream(append_rotated, stream, q, k_new, v_new, cache, layer, table, start,
                           kv_len, rotary, offsets, inplace)
-    tp, rows, max_pages, op = _rows(cache, table, k_new, offsets)
+    shape = k_new.shape
+    tp, rows, max_pages, op = _rows(cache, table, shape, offsets)
     index = cache.index
     if rotary.index != index or rotary.d != cache.d:
         raise ValueError(f"rotary: made for d = {rotary.d} on device {rotary.index}")
-    shape = k_new.shape
     if shape[1] != cache.h_kv:
         raise ValueError("k_new: expected the cache's K/V heads")
     H, qo, qs, qos = 0, None, None, None
     if q is not None:
-        if q.dim() != 4:
+        qshape = q.shape
+        if len(qshape) != 4:
             raise ValueError("q: expected [B, H, N, d]")
-        H = q.shape[1]
+        H = qshape[1]
         qs = rope.view("q", q, (shape[0], H, shape[2], cache.d), index)
         qo, qos = (q, qs) if inplace else rope.out_like(q)
     _check(fa.load().fa_paged_append_rotated(
         qs, qos, H, rope.view("k_new", k_new, shape, index), rope.view("v_new", v_new, shape, index),
         cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
-        _ints("kv_len", kv_len, (rows,), index), op, rows, shape[2], rotary.ref,
+        _ints("kv_len", kv_len, (rows,), index), op, rows, shape[2], rotary.address,
         _current_raw_stream(index)), "fa_paged_append_rotated")
     return qo
 
@@ -284,9 +289,10 @@ def prefill(q, cache, layer, table, start, kv_len, offsets=None, scale=None, cau
     if stream is not None:
         return _on_stream(prefill, stream, q, cache, layer, table, start, kv_len, offsets, scale,
                           causal, window, sinks, ws)
-    tp, rows, max_pages, op = _rows(cache, table, q, offsets)
+    shape = q.shape
+    tp, rows, max_pages, op = _rows(cache, table, shape, offsets)
     index = cache.index
-    B, H, N, d = shape = q.shape
+    B, H, N, d = shape
     sizes = ("prefill", rows, H, N, op is not None)
     need = cache._need.get(sizes)
     if need is None:
@@ -294,9 +300,14 @@ def prefill(q, cache, layer, table, start, kv_len, offsets=None, scale=None, cau
             rows, H, N, cache.h_kv, d, int(op is not None)))
     qs = rope.view("q", q, shape, index)
     o, os = rope.out_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    ws, wp = _bytes(ws, need, q)
-    left, right = fa._window(window)
+    device = q.device
+    lse = _empty((B, H, N), dtype=_fp32, device=device)
+    if ws is None:
+        ws = _empty(need, dtype=_uint8, device=device)
+        wp = ws.data_ptr()
+    else:
+        ws, wp = _bytes(ws, need, q)
+    left, right = (-1, -1) if window is None else fa._window(window)
     _check(fa.load().fa_prefill_paged(
         qs, cache.ref, layer, tp, max_pages, _ints("start", start, (rows,), index),
         _ints("kv_len", kv_len, (rows,), index), op, os, lse.data_ptr(), rows, H, N,

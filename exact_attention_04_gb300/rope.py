@@ -18,6 +18,7 @@ paged.append_rotated is the same turn on the way into the paged cache.
 """
 import ctypes
 import math
+import struct
 from fractions import Fraction
 
 import numpy as np
@@ -27,8 +28,8 @@ from . import fa
 
 _current_device = torch.cuda.current_device
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
-_bf16, _int32, _strided = torch.bfloat16, torch.int32, fa.FaStrided
-_load = fa.load
+_bf16, _int32, _empty_like, _load = torch.bfloat16, torch.int32, torch.empty_like, fa.load
+_pack = struct.Struct("Pqqq").pack     # fa_strided_t
 
 
 def frequencies(dims, base=10000.0, scaling=None):
@@ -124,11 +125,12 @@ class Rotary:
         self.index = self.turns.get_device()
         self.struct = fa.FaRotary(self.turns.data_ptr(), self.magnitude, dims,
                                   int(self.interleaved))
-        self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 def view(name, t, shape, index):
-    """The fa_strided_t of a bf16 tensor of this shape on device `index`."""
+    """The fa_strided_t, packed, of a bf16 tensor of this shape on device
+    `index`."""
     if t.dtype is not _bf16 or t.shape != shape or t.get_device() != index:
         raise ValueError(f"{name}: expected a bf16 CUDA tensor {list(shape)} on the current device")
     b, h, n, c = t.stride()
@@ -139,14 +141,14 @@ def view(name, t, shape, index):
         for s, size in ((b, shape[0]), (h, shape[1]), (n, shape[2])):
             if s % 8 and size > 1:
                 raise ValueError(f"{name}: strides must be multiples of 8")
-    return _strided(p, b, h, n)
+    return _pack(p, b, h, n)
 
 
 def out_like(t):
     """(a tensor like t, dense, its fa_strided_t)."""
-    o = torch.empty_like(t)
+    o = _empty_like(t)
     b, h, n, _ = o.stride()
-    return o, _strided(o.data_ptr(), b, h, n)
+    return o, _pack(o.data_ptr(), b, h, n)
 
 
 def ints(name, t, shape, index):
@@ -160,34 +162,31 @@ def ints(name, t, shape, index):
     return t.data_ptr()
 
 
-def device_of(q, rotary):
-    index = q.get_device()
-    shape = q.shape
-    if len(shape) != 4 or index < 0 or index != _current_device():
-        raise ValueError("q: expected a tensor [B, H, N, d] on the current CUDA device")
-    if rotary.index != index or rotary.d != shape[3]:
-        raise ValueError(f"rotary: made for d = {rotary.d} on device {rotary.index}")
-    return index
-
-
 def _call(q, k, rotary, start, pos, inplace, back, stream):
     if stream is not None:
         with torch.cuda.stream(stream):
             return _call(q, k, rotary, start, pos, inplace, back, None)
-    index = device_of(q, rotary)
-    B, H, N, d = shape = q.shape
+    shape, index = q.shape, q.get_device()
+    if len(shape) != 4 or index < 0 or index != _current_device():
+        raise ValueError("q: expected a tensor [B, H, N, d] on the current CUDA device")
+    B, H, N, d = shape
+    if rotary.index != index or rotary.d != d:
+        raise ValueError(f"rotary: made for d = {rotary.d} on device {rotary.index}")
     qs = view("q", q, shape, index)
     qo, qos = (q, qs) if inplace else out_like(q)
     h_kv, ko, ks, kos = 0, None, None, None
     if k is not None:
-        if k.dim() != 4:
+        kshape = k.shape
+        if len(kshape) != 4:
             raise ValueError("k: expected a tensor [B, H_kv, N, d]")
-        h_kv = k.shape[1]
+        h_kv = kshape[1]
         ks = view("k", k, (B, h_kv, N, d), index)
         ko, kos = (k, ks) if inplace else out_like(k)
     status = _load().fa_rotate(
-        qs, qos, H, ks, kos, h_kv, B, N, d, ints("start", start, (B,), index),
-        ints("pos", pos, (B, N), index), rotary.ref, back, _current_raw_stream(index))
+        qs, qos, H, ks, kos, h_kv, B, N, d,
+        start if start is None else ints("start", start, (B,), index),
+        pos if pos is None else ints("pos", pos, (B, N), index), rotary.address, back,
+        _current_raw_stream(index))
     if status:
         raise fa.FAError(status, "fa_rotate")
     return qo, ko

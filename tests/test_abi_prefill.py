@@ -47,11 +47,11 @@ def test_structure_layouts_match_the_header(tmp_path, struct, name):
 
 
 def strided(p=OK, b=1 << 16, h=1 << 10, t=64):
-    return fa.FaStrided(p, b, h, t)
+    return ctypes.byref(fa.FaStrided(p, b, h, t))
 
 
 def rotary(turns=OK, magnitude=1.0, dims=64, interleaved=0):
-    return fa.FaRotary(turns, magnitude, dims, interleaved)
+    return ctypes.byref(fa.FaRotary(turns, magnitude, dims, interleaved))
 
 
 def rotate(lib, q=None, qo=None, H=4, k=None, ko=None, h_kv=2, B=2, N=16, d=64, start=0, pos=0,
@@ -212,13 +212,18 @@ def test_wrappers_refuse_what_is_not_on_the_gpu():
         rope.view("q", torch.zeros(1, 2, 3, 65, dtype=torch.bfloat16)[..., :64], x.shape, -1)
     with pytest.raises(ValueError):
         rope.view("q", x.transpose(2, 3).contiguous().transpose(2, 3), x.shape, -1)
-    v = rope.view("q", x.transpose(1, 2).contiguous().transpose(1, 2), x.shape, -1)
+    def unpacked(b):
+        assert len(b) == ctypes.sizeof(fa.FaStrided)
+        return fa.FaStrided.from_buffer_copy(b)
+
+    v = unpacked(rope.view("q", x.transpose(1, 2).contiguous().transpose(1, 2), x.shape, -1))
     assert (v.batch_stride, v.head_stride, v.token_stride) == (384, 64, 128)
     o, v = rope.out_like(x.transpose(1, 2).contiguous().transpose(1, 2))
+    v = unpacked(v)
     assert o.stride() == (384, 64, 128, 1) and v.p == o.data_ptr()
     assert (v.batch_stride, v.head_stride, v.token_stride) == (384, 64, 128)
     wide = torch.zeros(1, 3, 4, 72, dtype=torch.bfloat16)[:, :, :2, :64].transpose(1, 2)
-    assert rope.view("q", wide, wide.shape, -1).token_stride == 288
+    assert unpacked(rope.view("q", wide, wide.shape, -1)).token_stride == 288
     o, _ = rope.out_like(wide)
     assert o.transpose(1, 2).is_contiguous() or o.is_contiguous()
     with pytest.raises(ValueError):

@@ -1,5 +1,7 @@
 """Attention of a chunk of new tokens over the paged cache on the GPU, against
 a plain implementation, and together with the cache's other calls."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -299,7 +301,7 @@ def test_tokens_of_no_row_stay():
     ov = fa.FaStrided(buf.data_ptr(), 0, d + 8, (H + 1) * (d + 8))
     st = fa.load().fa_prefill_paged(
         rope.view("q", q, q.shape, 0), cache.ref, 0, table.data_ptr(), table.shape[1],
-        start.data_ptr(), kv_len.data_ptr(), offsets.data_ptr(), ov, lse.data_ptr(), 2, H, T,
+        start.data_ptr(), kv_len.data_ptr(), offsets.data_ptr(), ctypes.byref(ov), lse.data_ptr(), 2, H, T,
         d ** -0.5, 1, -1, -1, 0, ws.data_ptr(), ws.numel(), None)
     assert st == fa.FA_OK
     fa.fa_check()
