@@ -34,8 +34,8 @@
 // pipe, as in the forward (H = 32, h_kv = 8, N = 8192, d = 128, not causal, pages
 // of 16 and of 128: 714 and 717 us, 0.80 of the bf16 peak, the forward over
 // contiguous K and V 672; d = 256, H = 16, h_kv = 4: 692 and 676 against 667; d =
-// 64, B = 2, H = 16: 709 and 597 against 590, where the producers' eight copies a
-// tile of 16-token pages are the pace).  Few rows: HBM (32 rows of 4 tokens after
+// 64, B = 2, H = 16: 624 and 600 against 590, where eight copies a tile of 16-token
+// pages keep the producers busy).  Few rows: HBM (32 rows of 4 tokens after
 // 8192, H = 32, h_kv = 8, d = 128: 1077 MB in 165 us, 0.96 of the copy bandwidth).
 // Short calls: the chain plan (4 us), first loads (4), a tile or two, and join (3).
 #include <climits>
@@ -460,9 +460,9 @@ struct Cfg {
   static constexpr int WARPS = EPI_WARP0 + 4 + 1;
   static constexpr int THREADS = 32 * WARPS;
   // a tile's mask slot is free again before the producer reaches the tile
-  // kRing further on: it writes tile g's mask once K of tile g - 1 is on its
-  // way, when S of g - 1 - STAGES is done, so that the softmax has read the
-  // mask of g - 1 - STAGES - NSB (before it lets go of the S buffer)
+  // kRing further on: it writes tile g's mask, at the earliest, once K of tile
+  // g - 1 is on its way, when S of g - 1 - STAGES is done, so that the softmax
+  // has read the mask of g - 1 - STAGES - NSB (before it lets go of the S buffer)
   static_assert(1 + STAGES + NSB <= kRing, "mask ring");
 };
 
@@ -644,6 +644,23 @@ __device__ __forceinline__ void key_words(const PrefillParams& p, const B& boxes
   }
 }
 
+// A key tile's mask; whole: the slots whose masks hide nothing.
+template <class B>
+__device__ __forceinline__ void set_mask(const PrefillParams& p, const B& boxes, int j, int page,
+                                         uint32_t& whole, int slot, uint32_t* words) {
+  const int lane = threadIdx.x & 31;
+  const int keys = p.ppt ? p.kt : p.page_size - boxes.slot0(j);
+  if (boxes.count <= 32 && keys >= p.kt &&
+      __all_sync(0xffffffffu, lane >= boxes.count || boxes.exists(page))) {
+    if (lane < 4) words[lane] = bits_below(p.kt - 32 * lane);
+    whole |= 1u << slot;
+  } else {
+    key_words(p, boxes, j, words);
+    whole &= ~(1u << slot);
+  }
+  __syncwarp();
+}
+
 // 16 bytes (part e % 8 of key e / 8, whatever the swizzle's order) of the 64
 // columns c of a tile.
 template <class C>
@@ -768,27 +785,40 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
       const Boxes<D, GROUPED> boxes(p, t);
       Walk walk(t);
       int ahead = t.nst > 0 ? boxes.entry(walk.j, boxes.m) : 0;
+      // the keys of every tile are all there if its pages are (asking tile by tile
+      // where a page's last tile is smaller: 685 us where 624 stand below, for 36.8
+      // instead of 37.2 with pages of 1500)
+      const bool plain = boxes.count <= 32 && (p.ppt || p.page_size % BN == 0);
       for (int j = 0; j < t.nst; ++j) {
         const int jt = walk.j, page = ahead;
         walk.next(t);
         if (j + 1 < t.nst) ahead = boxes.entry(walk.j, boxes.m);
-        // which keys exist: mostly all, as the mask's slot says already
+        // which keys exist: mostly all, as the mask's slot says already.  One vote
+        // on this and on the wait, with all it takes ready before: with a vote each
+        // d = 64, N = 8192, pages of 16 take 709 us, not 624.  With one stage the
+        // wait is what everyone waits for, and nothing follows it (d = 256, two
+        // sequences of 3001: 296 us, with one vote 304).
         const int slot = g % kRing;
-        const int keys = p.ppt ? p.kt : p.page_size - boxes.slot0(jt);
-        if (boxes.count <= 32 && keys >= p.kt &&
-            __all_sync(0xffffffffu, lane >= boxes.count || boxes.exists(page))) {
-          if (!(whole >> slot & 1u)) {
-            if (lane < 4) sm.mask[slot][lane] = bits_below(p.kt - 32 * lane);
-            whole |= 1u << slot;
+        int fine = plain && (whole >> slot & 1u) && (lane >= boxes.count || boxes.exists(page));
+        if constexpr (C::STAGES == 1) {
+          if (!__all_sync(0xffffffffu, fine))
+            set_mask(p, boxes, jt, page, whole, slot, sm.mask[slot]);
+          if (!mbar_wait_warp(&sm.k_empty[st.at], st.phase ^ 1, abort, kWaitTimeoutNs)) {
+            fail(p.status, abort, kSiteK);
+            ok = false;
+            break;
           }
         } else {
-          key_words(p, boxes, jt, sm.mask[slot]);
-          whole &= ~(1u << slot);
-        }
-        if (!mbar_wait_warp(&sm.k_empty[st.at], st.phase ^ 1, abort, kWaitTimeoutNs)) {
-          fail(p.status, abort, kSiteK);
-          ok = false;
-          break;
+          asm volatile("" : "+r"(fine));
+          const bool got = mbar_wait(&sm.k_empty[st.at], st.phase ^ 1, abort, kWaitTimeoutNs);
+          if (!__all_sync(0xffffffffu, got && fine)) {
+            if (!__all_sync(0xffffffffu, got)) {
+              fail(p.status, abort, kSiteK);
+              ok = false;
+              break;
+            }
+            set_mask(p, boxes, jt, page, whole, slot, sm.mask[slot]);
+          }
         }
         if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[st.at], p.kt * (D * 2));
         boxes.load(jt, page, sm.k[st.at], &p.tk, &sm.k_full[st.at]);
