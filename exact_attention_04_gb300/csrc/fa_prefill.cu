@@ -244,11 +244,10 @@ __device__ __forceinline__ void plan_tile(const PrefillParams& p, const int* row
 // walks into equal pieces of about W / (k CTAs) tiles, k = 1 .. kMostRounds; or,
 // where the walks are about alike, those behind the last whole round of tiles
 // over the CTAs into 2 .. kMostTail pieces; or not at all: whichever ends first
-// by the estimate below.  The code runs once,
-// from instruction caches that hold none of it, so it is kept short: three
-// passes over the tiles through one loop body.
+// by the estimate below.  The code runs once, from instruction caches that hold
+// none of it, so it is kept short: three passes over the tiles through one loop
+// body.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefillParams p) {
-  __shared__ int sm[kPlanThreads / 32];
   __shared__ long long sm_long[kPlanThreads / 32];
   __shared__ int sm_rows[kPlanRows + 1];
   __shared__ unsigned long long sum;
@@ -319,9 +318,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
       } else {
         const int c = !in ? 0 : (n > cut && i0 + tid >= cut_from ? (n + cut - 1) / cut : 1);
-        int total;
-        const int at = before + block_scan(c, sm, total);
-        before += total;
+        // Where a thread has one tile, the longest pieces go first, by quarters of
+        // the longest: the short ones level the CTAs (in the tiles' order / so: two
+        // chunks of 512 beside fourteen single tokens 95 / 87 us, three of 1000 245
+        // / 212, four of 300 140 / 132; four prompts from 0 on alike).  More tiles
+        // level themselves, and their rows' keys should stay together in L2.  16
+        // bits a quarter: cuts make at most kMostRounds CTAs' pieces beside a
+        // tile's first.
+        int quarter = 0;
+        if (once && c > 0) {
+          const float m = static_cast<float>(cut_from > 0 ? most : min(most, cut));
+          quarter = static_cast<int>(fminf(fmaxf(4.f - __fdividef(4.f * n, c * m), 0.f), 3.f));
+        }
+        long long total;
+        const long long ahead =
+            block_scan(static_cast<long long>(c) << (16 * quarter), sm_long, total);
+        int at = before + static_cast<int>(ahead);
+        if (once) {
+          at = static_cast<int>(ahead >> (16 * quarter) & 0xffff);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const int x = static_cast<int>(total & 0xffff);
+            if (k < quarter) at += x;
+            before += x;
+            total >>= 16;
+          }
+        }
+        before += static_cast<int>(total);
         int slot = -1;
         const bool room = c > 0 && at + c <= p.cap_entries;
         if (room && c > 1) {
@@ -386,6 +409,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         int from = 0, limit = INT_MAX;
         float whole = 0.f, pieces = static_cast<float>(tiles) * p.units, length = longest,
               rest = W, extra = 1.f;
+        const bool alike = W * 1.1f > longest * pieces;
         bool can = k < 0;
         if (k >= 0 && k < kMostRounds) {
           limit = most_of[k];
@@ -396,14 +420,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           const int rounds = static_cast<int>(pieces / p.grid);
           from = static_cast<int>(static_cast<long long>(rounds) * p.grid / p.units);
           limit = (most + c - 1) / c;
-          can = rounds > 0 && limit < most && W * 1.1f > longest * pieces;
+          can = rounds > 0 && limit < most && alike;
           pieces = static_cast<float>(tiles - from) * p.units * c;
           length = limit;
           rest = W - W / tiles * from;
           whole = rounds * (longest + 1.f);
         }
         if (k >= 0) extra = kCutTiles;
-        const float even = (rest + pieces * extra) / p.grid + length;
+        // (level but for the last pieces: of any length, or short ones)
+        const float even = fmaxf((rest + pieces * extra) / p.grid +
+                                     (once && !alike ? 0.5f * length : length),
+                                 length + extra);
         float end = whole + fminf(ceilf(pieces / p.grid) * (length + extra), even);
         if (k >= 0) end += kJoinTiles + 0.5f * pieces / p.grid;   // (its parts' bytes)
         if (!can) end = INFINITY;
