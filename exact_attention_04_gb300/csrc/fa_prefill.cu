@@ -1077,10 +1077,14 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
         }
         float o[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          o[e] = __uint_as_float(orr[0][e]) * a[0];
+        for (int e = 0; e < 32; e += 2) {
+          const auto pair = [&](int h) {
+            return f2_make(__uint_as_float(orr[h][e]), __uint_as_float(orr[h][e + 1]));
+          };
+          uint64_t x = f2_mul(pair(0), f2_make(a[0], a[0]));
 #pragma unroll
-          for (int h = 1; h < C::NHALF; ++h) o[e] = fmaf(__uint_as_float(orr[h][e]), a[h], o[e]);
+          for (int h = 1; h < C::NHALF; ++h) x = f2_fma(pair(h), f2_make(a[h], a[h]), x);
+          f2_split(x, o[e], o[e + 1]);
         }
         if (!valid) continue;
         if (t.slot >= 0) {
