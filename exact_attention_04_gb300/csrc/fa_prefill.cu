@@ -24,20 +24,20 @@
 //            and O of its own
 //   then 4   epilogue: merge the halves, divide, store O and LSE
 //   last     V producer (K and V from one warp: N = 8192, d = 128, pages of 16
-//            1086 us against 752, of 128 783 against 760)
+//            1.44 times as long, of 128 1.03 times)
 // The recurrence and its roundings are those of the forward (fa_fwd.cu): S in
 // base-2 units, a reference maximum that moves only when a block exceeds it by
 // 2^24, P rounded to bf16 for the product (half a step, 2^-8 of a weight) and
 // summed unrounded.
 //
 // What bounds it.  Many query rows: the softmax's instructions and the tensor
-// pipe, as in the forward (H = 32, h_kv = 8, N = 8192, d = 128, not causal, pages
-// of 16 and of 128: 714 and 717 us, 0.80 of the bf16 peak, the forward over
-// contiguous K and V 672; d = 256, H = 16, h_kv = 4: 692 and 676 against 667; d =
-// 64, B = 2, H = 16: 624 and 600 against 590, where eight copies a tile of 16-token
-// pages keep the producers busy).  Few rows: HBM (32 rows of 4 tokens after
-// 8192, H = 32, h_kv = 8, d = 128: 1077 MB in 165 us, 0.96 of the copy bandwidth).
-// Short calls: the chain plan (4 us), first loads (4), a tile or two, and join (3).
+// pipe, as in the forward (N = 8192, not causal, pages of 16 / of 128 / the forward
+// over contiguous K and V: d = 128, H = 32, h_kv = 8 712 / 711 / 676 us, 0.80 of the
+// bf16 peak; d = 256, H = 16, h_kv = 4 688 / 675 / 668; d = 64, B = 2, H = 16 612 /
+// 595 / 594, where eight copies a tile of 16-token pages keep the producers busy).
+// Few rows: HBM (32 rows of 4 tokens after 8192, H = 32, h_kv = 8, d = 128: 1077 MB
+// in 166 us, 0.95 of the copy bandwidth).  Short calls: the chain plan (4 us), first
+// loads (4), a tile or two, and join (3).
 #include <climits>
 #include <cmath>
 
@@ -65,9 +65,9 @@ constexpr float kJoinTiles = 2.f;  // what joining takes, in key tiles
 constexpr int kMostRounds = 4;     // pieces of a cut call: at most so many a CTA, by its sum
 constexpr int kItems = 4;          // pieces announced ahead
 constexpr int kMostTail = 8;       // pieces of a tile behind the last whole round
-// What a cut tile's piece takes beside its own key tiles (2 / 6 / 9: 512 tokens
-// after 16000, d = 256, H = 16, h_kv = 4 218 / 164 / 168 us, d = 64, H = 16 90 / 75
-// / 79; two chunks of 512 beside fourteen single tokens 95 / 95 / 110).
+// What a cut tile's piece takes beside its own key tiles (3 / 6 / 9: 512 tokens
+// after 16000, d = 256, H = 16, h_kv = 4 217 / 164 / 168 us, d = 64, H = 16 86 / 72
+// / 74; four chunks of 300 138 / 132 / 149; two of 1024 305 / 305 / 288).
 constexpr float kCutTiles = 6.f;
 constexpr int kRing = 8;           // key tiles whose masks are kept
 
@@ -471,8 +471,8 @@ struct Cfg {
   // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
   // let the one S buffer be refilled once the softmax has loaded it.
   static constexpr bool SEP = D == 256;
-  // key halves a warp (d = 128, N = 8192: 713 us; one warp a row, with three S
-  // buffers, 848.  d = 256: one warp a row, since two O parts would not fit)
+  // key halves a warp (d = 128, N = 8192: 712 us; one warp a row, with three S
+  // buffers, 878.  d = 256: one warp a row, since two O parts would not fit)
   static constexpr int NHALF = D <= 128 ? 2 : 1;
   static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int NPB = SEP ? 2 : NSB;
@@ -1560,15 +1560,15 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   const int qb[3] = {s.gh, s.tpt, 1};
   // Pages of whole eights whose step is whole eights too may come in one box
   // each, with the keys' eights outermost: a copy holds its warp for some 56
-  // cycles, and tiles of few slots a page take many.  Where a page is more than
-  // 8 KB a head, boxes of 64 columns land sooner (whole / by 64 columns, N =
-  // 8192: d = 128, H = 32, h_kv = 8, pages of 8 1044 / 1482 us, 16 842 / 1063, 32
-  // 768 / 839, 64 771 / 737; d = 256, H = 16, h_kv = 4, 8 889 / 1861, 16 866 /
-  // 1003, 32 878 / 784).
+  // cycles, and tiles of few slots a page take many.  Pages past 32 slots take few
+  // enough in boxes of 64 columns, which land sooner (whole / by 64 columns, N =
+  // 8192: d = 128, H = 32, h_kv = 8, pages of 8 808 / 1287 us, 16 712 / 846, 32 719
+  // / 713, 64 733 / 718; d = 256, H = 16, h_kv = 4, 8 767 / 1409, 16 695 / 957, 32
+  // 677 / 769; 2048 tokens after 8000, 32 254 / 277, 40 271 / 265, 56 290 / 271).
   const long long eight = 8 * pool.token_stride;
   const long long step = pool.num_pages > 1 ? pool.page_stride / eight : pool.page_size / 8;
   const long long last = (pool.num_pages - 1) * step + pool.page_size / 8;   // eights in all
-  const bool grouped = pool.d > 64 && pool.page_size % 8 == 0 && pool.page_size * pool.d <= 4096 &&
+  const bool grouped = pool.d > 64 && pool.page_size % 8 == 0 && pool.page_size <= 32 &&
                        (pool.num_pages == 1 || pool.page_stride % eight == 0) && last < INT_MAX;
   const int slots = pool.page_size < fa::BN ? pool.page_size : fa::BN;
   if (grouped) {
