@@ -3,12 +3,12 @@
 // the other values stay.  A pair is (x_i, x_{i+P}), or (x_2i, x_2i+1) when
 // interleaved.  The gradient is the turn by -t.
 //
-// Bound by memory: each value is read and written once (268 MB in 41.2 us, 0.96
-// of the copy bandwidth; 906 MB of new tokens into pages in 135.5, 0.98).  A lane owns 16
-// bytes of a head, a warp 32 / (d / 8) tokens, and sine and cosine of a lane's
-// pairs serve all the heads that the warp walks, kUnroll heads at a time, the
-// next ones' loads in flight meanwhile.  The other half of a pair comes from the
-// lane that owns it (shuffles; where P is no multiple of 8, through shared
+// Bound by memory: each value is read and written once (268 MB in 41.3 us, 0.96
+// of the copy bandwidth; 906 MB of new tokens into pages in 135.3, 0.98).  A lane
+// owns 16 bytes of a head, a warp 32 / (d / 8) tokens, and sine and cosine of a
+// lane's pairs serve all the heads that the warp walks, kUnroll heads at a time,
+// the next ones' loads in flight meanwhile.  The other half of a pair comes from
+// the lane that owns it (shuffles; where P is no multiple of 8, through shared
 // memory), so the turn may be in place.
 #include <climits>
 #include <cmath>
