@@ -1547,7 +1547,7 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   if (!fa::shape_of(B, H, N, pool.h_kv, offsets != nullptr, 1, &s)) return FA_ERR_INVALID_ARG;
   const int batch = offsets ? 1 : B;
   if (!fa::strided_ok(q, batch, H, N, pool.d, true) ||
-      !fa::strided_ok(o, batch, H, N, pool.d, true))
+      !fa::strided_ok(o, batch, H, N, pool.d, true) || o->p == q->p)
     return FA_ERR_INVALID_ARG;
   const fa_status_t ds = fa::device_facts(&sms, &max_smem, &status);
   if (ds != FA_OK) return ds;

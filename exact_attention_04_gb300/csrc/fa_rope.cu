@@ -351,7 +351,8 @@ fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
   if (!fa::strided_ok(q, B, H, N, d, false) || !fa::strided_ok(q_out, B, H, N, d, true))
     return FA_ERR_INVALID_ARG;
   if (h_kv > 0 && (!fa::strided_ok(k, B, h_kv, N, d, false) ||
-                   !fa::strided_ok(k_out, B, h_kv, N, d, true)))
+                   !fa::strided_ok(k_out, B, h_kv, N, d, true) || q_out->p == k_out->p ||
+                   q_out->p == k->p || k_out->p == q->p))
     return FA_ERR_INVALID_ARG;
   if (!fa::aligned_to(start, 4) || !fa::aligned_to(pos, 4) || (start && pos))
     return FA_ERR_INVALID_ARG;
@@ -398,7 +399,8 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
       !fa::strided_ok(v_new, rows, h_kv, N, d, false))
     return FA_ERR_INVALID_ARG;
   if (H > 0 && (!fa::strided_ok(q, rows, H, N, d, false) ||
-                !fa::strided_ok(q_out, rows, H, N, d, true)))
+                !fa::strided_ok(q_out, rows, H, N, d, true) || q_out->p == k_new->p ||
+                q_out->p == v_new->p))
     return FA_ERR_INVALID_ARG;
   int sms = 0;
   const fa_status_t ds = fa::device_facts(&sms);

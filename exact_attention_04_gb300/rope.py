@@ -195,7 +195,7 @@ def _call(q, k, rotary, start, pos, inplace, back, stream):
 def rotate(q, k, rotary, start=None, pos=None, inplace=False, stream=None):
     """(q, k) turned; q [B, H, N, d], k [B, H_kv, N, d] or None.  Token t is at
     position t, start[b] + t (start: int32 [B]) or pos[b, t] (int32 [B, N]).
-    inplace: q and k themselves."""
+    inplace: q and k themselves (not one tensor as both)."""
     return _call(q, k, rotary, start, pos, inplace, 0, stream)
 
 

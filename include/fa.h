@@ -378,7 +378,8 @@ typedef struct fa_rotary {
  * NULL; both together are refused.  back != 0 turns by the negative angle:
  * the gradients of q_out and k_out to those of q and k (the transpose of a
  * turn; the magnitude is the same).  An output is its input (turned in place)
- * or apart from every input.  d is 64, 128 or 256; B * N is below 2^31 - 1 and
+ * or apart from every input, and the outputs are apart (tensors at one address
+ * are refused).  d is 64, 128 or 256; B * N is below 2^31 - 1 and
  * H + h_kv below 2^16.
  */
 fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
@@ -393,8 +394,8 @@ fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
  * - offsets int32[B + 1], rising: q is [1, H, N, d], k_new and v_new are [1,
  *   h_kv, N, d], and row b has the tokens offsets[b] .. offsets[b + 1] - 1 of
  *   the N.  Tokens of no row are neither read nor written.
- * Token t of row b is at position start[b] + t.  q_out (q or apart from it)
- * gets every token's queries turned; the turned keys and the values go into
+ * Token t of row b is at position start[b] + t.  q_out (q or apart from every
+ * input) gets every token's queries turned; the turned keys and the values go into
  * the token's page as fa_paged_append says (positions from 0 and below
  * kv_len[b], pages that exist).  H = 0: no queries, q and q_out ignored.
  * N is below 2^30, B * N (padded) below 2^31 - 1, H + 2 h_kv below 2^16.
@@ -410,7 +411,8 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
  * Attention of a chunk of new tokens per row over the paged cache, which holds
  * their keys and values already.  q, o: [B, H, N, d], or with offsets
  * (int32[B + 1], rising) [1, H, N, d] whose tokens offsets[b] ..
- * offsets[b + 1] - 1 are row b's; lse: fp32, contiguous, the same without d.
+ * offsets[b + 1] - 1 are row b's; o apart from q; lse: fp32, contiguous, the
+ * same without d.
  * Token t of row b is at position x = start[b] + t (a start outside [-2^30,
  * 2^30) counts as the nearest) and sees key j when j < kv_len[b] (clamped to
  * [0, max_pages * page_size]), its page exists, and
@@ -424,9 +426,8 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
  * h reads K/V head h / (H / h_kv), any group size.  Slots that no token of
  * their row sees may hold anything, NaN included (a value that is not finite
  * in a slot that one of the row's tokens sees may reach others of them).  The
- * GPU divides the work
- * from the lengths, along the keys too where rows are few; results repeat bit
- * for bit (on the same GPU model).
+ * GPU divides the work from the lengths, along the keys too where rows are few;
+ * results repeat bit for bit (on the same GPU model).
  *
  * workspace: fa_prefill_paged_workspace_bytes (packed != 0: with offsets; 0
  * for sizes that no call takes), 256-byte aligned, its contents irrelevant on

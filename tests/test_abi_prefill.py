@@ -46,6 +46,9 @@ def test_structure_layouts_match_the_header(tmp_path, struct, name):
     assert got == [ctypes.sizeof(struct)] + [getattr(struct, n).offset for n in names]
 
 
+APART = OK + (1 << 20)
+
+
 def strided(p=OK, b=1 << 16, h=1 << 10, t=64):
     return ctypes.byref(fa.FaStrided(p, b, h, t))
 
@@ -56,8 +59,9 @@ def rotary(turns=OK, magnitude=1.0, dims=64, interleaved=0):
 
 def rotate(lib, q=None, qo=None, H=4, k=None, ko=None, h_kv=2, B=2, N=16, d=64, start=0, pos=0,
            rot=None):
-    return lib.fa_rotate(q or strided(), qo or strided(), H, k or strided(), ko or strided(), h_kv,
-                         B, N, d, start or None, pos or None, rot or rotary(), 0, None)
+    return lib.fa_rotate(q or strided(), qo or strided(), H, k or strided(APART),
+                         ko or strided(APART), h_kv, B, N, d, start or None, pos or None,
+                         rot or rotary(), 0, None)
 
 
 # views that a written tensor of [2, 4, 16, 64] may not have, and no tensor may
@@ -83,6 +87,11 @@ def test_rotate_errors(lib):
     for bad in (dict(B=0), dict(N=0), dict(H=0), dict(h_kv=-1), dict(H=65535), dict(N=1 << 30),
                 dict(start=OK, pos=OK), dict(start=OK + 2), dict(pos=OK + 1)):
         assert rotate(lib, **bad) == BAD, bad
+    # one tensor as queries and keys, turned in place, and other outputs on inputs
+    assert rotate(lib, k=strided(), ko=strided()) == BAD
+    assert rotate(lib, qo=strided(APART), ko=strided(APART + 4096)) == BAD
+    assert rotate(lib, k=strided(), qo=strided(APART), ko=strided(APART)) == BAD
+    assert rotate(lib, qo=strided(APART + 4096), ko=strided()) == BAD
     assert lib.fa_rotate(None, strided(), 4, None, None, 0, 2, 16, 64, None, None, rotary(), 0,
                          None) == BAD
     assert lib.fa_rotate(strided(), strided(), 4, None, None, 2, 2, 16, 64, None, None, rotary(),
@@ -94,7 +103,8 @@ def test_rotate_errors(lib):
 def append(lib, cache=None, q=None, qo=None, H=4, k=None, v=None, layer=0, table=OK, most=4,
            start=OK, kv_len=OK, offsets=0, B=2, N=16, rot=None):
     return lib.fa_paged_append_rotated(
-        q or strided(), qo or strided(), H, k or strided(), v or strided(), cache or pool(), layer,
+        q or strided(), qo or strided(), H, k or strided(APART), v or strided(2 * APART - OK),
+        cache or pool(), layer,
         table, most, start, kv_len, offsets or None, B, N, rot or rotary(), None)
 
 
@@ -106,6 +116,8 @@ def test_append_rotated_errors(lib):
             assert append(lib, **{name: strided(**change)}) == BAD, (change, name)
     for change in SHARED:
         assert append(lib, qo=strided(**change)) == BAD, change
+    # queries on top of the keys or the values that are read
+    assert append(lib, k=strided()) == BAD and append(lib, v=strided()) == BAD
     for bad in (dict(layer=-1), dict(layer=2), dict(table=0), dict(table=OK + 2), dict(most=0),
                 dict(most=1 << 26), dict(start=0), dict(kv_len=0), dict(start=OK + 2),
                 dict(kv_len=OK + 1), dict(offsets=OK + 2), dict(B=0), dict(N=0), dict(H=-1),
@@ -118,13 +130,14 @@ def prefill(lib, q=None, cache=None, layer=0, table=OK, most=4, start=OK, kv_len
             o=None, lse=OK, B=2, H=4, N=16, scale=0.1, left=-1, right=-1, sinks=0, ws=WS,
             nbytes=BIG):
     return lib.fa_prefill_paged(q or strided(), cache or pool(), layer, table, most, start, kv_len,
-                                offsets or None, o or strided(), lse, B, H, N, scale, 1, left,
+                                offsets or None, o or strided(APART), lse, B, H, N, scale, 1, left,
                                 right, sinks, ws, nbytes, None)
 
 
 def test_prefill_errors(lib):
     for change, status in POOL_ERRORS:
         assert prefill(lib, cache=pool(**change)) == status, change
+    assert prefill(lib, o=strided()) == BAD              # over the queries
     for change in NO_VIEW + SHARED:
         for name in ("q", "o"):
             assert prefill(lib, **{name: strided(**change)}) == BAD, (change, name)

@@ -80,6 +80,11 @@ PREFILL = [
     (4, 2, 128, 16, "hnd", [300, 10], [100, 40], False, None, 0),       # all of kv_len
     (4, 2, 64, 16, "hnd", [300, 10], [100, 40], False, (30, 20), 2),
     (2, 2, 256, 300, "hnd", [200], [180], False, (-1, 7), 0),
+    # rows of very different lengths: the long pieces first, and more tiles than
+    # are put in order
+    (16, 4, 128, 16, "hnd", [3000, 0, 5, 900, 1500, 40, 0, 2200], [1, 90, 1, 64, 2, 1, 33, 30], True,
+     None, 0),
+    (32, 1, 64, 32, "hnd", [0, 700, 30], [700, 333, 120], True, None, 0),
 ]
 
 
