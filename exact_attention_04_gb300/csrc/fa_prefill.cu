@@ -1307,22 +1307,24 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
 // ---------------------------------------------------------------- the join
 
 // Cut tiles: per row LSE = log sum_s exp(LSE_s) and O = sum_s exp(LSE_s - LSE)
-// O_s, pieces in order.  Bound by L2's and HBM's latency.  Few pieces: eight
-// rows a warp, whose loads are in flight together (64 tiles of 128 rows in two
-// pieces, 8 heads, d = 128: 67 MB in 22 us with cold caches; a row a warp took 24
-// us more); many: a block a row, its warps every fourth piece each.  A kernel of
-// its own: the last CTA to finish a tile joining it ran cold code on one SM (one
-// row of 5 tokens after 1000 17 us a call, 40 so).
+// O_s, pieces in order of a tree.  Bound by L2's and HBM's latency.  Up to eight
+// pieces: a warp has all the pieces of 1, 2 or 4 rows in flight together (eight
+// rows piece after piece / so: 64 tokens after 4000, d = 64 24 / 19 us, 128 after
+// 8000, d = 128 41 / 37, 32 rows of 4 tokens 183 / 180, 2048 tokens after 30720 691
+// / 688); more: a block a row, its warps every fourth piece each.  A kernel of its
+// own: the last CTA to finish a tile joining it ran cold code on one SM (one row
+// of 5 tokens after 1000 17 us a call, 40 so).
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefillParams p) {
   grid_dependency_wait();
-  constexpr int PER = D / 32, V = PER == 2 ? 2 : 4, W = 4, ROWS = 8, FEW = 8;
+  constexpr int PER = D / 32, V = PER == 2 ? 2 : 4, W = 4, SLOTS = 8;
   __shared__ float sm_o[W][D];
   __shared__ float sm_w[W];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Counters c = *p.counters;
-  const bool wide = c.most > FEW;
-  const int per = wide ? 1 : ROWS;                       // rows of a warp (or block)
+  const bool wide = c.most > SLOTS;
+  const int shift = c.most <= 2 ? 2 : (c.most <= 4 ? 1 : 0);
+  const int per = 1 << (wide ? 0 : shift);               // rows of a warp (or block)
   const int groups = (p.slot_rows + per - 1) / per;      // of a tile and unit
   const long long total = static_cast<long long>(c.joins) * p.units * groups;
   const long long step = wide ? gridDim.x : gridDim.x * W;
@@ -1367,38 +1369,56 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Prefi
         p.lse[(static_cast<long long>(j.batch) * p.H + h0 + h) * p.N + tok] = lse;
     };
     if (!wide) {
-      // weights: lane l has row l % 8's pieces l / 8 and l / 8 + 4
-      const int r = r0 + lane % ROWS, s = lane / ROWS;
-      const float a = s < j.pieces ? p.lse_part[at(s, r)] : -INFINITY;
-      const float b = s + 4 < j.pieces ? p.lse_part[at(s + 4, r)] : -INFINITY;
-      float m = fmaxf(a, b);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      // slot i (lane, and of v): row i % per, piece i / per
+      const int i8 = lane % SLOTS, s = i8 >> shift;
+      const float a = s < j.pieces ? p.lse_part[at(s, r0 + (i8 & (per - 1)))] : -INFINITY;
+      float v[SLOTS][PER];
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        if ((i >> shift) < j.pieces) {
+          load(i >> shift, r0 + (i & (per - 1)), v[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) v[i][e] = 0.f;
+        }
+      }
+      float m = a;
+#pragma unroll
+      for (int o = SLOTS / 2; o; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, m, o);
+        if (o >= per) m = fmaxf(m, y);
+      }
       const float base = m == -INFINITY ? 0.f : m;
       // (a NaN stays one: the sum is taken over the values themselves)
-      float wa = expf(a - base), wb = expf(b - base);
-      float sum = wa + wb;
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      float w = expf(a - base), sum = w;
+#pragma unroll
+      for (int o = SLOTS / 2; o; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, sum, o);
+        if (o >= per) sum += y;
+      }
+      w *= sum == 0.f ? 0.f : 1.f / sum;
       const float lse = sum == 0.f ? -INFINITY : base + logf(sum);
-      wa *= inv;
-      wb *= inv;
-      float acc[ROWS][PER] = {};
-#pragma unroll 1
-      for (int s = 0; s < j.pieces; ++s) {
-        float v[ROWS][PER];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) load(s, r0 + i, v[i]);
+      for (int i = 0; i < SLOTS; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const float w = __shfl_sync(0xffffffffu, s < 4 ? wa : wb, (s & 3) * ROWS + i);
+        for (int e = 0; e < PER; ++e) v[i][e] *= wi;
+      }
 #pragma unroll
-          for (int e = 0; e < PER; ++e) acc[i][e] = fmaf(w, v[i][e], acc[i][e]);
+      for (int o = SLOTS / 2; o; o >>= 1) {
+        if (o >= per) {
+#pragma unroll
+          for (int i = 0; i < o; ++i) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[i][e] += v[i + o][e];
+          }
         }
       }
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) store(r0 + i, acc[i], __shfl_sync(0xffffffffu, lse, i));
+      for (int i = 0; i < SLOTS / 2; ++i) {
+        const float x = __shfl_sync(0xffffffffu, lse, i);
+        if (i < per) store(r0 + i, v[i], x);
+      }
       continue;
     }
     float m = -INFINITY;
