@@ -103,7 +103,7 @@ struct PrefillParams {
   int B, H, N, h_kv;
   int group, gh, parts, units;     // query heads of a K/V head, of a tile; tiles a group; units
   int tpt;                         // tokens of a tile
-  FastDiv fd_units, fd_parts, fd_gh, fd_tn;
+  FastDiv fd_units, fd_parts, fd_gh, fd_tn, fd_grid;
   int max_pages, num_pages, page_size;
   int ppt, tpp, kt;                // pages of a key tile (0: tpp tiles a page), keys of one
   int groups, eights;              // eights of slots from page to page in tk, tv, and in all; or 0
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           longest = max(longest, n);
         }
       } else if (pass == 1) {
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < kMostRounds; ++k) {
           // (an estimate: quotients in fp32)
           const float c = fmaxf(ceilf(__fdividef(n, most_of[k])), 1.f);
@@ -407,32 +407,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const float W = static_cast<float>(sum) * p.units, longest = most;
         const int k = lane - 1, c = lane - kMostRounds + 1;
         int from = 0, limit = INT_MAX;
-        float whole = 0.f, pieces = static_cast<float>(tiles) * p.units, length = longest,
-              rest = W, extra = 1.f;
+        int pieces = tiles * p.units;
+        float whole = 0.f, length = longest, rest = W, extra = 1.f;
         const bool alike = W * 1.1f > longest * pieces;
         bool can = k < 0;
         if (k >= 0 && k < kMostRounds) {
           limit = most_of[k];
           can = most > limit;
-          pieces = static_cast<float>(pieces_of[k]) * p.units;
+          pieces = pieces_of[k] * p.units;
           length = longest_of[k];
         } else if (k >= kMostRounds && c <= kMostTail) {
-          const int rounds = static_cast<int>(pieces / p.grid);
-          from = static_cast<int>(static_cast<long long>(rounds) * p.grid / p.units);
-          limit = (most + c - 1) / c;
+          const int rounds = p.fd_grid.div(pieces);
+          from = p.fd_units.div(rounds * p.grid);
+          limit = static_cast<int>(__fdividef(longest, c) * 1.000001f) + 1;
           can = rounds > 0 && limit < most && alike;
-          pieces = static_cast<float>(tiles - from) * p.units * c;
+          pieces = (tiles - from) * p.units * c;
           length = limit;
-          rest = W - W / tiles * from;
+          rest = W - __fdividef(W, tiles) * from;
           whole = rounds * (longest + 1.f);
         }
         if (k >= 0) extra = kCutTiles;
         // (level but for the last pieces: of any length, or short ones)
-        const float even = fmaxf((rest + pieces * extra) / p.grid +
+        const float even = fmaxf(__fdividef(rest + pieces * extra, p.grid) +
                                      (once && !alike ? 0.5f * length : length),
                                  length + extra);
-        float end = whole + fminf(ceilf(pieces / p.grid) * (length + extra), even);
-        if (k >= 0) end += kJoinTiles + 0.5f * pieces / p.grid;   // (its parts' bytes)
+        float end = whole + fminf((p.fd_grid.div(pieces - 1) + 1) * (length + extra), even);
+        if (k >= 0) end += kJoinTiles + __fdividef(0.5f * pieces, p.grid);   // (its parts' bytes)
         if (!can) end = INFINITY;
         float best = end;
 #pragma unroll
@@ -1627,6 +1627,7 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   p.units = s.units;
   p.tpt = s.tpt;
   p.fd_units = fa::FastDiv::of(s.units);
+  p.fd_grid = fa::FastDiv::of(sms);
   p.fd_parts = fa::FastDiv::of(s.parts);
   p.fd_gh = fa::FastDiv::of(s.gh);
   p.fd_tn = fa::FastDiv::of((N + s.tpt - 1) / s.tpt);
