@@ -115,7 +115,7 @@ struct PrefillParams {
   int* row_tiles;                  // [B + 1] tiles before a row (offsets)
   Entry* entries;
   JoinEntry* joins;
-  int cap_entries, cap_slots;      // (slots: times units)
+  int cap_tiles, cap_slots;        // (slots: times units)
   int slot_rows;
   float* o_part;
   float* lse_part;
@@ -266,8 +266,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   int tiles;
   int* rows = p.B <= kPlanRows ? sm_rows : p.row_tiles;
   if (p.offsets) {
-    // (offsets that do not rise may name a token again and again: what is past
-    // the list's room is left out)
+    // (offsets that do not rise may name a token again and again: tiles past
+    // those that rising ones can make are left out, so that there is room for
+    // every piece of the others; prefill_shape)
     long long before = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
       const int b = b0 + tid;
@@ -278,10 +279,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         n = (end - begin + p.tpt - 1) / p.tpt;
       }
       const long long at = before + block_scan(n, sm_long, total);
-      if (b < p.B) rows[b] = static_cast<int>(min(at, static_cast<long long>(p.cap_entries)));
+      if (b < p.B) rows[b] = static_cast<int>(min(at, static_cast<long long>(p.cap_tiles)));
       before += total;
     }
-    tiles = static_cast<int>(min(before, static_cast<long long>(p.cap_entries)));
+    tiles = static_cast<int>(min(before, static_cast<long long>(p.cap_tiles)));
     if (tid == 0) rows[p.B] = tiles;
   } else {
     tiles = p.B * ((p.N + p.tpt - 1) / p.tpt);
@@ -346,8 +347,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         before += static_cast<int>(total);
         int slot = -1;
-        const bool room = c > 0 && at + c <= p.cap_entries;
-        if (room && c > 1) {
+        if (c > 1) {
           slot = atomicAdd(&slots, c);
           if (slot + c <= p.cap_slots) {
             JoinEntry j = {p.offsets ? 0 : e.row, e.n0, e.ntok, slot, c, {0, 0, 0}};
@@ -367,11 +367,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           p.entries[at + k] = x;
         };
         constexpr int OWN = 6;
-        if (room && c <= OWN) {
+        if (c <= OWN) {
 #pragma unroll 1
           for (int k = 0; k < c; ++k) put(e, n, c, k, slot, at);
         }
-        for (unsigned m = __ballot_sync(0xffffffffu, room && c > OWN); m; m &= m - 1) {
+        for (unsigned m = __ballot_sync(0xffffffffu, c > OWN); m; m &= m - 1) {
           const int l = __ffs(m) - 1;
           const auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
           const Entry x = {from(e.row), from(e.n0), from(e.ntok), from(e.pos0), from(e.len), 0, 0,
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __syncthreads();
   if (tid == 0) {
     Counters c;
-    c.items = static_cast<unsigned>(min(before, p.cap_entries)) * p.units;
+    c.items = static_cast<unsigned>(before) * p.units;
     c.next = p.grid;
     c.joins = joins;
     c.most = join_most;
@@ -1459,13 +1459,20 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Prefi
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Everything that the sizes determine; false for sizes that no call takes.
-struct Shape {
+}  // namespace
+
+// Everything that the sizes determine.
+struct PrefillShape {
   int group, gh, parts, units, tpt, slot_rows;
-  long long tiles, entries, slots;       // (slots: of all units)
+  long long tiles, entries, slots;       // at most; (slots: of all units)
 };
 
-bool shape_of(int B, int H, int N, int h_kv, bool packed, int num_sms, Shape* s) {
+// False for sizes that no call takes.  The list has room for every piece of
+// `tiles` tiles: in pieces of more than W / (k CTAs), k <= kMostRounds, with W
+// the key tiles of all units, they have less than k CTAs / units pieces beside
+// the first of each, and less than twice that in tiles that are cut; behind the
+// last whole round less than CTAs / units + 1 tiles have kMostTail at most.
+bool prefill_shape(int B, int H, int N, int h_kv, bool packed, int num_sms, PrefillShape* s) {
   if (B < 1 || H < 1 || N < 1 || h_kv < 1 || H % h_kv || N >= kMaxPositions) return false;
   s->group = H / h_kv;
   s->parts = (s->group + BM - 1) / BM;
@@ -1482,11 +1489,13 @@ bool shape_of(int B, int H, int N, int h_kv, bool packed, int num_sms, Shape* s)
          (packed || static_cast<long long>(B) * N < INT_MAX);
 }
 
+namespace {
+
 struct Layout {
   size_t rows, entries, joins, o_part, lse_part, total;
 };
 
-Layout layout_of(const Shape& s, int B, int d) {
+Layout layout_of(const PrefillShape& s, int B, int d) {
   Layout l;
   l.rows = 256;
   l.entries = l.rows + up256((static_cast<size_t>(B) + 1) * sizeof(int));
@@ -1538,8 +1547,8 @@ extern "C" {
 size_t fa_prefill_paged_workspace_bytes(int B, int H, int N, int h_kv, int d, int packed) {
   int sms = 0;
   if (fa::device_facts(&sms) != FA_OK) sms = 152;
-  fa::Shape s;
-  if ((d != 64 && d != 128 && d != 256) || !fa::shape_of(B, H, N, h_kv, packed != 0, sms, &s))
+  fa::PrefillShape s;
+  if ((d != 64 && d != 128 && d != 256) || !fa::prefill_shape(B, H, N, h_kv, packed != 0, sms, &s))
     return 0;
   return fa::layout_of(s, B, d).total;
 }
@@ -1562,16 +1571,16 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   if (!(scale > 0.f && scale <= 3.402823466e38f)) return FA_ERR_INVALID_ARG;
   int sms = 0, max_smem = 0;
   int* status = nullptr;
-  fa::Shape s;
+  fa::PrefillShape s;
   // (the sizes are checked before the device is asked)
-  if (!fa::shape_of(B, H, N, pool.h_kv, offsets != nullptr, 1, &s)) return FA_ERR_INVALID_ARG;
+  if (!fa::prefill_shape(B, H, N, pool.h_kv, offsets != nullptr, 1, &s)) return FA_ERR_INVALID_ARG;
   const int batch = offsets ? 1 : B;
   if (!fa::strided_ok(q, batch, H, N, pool.d, true) ||
       !fa::strided_ok(o, batch, H, N, pool.d, true) || o->p == q->p)
     return FA_ERR_INVALID_ARG;
   const fa_status_t ds = fa::device_facts(&sms, &max_smem, &status);
   if (ds != FA_OK) return ds;
-  if (!fa::shape_of(B, H, N, pool.h_kv, offsets != nullptr, sms, &s)) return FA_ERR_INVALID_ARG;
+  if (!fa::prefill_shape(B, H, N, pool.h_kv, offsets != nullptr, sms, &s)) return FA_ERR_INVALID_ARG;
   const fa::Layout l = fa::layout_of(s, B, pool.d);
   if (workspace_bytes < l.total) return FA_ERR_INVALID_ARG;
   fa::PrefillParams p = {};
@@ -1654,7 +1663,7 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
   p.joins = reinterpret_cast<fa::JoinEntry*>(ws + l.joins);
   p.o_part = reinterpret_cast<float*>(ws + l.o_part);
   p.lse_part = reinterpret_cast<float*>(ws + l.lse_part);
-  p.cap_entries = static_cast<int>(s.entries);
+  p.cap_tiles = static_cast<int>(s.tiles);
   p.cap_slots = static_cast<int>(s.slots / s.units);
   p.slot_rows = s.slot_rows;
   p.grid = sms;
