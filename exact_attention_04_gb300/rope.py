@@ -135,7 +135,7 @@ def view(name, t, shape, index):
         raise ValueError(f"{name}: expected a bf16 CUDA tensor {list(shape)} on the current device")
     b, h, n, c = t.stride()
     p = t.data_ptr()
-    if (c | p & 15 | (b | h | n) & 7) != 1:        # not d contiguous, 16 bytes, eights
+    if c != 1 or p & 15 | (b | h | n) & 7:         # not d contiguous, 16 bytes, eights
         if (c != 1 and shape[3] > 1) or p % 16:
             raise ValueError(f"{name}: d must be contiguous and the tensor 16-byte aligned")
         for s, size in ((b, shape[0]), (h, shape[1]), (n, shape[2])):
