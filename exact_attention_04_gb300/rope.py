@@ -147,7 +147,10 @@ def view(name, t, shape, index):
 def out_like(t):
     """(a tensor like t, dense, its fa_strided_t)."""
     o = _empty_like(t)
-    b, h, n, _ = o.stride()
+    b, h, n, c = o.stride()
+    if c != 1:             # (like an expanded input with an axis of one at stride one)
+        o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        b, h, n, _ = o.stride()
     return o, _pack(o.data_ptr(), b, h, n)
 
 
