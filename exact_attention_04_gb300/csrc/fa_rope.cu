@@ -126,6 +126,13 @@ __device__ __forceinline__ uint4 turn(uint4 x, const float* c, const float* s, i
       r[i] = pack_bf16x2(fmaf(bf16_lo(w[i]), c[2 * i], other[2 * i] * s[2 * i]),
                          fmaf(bf16_hi(w[i]), c[2 * i + 1], other[2 * i + 1] * s[2 * i + 1]));
   }
+  if constexpr (PAIRS != kHalves) {
+    // values behind the pairs stay: as numbers turned by nothing, an infinity
+    // would become 0 inf, and in its neighbour too
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * ch + i >= half) r[i] = w[i];
+  }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 

@@ -277,3 +277,53 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         want = rope.rotate(q, k, rotary, start=start)
         assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+# values of every kind: infinities, NaN (also with a payload), -0, the largest
+# and the smallest
+KINDS = [0x7f80, 0xff80, 0x7fc0, 0xffc1, 0x7fa5, 0x8000, 0x0000, 0x7f7f, 0xff7f, 0x0001, 0x8001,
+         0x3f80]
+
+
+@pytest.mark.parametrize("d,dims", [(64, 38), (64, 2), (64, 32), (64, 60), (128, 102), (128, 126),
+                                    (128, 64), (256, 90), (256, 254)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_values_behind_the_pairs_stay(d, dims, interleaved):
+    """Bit for bit, whatever they are and wherever the border falls, and they
+    change no turned value: apart, in place, back, and on the way into the
+    pages."""
+    B, H, h_kv, N, page = 2, 3, 2, 13, 8
+    rotary = rope.Rotary(d, dims, interleaved=interleaved)
+    finite = [randn(B, h, N, d, seed=h) for h in (H, h_kv)]
+    kinds = torch.tensor(KINDS, dtype=torch.int32).to(torch.int16).cuda()
+    odd = []
+    for i, x in enumerate(finite):
+        y = x.clone()
+        at = torch.arange(y[..., dims:].numel(), device="cuda") * 7 + i
+        # (each value's place moves from token to token)
+        at += torch.arange(N, device="cuda").repeat_interleave(d - dims).repeat(B * x.shape[1])
+        y[..., dims:] = kinds[at % len(KINDS)].view(torch.bfloat16).view(y[..., dims:].shape)
+        odd.append(y)
+
+    def bits(x):
+        return x.contiguous().view(torch.int16)
+
+    for call in (rope.rotate, rope.rotate_back):
+        want = call(*finite, rotary)
+        got = call(*odd, rotary)
+        same = call(*(x.clone() for x in odd), rotary, inplace=True)
+        for x, w, g, s in zip(odd, want, got, same):
+            assert torch.equal(bits(g)[..., :dims], bits(w)[..., :dims])
+            assert torch.equal(bits(g)[..., dims:], bits(x)[..., dims:])
+            assert torch.equal(bits(s), bits(g))
+    q, k = rope.rotate(*odd, rotary)
+    start, kv_len = cuda([0] * B, [N] * B)
+    table = torch.arange(B * 2, dtype=torch.int32, device="cuda").view(B, 2)
+    for inplace in (False, True):
+        kp, vp = pools(1, B * 2, h_kv, page, d, 0)
+        qa = paged.append_rotated(odd[0].clone(), odd[1], odd[1], paged.PagedKV(kp, vp), 0, table,
+                                  start, kv_len, rotary, inplace=inplace)
+        assert torch.equal(bits(qa), bits(q))
+        for pool, x in ((kp, k), (vp, odd[1])):
+            rows = pool[0].view(B, 2, h_kv, page, d).transpose(1, 2).reshape(B, h_kv, 16, d)
+            assert torch.equal(bits(rows[:, :, :N]), bits(x))
