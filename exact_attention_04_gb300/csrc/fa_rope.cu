@@ -334,10 +334,16 @@ RotTensor rot_tensor(const fa_strided_t* x, const fa_strided_t* y, int heads) {
                    y ? y->batch_stride : 0, y ? y->head_stride : 0, y ? y->token_stride : 0, heads};
 }
 
+// Whether b is a itself, seen alike (turned in place).
 bool same(const fa_strided_t* a, const fa_strided_t* b, int B, int H, int N) {
   return a->p == b->p && (B == 1 || a->batch_stride == b->batch_stride) &&
          (H == 1 || a->head_stride == b->head_stride) &&
          (N == 1 || a->token_stride == b->token_stride);
+}
+
+// An output at its input's address, but seen through other strides.
+bool crossed(const fa_strided_t* a, const fa_strided_t* b, int B, int H, int N) {
+  return a->p == b->p && !same(a, b, B, H, N);
 }
 
 }  // namespace
@@ -355,11 +361,12 @@ fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
   if (B < 1 || N < 1 || H < 1 || h_kv < 0 || static_cast<long long>(H) + h_kv > 65535 ||
       static_cast<long long>(B) * N >= INT_MAX)
     return FA_ERR_INVALID_ARG;
-  if (!fa::strided_ok(q, B, H, N, d, false) || !fa::strided_ok(q_out, B, H, N, d, true))
+  if (!fa::strided_ok(q, B, H, N, d, false) || !fa::strided_ok(q_out, B, H, N, d, true) ||
+      fa::crossed(q, q_out, B, H, N))
     return FA_ERR_INVALID_ARG;
   if (h_kv > 0 && (!fa::strided_ok(k, B, h_kv, N, d, false) ||
                    !fa::strided_ok(k_out, B, h_kv, N, d, true) || q_out->p == k_out->p ||
-                   q_out->p == k->p || k_out->p == q->p))
+                   q_out->p == k->p || k_out->p == q->p || fa::crossed(k, k_out, B, h_kv, N)))
     return FA_ERR_INVALID_ARG;
   if (!fa::aligned_to(start, 4) || !fa::aligned_to(pos, 4) || (start && pos))
     return FA_ERR_INVALID_ARG;
@@ -407,7 +414,7 @@ fa_status_t fa_paged_append_rotated(const fa_strided_t* q, const fa_strided_t* q
     return FA_ERR_INVALID_ARG;
   if (H > 0 && (!fa::strided_ok(q, rows, H, N, d, false) ||
                 !fa::strided_ok(q_out, rows, H, N, d, true) || q_out->p == k_new->p ||
-                q_out->p == v_new->p))
+                q_out->p == v_new->p || fa::crossed(q, q_out, rows, H, N)))
     return FA_ERR_INVALID_ARG;
   int sms = 0;
   const fa_status_t ds = fa::device_facts(&sms);

@@ -379,8 +379,8 @@ typedef struct fa_rotary {
  * the gradients of q_out and k_out to those of q and k (the transpose of a
  * turn; the magnitude is the same).  An output is its input (turned in place)
  * or apart from every input, and the outputs are apart (tensors at one address
- * are refused).  d is 64, 128 or 256; B * N is below 2^31 - 1 and
- * H + h_kv below 2^16.
+ * are refused, and an output at its input's address through other strides).
+ * d is 64, 128 or 256; B * N is below 2^31 - 1 and H + h_kv below 2^16.
  */
 fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
                       const fa_strided_t* k, const fa_strided_t* k_out, int h_kv, int B, int N,

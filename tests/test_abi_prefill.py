@@ -100,6 +100,27 @@ def test_rotate_errors(lib):
                          None) == BAD
 
 
+def test_in_place_is_at_the_same_strides(lib):
+    """An output at its input's address that sees it through other strides
+    would overwrite what is still to be read; of axes of one strides do not
+    count."""
+    others = dict(b=1 << 17), dict(h=1 << 11), dict(h=64, t=256)
+    for change in others:
+        assert rotate(lib, qo=strided(**change)) == BAD, change
+        assert rotate(lib, k=strided(APART), ko=strided(APART, **change)) == BAD, change
+        assert append(lib, qo=strided(**change)) == BAD, change
+    if torch.cuda.is_available():
+        return
+    # taken: without a GPU a call gets as far as the device
+    for change in others:
+        assert rotate(lib, qo=strided(3 * APART, **change)) not in (fa.FA_OK, BAD), change
+        assert rotate(lib, ko=strided(3 * APART, **change)) not in (fa.FA_OK, BAD), change
+        assert append(lib, qo=strided(3 * APART, **change)) not in (fa.FA_OK, BAD), change
+    for call in (rotate, append):
+        for kw in (dict(), dict(B=1, qo=strided(b=8)), dict(N=1, qo=strided(t=4))):
+            assert call(lib, **kw) not in (fa.FA_OK, BAD), kw
+
+
 def append(lib, cache=None, q=None, qo=None, H=4, k=None, v=None, layer=0, table=OK, most=4,
            start=OK, kv_len=OK, offsets=0, B=2, N=16, rot=None):
     return lib.fa_paged_append_rotated(
