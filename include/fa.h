@@ -393,7 +393,7 @@ fa_status_t fa_rotate(const fa_strided_t* q, const fa_strided_t* q_out, int H,
  *   row b has N tokens;
  * - offsets int32[B + 1], rising: q is [1, H, N, d], k_new and v_new are [1,
  *   h_kv, N, d], and row b has the tokens offsets[b] .. offsets[b + 1] - 1 of
- *   the N.  Tokens of no row are neither read nor written.
+ *   the N.  Tokens of no row are not written; they may be read, to no effect.
  * Token t of row b is at position start[b] + t.  q_out (q or apart from every
  * input) gets every token's queries turned; the turned keys and the values go into
  * the token's page as fa_paged_append says (positions from 0 and below

@@ -327,3 +327,27 @@ def test_values_behind_the_pairs_stay(d, dims, interleaved):
         for pool, x in ((kp, k), (vp, odd[1])):
             rows = pool[0].view(B, 2, h_kv, page, d).transpose(1, 2).reshape(B, h_kv, 16, d)
             assert torch.equal(bits(rows[:, :, :N]), bits(x))
+
+
+@pytest.mark.parametrize("d,interleaved", [(64, False), (128, True), (256, False)])
+def test_tokens_of_no_row_have_no_effect(d, interleaved):
+    """Whatever they hold: the rows' results are the same, and nothing is
+    written in their place."""
+    H, h_kv, page, T = 6, 2, 16, 90
+    rotary = rope.Rotary(d, interleaved=interleaved)
+    qkv = randn(1, T, H + 2 * h_kv, d).transpose(1, 2)
+    offsets, start, kv_len = cuda([3, 20, 20, 71], [5, 0, 30], [22, 4, 81])
+    table = torch.arange(18, dtype=torch.int32, device="cuda").view(3, 6)
+    outs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        x = qkv.clone()
+        x[:, :, :3], x[:, :, 71:] = fill, fill
+        q, kn, vn = x.split([H, h_kv, h_kv], 1)
+        kp, vp = pools(1, 18, h_kv, page, d, 0)
+        got = paged.append_rotated(q, kn, vn, paged.PagedKV(kp, vp), 0, table, start, kv_len,
+                                   rotary, offsets, inplace=True)
+        outs.append((got[:, :, 3:71].clone(), kp, vp))
+        for part in (got[:, :, :3], got[:, :, 71:]):
+            assert torch.equal(part, torch.full_like(part, fill)) or part.isnan().all() and fill != fill
+    for other in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
