@@ -61,8 +61,9 @@ __device__ __forceinline__ void row_tokens(const int* offsets, int b, int N, int
 // The angle of `pos` at `turns` 2^-64 turns a position, as sine and cosine
 // times `magnitude`.  The product modulo 2^64 is the angle's exact fraction of
 // a turn at any position (a product in fp32 would lose it from some thousands
-// on); its upper 32 bits become a float of half turns in [-1, 1), off by at
-// most 2^-25 of itself.
+// on).  Its upper 32 bits (what is cut off is below 2^-32 turns) become a float
+// of half turns in [-1, 1], rounded by at most 2^-24 of itself and 2^-25 in
+// all: together below 2^-26 + 2^-32 turns, 2^-23.3 radians.
 __device__ __forceinline__ void rotary_angle(unsigned long long turns, long long pos, float magnitude,
                                              float& s, float& c) {
   const unsigned long long a = turns * static_cast<unsigned long long>(pos);

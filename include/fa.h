@@ -361,8 +361,9 @@ typedef struct fa_strided {
  *   m (a cos - b sin),  m (a sin + b cos)   with m = magnitude;
  * values from dims on stay as they are.  turns: device memory, dims/2 values,
  * 8-byte aligned: a pair's angle per position as a fraction of a turn (modulo
- * one) times 2^64, which makes the angle exact to 2^-32 turns at any
- * position.  Sums are fp32; results are rounded to bf16 once.
+ * one) times 2^64.  At any position the angle is within 2^-26 + 2^-32 turns of
+ * x turns[i] 2^-64 modulo one (2^-26: its rounding to fp32; sine and cosine are
+ * fp32).  Sums are fp32; results are rounded to bf16 once.
  */
 typedef struct fa_rotary {
   const unsigned long long* turns;

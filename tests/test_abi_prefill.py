@@ -220,6 +220,29 @@ def test_turns():
             rope.turns_of([bad])
 
 
+def test_the_angle_in_fp32():
+    """A 64-bit fraction of a turn as the kernels take it, the upper 32 bits as
+    a float of half turns: within 2^-26 + 2^-32 turns, at the borders between
+    floats and next to half a turn above all, where it is more than 2^-32 off;
+    and no more than the plain turn's bound leaves for it."""
+    rng = np.random.default_rng(0)
+    whole = rng.integers(0, 1 << 64, 200000, dtype=np.uint64)
+    near = [(sign * (1 << b) + e) % (1 << 64) for b in range(32, 64) for sign in (1, -1)
+            for e in (-(1 << 39), -(1 << 38) - 1, -(1 << 33), -1, 0, 1, (1 << 38) + 1, (1 << 39))]
+    most = 0
+    for a in [int(x) for x in whole] + near + [(1 << 63) - 1, 1 << 63, (1 << 64) - 1]:
+        top = (a >> 32) - (1 << 32) * (a >> 63)          # the upper half as a signed int
+        half_turns = Fraction(float(np.float32(top))) / (1 << 31)
+        assert -1 <= half_turns <= 1
+        off = abs(half_turns / 2 - Fraction(a - (1 << 64) * (a >> 63), 1 << 64))
+        most = max(most, off)
+        assert off < Fraction(1, 1 << 26) + Fraction(1, 1 << 32)
+    assert most > Fraction(1, 1 << 32) * 32
+    # rope_ref's 2^-20 of (|a| + |b|) m: this, 2 units of sine and cosine below
+    # one, and 3 roundings of the products and their sum
+    assert 2 * math.pi * (2.0 ** -26 + 2.0 ** -32) + 2 * 2.0 ** -24 + 3 * 2.0 ** -24 < 2.0 ** -21
+
+
 def test_rotary_refuses():
     for bad in (dict(d=96), dict(d=64, dims=66), dict(d=64, dims=0), dict(d=64, dims=7),
                 dict(d=64, freqs=np.ones(31)), dict(d=64, magnitude=math.inf),
