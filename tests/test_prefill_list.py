@@ -16,7 +16,8 @@ import torch
 import paged_ref as R
 import rope_ref as P
 from exact_attention_04_gb300 import build as fabuild
-from exact_attention_04_gb300 import fa, paged, rope
+from exact_attention_04_gb300 import fa, paged
+from test_gpu_paged import cuda, pools
 
 SHAPE = "_ZN2fa13prefill_shapeEiiiibiPNS_12PrefillShapeE"  # fa::prefill_shape, Itanium ABI
 ROUNDS, TAIL = 4, 8          # ways to cut: rounds of all CTAs, pieces behind the last whole one
@@ -127,6 +128,21 @@ def test_every_piece_has_room(shape, seed):
 ENTRY = ("row", "n0", "ntok", "pos0", "len", "s0", "s1", "slot", "jlo", "ns", "rlo", "rhi")
 
 
+def left_list(ws, s, B):
+    """(the pieces that a call left in its workspace, cut tiles, most pieces of
+    one)."""
+    raw = ws.cpu().numpy()
+    items, _, joins, most = raw[:16].view(np.int32)
+    assert items % s.units == 0 and 0 < items // s.units <= s.entries
+    at = 256 + -(-(B + 1) * 4 // 256) * 256
+    rows = raw[at:at + items // s.units * 48].view(np.int32).reshape(-1, 12)
+    return [dict(zip(ENTRY, map(int, row))) for row in rows], joins, most
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fill", [0, 0x7f, 255])
 @pytest.mark.parametrize("long_row", [1, 3, 17])
@@ -154,17 +170,12 @@ def test_the_list_of_fallen_offsets(shape, long_row, fill):
     ws.fill_(fill)
     o, lse = paged.prefill(q, cache, 0, table, start, kv_len, off, ws=ws)
     fa.fa_check()
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    s = shape(B, H, T, 1, True, sms)
-    raw = ws.cpu().numpy()
-    items, _, joins, most_of_one = raw[:16].view(np.int32)
-    assert items % s.units == 0 and 0 < items // s.units <= s.entries
-    at = 256 + -(-(B + 1) * 4 // 256) * 256
-    got = raw[at:at + items // s.units * 48].view(np.int32).reshape(-1, 12)
+    s = shape(B, H, T, 1, True, sms())
+    got, joins, most_of_one = left_list(ws, s, B)
     want = tiles_of(offsets, T, s.tpt, s.tiles)
     assert len(want) == s.tiles                          # (some tiles were left out)
     spans = {}
-    for e in (dict(zip(ENTRY, row)) for row in got):
+    for e in got:
         assert e["row"] in rows + [0] and 0 <= e["n0"] < T and 0 < e["ntok"] <= s.tpt
         assert e["n0"] + e["ntok"] <= T and e["len"] == keys[e["row"]]
         spans.setdefault((e["row"], e["n0"]), []).append((e["s0"], e["s1"]))
@@ -180,3 +191,116 @@ def test_the_list_of_fallen_offsets(shape, long_row, fill):
     r = P.prefill(q[:, :, :first], k, v, 0, table[:1], start, kv_len, [0, first])
     R.check(r, "o", o[:, :, :first])
     R.check(r, "lse", lse[:, :, :first])
+
+
+CUT = [
+    # H, h_kv, d, page, layout, have, new, extra keys, causal, window, sinks, missing pages
+    (4, 1, 64, 16, "hnd", [60000], [5], 0, True, (40000, 0), 9000, 0.0),
+    (8, 2, 128, 16, "nhd", [30000, 40], [3, 2], 5, True, (20000, 0), 5000, 0.0),
+    (4, 2, 256, 32, "hnd", [30000], [2], 0, True, (20000, -1), 6000, 0.0),
+    (2, 1, 128, 24, "hnd", [50000], [9], 0, True, (40000, 0), 7000, 0.2),
+    (4, 1, 128, 5, "hnd", [40000], [3], 0, True, (30000, 0), 5100, 0.1),
+    (2, 1, 64, 160, "hnd", [50000], [4], 0, True, (35000, 0), 8400, 0.1),
+    (4, 1, 256, 300, "nhd", [50000], [3], 40, True, (30000, 0), 9200, 0.2),
+    (4, 4, 64, 16, "hnd", [6000, 3000], [7, 2], 0, False, None, 0, 0.0),
+    (8, 2, 128, 200, "hnd", [5000], [6], 0, False, None, 0, 0.2),
+    (4, 2, 256, 16, "nhd", [16000], [5], 0, False, None, 0, 0.0),
+    (4, 2, 128, 16, "hnd", [30000], [5], 900, False, (20000, 700), 5000, 0.0),
+    (2, 2, 64, 3, "hnd", [30000], [5], 500, False, (20000, 300), 4000, 0.1),
+    (150, 1, 64, 16, "hnd", [5000], [2], 0, True, None, 0, 0.1),         # a group of two tiles
+    (130, 1, 128, 32, "hnd", [30000], [1], 0, True, (22000, 0), 5000, 0.0),
+    (4, 1, 128, 16, "hnd", [9000, 0, 5000], [200, 300, 1], 0, True, (6000, 0), 1700, 0.1),
+    # few key tiles: a piece each
+    (4, 1, 64, 16, "hnd", [2000, 900], [5, 40], 0, True, (600, 0), 500, 0.1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,h_kv,d,page,layout,have,new,extra,causal,window,sinks,missing", CUT)
+def test_cut_walks(shape, H, h_kv, d, page, layout, have, new, extra, causal, window, sinks,
+                   missing):
+    """Walks that are cut under every mask: pieces that begin among the sinks'
+    tiles, that hold the step from these to the window, missing pages, and NaN
+    or infinities in every slot that no token of the row sees."""
+    rng = np.random.default_rng(d + page)
+    B, T, lens = len(have), sum(new), np.add(have, new) + extra
+    most = -(-int(max(lens)) // page)
+    pages = int(sum(-(-int(n) // page) for n in lens)) + 3
+    table, kv_len, _ = R.random_cache(rng, B, most, page, pages, lens, missing=missing)
+    clean = pools(1, pages, h_kv, page, d, 1, layout)
+    dirty = pools(1, pages, h_kv, page, d, 1, layout, float("nan"))
+    dirty[1].fill_(float("inf"))
+    left, right = (-1, -1) if window is None else window
+    for r, (a, m) in enumerate(zip(have, new)):
+        j, x = np.arange(lens[r])[None], a + np.arange(m)[:, None]
+        ok = np.ones((m, lens[r]), bool)
+        if causal:
+            ok &= j <= x
+        if right >= 0:
+            ok &= j <= x + right
+        if left >= 0:
+            ok &= (j >= x - left) | (j < sinks)
+        j = np.nonzero(ok.any(0))[0]
+        j = j[table[r, j // page] >= 0]
+        at, slot = (torch.from_numpy(y).long().cuda() for y in (table[r, j // page], j % page))
+        for to, of in zip(dirty, clean):
+            to[0, at, :, slot] = of[0, at, :, slot]
+    offsets = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn(1, H, T, d, generator=torch.Generator().manual_seed(5)).to(
+        torch.bfloat16).cuda()
+    table, start, kv_len, offsets = cuda(table, have, kv_len, offsets)
+    cache = paged.PagedKV(*dirty)
+    kw = dict(causal=causal, window=window, sinks=sinks)
+    ws = paged.prefill_workspace(cache, B, H, T, packed=True)
+    ws.fill_(255)
+    o, lse = paged.prefill(q, cache, 0, table, start, kv_len, offsets, ws=ws, **kw)
+    fa.fa_check()
+    got, joins, _ = left_list(ws, shape(B, H, T, h_kv, True, sms()), B)
+    assert joins > 0
+    if sinks:
+        assert any(0 < e["s0"] < e["ns"] for e in got)
+    if sinks > 500 and sms() == 152:
+        assert any(e["slot"] >= 0 and e["s0"] < e["ns"] < e["s1"] for e in got)
+    r = P.prefill(q, *clean, 0, table, start, kv_len, offsets, **kw)
+    R.check(r, "o", o)
+    R.check(r, "lse", lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,h_kv,N,d,page,new,causal,window,sinks", [
+    (16, 4, 9000, 128, 16, 2496, True, (6000, 0), 300),
+    (16, 4, 8000, 256, 32, 2496, True, (4000, 0), 5),
+    (16, 16, 6000, 64, 16, 1280, True, (1500, 0), 200),
+    (16, 16, 5000, 64, 160, 1280, False, None, 0),
+    (16, 4, 6000, 128, 24, 2496, False, (1500, 700), 0),
+    (4, 4, 9000, 256, 16, 4992, False, None, 0)])
+def test_cut_rounds_are_forward_s(shape, H, h_kv, N, d, page, new, causal, window, sinks):
+    """Many tiles, of which those behind the last whole round are cut, under
+    windows and without causality, against the forward of the whole sequence."""
+    g = torch.Generator().manual_seed(N + d)
+    q, k, v = (torch.randn(1, h, N, d, generator=g).to(torch.bfloat16).cuda()
+               for h in (H, h_kv, h_kv))
+    most = -(-N // page)
+    pool = torch.zeros(2, 1, most, h_kv, page, d, dtype=torch.bfloat16, device="cuda")
+    order = torch.randperm(most, generator=g).cuda()
+    for i, t in enumerate((k, v)):
+        padded = torch.zeros(1, h_kv, most * page, d, dtype=torch.bfloat16, device="cuda")
+        padded[:, :, :N] = t
+        pool[i, 0, order] = padded.view(h_kv, most, page, d).transpose(0, 1)
+    table, start, kv_len = order.to(torch.int32)[None], *cuda([N - new], [N])
+    cache = paged.PagedKV(pool[0], pool[1])
+    ws = paged.prefill_workspace(cache, 1, H, new)
+    ws.fill_(255)
+    kw = dict(causal=causal, window=window, sinks=sinks)
+    o, lse = paged.prefill(q[:, :, N - new:], cache, 0, table, start, kv_len, ws=ws, **kw)
+    fa.fa_check()
+    s = shape(1, H, new, h_kv, False, sms())
+    got, joins, _ = left_list(ws, s, 1)
+    if sms() == 152:
+        assert joins > 0
+    assert any(e["slot"] < 0 for e in got) or not joins
+    want, want_lse = (t[:, :, N - new:] for t in fa.forward(q, k, v, **kw))
+    mean = fa.forward(q, k, v.abs(), **kw)[0][:, :, N - new:].float() * 1.02
+    bound = 2.02 * ((R.BF16 + R.F32) * mean + R.BF16 * want.float().abs()) + R.TINY
+    assert ((o.float() - want.float()).abs() <= bound).all()
+    assert (lse - want_lse).abs().max() <= 2e-4
