@@ -1041,8 +1041,10 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
       }
       const uint32_t ph = e_it & 1;
       ++e_it;
-      if (!mbar_wait_warp(&sm.stats_full, ph, abort, kWaitTimeoutNs) ||
-          !mbar_wait_warp(&sm.o_done, ph, abort, kWaitTimeoutNs)) {
+      // (a wait for the whole piece: up to 17 us a key tile, in pages of one)
+      const uint64_t limit = kWaitTimeoutNs + 100000ull * t.nst;
+      if (!mbar_wait_warp(&sm.stats_full, ph, abort, limit) ||
+          !mbar_wait_warp(&sm.o_done, ph, abort, limit)) {
         fail(p.status, abort, kSiteEpi);
         break;
       }

@@ -495,3 +495,25 @@ def test_serving_steps(d, page, window, sinks):
         kv_len = new_len
         if window is not None:
             table, ref = paged.trim(cache, table, kv_len, ref, window[0], sinks)
+
+
+def test_a_walk_of_more_than_two_seconds():
+    """A piece that takes longer than a single wait may (16.6 million keys in
+    pages of one, a row of as many K/V heads as CTAs, so that none is cut): the
+    epilogue's wait grows with its key tiles.  All keys are one and values are
+    -1, 0, 1, so that every sum is a whole number below 2^24: O is V, and LSE
+    the score and the logarithm of the keys."""
+    n, d = 16_600_000, 256
+    H = torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(0)
+    k = randn(1, 1, H, 1, d)
+    v = torch.randint(-1, 2, (1, 1, H, 1, d), generator=g).to(torch.bfloat16).cuda()
+    q = randn(1, H, 1, d, seed=1)
+    table = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    start, kv_len = cuda([n - 1], [n])
+    o, lse = paged.prefill(q, paged.PagedKV(k, v), 0, table, start, kv_len)
+    fa.fa_check()
+    assert torch.equal(o[0, :, 0], v[0, 0, :, 0])
+    s = (P.f64(q)[0, :, 0] * P.f64(k)[0, 0, :, 0]).sum(-1) * d ** -0.5
+    # an LSE next to 17 has fp32 steps of 2^-19
+    assert (P.f64(lse)[0, :, 0] - s - np.log(n)).abs().max() <= R.F32 + 2.0 ** -18
