@@ -70,6 +70,11 @@ constexpr int kMostTail = 8;       // pieces of a tile behind the last whole rou
 // / 74; four chunks of 300 138 / 132 / 149; two of 1024 305 / 305 / 288).
 constexpr float kCutTiles = 6.f;
 constexpr int kRing = 8;           // key tiles whose masks are kept
+// The epilogue's wait for a piece: 2^23 key tiles of up to 17 us (d = 256, pages
+// of one).  The roles that work tile by tile give up after kWaitTimeoutNs, and
+// raise the flag that ends this wait too.  (A limit by the piece's tiles: d = 64,
+// N = 8192, pages of 128 594 / 602 us.)
+constexpr unsigned long long kPieceTimeoutNs = 200000000000ull;
 
 // A piece as the plan lists it, for every unit (K/V head, part of its group).
 struct alignas(16) Entry {
@@ -1041,10 +1046,8 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
       }
       const uint32_t ph = e_it & 1;
       ++e_it;
-      // (a wait for the whole piece: up to 17 us a key tile, in pages of one)
-      const uint64_t limit = kWaitTimeoutNs + 100000ull * t.nst;
-      if (!mbar_wait_warp(&sm.stats_full, ph, abort, limit) ||
-          !mbar_wait_warp(&sm.o_done, ph, abort, limit)) {
+      if (!mbar_wait_warp(&sm.stats_full, ph, abort, kPieceTimeoutNs) ||
+          !mbar_wait_warp(&sm.o_done, ph, abort, kPieceTimeoutNs)) {
         fail(p.status, abort, kSiteEpi);
         break;
       }
