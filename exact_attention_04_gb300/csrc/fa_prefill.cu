@@ -32,12 +32,14 @@
 //
 // What bounds it.  Many query rows: the softmax's instructions and the tensor
 // pipe, as in the forward (N = 8192, not causal, pages of 16 / of 128 / the forward
-// over contiguous K and V: d = 128, H = 32, h_kv = 8 712 / 711 / 676 us, 0.80 of the
-// bf16 peak; d = 256, H = 16, h_kv = 4 688 / 675 / 668; d = 64, B = 2, H = 16 612 /
-// 595 / 594, where eight copies a tile of 16-token pages keep the producers busy).
+// over contiguous K and V: d = 128, H = 32, h_kv = 8 713 / 712 / 678 us, 0.80 of the
+// bf16 peak; d = 256, H = 16, h_kv = 4 695 / 672 / 668; d = 64, B = 2, H = 16 612 /
+// 595 / 593, where eight copies a tile of 16-token pages keep the producers busy).
 // Few rows: HBM (32 rows of 4 tokens after 8192, H = 32, h_kv = 8, d = 128: 1077 MB
 // in 166 us, 0.95 of the copy bandwidth).  Short calls: the chain plan (4 us), first
-// loads (4), a tile or two, and join (3).
+// loads (4), a tile or two, and join (3 where something is cut): one row of 5
+// tokens after 500 / 1000 / 1050, H = 32, h_kv = 8, d = 128 15 / 18 / 15 us, of which
+// only the last, of nine key tiles, is cut by the estimate.
 #include <climits>
 #include <cmath>
 
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         int from = 0, limit = INT_MAX;
         int pieces = tiles * p.units;
         float whole = 0.f, length = longest, rest = W, extra = 1.f;
+        // (within 2 / 10 / 30 / 100 %: 2048 tokens after 14336 386 / 345 / 345 / 345 us,
+        // after 30720 728 / 686 / 686 / 686; other chunks are one or the other by far)
         const bool alike = W * 1.1f > longest * pieces;
         bool can = k < 0;
         if (k >= 0 && k < kMostRounds) {
@@ -432,7 +436,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           whole = rounds * (longest + 1.f);
         }
         if (k >= 0) extra = kCutTiles;
-        // (level but for the last pieces: of any length, or short ones)
+        // (level but for the last pieces: of any length, or short ones, of which half
+        // the longest is left: none of it / a quarter / half / three quarters / all, 32
+        // rows of which four bring 300 tokens, H = 16, h_kv = 4 138 / 137 / 126 / 125 /
+        // 124 us, four chunks of 300 73 / 73 / 73 / 68 / 73, two of 1024 289 / 289 / 306 /
+        // 306 / 306; others alike)
         const float even = fmaxf(__fdividef(rest + pieces * extra, p.grid) +
                                      (once && !alike ? 0.5f * length : length),
                                  length + extra);
@@ -476,8 +484,9 @@ struct Cfg {
   // d = 256: O takes 256 columns of tensor memory, and P buffers of their own
   // let the one S buffer be refilled once the softmax has loaded it.
   static constexpr bool SEP = D == 256;
-  // key halves a warp (d = 128, N = 8192: 712 us; one warp a row, with three S
-  // buffers, 878.  d = 256: one warp a row, since two O parts would not fit)
+  // key halves a warp (d = 128, N = 8192, pages of 16 / 128: 713 / 712 us; one warp
+  // a row, with three S buffers, 882 / 958.  d = 256: one warp a row, since two O
+  // parts would not fit)
   static constexpr int NHALF = D <= 128 ? 2 : 1;
   static constexpr int NSB = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int NPB = SEP ? 2 : NSB;
@@ -1318,7 +1327,7 @@ __global__ void __launch_bounds__(Cfg<D, GROUPED>::THREADS, 1)
 // 8000, d = 128 41 / 37, 32 rows of 4 tokens 183 / 180, 2048 tokens after 30720 691
 // / 688); more: a block a row, its warps every fourth piece each.  A kernel of its
 // own: the last CTA to finish a tile joining it ran cold code on one SM (one row
-// of 5 tokens after 1000 17 us a call, 40 so).
+// of 5 tokens after some 1000, when a call took 17 us, 40).
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefillParams p) {
   grid_dependency_wait();

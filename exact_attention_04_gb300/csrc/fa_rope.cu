@@ -28,7 +28,8 @@ using namespace ptx;
 
 // Warps of a block, and heads whose loads are in flight together: small blocks
 // even the last wave out (H = 16 + 16, N = 8192, B = 2, d = 128: 4 / 8 / 16 warps
-// 41.2 / 44.4 / 58.5 us; 2 / 4 / 8 heads 48.5 / 44.4 / 49.5 with 8).
+// 41.3 / 45.9 / 78.0 us; 2 / 4 / 8 heads 44.8 / 41.3 / 44.9; 36864 new tokens, 32 + 8
+// + 8 heads, into pages 141 / 137 / 139).
 constexpr int kWarps = 4;
 constexpr int kUnroll = 4;
 
