@@ -34,9 +34,10 @@
  *   dimension, or a GPU that is not sm_103), FA_ERR_CUDA (a CUDA call or
  *   kernel launch failed; cudaGetLastError() holds the detail).  Argument
  *   errors are reported before anything is enqueued.
- * - Kernels never spin forever: every wait inside them gives up after about
- *   two seconds, records FA_ERR_TIMEOUT in a per-device status word and
- *   returns; fa_check() reports and clears it.
+ * - Kernels never spin forever: every wait inside them for a step of the work
+ *   gives up after about two seconds, records FA_ERR_TIMEOUT in a per-device
+ *   status word and returns, which ends the other waits of its block too;
+ *   fa_check() reports and clears it.
  */
 #ifndef FA_H_
 #define FA_H_
