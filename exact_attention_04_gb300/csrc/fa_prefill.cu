@@ -1594,7 +1594,8 @@ fa_status_t fa_prefill_paged(const fa_strided_t* q, const fa_paged_kv_t* cache, 
     return FA_ERR_INVALID_ARG;
   const fa_status_t ds = fa::device_facts(&sms, &max_smem, &status);
   if (ds != FA_OK) return ds;
-  if (!fa::prefill_shape(B, H, N, pool.h_kv, offsets != nullptr, sms, &s)) return FA_ERR_INVALID_ARG;
+  if (!fa::prefill_shape(B, H, N, pool.h_kv, offsets != nullptr, sms, &s))
+    return FA_ERR_INVALID_ARG;
   const fa::Layout l = fa::layout_of(s, B, pool.d);
   if (workspace_bytes < l.total) return FA_ERR_INVALID_ARG;
   fa::PrefillParams p = {};

@@ -348,6 +348,6 @@ def test_tokens_of_no_row_have_no_effect(d, interleaved):
                                    rotary, offsets, inplace=True)
         outs.append((got[:, :, 3:71].clone(), kp, vp))
         for part in (got[:, :, :3], got[:, :, 71:]):
-            assert torch.equal(part, torch.full_like(part, fill)) or part.isnan().all() and fill != fill
+            assert part.isnan().all() if fill != fill else (part == fill).all()
     for other in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
